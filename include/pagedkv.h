@@ -358,6 +358,74 @@ pkv_status pkv_reshape_and_cache(const void* k, const void* v, void* k_cache, vo
                                  pkv_dtype dtype, cudaStream_t stream);
 
 /*
+ * The new tokens' way into the cache in one pass: per-head norm of queries and
+ * keys, rotation by position, and the cache write (pkv_reshape_and_cache) of
+ * the rotated keys and the values.  For models whose query heads share
+ * key/value heads (num_kv_heads <= num_heads) or that have one of each.
+ * For token t and head row x of its queries or keys, in fp32 and rounded once
+ * at the end:
+ *   x <- x / sqrt(mean(x^2) + eps) * weight     when that kind's weight is given
+ *   pair i of x turns by the angle positions[t] * f_i:
+ *     (a, b) <- rope_scale * (a cos - b sin, b cos + a sin)
+ * Pair i, i < rot_dim / 2, is (x[i], x[i + rot_dim / 2]) or, with interleaved
+ * != 0, (x[2i], x[2i + 1]); elements from rot_dim on are normed but not turned.
+ * rot_dim is a multiple of 8 in [0, head_dim]; 0 turns nothing (phases may be
+ * NULL).  Query rows go to q_out for every token; key and value rows to slot
+ * slot_mapping[t] of the caches, for tokens whose slot is not negative (values
+ * bit for bit).  Distinct slots, a slot past the pool (skipped,
+ * PKV_DEVERR_BAD_SLOT; its query is still written) and num_tokens == 0 are as
+ * in pkv_reshape_and_cache.
+ *   q_out         [num_tokens][num_heads][head_dim]; may be q (same address,
+ *                 q_stride == num_heads * head_dim), else it shares no memory
+ *                 with q, k or v (PKV_ERR_INVALID)
+ *   q, k, v       row t at t * stride elements (strides: multiples of 8, at
+ *                 least heads * head_dim), its heads side by side: slices of a
+ *                 joint projection's output are taken as they are
+ *   k_cache, ...  [num_blocks][num_kv_heads][block_size][head_dim]
+ *   positions     int32 [num_tokens] (any value; 0 turns nothing)
+ *   phases        uint64 [rot_dim / 2], device: f_i in 2^-64 turns per position,
+ *                 modulo 2^64 (pkv_rope_phases).  Angles are exact modulo one
+ *                 turn at any position.
+ *   q_weight, k_weight   fp32 [head_dim], device, 16-byte aligned; NULL: no norm
+ * One launch on `stream`, no workspace.
+ */
+pkv_status pkv_norm_rope_and_cache(void* q_out, const void* q, const void* k, const void* v,
+                                   int64_t q_stride, int64_t k_stride, int64_t v_stride,
+                                   void* k_cache, void* v_cache, const int64_t* slot_mapping,
+                                   const int32_t* positions, const uint64_t* phases, int rot_dim,
+                                   int interleaved, float rope_scale, const float* q_weight,
+                                   const float* k_weight, float eps, int num_tokens,
+                                   int num_heads, int num_kv_heads, int head_dim, int block_size,
+                                   int64_t num_blocks, pkv_dtype dtype, cudaStream_t stream);
+
+/*
+ * Rotation frequencies (host only).  pkv_rope_inv_freq writes inv_freq[rot_dim
+ * / 2], radians per position, and the factor to pass as rope_scale:
+ *   PKV_ROPE_PLAIN     f_i = base^(-2i / rot_dim), factor 1
+ *   PKV_ROPE_LINEAR    f_i / factor: positions squeezed into the trained length
+ *   PKV_ROPE_BASE      base replaced by base * factor^(rot_dim / (rot_dim - 2)):
+ *                      the slowest pair is slowed by factor, the fastest kept
+ *   PKV_ROPE_BY_PARTS  pairs that make more than beta_fast turns over
+ *                      original_len positions kept, those that make fewer than
+ *                      beta_slow slowed by factor, a linear ramp over the pairs
+ *                      between; rope_scale = 0.1 ln(factor) + 1
+ * (original_len and the betas are read for BY_PARTS only; factor >= 1 for all
+ * but PLAIN).  pkv_rope_phases turns n frequencies into the fixed-point form
+ * that pkv_norm_rope_and_cache reads (copy them to the device once).
+ */
+typedef enum {
+    PKV_ROPE_PLAIN = 0,
+    PKV_ROPE_LINEAR = 1,
+    PKV_ROPE_BASE = 2,
+    PKV_ROPE_BY_PARTS = 3
+} pkv_rope_scaling;
+
+pkv_status pkv_rope_inv_freq(int rot_dim, double base, pkv_rope_scaling scaling, double factor,
+                             int original_len, double beta_fast, double beta_slow,
+                             double* inv_freq, float* rope_scale);
+pkv_status pkv_rope_phases(const double* inv_freq, int n, uint64_t* phases);
+
+/*
  * For each pair p: k_cache[dst] = k_cache[src] and v_cache[dst] = v_cache[src],
  * whole blocks (all heads).  Destinations must be distinct and must not be the
  * source of any pair in the same call (copy-on-write always copies into a

@@ -5,9 +5,13 @@
 // stores, consecutive threads on consecutive 16-byte pieces of a row.
 #include <cuda_runtime.h>
 
+#include "launch.cuh"
 #include "pkv_internal.h"
 
 namespace {
+
+using pkv::launch_pdl;
+using pkv::pdl_wait_then_release;
 
 __device__ __forceinline__ uint4 ld_nc_v4(const void* p) {
     uint4 r;
@@ -15,30 +19,6 @@ __device__ __forceinline__ uint4 ld_nc_v4(const void* p) {
                  : "=r"(r.x), "=r"(r.y), "=r"(r.z), "=r"(r.w)
                  : "l"(p));
     return r;
-}
-
-// Programmatic dependent launch: wait for the preceding kernel in the stream
-// before touching memory (a no-op without the dependency), then let the next
-// kernel's CTAs be scheduled while this one runs.
-__device__ __forceinline__ void pdl_wait_then_release() {
-    asm volatile("griddepcontrol.wait;" ::: "memory");
-    asm volatile("griddepcontrol.launch_dependents;" ::: "memory");
-}
-
-template <typename... Args>
-cudaError_t launch_pdl(void (*kernel)(Args...), dim3 grid, dim3 block, cudaStream_t stream,
-                       Args... args) {
-    cudaLaunchAttribute attr[1];
-    attr[0].id = cudaLaunchAttributeProgrammaticStreamSerialization;
-    attr[0].val.programmaticStreamSerializationAllowed = 1;
-    cudaLaunchConfig_t cfg = {};
-    cfg.gridDim = grid;
-    cfg.blockDim = block;
-    cfg.dynamicSmemBytes = 0;
-    cfg.stream = stream;
-    cfg.attrs = attr;
-    cfg.numAttrs = 1;
-    return cudaLaunchKernelEx(&cfg, kernel, args...);
 }
 
 // One row = one (token, head): VPR 16-byte pieces of K and as many of V (8

@@ -74,6 +74,12 @@ def lib():
             "pkv_paged_attention_prefill_write": ([P, P, P, P, P, P, P, P, P, f32, i32, i32, i32,
                                                    i32, i32, i64, i32, i32, i32, P], i32),
             "pkv_reshape_and_cache": ([P, P, P, P, P, i32, i32, i32, i32, i64, i32, P], i32),
+            "pkv_rope_inv_freq": ([i32, ctypes.c_double, i32, ctypes.c_double, i32,
+                                   ctypes.c_double, ctypes.c_double, P, ctypes.POINTER(f32)],
+                                  i32),
+            "pkv_rope_phases": ([P, i32, P], i32),
+            "pkv_norm_rope_and_cache": ([P, P, P, P, i64, i64, i64, P, P, P, P, P, i32, i32, f32,
+                                         P, P, f32, i32, i32, i32, i32, i32, i64, i32, P], i32),
             "pkv_copy_blocks": ([P, P, P, i32, i32, i32, i32, i64, i32, P], i32),
             "pkv_swap_blocks": ([P, P, P, P, P, i32, i32, i32, i32, i64, i64, i32, P], i32),
             "pkv_get_device_error": ([ctypes.POINTER(ctypes.c_int32), i32, P], i32),
@@ -412,6 +418,121 @@ def reshape_and_cache(k, v, k_cache, v_cache, slot_mapping, stream=None):
                                        _dev(v_cache, "v_cache"),
                                        _dev(slot_mapping, "slot_mapping", torch.int64, 1),
                                        T, H, D, B, nb, _dtype_code(k.dtype), _stream(stream)))
+
+
+ROPE_SCALINGS = {"plain": 0, "linear": 1, "base": 2, "by_parts": 3}
+
+
+def rope_inv_freq(rot_dim, base=10000.0, scaling="plain", factor=1.0, original_len=0,
+                  beta_fast=32.0, beta_slow=1.0):
+    """(inv_freq float64 [rot_dim // 2] in radians per position, rope_scale):
+    the rotation frequencies, plain or scaled for longer contexts ("linear",
+    "base" or "by_parts")."""
+    if scaling not in ROPE_SCALINGS:
+        raise ValueError("scaling must be one of %s" % ", ".join(ROPE_SCALINGS))
+    freq = np.empty(max(int(rot_dim) // 2, 1), dtype=np.float64)
+    rs = ctypes.c_float(0.0)
+    _check("pkv_rope_inv_freq",
+           lib().pkv_rope_inv_freq(int(rot_dim), float(base), ROPE_SCALINGS[scaling],
+                                   float(factor), int(original_len), float(beta_fast),
+                                   float(beta_slow), freq.ctypes.data_as(ctypes.c_void_p),
+                                   ctypes.byref(rs)))
+    return freq, rs.value
+
+
+def rope_phases(inv_freq, device="cuda"):
+    """Frequencies (radians per position) as the int64 tensor of 2^-64 turns
+    per position that norm_rope_and_cache reads; made once and kept."""
+    torch = _torch()
+    f = np.ascontiguousarray(inv_freq, dtype=np.float64).reshape(-1)
+    out = np.empty(f.shape[0], dtype=np.int64)
+    _check("pkv_rope_phases",
+           lib().pkv_rope_phases(f.ctypes.data_as(ctypes.c_void_p), f.shape[0],
+                                 out.ctypes.data_as(ctypes.c_void_p)))
+    return torch.from_numpy(out).to(device)
+
+
+def _ptr(t, name, dev, dtype):
+    """data_ptr of a contiguous CUDA tensor of that device and type."""
+    if t.get_device() != dev:
+        raise ValueError("%s must be a CUDA tensor on the device of q" % name)
+    if t.dtype != dtype:
+        raise TypeError("%s must be %s, got %s" % (name, dtype, t.dtype))
+    if not t.is_contiguous():
+        raise ValueError("%s must be contiguous" % name)
+    return t.data_ptr()
+
+
+def _rows(t, name, dev, dtype):
+    """(data_ptr, token stride) of [tokens, heads, head_dim] whose heads lie side
+    by side; tokens may be apart (a slice of a joint projection's output)."""
+    if t.get_device() != dev:
+        raise ValueError("%s must be a CUDA tensor on the device of q" % name)
+    if t.dtype != dtype:
+        raise TypeError("%s must be %s, got %s" % (name, dtype, t.dtype))
+    T, H, D = t.shape
+    st = t.stride()
+    if (D > 1 and st[2] != 1) or (H > 1 and st[1] != D):
+        raise ValueError("%s must have its heads side by side in each token's row" % name)
+    # one token has no next one: any stride will do
+    return t.data_ptr(), st[0] if T > 1 else H * D
+
+
+def _run(fn, dev, stream, args):
+    """The library call `fn` with the given device current, on `stream` (or that
+    device's current one)."""
+    torch = _torch()
+    if torch.cuda.current_device() != dev:
+        with torch.cuda.device(dev):
+            return _run(fn, dev, stream, args)
+    handle = stream.cuda_stream if stream is not None else \
+        torch._C._cuda_getCurrentRawStream(dev)
+    st = getattr(lib(), fn)(*args, handle)
+    if st != PKV_OK:
+        _check(fn, st)
+
+
+def norm_rope_and_cache(q_out, q, k, v, k_cache, v_cache, slot_mapping, positions, phases,
+                        q_weight=None, k_weight=None, eps=1e-6, rope_scale=1.0,
+                        interleaved=False, stream=None):
+    """The new tokens' norm (where a weight is given), rotation and cache write
+    in one pass: turned queries [T, H, D] to q_out (which may be q), turned keys
+    and the values [T, HK, D] to their slots of the caches [blocks, HK, B, D].
+    q, k and v may be slices of one projection's output.  phases: rope_phases()
+    of rot_dim / 2 frequencies, or None to turn nothing; weights: fp32 [D]."""
+    torch = _torch()
+    T, H, D = q.shape
+    nb, HK, B, D2 = k_cache.shape
+    dev, dt = q.get_device(), q.dtype
+    if D2 != D or k.shape != (T, HK, D) or v.shape != (T, HK, D) or \
+            v_cache.shape != k_cache.shape:
+        raise ValueError("q/k/v/cache shape mismatch")
+    if q_out.shape != q.shape:
+        raise ValueError("q_out must have q's shape")
+    if slot_mapping.shape != (T,) or positions.shape != (T,):
+        raise ValueError("slot_mapping and positions must be [num_tokens]")
+    if dev < 0:
+        raise ValueError("q must be a CUDA tensor")
+    qp, qs = _rows(q, "q", dev, dt)
+    kp, ks = _rows(k, "k", dev, dt)
+    vp, vs = _rows(v, "v", dev, dt)
+    rot, ph = 0, None
+    if phases is not None:
+        if phases.dim() != 1:
+            raise ValueError("phases must be [rot_dim / 2]")
+        rot, ph = 2 * phases.shape[0], _ptr(phases, "phases", dev, torch.int64)
+    wp = []
+    for w, n in ((q_weight, "q_weight"), (k_weight, "k_weight")):
+        if w is not None and w.shape != (D,):
+            raise ValueError("%s must be [head_dim]" % n)
+        wp.append(None if w is None else _ptr(w, n, dev, torch.float32))
+    _run("pkv_norm_rope_and_cache", dev, stream,
+         (_ptr(q_out, "q_out", dev, dt), qp, kp, vp, qs, ks, vs,
+          _ptr(k_cache, "k_cache", dev, dt), _ptr(v_cache, "v_cache", dev, dt),
+          _ptr(slot_mapping, "slot_mapping", dev, torch.int64),
+          _ptr(positions, "positions", dev, torch.int32), ph, rot, 1 if interleaved else 0,
+          float(rope_scale), wp[0], wp[1], float(eps), T, H, HK, D, B, nb, _dtype_code(dt)))
+    return q_out
 
 
 def copy_blocks(k_cache, v_cache, pairs, stream=None):
