@@ -229,11 +229,51 @@ pkv_status pkv_contiguous_attention_decode(void* out, const void* q, const void*
                                            size_t workspace_bytes, cudaStream_t stream);
 
 /*
+ * Decode attention for query heads that share key/value heads (num_heads a
+ * multiple of num_kv_heads; equal counts are the ungrouped case), with capped
+ * scores, a sliding window and a distance bias.  With G = num_heads /
+ * num_kv_heads, n = context_lens[s], p = n - 1, query head h:
+ *   z_t = scale * q[s][h] . K_s[t][h / G]
+ *   z_t = softcap * tanh(z_t / softcap)          when softcap > 0
+ *   z_t = z_t + slopes[h] * (t - p)              when slopes is not NULL
+ *   out[s][h] = sum_t softmax_t(z) V_s[t][h / G],   lo <= t < n,
+ * lo = max(0, n - window) when window > 0, else 0.  fp32 arithmetic (weights
+ * keep at least 16 bits in the products with V), one rounding at the end.
+ * context_lens[s] == 0 gives a zero row.
+ *   k_cache, v_cache  [num_blocks][num_kv_heads][block_size][head_dim]
+ *   q, out            [num_seqs][num_heads][head_dim]
+ *   slopes            fp32 [num_heads], device, or NULL
+ * Table entries of blocks that hold no visible token (past the context, or
+ * before the window: a server may have given those back) are not used, and
+ * what the pool holds at hidden tokens does not matter.  A bad entry sets
+ * PKV_DEVERR_BAD_BLOCK and a context length out of range
+ * PKV_DEVERR_BAD_CONTEXT (clamped).  num_blocks * num_kv_heads * block_size
+ * must stay below 2^31 (the tiled copies address cache rows with 32-bit
+ * coordinates).  The split of the work depends on the sizes and lengths alone:
+ * results are bit-identical from call to call on one GPU.  Two launches on
+ * `stream`.
+ * workspace: device, >= pkv_decode_grouped_workspace_size(...) bytes, 256-byte
+ * aligned, no initialisation; two calls in flight at once must not share it.
+ * (The pages' formula, zhaifeiyue.github.io detail page, with K/V heads shared
+ * by query heads and its scores changed as above.)
+ */
+pkv_status pkv_decode_grouped_workspace_size(int num_seqs, int num_heads, int num_kv_heads,
+                                             int head_dim, int block_size, int max_blocks_per_seq,
+                                             size_t* bytes);
+pkv_status pkv_paged_attention_decode_grouped(
+    void* out, const void* q, const void* k_cache, const void* v_cache,
+    const int32_t* block_tables, const int32_t* context_lens, const float* slopes, float scale,
+    float softcap, int window, int num_seqs, int num_heads, int num_kv_heads, int head_dim,
+    int block_size, int max_blocks_per_seq, int64_t num_blocks, pkv_dtype dtype, void* workspace,
+    size_t workspace_bytes, cudaStream_t stream);
+
+/*
  * Bound, in nanoseconds, of the decode kernels' pipeline waits (a consumer
  * warp waiting for a ring stage's copy, the producer waiting for a free stage
  * or for a claimed chunk's query slice, the consumer warps meeting at the end
- * of a piece), for every later launch of pkv_paged_attention_decode and
- * pkv_paged_attention_decode_noalloc from any host thread.  Default 1 s; at
+ * of a piece), for every later launch of pkv_paged_attention_decode, its
+ * _noalloc, _append, _shared and _grouped forms and
+ * pkv_contiguous_attention_decode from any host thread.  Default 1 s; at
  * most 10 s (larger values: PKV_ERR_INVALID, nothing changed).  A wait that
  * runs out sets PKV_DEVERR_TIMEOUT; the CTA then stops issuing copies, its
  * other waits give up at once, its results for the call are not valid, and it

@@ -39,11 +39,16 @@ def attend(q, kc, vc, tables, ctx, query_start, scale, softcap=0.0, window=0, sl
     out = np.full((rows, H, D), np.nan)
     for s, n in enumerate(ctx):
         n = int(n)
-        blocks = [int(tables[s][t // B]) for t in range(0, n, B)]
-        if n:
-            k = np.concatenate([kc[b] for b in blocks], axis=1)[:, :n]
-            v = np.concatenate([vc[b] for b in blocks], axis=1)[:, :n]
         first, last = int(query_start[s]), int(query_start[s + 1])
+        if last == first:
+            continue
+        # the blocks that hold a token some row sees
+        seen = max(0, n - (last - first) - window + 1) if window > 0 else 0
+        base = seen // B * B
+        blocks = [int(tables[s][t // B]) for t in range(base, n, B)]
+        if n:
+            k = np.concatenate([kc[b] for b in blocks], axis=1)
+            v = np.concatenate([vc[b] for b in blocks], axis=1)
         for r in range(first, last):
             p = n - (last - first) + (r - first)
             lo = max(0, p - window + 1) if window > 0 else 0
@@ -52,11 +57,11 @@ def attend(q, kc, vc, tables, ctx, query_start, scale, softcap=0.0, window=0, sl
                 continue
             for h in range(H):
                 g = h // (H // HK)
-                z = k[g, lo:p + 1] @ q[r, h] * scale
+                z = k[g, lo - base:p + 1 - base] @ q[r, h] * scale
                 if softcap > 0:
                     z = softcap * np.tanh(z / softcap)
                 if slopes is not None:
                     z = z + float(slopes[h]) * (np.arange(lo, p + 1) - p)
                 e = np.exp(z - z.max())
-                out[r, h] = (e @ v[g, lo:p + 1]) / e.sum()
+                out[r, h] = (e @ v[g, lo - base:p + 1 - base]) / e.sum()
     return out

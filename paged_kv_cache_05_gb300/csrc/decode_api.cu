@@ -6,9 +6,8 @@
 #include <mutex>
 #include <random>
 
-#include <cudaTypedefs.h>
-
 #include "pkv_internal.h"
+#include "tensor_map.h"
 
 namespace {
 
@@ -67,36 +66,6 @@ cudaError_t ctas_per_sm(const pkv::DecodeKernel* k, int dev, size_t smem, int* o
 }
 
 bool aligned(const void* p, uintptr_t a) { return (reinterpret_cast<uintptr_t>(p) & (a - 1)) == 0; }
-
-// The driver's tiled tensor-map encoder (a host computation), looked up once.
-PFN_cuTensorMapEncodeTiled_v12000 map_encoder() {
-    static PFN_cuTensorMapEncodeTiled_v12000 fn = nullptr;
-    static std::once_flag once;
-    std::call_once(once, [] {
-        void* p = nullptr;
-        cudaDriverEntryPointQueryResult q;
-        if (cudaGetDriverEntryPointByVersion("cuTensorMapEncodeTiled", &p, 12000,
-                                             cudaEnableDefault, &q) == cudaSuccess &&
-            q == cudaDriverEntryPointSuccess)
-            fn = reinterpret_cast<PFN_cuTensorMapEncodeTiled_v12000>(p);
-    });
-    return fn;
-}
-
-// A pool [num_blocks][H][B][D] seen as rows of D 16-bit elements; boxes of
-// 64 columns x box_rows rows, 128-byte swizzle (the shared-prefix steps).
-bool pool_map(CUtensorMap* m, bool bf16, const void* pool, int64_t rows, int D, int box_rows) {
-    const PFN_cuTensorMapEncodeTiled_v12000 fn = map_encoder();
-    if (!fn || rows >= (1LL << 31)) return false;
-    const cuuint64_t dims[2] = {(cuuint64_t)D, (cuuint64_t)rows};
-    const cuuint64_t strides[1] = {(cuuint64_t)D * 2};
-    const cuuint32_t box[2] = {64, (cuuint32_t)box_rows};
-    const cuuint32_t estr[2] = {1, 1};
-    return fn(m, bf16 ? CU_TENSOR_MAP_DATA_TYPE_BFLOAT16 : CU_TENSOR_MAP_DATA_TYPE_FLOAT16, 2,
-              const_cast<void*>(pool), dims, strides, box, estr, CU_TENSOR_MAP_INTERLEAVE_NONE,
-              CU_TENSOR_MAP_SWIZZLE_128B, CU_TENSOR_MAP_L2_PROMOTION_L2_256B,
-              CU_TENSOR_MAP_FLOAT_OOB_FILL_NONE) == CUDA_SUCCESS;
-}
 
 // Host-only checks shared by the workspace query and the launch.
 pkv_status check_shape(int S, int H, int D, int B, int max_blocks, int partition_size,
@@ -214,6 +183,8 @@ pkv_status launch_decode(const char* fn, const pkv::DecodeKernel* k, pkv::Decode
 }
 
 }  // namespace
+
+uint64_t pkv::decode_wait_ns() { return g_wait_ns.load(std::memory_order_relaxed); }
 
 extern "C" {
 
@@ -398,8 +369,8 @@ pkv_status pkv_paged_attention_decode_shared(void* out, const void* q, const voi
         const int64_t rows = num_blocks * num_heads * (int64_t)block_size;
         const int sub = pkv::step_tokens(head_dim);
         const int box = block_size < sub ? block_size : sub;
-        groups = pool_map(&tk, dtype == PKV_BF16, k_cache, rows, head_dim, box) &&
-                 pool_map(&tv, dtype == PKV_BF16, v_cache, rows, head_dim, box);
+        groups = pkv::pool_map(&tk, dtype == PKV_BF16, k_cache, rows, head_dim, box) &&
+                 pkv::pool_map(&tv, dtype == PKV_BF16, v_cache, rows, head_dim, box);
     }
     const pkv::DecodeKernel* k =
         groups ? (dtype == PKV_F16 ? pkv::decode_kernel_shared_f16(head_dim, block_size)

@@ -173,6 +173,9 @@ const DecodeKernel* decode_kernel_shared_bf16(int D, int B);
 // taken from the call's k_new / v_new and written into its cache slot
 enum : int { kModePaged = 0, kModeContig = 1, kModeShared = 2, kModeAppend = 3 };
 
+// Bound of the decode kernels' pipeline waits, in ns (pkv_set_decode_wait_limit).
+uint64_t decode_wait_ns();
+
 // ---- cache kernels -----------------------------------------------------------
 cudaError_t launch_reshape_and_cache(const void* k, const void* v, void* k_cache, void* v_cache,
                                      const int64_t* slots, int T, int H, int D, int B,

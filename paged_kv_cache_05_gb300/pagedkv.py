@@ -74,6 +74,10 @@ def lib():
             "pkv_paged_attention_prefill_write": ([P, P, P, P, P, P, P, P, P, f32, i32, i32, i32,
                                                    i32, i32, i64, i32, i32, i32, P], i32),
             "pkv_reshape_and_cache": ([P, P, P, P, P, i32, i32, i32, i32, i64, i32, P], i32),
+            "pkv_decode_grouped_workspace_size": ([i32, i32, i32, i32, i32, i32,
+                                                   ctypes.POINTER(sz)], i32),
+            "pkv_paged_attention_decode_grouped": ([P, P, P, P, P, P, P, f32, f32, i32, i32, i32,
+                                                    i32, i32, i32, i32, i64, i32, P, sz, P], i32),
             "pkv_rope_inv_freq": ([i32, ctypes.c_double, i32, ctypes.c_double, i32,
                                    ctypes.c_double, ctypes.c_double, P, ctypes.POINTER(f32)],
                                   i32),
@@ -317,6 +321,64 @@ def contiguous_attention_decode(out, q, k, v, context_lens, scale, partition_siz
                _dev(context_lens, "context_lens", torch.int32, 1), float(scale), S, H, D, T,
                _dtype_code(q.dtype), int(partition_size), _dev(workspace, "workspace"),
                workspace.numel() * workspace.element_size(), _stream(stream)))
+    return out
+
+
+def decode_grouped_workspace_size(num_seqs, num_heads, num_kv_heads, head_dim, block_size,
+                                  max_blocks_per_seq) -> int:
+    out = ctypes.c_size_t(0)
+    _check("pkv_decode_grouped_workspace_size",
+           lib().pkv_decode_grouped_workspace_size(num_seqs, num_heads, num_kv_heads, head_dim,
+                                                   block_size, max_blocks_per_seq,
+                                                   ctypes.byref(out)))
+    return out.value
+
+
+def alloc_grouped_workspace(num_seqs, num_heads, num_kv_heads, head_dim, block_size,
+                            max_blocks_per_seq, device="cuda"):
+    """A device buffer of the size paged_attention_decode_grouped needs."""
+    torch = _torch()
+    n = decode_grouped_workspace_size(num_seqs, num_heads, num_kv_heads, head_dim, block_size,
+                                      max_blocks_per_seq)
+    return torch.empty(n, dtype=torch.uint8, device=device)
+
+
+def paged_attention_decode_grouped(out, q, k_cache, v_cache, block_tables, context_lens, scale,
+                                   softcap=0.0, window=0, slopes=None, workspace=None,
+                                   stream=None):
+    """Decode attention of H query heads over HK shared K/V heads (H a multiple
+    of HK): q, out [S, H, D], caches [blocks, HK, B, D]; scores capped by
+    softcap * tanh(z / softcap), limited to the last `window` tokens and biased
+    by slopes[h] * (t - p), where given."""
+    torch = _torch()
+    S, H, D = q.shape
+    nb, HK, B, D2 = k_cache.shape
+    dev, dt = q.get_device(), q.dtype
+    if D2 != D or v_cache.shape != k_cache.shape:
+        raise ValueError("q / cache shape mismatch")
+    if out.shape != q.shape:
+        raise ValueError("out must have q's shape")
+    if block_tables.dim() != 2 or block_tables.shape[0] != S or context_lens.shape != (S,):
+        raise ValueError("block_tables must be [num_seqs, max_blocks], context_lens [num_seqs]")
+    if dev < 0:
+        raise ValueError("q must be a CUDA tensor")
+    width = block_tables.shape[1]
+    sp = None
+    if slopes is not None:
+        if slopes.shape != (H,):
+            raise ValueError("slopes must be [num_heads]")
+        sp = _ptr(slopes, "slopes", dev, torch.float32)
+    if workspace is None:
+        workspace = alloc_grouped_workspace(S, H, HK, D, B, width, q.device)
+        if stream is not None:
+            workspace.record_stream(stream)
+    _run("pkv_paged_attention_decode_grouped", dev, stream,
+         (_ptr(out, "out", dev, dt), _ptr(q, "q", dev, dt), _ptr(k_cache, "k_cache", dev, dt),
+          _ptr(v_cache, "v_cache", dev, dt),
+          _ptr(block_tables, "block_tables", dev, torch.int32),
+          _ptr(context_lens, "context_lens", dev, torch.int32), sp, float(scale), float(softcap),
+          int(window), S, H, HK, D, B, width, nb, _dtype_code(dt),
+          _ptr(workspace, "workspace", dev, torch.uint8), workspace.shape[0]))
     return out
 
 
