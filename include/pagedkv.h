@@ -381,6 +381,28 @@ pkv_status pkv_paged_attention_prefill_write(void* out, const void* q, const voi
                                              int num_query_tokens, pkv_dtype dtype,
                                              cudaStream_t stream);
 
+/*
+ * The prompt phase for query heads that share key/value heads, with capped
+ * scores, a sliding window and a distance bias: query row query_start[s] + i,
+ * at position p = ctx - qlen + i, attends the tokens lo <= t <= p, lo = max(0,
+ * p - window + 1) when window > 0, else 0, with the scores of
+ * pkv_paged_attention_decode_grouped (scale, softcap, slopes[h] (t - p)) and
+ * K/V head h / (num_heads / num_kv_heads).  Lengths, rows, limits and errors
+ * are those of pkv_paged_attention_prefill; K/V are in the cache already
+ * (pkv_norm_rope_and_cache).  Blocks that no row of a 256-row item sees are
+ * not looked up for it, and tokens that none sees do not matter; an infinite
+ * or NaN V of a token that some row sees may show in the other rows of that
+ * item too (the rows share their products).  num_blocks * num_kv_heads *
+ * block_size must stay below 2^31.  Fifth-generation tensor cores, fp32
+ * accumulation, one launch, no workspace.
+ */
+pkv_status pkv_paged_attention_prefill_grouped(
+    void* out, const void* q, const void* k_cache, const void* v_cache,
+    const int32_t* block_tables, const int32_t* context_lens, const int32_t* query_start,
+    const float* slopes, float scale, float softcap, int window, int num_seqs, int num_heads,
+    int num_kv_heads, int head_dim, int block_size, int max_blocks_per_seq, int64_t num_blocks,
+    int max_query_len, int num_query_tokens, pkv_dtype dtype, cudaStream_t stream);
+
 /* ------------------------------------------------------------------------ */
 /* Cache maintenance                                                         */
 /* ------------------------------------------------------------------------ */

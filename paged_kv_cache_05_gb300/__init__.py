@@ -10,7 +10,8 @@ from .pagedkv import (BlockManager, OutOfBlocks, PagedKVError, alloc_grouped_wor
                       decode_shared_workspace_size, decode_workspace_size, get_device_error, lib, paged_attention_decode,
                       paged_attention_decode_append, paged_attention_decode_grouped,
                       paged_attention_decode_noalloc, paged_attention_decode_shared,
-                      norm_rope_and_cache, paged_attention_prefill, paged_attention_prefill_write,
+                      norm_rope_and_cache, paged_attention_prefill,
+                      paged_attention_prefill_grouped, paged_attention_prefill_write,
                       reshape_and_cache, rope_inv_freq, rope_phases, set_decode_wait_limit,
                       swap_blocks, version)
 
@@ -20,6 +21,7 @@ __all__ = ["BlockManager", "OutOfBlocks", "PagedKVError", "alloc_grouped_workspa
            "decode_shared_workspace_size", "decode_workspace_size", "get_device_error", "lib", "paged_attention_decode",
            "paged_attention_decode_append", "paged_attention_decode_grouped",
            "paged_attention_decode_noalloc", "paged_attention_decode_shared",
-           "norm_rope_and_cache", "paged_attention_prefill", "paged_attention_prefill_write",
+           "norm_rope_and_cache", "paged_attention_prefill",
+           "paged_attention_prefill_grouped", "paged_attention_prefill_write",
            "reshape_and_cache", "rope_inv_freq", "rope_phases", "set_decode_wait_limit",
            "swap_blocks", "version"]

@@ -1,0 +1,112 @@
+// C ABI of the prompt phase with shared key/value heads, capped scores, a
+// sliding window and a distance bias: argument checks, tensor maps, dispatch to
+// the kind of kernel the arguments ask for.
+#include <cmath>
+
+#include "prefill_kernel.cuh"
+
+extern "C" {
+
+pkv_status pkv_paged_attention_prefill_grouped(
+    void* out, const void* q, const void* k_cache, const void* v_cache,
+    const int32_t* block_tables, const int32_t* context_lens, const int32_t* query_start,
+    const float* slopes, float scale, float softcap, int window, int num_seqs, int num_heads,
+    int num_kv_heads, int head_dim, int block_size, int max_blocks_per_seq, int64_t num_blocks,
+    int max_query_len, int num_query_tokens, pkv_dtype dtype, cudaStream_t stream) {
+    const char* fn = "pkv_paged_attention_prefill_grouped";
+    if (num_seqs < 0 || num_seqs > 65535)
+        return pkv::fail(PKV_ERR_INVALID, "%s: num_seqs must be in [0, 65535]", fn);
+    if (num_heads < 1 || num_heads > 65535 || num_kv_heads < 1 || num_heads % num_kv_heads != 0)
+        return pkv::fail(PKV_ERR_INVALID,
+                         "%s: num_heads must be a multiple of num_kv_heads, at most 65535", fn);
+    if (head_dim != 64 && head_dim != 128)
+        return pkv::fail(PKV_ERR_INVALID, "%s: head_dim must be 64 or 128", fn);
+    if (block_size != 8 && block_size != 16 && block_size != 32 && block_size != 64)
+        return pkv::fail(PKV_ERR_INVALID, "%s: block_size must be 8, 16, 32 or 64", fn);
+    if (max_blocks_per_seq < 1 || max_query_len < 0 || num_query_tokens < 0)
+        return pkv::fail(PKV_ERR_INVALID, "%s: bad sizes", fn);
+    if ((int64_t)max_blocks_per_seq * block_size >= (1LL << 31))
+        return pkv::fail(PKV_ERR_INVALID, "%s: context capacity overflows", fn);
+    // the tiled copies address cache rows (block, head, token) with 32-bit coordinates
+    if (num_blocks < 1 || num_blocks > ((1LL << 31) - 1) / ((int64_t)num_kv_heads * block_size))
+        return pkv::fail(PKV_ERR_INVALID,
+                         "%s: num_blocks must be >= 1, and num_blocks * num_kv_heads * block_size "
+                         "below 2^31",
+                         fn);
+    if (dtype != PKV_F16 && dtype != PKV_BF16)
+        return pkv::fail(PKV_ERR_INVALID, "%s: unknown dtype", fn);
+    {
+        // the work schedule sums item costs in 64 bits: a bound far above any
+        // call whose tensors fit in memory
+        const double units = (double)((num_heads + 1) / 2) * num_seqs *
+                             (double)(((int64_t)max_query_len + kRows - 1) / kRows);
+        const double unit_cost =
+            kPairCost * ((double)max_blocks_per_seq * block_size / kBN + 1.0) + kItemCost;
+        if (units * unit_cost >= 0x1p60)
+            return pkv::fail(PKV_ERR_INVALID, "%s: too much work for one call", fn);
+    }
+    if (!std::isfinite(scale)) return pkv::fail(PKV_ERR_INVALID, "%s: scale is not finite", fn);
+    if (!(softcap >= 0.f) || !std::isfinite(softcap))
+        return pkv::fail(PKV_ERR_INVALID, "%s: softcap must be finite and not negative", fn);
+    if (window < 0) return pkv::fail(PKV_ERR_INVALID, "%s: window must not be negative", fn);
+    if (num_seqs == 0 || max_query_len == 0 || num_query_tokens == 0) return PKV_OK;
+    if (!out || !q || !k_cache || !v_cache || !block_tables || !context_lens || !query_start)
+        return pkv::fail(PKV_ERR_INVALID, "%s: NULL pointer", fn);
+    if (!aligned(out, 16) || !aligned(q, 16) || !aligned(k_cache, 16) || !aligned(v_cache, 16))
+        return pkv::fail(PKV_ERR_INVALID, "%s: out, q and the caches must be 16-byte aligned", fn);
+    if (!aligned(block_tables, 4) || !aligned(context_lens, 4) || !aligned(query_start, 4) ||
+        !aligned(slopes, 4))
+        return pkv::fail(PKV_ERR_INVALID,
+                         "%s: block_tables, context_lens, query_start and slopes must be 4-byte "
+                         "aligned",
+                         fn);
+    int32_t* err = pkv::device_error_word();
+    if (!err) return pkv::fail(PKV_ERR_CUDA, "%s: no CUDA device", fn);
+
+    const bool bf16 = dtype == PKV_BF16;
+    CUtensorMap tq, tk, tv;
+    {
+        // q: [tokens][heads][D], one box = 128 tokens x 64 elements of one head
+        const cuuint64_t D = (cuuint64_t)head_dim;
+        const cuuint64_t dims[3] = {D, (cuuint64_t)num_heads, (cuuint64_t)num_query_tokens};
+        const cuuint64_t strides[2] = {D * 2, (cuuint64_t)num_heads * D * 2};
+        const cuuint32_t box[3] = {64, 1, (cuuint32_t)kBM};
+        if (!make_map(&tq, bf16, 3, q, dims, strides, box))
+            return pkv::fail(PKV_ERR_CUDA, "%s: tensor map of q", fn);
+    }
+    const int64_t rows = num_blocks * num_kv_heads * block_size;
+    if (!pkv::pool_map(&tk, bf16, k_cache, rows, head_dim, block_size) ||
+        !pkv::pool_map(&tv, bf16, v_cache, rows, head_dim, block_size))
+        return pkv::fail(PKV_ERR_CUDA, "%s: tensor map of the caches", fn);
+
+    const double log2e = 1.4426950408889634;
+    PrefillArgs a = {};
+    a.out = out;
+    a.out_v8 = aligned(out, 32) ? 1 : 0;
+    a.block_tables = block_tables;
+    a.context_lens = context_lens;
+    a.query_start = query_start;
+    a.scale_log2 = (float)(softcap > 0.f ? 2.0 * log2e * scale / softcap : log2e * scale);
+    a.S = num_seqs;
+    a.H = num_heads;
+    a.B = block_size;
+    a.max_blocks = max_blocks_per_seq;
+    a.max_query_len = max_query_len;
+    a.num_tokens = num_query_tokens;
+    a.HK = num_kv_heads;
+    a.G = num_heads / num_kv_heads;
+    a.window = window;
+    a.cap_log2 = (float)(log2e * softcap);
+    a.slopes = slopes;
+    a.q_items = (max_query_len + kRows - 1) / kRows;
+    a.num_blocks = num_blocks;
+    a.err = err;
+    const int kind = kGrouped | (softcap > 0.f ? kCapped : 0) | (slopes ? kBiased : 0);
+    const cudaError_t e =
+        bf16 ? pkv::launch_prefill_grouped_bf16(tq, tk, tv, a, head_dim, kind, stream)
+             : pkv::launch_prefill_grouped_f16(tq, tk, tv, a, head_dim, kind, stream);
+    if (e != cudaSuccess) return pkv::cuda_fail(e, fn);
+    return PKV_OK;
+}
+
+}  // extern "C"

@@ -78,6 +78,9 @@ def lib():
                                                    ctypes.POINTER(sz)], i32),
             "pkv_paged_attention_decode_grouped": ([P, P, P, P, P, P, P, f32, f32, i32, i32, i32,
                                                     i32, i32, i32, i32, i64, i32, P, sz, P], i32),
+            "pkv_paged_attention_prefill_grouped": ([P, P, P, P, P, P, P, P, f32, f32, i32, i32,
+                                                     i32, i32, i32, i32, i32, i64, i32, i32, i32,
+                                                     P], i32),
             "pkv_rope_inv_freq": ([i32, ctypes.c_double, i32, ctypes.c_double, i32,
                                    ctypes.c_double, ctypes.c_double, P, ctypes.POINTER(f32)],
                                   i32),
@@ -434,6 +437,44 @@ def paged_attention_prefill_write(out, q, k, v, k_cache, v_cache, block_tables, 
                _dev(query_start, "query_start", torch.int32, 1), float(scale), S, H, D, B,
                block_tables.shape[1], nb, int(max_query_len), T, _dtype_code(q.dtype),
                _stream(stream)))
+    return out
+
+
+def paged_attention_prefill_grouped(out, q, k_cache, v_cache, block_tables, context_lens,
+                                    query_start, scale, max_query_len, softcap=0.0, window=0,
+                                    slopes=None, stream=None):
+    """paged_attention_prefill for H query heads over HK shared K/V heads (H a
+    multiple of HK): q, out [T, H, D], caches [blocks, HK, B, D]; scores capped
+    by softcap * tanh(z / softcap), limited to the last `window` tokens and
+    biased by slopes[h] * (t - p), where given."""
+    torch = _torch()
+    T, H, D = q.shape
+    nb, HK, B, D2 = k_cache.shape
+    S = context_lens.shape[0]
+    dev, dt = q.get_device(), q.dtype
+    if D2 != D or v_cache.shape != k_cache.shape:
+        raise ValueError("q / cache shape mismatch")
+    if out.shape != q.shape:
+        raise ValueError("out must have q's shape")
+    if block_tables.dim() != 2 or block_tables.shape[0] != S or query_start.shape != (S + 1,) or \
+            context_lens.dim() != 1:
+        raise ValueError("block_tables [S, max_blocks], context_lens [S], query_start [S+1] "
+                         "expected")
+    if dev < 0:
+        raise ValueError("q must be a CUDA tensor")
+    sp = None
+    if slopes is not None:
+        if slopes.shape != (H,):
+            raise ValueError("slopes must be [num_heads]")
+        sp = _ptr(slopes, "slopes", dev, torch.float32)
+    _run("pkv_paged_attention_prefill_grouped", dev, stream,
+         (_ptr(out, "out", dev, dt), _ptr(q, "q", dev, dt), _ptr(k_cache, "k_cache", dev, dt),
+          _ptr(v_cache, "v_cache", dev, dt),
+          _ptr(block_tables, "block_tables", dev, torch.int32),
+          _ptr(context_lens, "context_lens", dev, torch.int32),
+          _ptr(query_start, "query_start", dev, torch.int32), sp, float(scale), float(softcap),
+          int(window), S, H, HK, D, B, block_tables.shape[1], nb, int(max_query_len), T,
+          _dtype_code(dt)))
     return out
 
 
