@@ -19,8 +19,13 @@
 // space is cut into equal ranges, one per CTA of a persistent grid, and each
 // into equal ranges for its WARPS, whatever the mix of lengths: until they are
 // done, a CTA's warps share nothing.  A warp walks its range with a ring of
-// kStages stages of its own, into which it issues tiled bulk copies of whole
-// cache rows (128-byte swizzle) kStages steps ahead, one mbarrier a stage.
+// kStages stages of its own.  One more warp fills the rings, a lane each: it
+// walks the ring's range too, looks up the blocks of the step after the one it
+// copies, and issues tiled bulk copies of whole cache rows (128-byte swizzle)
+// as soon as a stage is free.  (Copies issued by the computing warps themselves
+// took 900 of a step's 2100 cycles.)  Two shallow stages a warp are enough:
+// deeper rings only queue up more in the memory system, where the lookups and
+// queries of the next row then wait behind them.
 //   S = Q K^T: the heads are the product's 16 rows, the tokens its columns;
 //   online softmax in log2 units, a row's statistics in the four lanes that
 //   hold it; P goes straight from S's registers to the operand of O += P V.
@@ -51,24 +56,10 @@ namespace {
 
 using namespace pkv::dec;
 
-#ifndef PKV_GW
-#define PKV_GW 8
-#endif
-#ifndef PKV_GS
-#define PKV_GS 2
-#endif
-#ifndef PKV_GT
-#define PKV_GT 16
-#endif
-#ifndef PKV_GM
-#define PKV_GM 8
-#endif
-constexpr int kWarps = PKV_GW;                   // ranges per CTA
-constexpr int kThreads = kWarps * 32;
-constexpr int kStages = PKV_GS;                  // ring stages per warp
-constexpr int kStepTokens = PKV_GT;              // tokens a step at head_dim 128, twice that at 64
+constexpr int kStages = 2;                  // ring stages per warp
+constexpr int kStepTokens = 16;             // tokens a step at head_dim 128, twice that at 64
 constexpr int kMaxCtas = 512;
-constexpr int kMinSteps = PKV_GM;                // fewest steps of a CTA
+constexpr int kMinSteps = 2;                // fewest steps of a CTA
 constexpr float kRaiseLog2 = 8.f;           // raise the running max only past this growth
 constexpr float kLog2e = 1.4426950408889634f;
 
@@ -126,6 +117,11 @@ struct Part {
     int last;                               // the CTA that holds the row's last step
 };
 
+// Where a warp's range begins, for the lane that fills its ring.
+struct Start {
+    int s, hk, gc, j, left;
+};
+
 struct Args {
     void* out;
     const void* q;
@@ -147,6 +143,10 @@ struct Args {
 
 template <int D, bool WIDE>
 struct Geo {
+    // Warps that compute, a range each: with the one that copies, 8 (225-249
+    // registers) or 12 (168) of them fill the register file.
+    static constexpr int WARPS = D == 64 ? 11 : 7;
+    static constexpr int THREADS = WARPS * 32;          // (32 more copy)
     static constexpr int ST = kStepTokens * 128 / D;    // tokens of a step
     static constexpr int SUBS = ST / 16;
     static constexpr int HPR = WIDE ? 16 : 8;           // heads of a row
@@ -156,12 +156,14 @@ struct Geo {
     static constexpr int PART = HPR * (D + 2) * 4;      // a part: acc[HPR][D], (m, l)[HPR]
     // the parts of rows that begin in a warp take the place of its ring
     static_assert(PART <= RING && PART % 16 == 0, "part");
-    static constexpr int PARTS_OFF = kWarps * RING;
-    static constexpr int BAR_OFF = PARTS_OFF + kWarps * PART;
-    static constexpr int CTX_OFF = BAR_OFF + 8 * kWarps * kStages;
-    static constexpr int PREFIX_OFF = CTX_OFF + 4 * kThreads;
-    static constexpr int META_OFF = (PREFIX_OFF + 4 * (kThreads + 1) + 15) / 16 * 16;
-    static constexpr int SMEM = 1024 + META_OFF + 2 * kWarps * (int)sizeof(Part) + 4 * kWarps;
+    static constexpr int PARTS_OFF = WARPS * RING;
+    static constexpr int BAR_OFF = PARTS_OFF + WARPS * PART;
+    static constexpr int CTX_OFF = BAR_OFF + 16 * WARPS * kStages;   // full, empty
+    static constexpr int PREFIX_OFF = CTX_OFF + 4 * THREADS;
+    static constexpr int META_OFF = (PREFIX_OFF + 4 * (THREADS + 1) + 15) / 16 * 16;
+    static constexpr int START_OFF = META_OFF + 2 * WARPS * (int)sizeof(Part);
+    static constexpr int SMEM = 1024 + START_OFF + WARPS * (int)sizeof(Start) + 4 * WARPS;
+    static constexpr int BOXES = ST / 8;                // most boxes (block pieces) of a step
     static_assert(SMEM <= 232448, "shared memory");
 };
 
@@ -183,7 +185,7 @@ __device__ __forceinline__ Seq seq_of(const Args& a, int c) {
 // thread has one sequence at most) and the steps before each thread's ones.
 struct Batch {
     const int* ctx;
-    const int* prefix;                      // [kThreads + 1]
+    const int* prefix;                      // [computing threads + 1]
     int per;                                // sequences a thread
 };
 
@@ -211,12 +213,12 @@ struct Cursor {
 };
 
 // Step x of the space: its sequence, row and step (one warp).
-template <int ST>
+template <int ST, int WARPS>
 __device__ __forceinline__ Cursor<ST> locate(const Args& a, const Batch& b, int64_t x, int lane) {
     const int rows = a.HK * a.chunks;
     // the sequence holds step P of the batch counted once per sequence
     const int P = (int)quotient(x, rows);
-    constexpr int kEach = kThreads / 32;
+    constexpr int kEach = WARPS;            // threads a lane
     const int g = __popc(__ballot_sync(kFull, b.prefix[lane * kEach] <= P)) - 1;
     const int t = g * kEach +
                   __popc(__ballot_sync(kFull, lane < kEach && b.prefix[g * kEach + lane % kEach] <= P)) - 1;
@@ -248,27 +250,111 @@ __device__ __forceinline__ Cursor<ST> locate(const Args& a, const Batch& b, int6
     const int64_t in = x - (int64_t)before * rows;
     const int row = (int)quotient(in, c.q.steps);
     c.j = (int)(in - (int64_t)row * c.q.steps);
-    c.hk = row / a.chunks;
+    c.hk = a.chunks == 1 ? row : row / a.chunks;
     c.gc = row - c.hk * a.chunks;
     return c;
 }
 
-// One warp's range: the steps [x, x + left).  Its parts go to shared memory,
-// described in meta[0] (a row that began before the range) and meta[1] (a row
-// that begins in it and goes on).
+// The copies of a CTA's rings, one warp: lane i fills warp i's ring with the
+// steps of its range.  Returns once every copy has been issued (or a wait for a
+// free stage ran out: false), the copies themselves still in flight.
 template <typename T, int D, bool WIDE>
-__device__ __forceinline__ void walk(const CUtensorMap& tk, const CUtensorMap& tv, const Args& a,
-                                     const Batch& b, const int64_t x, const int left,
-                                     unsigned char* gring, unsigned char* part0, uint64_t* full,
+__device__ __forceinline__ bool fill(const CUtensorMap& tk, const CUtensorMap& tv, const Args& a,
+                                     const Batch& b, unsigned char* base, uint64_t* bars,
+                                     const Start* starts, int& issued) {
+    using C = Geo<D, WIDE>;
+    constexpr int ST = C::ST, NB = C::BOXES;
+    const int lane = threadIdx.x & 31, w = lane < C::WARPS ? lane : 0;
+    uint64_t* full = bars + w * kStages;
+    uint64_t* empty = bars + (C::WARPS + w) * kStages;
+    const uint32_t ring = smem_addr(base + w * C::RING);
+    const Start from = starts[w];
+    const int left = lane < C::WARPS ? from.left : 0;
+
+    Cursor<ST> c, ahead;                    // the step to copy, the one to look up
+    c.s = from.s;
+    c.hk = from.hk;
+    c.gc = from.gc;
+    c.j = from.j;
+    if (left > 0) c.q = seq_of<ST>(a, b.ctx[c.s]);
+    ahead = c;
+    int blk[NB], next[NB];                  // physical blocks, a box each
+    int looked = 0;                         // steps looked up
+    auto look = [&](int (&e)[NB]) {
+        if (looked >= left) return;
+        const int t0 = (ahead.q.j0 + ahead.j) * ST;
+        const int32_t* row = a.tables + (int64_t)ahead.s * a.max_blocks;
+#pragma unroll
+        for (int i = 0; i < NB; ++i) {
+            const int tok = t0 + i * a.tpc;
+            if (i * a.tpc < ST && tok < ahead.q.n && tok + a.tpc > ahead.q.lo)
+                e[i] = row[tok >> a.lgB];
+        }
+        ++looked;
+        ahead.next(a, b);
+    };
+    look(blk);
+    look(next);
+    issued = 0;
+    int st = 0;
+    uint32_t phase = 1;                     // of empty: the first round finds every stage free
+    uint64_t since = 0;
+    while (__any_sync(kFull, issued < left)) {
+        const bool go = issued < left && mbar_try_wait(empty + st, phase);
+        if (!__any_sync(kFull, go)) {
+            const uint64_t now = global_ns();
+            if (since == 0) since = now;
+            if (now - since > a.wait_ns) return false;
+            __nanosleep(32);
+            continue;
+        }
+        since = 0;
+        if (go) {
+            const int t0 = (c.q.j0 + c.j) * ST;
+            const int t1 = min(t0 + ST, c.q.n), f = max(t0, c.q.lo) & -a.tpc;
+            mbar_arrive_expect_tx(full + st, (uint32_t)((t1 - f + a.tpc - 1) & -a.tpc) *
+                                                 (uint32_t)(4 * D));
+#pragma unroll
+            for (int i = 0; i < NB; ++i) {
+                const int tok = t0 + i * a.tpc;
+                if (i * a.tpc >= ST || tok < f || tok >= t1) continue;
+                if ((unsigned)blk[i] >= (unsigned)a.num_blocks) {
+                    atomicOr(a.err, PKV_DEVERR_BAD_BLOCK);
+                    blk[i] = 0;                             // a valid row; flagged
+                }
+                const int y = ((blk[i] * a.HK + c.hk) << a.lgB) + (tok & ((1 << a.lgB) - 1));
+                const uint32_t dst = ring + st * C::STAGE + i * a.tpc * (2 * D);
+                tensor_g2s3(dst, &tk, 0, 0, y, full + st);
+                tensor_g2s3(dst + C::HALF, &tv, 0, 0, y, full + st);
+            }
+            ++issued;
+            c.next(a, b);
+            if (++st == kStages) {
+                st = 0;
+                phase ^= 1u;
+            }
+#pragma unroll
+            for (int i = 0; i < NB; ++i) blk[i] = next[i];
+            look(next);
+        }
+    }
+    return true;
+}
+
+// One warp's range: `left` steps from step x, at cc.  Its parts go to shared
+// memory, described in meta[0] (a row that began before the range) and meta[1]
+// (a row that begins in it and goes on).
+template <typename T, int D, bool WIDE>
+__device__ __forceinline__ void walk(const Args& a, const Batch& b, Cursor<Geo<D, WIDE>::ST> cc,
+                                     const int64_t x, const int left, unsigned char* gring,
+                                     unsigned char* part0, uint64_t* full, uint64_t* empty,
                                      Part* meta, const Cut& cut) {
     using C = Geo<D, WIDE>;
     constexpr int ST = C::ST, SUBS = C::SUBS, HPR = C::HPR, NH = WIDE ? 2 : 1;
     constexpr int QW = WIDE ? 4 : 2;
     const int lane = threadIdx.x & 31;
     const int r = lane >> 2, kq = lane & 3;
-
-    Cursor<ST> ic = locate<ST>(a, b, x, lane);   // the next step to copy
-    Cursor<ST> cc = ic;                          // the next step to compute
+    const uint32_t ring = smem_addr(gring);
 
     // a row's query fragments: head r (and r + 8), elements 16 kk + 2 kq and + 8
     auto load_q = [&](uint32_t (&qf)[D / 16][QW], const Cursor<ST>& c) {
@@ -285,91 +371,9 @@ __device__ __forceinline__ void walk(const CUtensorMap& tk, const CUtensorMap& t
             }
         }
     };
-    // The next row's fragments are loaded when the copies reach it, so that
-    // their latency passes beside the current row's last steps: tag counts rows.
+    // this row's, and the next one's, loaded while this one runs
     uint32_t qa[D / 16][QW], qn[D / 16][QW];
-    int copy_row = 0, row_no = 0, tag = 0;
-    load_q(qn, ic);
-
-    const uint32_t ring = smem_addr(gring);
-    int issued = 0;
-    // Block-table windows of 32 entries, in the lanes (a step's blocks, at most
-    // 8 and aligned to their number, never straddle one): the current one, the
-    // one after it, the sequence's first and the next sequence's first.
-    int tab_s = -1, win = 0, tab = 0, tab_after = 0, tab_first = 0, win_first = 0;
-    int seq_s = -1, seq_tab = 0;
-    auto entries = [&](int s, const Seq& q, int from) -> int {
-        const int i = from + lane;
-        return i <= (q.n - 1) >> a.lgB ? a.tables[(int64_t)s * a.max_blocks + i] : -1;
-    };
-    auto first_window = [&](const Seq& q) { return (q.lo >> a.lgB) & ~7; };
-    // Copy the step at ic into stage `st`: boxes of tpc tokens, those with a
-    // visible one.
-    auto issue = [&](int st) {
-        const int t0 = (ic.q.j0 + ic.j) * ST;
-        const int t1 = min(t0 + ST, ic.q.n);
-        int tok = max(t0, ic.q.lo) & -a.tpc;
-        const int first = tok >> a.lgB;
-        if (ic.s != tab_s) {                        // another sequence
-            win_first = first_window(ic.q);
-            tab_first = seq_s == ic.s ? seq_tab : entries(ic.s, ic.q, win_first);
-            tab_s = ic.s;
-            win = -32;
-            // look up the one after it
-            seq_s = ic.s;
-            Seq q;
-            do {
-                ++seq_s;
-                q = seq_of<ST>(a, seq_s < a.S ? b.ctx[seq_s] : 1);
-            } while (q.steps == 0);
-            if (seq_s < a.S) seq_tab = entries(seq_s, q, first_window(q));
-        }
-        if ((unsigned)(first - win) >= 32u) {
-            if (first == win + 32 && win >= 0) {
-                win = first;
-                tab = tab_after;
-            } else if ((unsigned)(first - win_first) < 32u) {
-                win = win_first;
-                tab = tab_first;
-            } else {
-                win = first & ~7;
-                tab = entries(ic.s, ic.q, win);
-            }
-            tab_after = entries(ic.s, ic.q, win + 32);
-        }
-        if (lane == 0)
-            mbar_arrive_expect_tx(full + st, (uint32_t)((t1 - tok + a.tpc - 1) & -a.tpc) *
-                                                 (uint32_t)(4 * D));
-        for (; tok < t1; tok += a.tpc) {
-            int phys = __shfl_sync(kFull, tab, (tok >> a.lgB) - win);
-            if (lane == 0) {
-                if ((unsigned)phys >= (unsigned)a.num_blocks) {
-                    atomicOr(a.err, PKV_DEVERR_BAD_BLOCK);
-                    phys = 0;                               // a valid row; flagged
-                }
-                const int y = ((phys * a.HK + ic.hk) << a.lgB) + (tok & ((1 << a.lgB) - 1));
-                const uint32_t dst = ring + st * C::STAGE + (tok - t0) * (2 * D);
-                tensor_g2s3(dst, &tk, 0, 0, y, full + st);
-                tensor_g2s3(dst + C::HALF, &tv, 0, 0, y, full + st);
-            }
-        }
-        ++issued;
-        if (ic.next(a, b)) {
-            ++copy_row;
-            if (!WIDE && issued < left && tag <= row_no) {
-                load_q(qn, ic);
-                tag = copy_row;
-            }
-        }
-    };
-
-    for (int i = 0; i < kStages && issued < left; ++i) issue(i);
-
-    float m[NH], l[NH], slope[NH];
-    float acc[D / 8][4];
-    bool began_before = cc.j > 0;
-    int heads = 0;
-    bool fresh = true, ok = true;
+    load_q(qn, cc);
 
     // Fragment addresses in a stage's K (or V): a token is D / 64 lines of 128
     // bytes, chunk c of line i at c ^ (i % 8).  Lane (mi, mr) addresses row mr of
@@ -386,206 +390,204 @@ __device__ __forceinline__ void walk(const CUtensorMap& tk, const CUtensorMap& t
 
     int st = 0;
     uint32_t phase = 0;
-    for (int done = 0; done < left; ++done) {
-        if (fresh) {
-            fresh = false;
-            if (tag == row_no) {
+    bool began_before = cc.j > 0;
+    for (int done = 0; done < left;) {
+        const int heads = min(HPR, a.G - cc.gc * HPR);
+        const int part_steps = min(left - done, cc.q.steps - cc.j);
+        float m[NH], l[NH], slope[NH];
+        float acc[D / 8][4];
 #pragma unroll
-                for (int kk = 0; kk < D / 16; ++kk)
-#pragma unroll
-                    for (int e = 0; e < QW; ++e) qa[kk][e] = qn[kk][e];
-            } else {
-                load_q(qa, cc);
-            }
-            heads = min(HPR, a.G - cc.gc * HPR);
-#pragma unroll
-            for (int i = 0; i < NH; ++i) {
-                m[i] = -INFINITY;
-                l[i] = 0.f;
-                slope[i] = a.slopes && r + 8 * i < heads
-                               ? a.slopes[cc.hk * a.G + cc.gc * HPR + r + 8 * i] * kLog2e : 0.f;
-            }
-#pragma unroll
-            for (int i = 0; i < D / 8; ++i)
-#pragma unroll
-                for (int e = 0; e < 4; ++e) acc[i][e] = 0.f;
+        for (int i = 0; i < NH; ++i) {
+            m[i] = -INFINITY;
+            l[i] = 0.f;
+            slope[i] = a.slopes && r + 8 * i < heads
+                           ? a.slopes[cc.hk * a.G + cc.gc * HPR + r + 8 * i] * kLog2e : 0.f;
         }
-        if (!wait_phase(full + st, phase, nullptr, a.wait_ns)) {
-            ok = false;
-            break;
-        }
-        const int t0 = (cc.q.j0 + cc.j) * ST;
-        const bool edge = t0 < cc.q.lo || t0 + ST > cc.q.n;
-        const uint32_t sk = ring + st * C::STAGE, sv = sk + C::HALF;
-        if (edge) {
-            // V rows of hidden tokens
-            for (int i = lane; i < ST * (D / 8); i += 32) {
-                const int tok = t0 + i / (D / 8);
-                if (tok < cc.q.lo || tok >= cc.q.n)
-                    *reinterpret_cast<uint4*>(gring + st * C::STAGE + C::HALF + i * 16) =
-                        make_uint4(0u, 0u, 0u, 0u);
-            }
-            __syncwarp();
-        }
-
-        // z[u][v][2 i + e]: head r + 8 i, token t0 + 16 u + 8 v + 2 kq + e
-        float z[SUBS][2][4];
 #pragma unroll
-        for (int u = 0; u < SUBS; ++u)
+        for (int i = 0; i < D / 8; ++i)
 #pragma unroll
-            for (int e = 0; e < 4; ++e) z[u][0][e] = z[u][1][e] = 0.f;
+            for (int e = 0; e < 4; ++e) acc[i][e] = 0.f;
 #pragma unroll
         for (int kk = 0; kk < D / 16; ++kk)
 #pragma unroll
-            for (int u = 0; u < SUBS; ++u) {
-                uint32_t kb[4];
-                ldsm_x4(kb, sk + u * (16 * 2 * D) + at(krow, kk));
-                const uint32_t af[4] = {qa[kk][0], WIDE ? qa[kk][QW - 2] : 0u, qa[kk][1],
-                                        WIDE ? qa[kk][QW - 1] : 0u};
-                mma16816<T>(z[u][0], af, kb[0], kb[1]);
-                mma16816<T>(z[u][1], af, kb[2], kb[3]);
+            for (int e = 0; e < QW; ++e) qa[kk][e] = qn[kk][e];
+        Cursor<ST> nc = cc;                 // the next row
+        nc.j = nc.q.steps - 1;
+        if (done + part_steps < left) {
+            nc.next(a, b);
+            load_q(qn, nc);
+        }
+
+        for (int k = 0; k < part_steps; ++k) {
+            if (!__all_sync(kFull, wait_phase(full + st, phase, nullptr, a.wait_ns))) {
+                if (lane == 0) atomicOr(a.err, PKV_DEVERR_TIMEOUT);
+                return;
             }
-        auto each = [&](auto f) {
+            const int t0 = (cc.q.j0 + cc.j + k) * ST;
+            const bool edge = t0 < cc.q.lo || t0 + ST > cc.q.n;
+            const uint32_t sk = ring + st * C::STAGE, sv = sk + C::HALF;
+            if (edge) {
+                // V rows of hidden tokens
+                for (int i = lane; i < ST * (D / 8); i += 32) {
+                    const int tok = t0 + i / (D / 8);
+                    if (tok < cc.q.lo || tok >= cc.q.n)
+                        *reinterpret_cast<uint4*>(gring + st * C::STAGE + C::HALF + i * 16) =
+                            make_uint4(0u, 0u, 0u, 0u);
+                }
+                __syncwarp();
+            }
+
+            // z[u][v][2 i + e]: head r + 8 i, token t0 + 16 u + 8 v + 2 kq + e
+            float z[SUBS][2][4];
 #pragma unroll
             for (int u = 0; u < SUBS; ++u)
 #pragma unroll
-                for (int v = 0; v < 2; ++v)
+                for (int e = 0; e < 4; ++e) z[u][0][e] = z[u][1][e] = 0.f;
 #pragma unroll
-                    for (int i = 0; i < NH; ++i)
+            for (int kk = 0; kk < D / 16; ++kk)
 #pragma unroll
-                        for (int e = 0; e < 2; ++e)
-                            f(z[u][v][2 * i + e], t0 + u * 16 + v * 8 + 2 * kq + e, i);
-        };
-        each([&](float& y, int, int) { y *= a.score; });
-        if (a.cap_log2 > 0.f)               // cap tanh(y) = cap (1 - 2 / (2^(2 log2(e) y) + 1))
-            each([&](float& y, int, int) {
-                y = a.cap_log2 * (1.f - __fdividef(2.f, ex2(y) + 1.f));
-            });
-        if (a.slopes)
-            each([&](float& y, int t, int i) { y += slope[i] * (float)(t - (cc.q.n - 1)); });
-        if (edge)
-            each([&](float& y, int t, int) {
-                if (t < cc.q.lo || t >= cc.q.n) y = -INFINITY;
-            });
-        float mx[NH], alpha[NH];
-#pragma unroll
-        for (int i = 0; i < NH; ++i) mx[i] = -INFINITY;
-        each([&](float& y, int, int i) { mx[i] = fmaxf(mx[i], y); });
-        bool raised = false;
-#pragma unroll
-        for (int i = 0; i < NH; ++i) {
-            mx[i] = fmaxf(mx[i], __shfl_xor_sync(kFull, mx[i], 1));
-            mx[i] = fmaxf(mx[i], __shfl_xor_sync(kFull, mx[i], 2));
-            const bool up = mx[i] > m[i] + kRaiseLog2 || m[i] == -INFINITY;
-            alpha[i] = up ? ex2(m[i] - mx[i]) : 1.f;
-            if (up) m[i] = mx[i];
-            raised |= up;
-        }
-        if (__any_sync(kFull, raised)) {
-#pragma unroll
-            for (int i = 0; i < NH; ++i) l[i] *= alpha[i];
-#pragma unroll
-            for (int i = 0; i < D / 8; ++i) {
-                acc[i][0] *= alpha[0];
-                acc[i][1] *= alpha[0];
-                acc[i][2] *= alpha[NH - 1];
-                acc[i][3] *= alpha[NH - 1];
-            }
-        }
-        each([&](float& y, int, int i) { y = ex2(y - m[i]); });
-        if (edge)                           // (m is -infinity where every visible score is)
-            each([&](float& y, int t, int) {
-                if (t < cc.q.lo || t >= cc.q.n) y = 0.f;
-            });
-        each([&](float& y, int, int i) { l[i] += y; });
-#pragma unroll
-        for (int u = 0; u < SUBS; ++u) {
-            uint32_t hi[2][NH], lo[2][NH];
-#pragma unroll
-            for (int v = 0; v < 2; ++v)
-#pragma unroll
-                for (int i = 0; i < NH; ++i) {
-                    const float p0 = z[u][v][2 * i], p1 = z[u][v][2 * i + 1];
-                    hi[v][i] = pack2<T>(p0, p1);
-                    const float2 h = unpack2<T>(hi[v][i]);
-                    lo[v][i] = pack2<T>(p0 - h.x, p1 - h.y);
+                for (int u = 0; u < SUBS; ++u) {
+                    uint32_t kb[4];
+                    ldsm_x4(kb, sk + u * (16 * 2 * D) + at(krow, kk));
+                    const uint32_t af[4] = {qa[kk][0], WIDE ? qa[kk][QW - 2] : 0u, qa[kk][1],
+                                            WIDE ? qa[kk][QW - 1] : 0u};
+                    mma16816<T>(z[u][0], af, kb[0], kb[1]);
+                    mma16816<T>(z[u][1], af, kb[2], kb[3]);
                 }
-            const uint32_t pa[4] = {hi[0][0], WIDE ? hi[0][NH - 1] : lo[0][0], hi[1][0],
-                                    WIDE ? hi[1][NH - 1] : lo[1][0]};
+            auto each = [&](auto f) {
 #pragma unroll
-            for (int c = 0; c < D / 16; ++c) {
-                uint32_t vb[4];
-                ldsm_x4_t(vb, sv + u * (16 * 2 * D) + at(vrow, c));
-                mma16816<T>(acc[2 * c], pa, vb[0], vb[1]);
-                mma16816<T>(acc[2 * c + 1], pa, vb[2], vb[3]);
-                if constexpr (WIDE) {
-                    const uint32_t pl[4] = {lo[0][0], lo[0][NH - 1], lo[1][0], lo[1][NH - 1]};
-                    mma16816<T>(acc[2 * c], pl, vb[0], vb[1]);
-                    mma16816<T>(acc[2 * c + 1], pl, vb[2], vb[3]);
-                }
-            }
-        }
-        // the stage is free: its values are in registers (and a zeroed row is
-        // written before the next copy lands over it)
-        if (edge) asm volatile("fence.proxy.async.shared::cta;" ::: "memory");
-        __syncwarp();
-        if (issued < left) issue(st);
-        if (++st == kStages) {
-            st = 0;
-            phase ^= 1u;
-        }
-
-        const bool row_end = cc.j + 1 == cc.q.steps;
-        if (row_end || done + 1 == left) {
-            // the row's part in this range ends here
-            const bool whole = row_end && !began_before;
-            // (a row that goes on is the warp's last: every copy has landed and
-            // been read, so its part may take the ring's place)
-            unsigned char* part = began_before ? part0 : gring;
+                for (int u = 0; u < SUBS; ++u)
+#pragma unroll
+                    for (int v = 0; v < 2; ++v)
+#pragma unroll
+                        for (int i = 0; i < NH; ++i)
+#pragma unroll
+                            for (int e = 0; e < 2; ++e)
+                                f(z[u][v][2 * i + e], t0 + u * 16 + v * 8 + 2 * kq + e, i);
+            };
+            each([&](float& y, int, int) { y *= a.score; });
+            if (a.cap_log2 > 0.f)           // cap tanh(y) = cap (1 - 2 / (2^(2 log2(e) y) + 1))
+                each([&](float& y, int, int) {
+                    y = a.cap_log2 * (1.f - __fdividef(2.f, ex2(y) + 1.f));
+                });
+            if (a.slopes)
+                each([&](float& y, int t, int i) { y += slope[i] * (float)(t - (cc.q.n - 1)); });
+            if (edge)
+                each([&](float& y, int t, int) {
+                    if (t < cc.q.lo || t >= cc.q.n) y = -INFINITY;
+                });
+            float mx[NH], alpha[NH];
+#pragma unroll
+            for (int i = 0; i < NH; ++i) mx[i] = -INFINITY;
+            each([&](float& y, int, int i) { mx[i] = fmaxf(mx[i], y); });
+            bool raised = false;
 #pragma unroll
             for (int i = 0; i < NH; ++i) {
-                float sum = l[i];
-                sum += __shfl_xor_sync(kFull, sum, 1);
-                sum += __shfl_xor_sync(kFull, sum, 2);
-                const int hr = r + 8 * i;
-                if (hr >= heads) continue;
-                const float inv = 1.f / sum;
-                uint32_t* o = reinterpret_cast<uint32_t*>(a.out) +
-                              ((int64_t)cc.s * a.H + cc.hk * a.G + cc.gc * HPR + hr) * (D / 2) + kq;
-                float2* pa = reinterpret_cast<float2*>(part) + hr * (D / 2) + kq;
+                mx[i] = fmaxf(mx[i], __shfl_xor_sync(kFull, mx[i], 1));
+                mx[i] = fmaxf(mx[i], __shfl_xor_sync(kFull, mx[i], 2));
+                const bool up = mx[i] > m[i] + kRaiseLog2 || m[i] == -INFINITY;
+                alpha[i] = up ? ex2(m[i] - mx[i]) : 1.f;
+                if (up) m[i] = mx[i];
+                raised |= up;
+            }
+            if (__any_sync(kFull, raised)) {
 #pragma unroll
-                for (int c = 0; c < D / 8; ++c) {
-                    const float o0 = WIDE ? acc[c][2 * i] : acc[c][0] + acc[c][2];
-                    const float o1 = WIDE ? acc[c][2 * i + 1] : acc[c][1] + acc[c][3];
-                    if (whole) o[c * 4] = pack2<T>(o0 * inv, o1 * inv);
-                    else pa[c * 4] = make_float2(o0, o1);
+                for (int i = 0; i < NH; ++i) l[i] *= alpha[i];
+#pragma unroll
+                for (int i = 0; i < D / 8; ++i) {
+                    acc[i][0] *= alpha[0];
+                    acc[i][1] *= alpha[0];
+                    acc[i][2] *= alpha[NH - 1];
+                    acc[i][3] *= alpha[NH - 1];
                 }
-                if (!whole && kq == 0)
-                    reinterpret_cast<float2*>(part + HPR * D * 4)[hr] = make_float2(m[i], sum);
             }
-            if (!whole && lane == 0) {
-                Part p;
-                p.s = cc.s;
-                p.row = cc.hk * a.chunks + cc.gc;
-                p.ended = row_end;
-                p.last = (int)cut.run_of(x + done + (cc.q.steps - 1 - cc.j));
-                meta[began_before ? 0 : 1] = p;
+            each([&](float& y, int, int i) { y = ex2(y - m[i]); });
+            if (edge)                       // (m is -infinity where every visible score is)
+                each([&](float& y, int t, int) {
+                    if (t < cc.q.lo || t >= cc.q.n) y = 0.f;
+                });
+            each([&](float& y, int, int i) { l[i] += y; });
+#pragma unroll
+            for (int u = 0; u < SUBS; ++u) {
+                uint32_t hi[2][NH], lo[2][NH];
+#pragma unroll
+                for (int v = 0; v < 2; ++v)
+#pragma unroll
+                    for (int i = 0; i < NH; ++i) {
+                        const float p0 = z[u][v][2 * i], p1 = z[u][v][2 * i + 1];
+                        hi[v][i] = pack2<T>(p0, p1);
+                        const float2 h = unpack2<T>(hi[v][i]);
+                        lo[v][i] = pack2<T>(p0 - h.x, p1 - h.y);
+                    }
+                const uint32_t pa[4] = {hi[0][0], WIDE ? hi[0][NH - 1] : lo[0][0], hi[1][0],
+                                        WIDE ? hi[1][NH - 1] : lo[1][0]};
+#pragma unroll
+                for (int c = 0; c < D / 16; ++c) {
+                    uint32_t vb[4];
+                    ldsm_x4_t(vb, sv + u * (16 * 2 * D) + at(vrow, c));
+                    mma16816<T>(acc[2 * c], pa, vb[0], vb[1]);
+                    mma16816<T>(acc[2 * c + 1], pa, vb[2], vb[3]);
+                    if constexpr (WIDE) {
+                        const uint32_t pl[4] = {lo[0][0], lo[0][NH - 1], lo[1][0], lo[1][NH - 1]};
+                        mma16816<T>(acc[2 * c], pl, vb[0], vb[1]);
+                        mma16816<T>(acc[2 * c + 1], pl, vb[2], vb[3]);
+                    }
+                }
             }
-            began_before = false;
-            fresh = true;
+            // the stage is free: its values are in registers (and a zeroed row
+            // is written before the next copy lands over it)
+            if (edge) asm volatile("fence.proxy.async.shared::cta;" ::: "memory");
+            __syncwarp();
+            if (lane == 0) mbar_arrive(empty + st);
+            if (++st == kStages) {
+                st = 0;
+                phase ^= 1u;
+            }
         }
-        if (cc.next(a, b)) ++row_no;
-    }
-    if (!ok) {
-        if (lane == 0) atomicOr(a.err, PKV_DEVERR_TIMEOUT);
-        // let every copy issued land before the CTA can end
-        for (int g = issued - kStages < 0 ? 0 : issued - kStages; g < issued; ++g)
-            wait_phase(full + g % kStages, (uint32_t)((g / kStages) & 1), nullptr, kWaitLimitNs);
+
+        // the row's part in this range ends here
+        done += part_steps;
+        const bool row_end = cc.j + part_steps == cc.q.steps;
+        const bool whole = row_end && !began_before;
+        // (a row that goes on is the warp's last: every copy has landed and been
+        // read, so its part may take the ring's place)
+        unsigned char* part = began_before ? part0 : gring;
+#pragma unroll
+        for (int i = 0; i < NH; ++i) {
+            float sum = l[i];
+            sum += __shfl_xor_sync(kFull, sum, 1);
+            sum += __shfl_xor_sync(kFull, sum, 2);
+            const int hr = r + 8 * i;
+            if (hr >= heads) continue;
+            const float inv = 1.f / sum;
+            uint32_t* o = reinterpret_cast<uint32_t*>(a.out) +
+                          ((int64_t)cc.s * a.H + cc.hk * a.G + cc.gc * HPR + hr) * (D / 2) + kq;
+            float2* pa = reinterpret_cast<float2*>(part) + hr * (D / 2) + kq;
+#pragma unroll
+            for (int c = 0; c < D / 8; ++c) {
+                const float o0 = WIDE ? acc[c][2 * i] : acc[c][0] + acc[c][2];
+                const float o1 = WIDE ? acc[c][2 * i + 1] : acc[c][1] + acc[c][3];
+                if (whole) o[c * 4] = pack2<T>(o0 * inv, o1 * inv);
+                else pa[c * 4] = make_float2(o0, o1);
+            }
+            if (!whole && kq == 0)
+                reinterpret_cast<float2*>(part + HPR * D * 4)[hr] = make_float2(m[i], sum);
+        }
+        if (!whole && lane == 0) {
+            Part p;
+            p.s = cc.s;
+            p.row = cc.hk * a.chunks + cc.gc;
+            p.ended = row_end;
+            p.last = row_end ? 0 : (int)cut.run_of(x + done - 1 + (cc.q.steps - cc.j - part_steps));
+            meta[began_before ? 0 : 1] = p;
+        }
+        began_before = false;
+        cc = nc;
     }
 }
 
 template <typename T, int D, bool WIDE>
-__global__ void __launch_bounds__(kThreads, 1)
+__global__ void __launch_bounds__(Geo<D, WIDE>::THREADS + 32, 1)
     grouped_decode_main(const __grid_constant__ CUtensorMap tk,
                         const __grid_constant__ CUtensorMap tv, const Args a) {
     using C = Geo<D, WIDE>;
@@ -596,28 +598,29 @@ __global__ void __launch_bounds__(kThreads, 1)
     int* ctx = reinterpret_cast<int*>(base + C::CTX_OFF);
     int* prefix = reinterpret_cast<int*>(base + C::PREFIX_OFF);
     Part* parts = reinterpret_cast<Part*>(base + C::META_OFF);   // of warp i: 2 i, 2 i + 1
-    int* sums = reinterpret_cast<int*>(parts + 2 * kWarps);
+    Start* starts = reinterpret_cast<Start*>(base + C::START_OFF);
+    int* sums = reinterpret_cast<int*>(starts + C::WARPS);
 
     const int tid = threadIdx.x, warp = tid >> 5, lane = tid & 31;
+    const bool copies = warp == C::WARPS;
     const int c = (int)blockIdx.x;
-    uint64_t* full = bars + warp * kStages;
-    if (tid == 0) {
+    if (copies && lane == 0) {
         prefetch_map(&tk);
         prefetch_map(&tv);
     }
-    if (lane == 0) {
-        for (int i = 0; i < kStages; ++i) mbar_init(full + i, 1);
-        fence_mbar_init();
-    }
-    if (lane < 2) parts[2 * warp + lane].s = -1;
+    if (!copies && lane < 2 * kStages) mbar_init(bars + lane / kStages * (C::WARPS * kStages) +
+                                                 warp * kStages + lane % kStages, 1);
+    if (!copies) fence_mbar_init();
+    if (!copies && lane < 2) parts[2 * warp + lane].s = -1;
     grid_dependency_wait();
 
     // steps before each thread's sequences
     Batch b;
-    b.per = (a.S + kThreads - 1) / kThreads;
+    b.per = (a.S + C::THREADS - 1) / C::THREADS;
     b.prefix = prefix;
     b.ctx = b.per > 1 ? a.ctx : ctx;
-    {
+    int incl = 0;
+    if (!copies) {
         int local = 0;
         for (int s = tid * b.per; s < a.S && s < (tid + 1) * b.per; ++s) {
             const int n = a.ctx[s];
@@ -625,25 +628,27 @@ __global__ void __launch_bounds__(kThreads, 1)
             local += seq_of<ST>(a, n).steps;
             if ((n < 0 || n > a.cap_tokens) && c == 0) atomicOr(a.err, PKV_DEVERR_BAD_CONTEXT);
         }
-        int incl = local;
+        incl = local;
 #pragma unroll
         for (int o = 1; o < 32; o <<= 1) {
             const int y = __shfl_up_sync(kFull, incl, o);
             if (lane >= o) incl += y;
         }
         if (lane == 31) sums[warp] = incl;
-        __syncthreads();
+    }
+    __syncthreads();
+    if (!copies) {
 #pragma unroll
-        for (int i = 0; i < kWarps; ++i)
+        for (int i = 0; i < C::WARPS; ++i)
             if (i < warp) incl += sums[i];
         prefix[tid + 1] = incl;
         if (tid == 0) prefix[0] = 0;
-        __syncthreads();
     }
+    __syncthreads();
     grid_launch_dependents();
 
     // this CTA's run of the steps, this warp's run of it
-    const int64_t X = (int64_t)(a.HK * a.chunks) * prefix[kThreads];
+    const int64_t X = (int64_t)(a.HK * a.chunks) * prefix[C::THREADS];
     const int64_t most = X / kMinSteps > 1 ? X / kMinSteps : 1;
     const int64_t used = X == 0 ? 0 : most < a.ctas ? most : a.ctas;
     bool recorded = false;
@@ -651,76 +656,89 @@ __global__ void __launch_bounds__(kThreads, 1)
         const Cut cut(X, used);
         const int64_t cx = cut.begin(c);
         const int cn = (int)(cut.begin(c + 1) - cx);
-        const int each = cn / kWarps, longer = cn - each * kWarps;
+        const int each = cn / C::WARPS, longer = cn - each * C::WARPS;
         const int64_t x = cx + warp * each + min(warp, longer);
-        const int left = each + (warp < longer);
-        unsigned char* gring = base + warp * C::RING;
-        if (left > 0)
-            walk<T, D, WIDE>(tk, tv, a, b, x, left, gring, base + C::PARTS_OFF + warp * C::PART,
-                             full, parts + 2 * warp, cut);
+        const int left = copies ? 0 : each + (warp < longer);
+        Cursor<ST> at;
+        if (left > 0) at = locate<ST, C::WARPS>(a, b, x, lane);
+        if (!copies && lane == 0) starts[warp] = {at.s, at.hk, at.gc, at.j, left};
+        __syncthreads();
+        if (copies) {
+            int issued = 0;
+            if (!fill<T, D, WIDE>(tk, tv, a, b, base, bars, starts, issued)) {
+                if (lane == 0) atomicOr(a.err, PKV_DEVERR_TIMEOUT);
+            }
+            // let every copy land before the CTA can end, whatever the others did
+            for (int g = issued - kStages < 0 ? 0 : issued - kStages; g < issued; ++g)
+                wait_phase(bars + lane * kStages + g % kStages, (uint32_t)((g / kStages) & 1),
+                           nullptr, kWaitLimitNs);
+        } else if (left > 0) {
+            walk<T, D, WIDE>(a, b, at, x, left, base + warp * C::RING,
+                             base + C::PARTS_OFF + warp * C::PART, bars + warp * kStages,
+                             bars + (C::WARPS + warp) * kStages, parts + 2 * warp, cut);
+        }
         __syncthreads();
 
         // Join the parts of each row, a head of a row a warp: a row begins with
         // an odd part, or with the CTA's first where it began in an earlier CTA.
         constexpr int V = D / 32;
-        int unit = 0;
-        for (int i = 0; i < 2 * kWarps;) {
-            if (parts[i].s < 0) {
-                ++i;
-                continue;
-            }
-            const int first = i;
-            const Part row = parts[first];
-            bool ended = false;
-            unsigned set = 0;
-            for (; i < 2 * kWarps && !ended; ++i)
-                if (parts[i].s >= 0) {
-                    set |= 1u << i;
-                    ended = parts[i].ended != 0;
-                }
-            const bool begins = (first & 1) != 0;
-            if (begins && !ended) {
+        const Part mine = parts[lane < 2 * C::WARPS ? lane : 0];
+        const unsigned held = __ballot_sync(kFull, lane < 2 * C::WARPS && mine.s >= 0);
+        const unsigned ends = __ballot_sync(kFull, lane < 2 * C::WARPS && mine.s >= 0 && mine.ended);
+        unsigned begins = held & 0xaaaaaaaau;
+        if (held) begins |= held & (0u - held);
+        for (int unit = 0; begins; begins &= begins - 1) {
+            const int first = __ffs(begins) - 1;
+            const unsigned from = held & (~0u << first), end = ends & (~0u << first);
+            const unsigned set = end ? from & (2u * (end & (0u - end)) - 1u) : from;
+            const bool starts_here = (first & 1) != 0;
+            const int s = __shfl_sync(kFull, mine.s, first);
+            const int row = __shfl_sync(kFull, mine.row, first);
+            if (starts_here && !end) {
                 recorded = true;
-                if (tid == 0) {
-                    Record rec;
-                    rec.s = row.s;
-                    rec.row = row.row;
-                    rec.last = row.last;
-                    rec.pad = 0;
-                    a.rec[c] = rec;
-                }
+                if (lane == first && warp == 0) a.rec[c] = {s, row, mine.last, 0};
             }
-            const int hk = row.row / a.chunks, gc = row.row - hk * a.chunks;
+            const int hk = a.chunks == 1 ? row : row / a.chunks, gc = row - hk * a.chunks;
             const int heads = min(HPR, a.G - gc * HPR);
-            for (int h = (warp + kWarps - unit % kWarps) % kWarps; h < heads; h += kWarps) {
+            for (int h = warp - unit % C::WARPS; h < heads; h += C::WARPS) {
+                if (h < 0 || copies) continue;
+                auto part = [&](int k) -> const unsigned char* {
+                    return base + (k & 1 ? (k >> 1) * C::RING : C::PARTS_OFF + (k >> 1) * C::PART);
+                };
+                // two parts at a time: most rows here have no more
                 float M = -INFINITY, L = 0.f, o[V];
 #pragma unroll
                 for (int e = 0; e < V; ++e) o[e] = 0.f;
-                auto part = [&](int k) -> const unsigned char* {
-                    return k & 1 ? base + (k >> 1) * C::RING : base + C::PARTS_OFF + (k >> 1) * C::PART;
-                };
-                for (unsigned left_set = set; left_set; left_set &= left_set - 1)
-                    M = fmaxf(M, reinterpret_cast<const float2*>(part(__ffs(left_set) - 1) +
-                                                                 HPR * D * 4)[h].x);
-                for (unsigned left_set = set; left_set; left_set &= left_set - 1) {
-                    const unsigned char* p = part(__ffs(left_set) - 1);
-                    const float2 ml = reinterpret_cast<const float2*>(p + HPR * D * 4)[h];
-                    const float* v = reinterpret_cast<const float*>(p) + h * D + lane * V;
-                    const float f = ex2(ml.x - M);
-                    L += f * ml.y;
+                for (unsigned to_do = set; to_do;) {
+                    const int k0 = __ffs(to_do) - 1;
+                    to_do &= to_do - 1;
+                    const bool two = to_do != 0;
+                    const int k1 = two ? __ffs(to_do) - 1 : k0;
+                    to_do &= to_do - 1;
+                    const unsigned char *p0 = part(k0), *p1 = part(k1);
+                    const float2 m0 = reinterpret_cast<const float2*>(p0 + HPR * D * 4)[h];
+                    float2 m1 = reinterpret_cast<const float2*>(p1 + HPR * D * 4)[h];
+                    const float* v0 = reinterpret_cast<const float*>(p0) + h * D + lane * V;
+                    const float* v1 = reinterpret_cast<const float*>(p1) + h * D + lane * V;
+                    if (!two) m1 = make_float2(-INFINITY, 0.f);
+                    const float top = fmaxf(M, fmaxf(m0.x, m1.x));
+                    const float f = k0 == first ? 0.f : ex2(M - top);
+                    const float f0 = ex2(m0.x - top), f1 = two ? ex2(m1.x - top) : 0.f;
+                    M = top;
+                    L = L * f + m0.y * f0 + m1.y * f1;
 #pragma unroll
-                    for (int e = 0; e < V; ++e) o[e] += f * v[e];
+                    for (int e = 0; e < V; ++e) o[e] = o[e] * f + v0[e] * f0 + v1[e] * f1;
                 }
-                if (begins && ended) {
-                    const float inv = 1.f / L;
+                if (starts_here && end) {
+                    const float inv = __fdividef(1.f, L);
                     uint32_t* out = reinterpret_cast<uint32_t*>(a.out) +
-                                    ((int64_t)row.s * a.H + hk * a.G + gc * HPR + h) * (D / 2) +
+                                    ((int64_t)s * a.H + hk * a.G + gc * HPR + h) * (D / 2) +
                                     lane * (V / 2);
 #pragma unroll
                     for (int e = 0; e < V / 2; ++e)
                         out[e] = pack2<T>(o[2 * e] * inv, o[2 * e + 1] * inv);
                 } else {
-                    const int64_t to = (2 * (int64_t)c + (begins ? 1 : 0)) * HPR + h;
+                    const int64_t to = (2 * (int64_t)c + (starts_here ? 1 : 0)) * HPR + h;
                     float* p = a.acc + to * D + lane * V;
 #pragma unroll
                     for (int e = 0; e < V; ++e) p[e] = o[e];
@@ -737,7 +755,7 @@ __global__ void __launch_bounds__(kThreads, 1)
     for (int s = c; s < a.S; s += gridDim.x) {
         if (b.ctx[s] > 0) continue;
         uint4* o = static_cast<uint4*>(a.out) + s * row_words;
-        for (int64_t i = tid; i < row_words; i += kThreads) o[i] = make_uint4(0u, 0u, 0u, 0u);
+        for (int64_t i = tid; i < row_words; i += C::THREADS + 32) o[i] = make_uint4(0u, 0u, 0u, 0u);
     }
 }
 
@@ -839,7 +857,7 @@ cudaError_t launch(const CUtensorMap& tk, const CUtensorMap& tv, const Args& a, 
     attr[0].val.programmaticStreamSerializationAllowed = 1;
     cudaLaunchConfig_t cfg = {};
     cfg.gridDim = dim3((unsigned)grid);
-    cfg.blockDim = dim3(kThreads);
+    cfg.blockDim = dim3(Geo<D, WIDE>::THREADS + 32);
     cfg.dynamicSmemBytes = smem;
     cfg.stream = stream;
     cfg.attrs = attr;
