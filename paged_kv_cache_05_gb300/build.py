@@ -2,16 +2,20 @@
 
 Each translation unit compiles in parallel; the objects are linked into
 ``paged_kv_cache_05_gb300/libpagedkv.so`` against the shared CUDA runtime.
+``_pkvbind.so`` beside it is the Python module of the grouped entry points
+(g++ against the installed torch's headers).
 Usage: ``python -m paged_kv_cache_05_gb300.build [--force] [--verbose]``.
 """
 from __future__ import annotations
 
 import argparse
 import concurrent.futures as cf
+import importlib.util
 import os
 import shutil
 import subprocess
 import sys
+import sysconfig
 
 PKG = os.path.dirname(os.path.abspath(__file__))
 ROOT = os.path.dirname(PKG)
@@ -19,6 +23,8 @@ CSRC = os.path.join(PKG, "csrc")
 INCLUDE = os.path.join(ROOT, "include")
 BUILD = os.path.join(PKG, "_build")
 LIB = os.path.join(PKG, "libpagedkv.so")
+BIND = os.path.join(PKG, "_pkvbind.so")
+BIND_SOURCE = "binding.cpp"
 SOURCES = ["errors.cu", "cache_ops.cu", "decode_api.cu", "decode_f16.cu", "decode_bf16.cu",
            "decode_shared_f16.cu", "decode_shared_bf16.cu", "decode_append_f16.cu",
            "decode_append_bf16.cu", "decode_noalloc.cu", "decode_grouped.cu", "prefill.cu",
@@ -53,7 +59,33 @@ def _deps_mtime() -> float:
 
 
 def up_to_date() -> bool:
-    return os.path.exists(LIB) and os.path.getmtime(LIB) >= _deps_mtime()
+    deps = _deps_mtime()
+    return all(os.path.exists(f) and os.path.getmtime(f) >= deps for f in (LIB, BIND))
+
+
+def _cuda_home(cc: str) -> str:
+    return os.environ.get("CUDA_HOME") or os.path.dirname(os.path.dirname(os.path.realpath(cc)))
+
+
+def _bind_commands(cc: str, out: str):
+    """Compile and link commands of the binding module."""
+    spec = importlib.util.find_spec("torch")
+    if spec is None:
+        raise RuntimeError("torch not found (the binding is compiled against its headers)")
+    torch = os.path.dirname(spec.origin)
+    cxx = os.environ.get("CXX") or "g++"
+    obj = os.path.join(BUILD, "binding.o")
+    inc = [INCLUDE, os.path.join(torch, "include"),
+           os.path.join(torch, "include", "torch", "csrc", "api", "include"),
+           os.path.join(_cuda_home(cc), "include"), sysconfig.get_paths()["include"]]
+    comp = [cxx, "-O2", "-std=c++17", "-fPIC", "-Wall"]
+    for i in inc:
+        comp += ["-isystem" if "torch" in i else "-I", i]
+    comp += ["-c", os.path.join(CSRC, BIND_SOURCE), "-o", obj]
+    tl = os.path.join(torch, "lib")
+    link = [cxx, "-shared", obj, "-o", out, "-L", tl, "-ltorch_python", "-ltorch_cpu", "-lc10",
+            "-lc10_cuda", "-L", PKG, "-l:libpagedkv.so", "-Wl,-rpath,$ORIGIN:" + tl]
+    return comp, link
 
 
 def build(force: bool = False, verbose: bool = False, jobs: int | None = None) -> str:
@@ -70,8 +102,17 @@ def build(force: bool = False, verbose: bool = False, jobs: int | None = None) -
             raise RuntimeError("compile failed: %s\n%s%s" % (" ".join(cmd), r.stdout, r.stderr))
         return obj, r.stdout + r.stderr
 
-    with cf.ThreadPoolExecutor(max_workers=jobs or len(SOURCES)) as ex:
+    def run(cmd, what):
+        r = subprocess.run(cmd, capture_output=True, text=True)
+        if r.returncode != 0:
+            raise RuntimeError("%s failed: %s\n%s%s" % (what, " ".join(cmd), r.stdout, r.stderr))
+
+    tmp_bind = BIND + ".tmp.%d" % os.getpid()
+    bind_compile, bind_link = _bind_commands(cc, tmp_bind)
+    with cf.ThreadPoolExecutor(max_workers=jobs or len(SOURCES) + 1) as ex:
+        bound = ex.submit(run, bind_compile, "compile")
         results = list(ex.map(compile_one, SOURCES))
+        bound.result()
     if verbose:
         for _, log in results:
             if log.strip():
@@ -84,6 +125,8 @@ def build(force: bool = False, verbose: bool = False, jobs: int | None = None) -
     if r.returncode != 0:
         raise RuntimeError("link failed: %s\n%s%s" % (" ".join(cmd), r.stdout, r.stderr))
     os.replace(tmp, LIB)
+    run(bind_link, "link")
+    os.replace(tmp_bind, BIND)
     return LIB
 
 

@@ -140,16 +140,22 @@ def _check(fn: str, status: int):
 
 
 # ----------------------------------------------------------------- torch side
+_torch_module = None
+
+
 def _torch():
-    import torch
-    return torch
+    global _torch_module
+    if _torch_module is None:
+        import torch
+        _torch_module = torch
+    return _torch_module
 
 
 def _dtype_code(t) -> int:
     torch = _torch()
-    if t == torch.float16:
+    if t is torch.float16:
         return PKV_F16
-    if t == torch.bfloat16:
+    if t is torch.bfloat16:
         return PKV_BF16
     raise TypeError("fp16 or bf16 storage expected, got %s" % t)
 
@@ -354,34 +360,17 @@ def paged_attention_decode_grouped(out, q, k_cache, v_cache, block_tables, conte
     softcap * tanh(z / softcap), limited to the last `window` tokens and biased
     by slopes[h] * (t - p), where given."""
     torch = _torch()
-    S, H, D = q.shape
-    nb, HK, B, D2 = k_cache.shape
-    dev, dt = q.get_device(), q.dtype
-    if D2 != D or v_cache.shape != k_cache.shape:
-        raise ValueError("q / cache shape mismatch")
-    if out.shape != q.shape:
-        raise ValueError("out must have q's shape")
-    if block_tables.dim() != 2 or block_tables.shape[0] != S or context_lens.shape != (S,):
-        raise ValueError("block_tables must be [num_seqs, max_blocks], context_lens [num_seqs]")
-    if dev < 0:
-        raise ValueError("q must be a CUDA tensor")
-    width = block_tables.shape[1]
-    sp = None
-    if slopes is not None:
-        if slopes.shape != (H,):
-            raise ValueError("slopes must be [num_heads]")
-        sp = _ptr(slopes, "slopes", dev, torch.float32)
     if workspace is None:
-        workspace = alloc_grouped_workspace(S, H, HK, D, B, width, q.device)
+        S, H, D = q.shape
+        HK, B = k_cache.shape[1:3]
+        workspace = alloc_grouped_workspace(S, H, HK, D, B, block_tables.shape[1], q.device)
         if stream is not None:
             workspace.record_stream(stream)
-    _run("pkv_paged_attention_decode_grouped", dev, stream,
-         (_ptr(out, "out", dev, dt), _ptr(q, "q", dev, dt), _ptr(k_cache, "k_cache", dev, dt),
-          _ptr(v_cache, "v_cache", dev, dt),
-          _ptr(block_tables, "block_tables", dev, torch.int32),
-          _ptr(context_lens, "context_lens", dev, torch.int32), sp, float(scale), float(softcap),
-          int(window), S, H, HK, D, B, width, nb, _dtype_code(dt),
-          _ptr(workspace, "workspace", dev, torch.uint8), workspace.shape[0]))
+    st = (_bind or _binding()).paged_attention_decode_grouped(
+        out, q, k_cache, v_cache, block_tables, context_lens, scale, softcap, window, slopes,
+        workspace, None if stream is None else stream.cuda_stream)
+    if st:
+        _check("pkv_paged_attention_decode_grouped", st)
     return out
 
 
@@ -448,33 +437,11 @@ def paged_attention_prefill_grouped(out, q, k_cache, v_cache, block_tables, cont
     by softcap * tanh(z / softcap), limited to the last `window` tokens and
     biased by slopes[h] * (t - p), where given."""
     torch = _torch()
-    T, H, D = q.shape
-    nb, HK, B, D2 = k_cache.shape
-    S = context_lens.shape[0]
-    dev, dt = q.get_device(), q.dtype
-    if D2 != D or v_cache.shape != k_cache.shape:
-        raise ValueError("q / cache shape mismatch")
-    if out.shape != q.shape:
-        raise ValueError("out must have q's shape")
-    if block_tables.dim() != 2 or block_tables.shape[0] != S or query_start.shape != (S + 1,) or \
-            context_lens.dim() != 1:
-        raise ValueError("block_tables [S, max_blocks], context_lens [S], query_start [S+1] "
-                         "expected")
-    if dev < 0:
-        raise ValueError("q must be a CUDA tensor")
-    sp = None
-    if slopes is not None:
-        if slopes.shape != (H,):
-            raise ValueError("slopes must be [num_heads]")
-        sp = _ptr(slopes, "slopes", dev, torch.float32)
-    _run("pkv_paged_attention_prefill_grouped", dev, stream,
-         (_ptr(out, "out", dev, dt), _ptr(q, "q", dev, dt), _ptr(k_cache, "k_cache", dev, dt),
-          _ptr(v_cache, "v_cache", dev, dt),
-          _ptr(block_tables, "block_tables", dev, torch.int32),
-          _ptr(context_lens, "context_lens", dev, torch.int32),
-          _ptr(query_start, "query_start", dev, torch.int32), sp, float(scale), float(softcap),
-          int(window), S, H, HK, D, B, block_tables.shape[1], nb, int(max_query_len), T,
-          _dtype_code(dt)))
+    st = (_bind or _binding()).paged_attention_prefill_grouped(
+        out, q, k_cache, v_cache, block_tables, context_lens, query_start, scale, max_query_len,
+        softcap, window, slopes, None if stream is None else stream.cuda_stream)
+    if st:
+        _check("pkv_paged_attention_prefill_grouped", st)
     return out
 
 
@@ -555,44 +522,24 @@ def rope_phases(inv_freq, device="cuda"):
     return torch.from_numpy(out).to(device)
 
 
-def _ptr(t, name, dev, dtype):
-    """data_ptr of a contiguous CUDA tensor of that device and type."""
-    if t.get_device() != dev:
-        raise ValueError("%s must be a CUDA tensor on the device of q" % name)
-    if t.dtype != dtype:
-        raise TypeError("%s must be %s, got %s" % (name, dtype, t.dtype))
-    if not t.is_contiguous():
-        raise ValueError("%s must be contiguous" % name)
-    return t.data_ptr()
+_bind = None
 
 
-def _rows(t, name, dev, dtype):
-    """(data_ptr, token stride) of [tokens, heads, head_dim] whose heads lie side
-    by side; tokens may be apart (a slice of a joint projection's output)."""
-    if t.get_device() != dev:
-        raise ValueError("%s must be a CUDA tensor on the device of q" % name)
-    if t.dtype != dtype:
-        raise TypeError("%s must be %s, got %s" % (name, dtype, t.dtype))
-    T, H, D = t.shape
-    st = t.stride()
-    if (D > 1 and st[2] != 1) or (H > 1 and st[1] != D):
-        raise ValueError("%s must have its heads side by side in each token's row" % name)
-    # one token has no next one: any stride will do
-    return t.data_ptr(), st[0] if T > 1 else H * D
-
-
-def _run(fn, dev, stream, args):
-    """The library call `fn` with the given device current, on `stream` (or that
-    device's current one)."""
-    torch = _torch()
-    if torch.cuda.current_device() != dev:
-        with torch.cuda.device(dev):
-            return _run(fn, dev, stream, args)
-    handle = stream.cuda_stream if stream is not None else \
-        torch._C._cuda_getCurrentRawStream(dev)
-    st = getattr(lib(), fn)(*args, handle)
-    if st != PKV_OK:
-        _check(fn, st)
+def _binding():
+    """The compiled binding of the grouped entry points (_pkvbind.so, built with
+    the library): their tensors are checked and described to the C ABI there,
+    which costs a few tenths of a microsecond instead of eight."""
+    global _bind
+    if _bind is None:
+        _torch()
+        lib()
+        try:
+            from . import _pkvbind
+        except ImportError as e:
+            raise RuntimeError("_pkvbind.so is not built or does not load (%s); run "
+                               "`python -m paged_kv_cache_05_gb300.build`" % e) from e
+        _bind = _pkvbind
+    return _bind
 
 
 def norm_rope_and_cache(q_out, q, k, v, k_cache, v_cache, slot_mapping, positions, phases,
@@ -603,38 +550,11 @@ def norm_rope_and_cache(q_out, q, k, v, k_cache, v_cache, slot_mapping, position
     and the values [T, HK, D] to their slots of the caches [blocks, HK, B, D].
     q, k and v may be slices of one projection's output.  phases: rope_phases()
     of rot_dim / 2 frequencies, or None to turn nothing; weights: fp32 [D]."""
-    torch = _torch()
-    T, H, D = q.shape
-    nb, HK, B, D2 = k_cache.shape
-    dev, dt = q.get_device(), q.dtype
-    if D2 != D or k.shape != (T, HK, D) or v.shape != (T, HK, D) or \
-            v_cache.shape != k_cache.shape:
-        raise ValueError("q/k/v/cache shape mismatch")
-    if q_out.shape != q.shape:
-        raise ValueError("q_out must have q's shape")
-    if slot_mapping.shape != (T,) or positions.shape != (T,):
-        raise ValueError("slot_mapping and positions must be [num_tokens]")
-    if dev < 0:
-        raise ValueError("q must be a CUDA tensor")
-    qp, qs = _rows(q, "q", dev, dt)
-    kp, ks = _rows(k, "k", dev, dt)
-    vp, vs = _rows(v, "v", dev, dt)
-    rot, ph = 0, None
-    if phases is not None:
-        if phases.dim() != 1:
-            raise ValueError("phases must be [rot_dim / 2]")
-        rot, ph = 2 * phases.shape[0], _ptr(phases, "phases", dev, torch.int64)
-    wp = []
-    for w, n in ((q_weight, "q_weight"), (k_weight, "k_weight")):
-        if w is not None and w.shape != (D,):
-            raise ValueError("%s must be [head_dim]" % n)
-        wp.append(None if w is None else _ptr(w, n, dev, torch.float32))
-    _run("pkv_norm_rope_and_cache", dev, stream,
-         (_ptr(q_out, "q_out", dev, dt), qp, kp, vp, qs, ks, vs,
-          _ptr(k_cache, "k_cache", dev, dt), _ptr(v_cache, "v_cache", dev, dt),
-          _ptr(slot_mapping, "slot_mapping", dev, torch.int64),
-          _ptr(positions, "positions", dev, torch.int32), ph, rot, 1 if interleaved else 0,
-          float(rope_scale), wp[0], wp[1], float(eps), T, H, HK, D, B, nb, _dtype_code(dt)))
+    st = (_bind or _binding()).norm_rope_and_cache(
+        q_out, q, k, v, k_cache, v_cache, slot_mapping, positions, phases, q_weight, k_weight,
+        eps, rope_scale, interleaved, None if stream is None else stream.cuda_stream)
+    if st:
+        _check("pkv_norm_rope_and_cache", st)
     return q_out
 
 
