@@ -1090,10 +1090,11 @@ __global__ void __launch_bounds__(threads_for(FUSED), 1)
                 auto capped = [&](float v) {
                     return a.cap_log2 * (1.f - 2.f * rcp(ex2(v * sl2) + 1.f));
                 };
-                auto biased = [&](float v, int e) {
-                    const float z = (KIND & kCapped) != 0 ? capped(v) : v * sl2;
-                    return z + slope * (float)(kb + e - qpos);
+                auto biased = [&](float v, float at_e) {
+                    return (KIND & kCapped) != 0 ? capped(v) + at_e : fmaf(v, sl2, at_e);
                 };
+                // the bias at key 0 of the tile; at key e: fmaf(slope, e, at0)
+                const float at0 = slope * (float)(kb - qpos);
                 // Row max of the visible scaled scores.  A full tile: both
                 // 64-column halves loaded before one wait, two max chains per
                 // half.  A tile crossing the diagonal runs once per query tile,
@@ -1116,7 +1117,8 @@ __global__ void __launch_bounds__(threads_for(FUSED), 1)
                             // serves: every score is formed
 #pragma unroll
                             for (int e = 0; e < 64; ++e)
-                                mx = fmaxf(mx, biased(__uint_as_float(r[e]), hh * 64 + e));
+                                mx = fmaxf(mx, biased(__uint_as_float(r[e]),
+                                                      fmaf(slope, (float)(hh * 64 + e), at0)));
                             continue;
                         }
                         float e0 = pos_scale ? -INFINITY : INFINITY, e1 = e0;
@@ -1147,11 +1149,12 @@ __global__ void __launch_bounds__(threads_for(FUSED), 1)
                             continue;
                         uint32_t r[32];
                         tmem_ld32(tS + (uint32_t)(q * 32), r);
+                        const float at_q = fmaf(slope, (float)(q * 32), at0);
                         auto score = [&](int e) {
                             const float v = __uint_as_float(r[e]);
                             const bool seen = e <= lq && (KIND == kPlain || e >= fq);
                             if constexpr ((KIND & kBiased) != 0)
-                                return seen ? biased(v, q * 32 + e) : -INFINITY;
+                                return seen ? biased(v, fmaf(slope, (float)e, at_q)) : -INFINITY;
                             else
                                 return seen ? v * sl2 : -INFINITY;
                         };
@@ -1196,14 +1199,16 @@ __global__ void __launch_bounds__(threads_for(FUSED), 1)
                         }
                         uint32_t r[32];
                         tmem_ld32(tS + (uint32_t)(q * 32), r);
+                        const float at_q = fmaf(slope, (float)(q * 32), at0) - m_new;
                         uint32_t pk[16];
                         uint32_t pr[kSplit ? 16 : 1];
 #pragma unroll
                         for (int e = 0; e < 32; e += 2) {
                             float p0, p1;
                             if constexpr ((KIND & kBiased) != 0) {
-                                p0 = biased(__uint_as_float(r[e]), q * 32 + e) - m_new;
-                                p1 = biased(__uint_as_float(r[e + 1]), q * 32 + e + 1) - m_new;
+                                p0 = biased(__uint_as_float(r[e]), fmaf(slope, (float)e, at_q));
+                                p1 = biased(__uint_as_float(r[e + 1]),
+                                            fmaf(slope, (float)(e + 1), at_q));
                             } else if constexpr ((KIND & kCapped) != 0) {
                                 p0 = capped(__uint_as_float(r[e])) - m_new;
                                 p1 = capped(__uint_as_float(r[e + 1])) - m_new;

@@ -17,13 +17,14 @@
 // number, go through sincospif (|angle| at most half a turn, error 2^-24 of
 // it), so no table of cosines is kept or read.
 //
-// Bound: HBM bytes (each row read once, written once; a token's angles cost
-// about as much arithmetic as one of its row pairs).  Layout of the work: a
-// warp takes one token, or one of `parts` equal shares of it when there are
-// few tokens; D/8 lanes hold a row (8 elements each, so that a lane owns the
-// same four pairs of every row it meets and computes their angles once), 2 or
-// 4 rows fill the warp, and kUnroll such passes are loaded before the first is
-// computed.
+// Bound: HBM bytes (each row read once, written once), with instruction issue
+// close behind (a first version at 170 instructions a pass was bound by it, at
+// 5.3 TB/s): hence one walk per kind of row, weights in registers, packed fp32
+// pairs.  Layout of the work: a warp takes one token, or one of `parts` equal
+// runs of its rows when there are few tokens; D/8 lanes hold a row (8 elements
+// each, so that a lane owns the same four pairs of every row it meets and
+// computes their angles once), 2 or 4 rows fill the warp (a pass), and kUnroll
+// passes are loaded before the first is computed.
 #include <cuda_bf16.h>
 #include <cuda_fp16.h>
 #include <cuda_runtime.h>
@@ -39,6 +40,11 @@ namespace {
 constexpr int kThreads = 128;
 constexpr int kWarps = kThreads / 32;
 constexpr int kUnroll = 4;
+// Resident blocks per SM that the registers are allotted for (73 a thread):
+// 16384 tokens of 32 + 8 + 8 heads of 128 take 63.1 us (6.38 TB/s), against 67.3
+// for 6 and 67.4 for 9.
+constexpr int kResident = 7;
+constexpr int kWarpsPerSm = 12;             // aimed at when there are few tokens
 
 struct RopeArgs {
     uint16_t* q_out;
@@ -75,132 +81,184 @@ __device__ __forceinline__ uint32_t pack2(float lo, float hi) {
     }
 }
 
-// A lane's eight elements of a row: four at offset a, four at offset b.
-struct Words {
-    uint2 a, b;
-};
+// Pairs of fp32 values in one 64-bit register, and the packed operations that
+// work on both at once.
+__device__ __forceinline__ uint64_t two(float a, float b) {
+    uint64_t r;
+    asm("mov.b64 %0, {%1, %2};" : "=l"(r) : "f"(a), "f"(b));
+    return r;
+}
+__device__ __forceinline__ float2 split(uint64_t v) {
+    float2 r;
+    asm("mov.b64 {%0, %1}, %2;" : "=f"(r.x), "=f"(r.y) : "l"(v));
+    return r;
+}
+__device__ __forceinline__ uint64_t mul2(uint64_t a, uint64_t b) {
+    uint64_t d;
+    asm("mul.rn.f32x2 %0, %1, %2;" : "=l"(d) : "l"(a), "l"(b));
+    return d;
+}
+__device__ __forceinline__ uint64_t fma2(uint64_t a, uint64_t b, uint64_t c) {
+    uint64_t d;
+    asm("fma.rn.f32x2 %0, %1, %2, %3;" : "=l"(d) : "l"(a), "l"(b), "l"(c));
+    return d;
+}
 
 template <typename T, int D, bool INTERLEAVED>
-__global__ void __launch_bounds__(kThreads) norm_rope_and_cache_kernel(const RopeArgs p) {
+__global__ void __launch_bounds__(kThreads, kResident) norm_rope_and_cache_kernel(const RopeArgs p) {
     pkv::pdl_wait_then_release();
     constexpr int LPR = D / 8;              // lanes per row
     constexpr int RPP = 32 / LPR;           // rows per pass
     const int lane = threadIdx.x & 31;
     const int64_t w = (int64_t)blockIdx.x * kWarps + (threadIdx.x >> 5);
-    const int64_t t = w / p.parts;
+    const int64_t t = p.parts == 1 ? w : w / p.parts;
     const int part = (int)(w - t * p.parts);
     if (t >= p.T) return;
+    // a lane holds four elements of a row at offset ea and four at eb; where its
+    // pairs turn, pair j is element j of each (interleaved: 2 j and 2 j + 1 of
+    // the eight, which are consecutive)
     const int li = lane % LPR, sub = lane / LPR;
-    const bool turns = li < p.rot / 8;      // this lane's pairs rotate
+    const bool turns = li < p.rot / 8;
     const int ea = INTERLEAVED ? 8 * li : turns ? 4 * li : 8 * li;
     const int eb = INTERLEAVED || !turns ? ea + 4 : p.rot / 2 + 4 * li;
 
-    // passes of the token: its query rows, then key rows, then value rows
-    const int nq = (p.H + RPP - 1) / RPP, nk = (p.HK + RPP - 1) / RPP;
-    const int n = nq + 2 * nk;
+    // passes of the token: its query rows, key rows, value rows; this warp takes
+    // an equal run of them, kUnroll loaded at a time
+    const int nq = (p.H + RPP - 1) / RPP, nk = (p.HK + RPP - 1) / RPP, n = nq + 2 * nk;
+    const int i0 = p.parts == 1 ? 0 : part * n / p.parts;
+    const int i1 = p.parts == 1 ? n : (part + 1) * n / p.parts;
     const int64_t slot = p.slots[t];
-    const bool stored = slot >= 0 && slot < p.num_slots;
-    if (slot >= p.num_slots && part == 0 && lane == 0) atomicOr(p.err, PKV_DEVERR_BAD_SLOT);
-    const int64_t blk = stored ? slot / p.B : 0;
-    const int64_t off = stored ? slot - blk * p.B : 0;
-    // first element of the lane's row in pass i, in the input and (dst) the output
-    auto row = [&](int i, const uint16_t** src, uint16_t** dst) -> bool {
-        if (i < nq) {
-            const int h = i * RPP + sub;
-            *src = p.q + t * p.q_stride + (int64_t)h * D;
-            *dst = p.q_out + (t * p.H + h) * D;
-            return h < p.H;
-        }
-        const bool key = i < nq + nk;
-        const int h = (i - nq - (key ? 0 : nk)) * RPP + sub;
-        *src = (key ? p.k + t * p.k_stride : p.v + t * p.v_stride) + (int64_t)h * D;
-        *dst = (key ? p.k_cache : p.v_cache) + ((blk * p.HK + h) * p.B + off) * D;
-        return h < p.HK && stored;
-    };
-
-    Words x[kUnroll];
-    auto load = [&](int i0) {
-#pragma unroll
-        for (int u = 0; u < kUnroll; ++u) {
-            const int i = i0 + u * p.parts;
-            const uint16_t* src;
-            uint16_t* dst;
-            x[u].a = x[u].b = make_uint2(0u, 0u);
-            if (i < n && row(i, &src, &dst)) {
-                x[u].a = *reinterpret_cast<const uint2*>(src + ea);
-                x[u].b = *reinterpret_cast<const uint2*>(src + eb);
-            }
-        }
-    };
-    load(part);
-
-    float c[4], s[4];
-    if (turns) {
-        const uint64_t pos = (uint64_t)(int64_t)p.positions[t];
+    const int pos = p.positions[t];
+    uint64_t c[4], s[4];
+    bool ready = false;
+    auto angles = [&]() {
+        ready = true;
+        if (!turns) return;
+        float cs[4], sn[4];
 #pragma unroll
         for (int j = 0; j < 4; ++j) {
-            const int turn = (int)((p.phases[4 * li + j] * pos) >> 32);   // 2^-32 turns
-            sincospif((float)turn * 0x1p-31f, &s[j], &c[j]);
-            c[j] *= p.rope_scale;
-            s[j] *= p.rope_scale;
+            const int turn = (int)((p.phases[4 * li + j] * (uint64_t)(int64_t)pos) >> 32);   // 2^-32 turns
+            sincospif((float)turn * 0x1p-31f, &sn[j], &cs[j]);
+            cs[j] *= p.rope_scale;
+            sn[j] *= p.rope_scale;
         }
-    }
-
-    for (int i0 = part; i0 < n; i0 += kUnroll * p.parts) {
-        if (i0 != part) load(i0);
+        if constexpr (INTERLEAVED) {
 #pragma unroll
-        for (int u = 0; u < kUnroll; ++u) {
-            const int i = i0 + u * p.parts;
-            if (i >= n) break;
-            const uint16_t* src;
-            uint16_t* dst;
-            const bool live = row(i, &src, &dst);
-            if (i < nq + nk) {
-                float f[8];
-                const uint32_t in[4] = {x[u].a.x, x[u].a.y, x[u].b.x, x[u].b.y};
+            for (int j = 0; j < 4; ++j) {
+                c[j] = two(cs[j], cs[j]);
+                s[j] = two(-sn[j], sn[j]);
+            }
+        } else {
+            c[0] = two(cs[0], cs[1]);
+            c[1] = two(cs[2], cs[3]);
+            s[0] = two(sn[0], sn[1]);
+            s[1] = two(sn[2], sn[3]);
+            s[2] = two(-sn[0], -sn[1]);
+            s[3] = two(-sn[2], -sn[3]);
+        }
+    };
+
+    // passes [from, to) of one kind: head h at src + h * D, its result at dst + h * dst_head
+    auto rows = [&](const uint16_t* src, uint16_t* dst, int64_t dst_head, int heads, int from,
+                    int to, const float* wt) {
+        uint64_t wv[4];
+        if (wt) {
+            const float4 wa = __ldg(reinterpret_cast<const float4*>(wt + ea));
+            const float4 wb = __ldg(reinterpret_cast<const float4*>(wt + eb));
+            wv[0] = two(wa.x, wa.y);
+            wv[1] = two(wa.z, wa.w);
+            wv[2] = two(wb.x, wb.y);
+            wv[3] = two(wb.z, wb.w);
+        }
+        heads = min(heads, to * RPP);
+        for (; from < to; from += kUnroll) {
+            uint2 xa[kUnroll], xb[kUnroll];
+            const int h0 = from * RPP + sub;
+            const uint16_t* in = src + h0 * D;
+#pragma unroll
+            for (int u = 0; u < kUnroll; ++u) {
+                xa[u] = xb[u] = make_uint2(0u, 0u);
+                if (h0 + u * RPP < heads) {
+                    xa[u] = *reinterpret_cast<const uint2*>(in + u * RPP * D + ea);
+                    xb[u] = *reinterpret_cast<const uint2*>(in + u * RPP * D + eb);
+                }
+            }
+            if (!ready) angles();
+#pragma unroll
+            for (int u = 0; u < kUnroll; ++u) {
+                if (from + u >= to) break;
+                const int h = h0 + u * RPP;
+                const uint32_t word[4] = {xa[u].x, xa[u].y, xb[u].x, xb[u].y};
+                uint64_t x[4];
 #pragma unroll
                 for (int e = 0; e < 4; ++e) {
-                    const float2 v = unpack2<T>(in[e]);
-                    f[2 * e] = v.x;
-                    f[2 * e + 1] = v.y;
+                    const float2 v = unpack2<T>(word[e]);
+                    x[e] = two(v.x, v.y);
                 }
-                const float* wt = i < nq ? p.q_weight : p.k_weight;
                 if (wt) {
-                    float sum = 0.f;
+                    uint64_t sq = mul2(x[0], x[0]);
 #pragma unroll
-                    for (int e = 0; e < 8; ++e) sum += f[e] * f[e];
+                    for (int e = 1; e < 4; ++e) sq = fma2(x[e], x[e], sq);
+                    const float2 v = split(sq);
+                    float sum = v.x + v.y;
 #pragma unroll
                     for (int o = LPR / 2; o > 0; o >>= 1)
                         sum += __shfl_xor_sync(0xffffffffu, sum, o);
                     const float r = rsqrtf(sum * (1.f / D) + p.eps);
-                    const float4 wa = __ldg(reinterpret_cast<const float4*>(wt + ea));
-                    const float4 wb = __ldg(reinterpret_cast<const float4*>(wt + eb));
-                    f[0] *= r * wa.x;
-                    f[1] *= r * wa.y;
-                    f[2] *= r * wa.z;
-                    f[3] *= r * wa.w;
-                    f[4] *= r * wb.x;
-                    f[5] *= r * wb.y;
-                    f[6] *= r * wb.z;
-                    f[7] *= r * wb.w;
+                    const uint64_t r2 = two(r, r);
+#pragma unroll
+                    for (int e = 0; e < 4; ++e) x[e] = mul2(x[e], mul2(wv[e], r2));
                 }
                 if (turns) {
+                    if constexpr (INTERLEAVED) {
 #pragma unroll
-                    for (int j = 0; j < 4; ++j) {
-                        const int ia = INTERLEAVED ? 2 * j : j, ib = INTERLEAVED ? 2 * j + 1 : j + 4;
-                        const float a = f[ia], b = f[ib];
-                        f[ia] = a * c[j] - b * s[j];
-                        f[ib] = b * c[j] + a * s[j];
+                        for (int e = 0; e < 4; ++e) {
+                            const float2 v = split(x[e]);
+                            x[e] = fma2(x[e], c[e], mul2(two(v.y, v.x), s[e]));
+                        }
+                    } else {
+#pragma unroll
+                        for (int e = 0; e < 2; ++e) {
+                            const uint64_t a = x[e], b = x[2 + e];
+                            x[e] = fma2(a, c[e], mul2(b, s[2 + e]));
+                            x[2 + e] = fma2(b, c[e], mul2(a, s[e]));
+                        }
                     }
                 }
-                x[u].a = make_uint2(pack2<T>(f[0], f[1]), pack2<T>(f[2], f[3]));
-                x[u].b = make_uint2(pack2<T>(f[4], f[5]), pack2<T>(f[6], f[7]));
-            }
-            if (live) {
-                *reinterpret_cast<uint2*>(dst + ea) = x[u].a;
-                *reinterpret_cast<uint2*>(dst + eb) = x[u].b;
+                uint32_t o[4];
+#pragma unroll
+                for (int e = 0; e < 4; ++e) {
+                    const float2 v = split(x[e]);
+                    o[e] = pack2<T>(v.x, v.y);
+                }
+                if (h < heads) {
+                    uint16_t* to = dst + h * dst_head;
+                    *reinterpret_cast<uint2*>(to + ea) = make_uint2(o[0], o[1]);
+                    *reinterpret_cast<uint2*>(to + eb) = make_uint2(o[2], o[3]);
+                }
             }
         }
+    };
+    rows(p.q + t * p.q_stride, p.q_out + t * p.H * D, D, p.H, i0, min(i1, nq), p.q_weight);
+    if (slot >= p.num_slots && part == 0 && lane == 0) atomicOr(p.err, PKV_DEVERR_BAD_SLOT);
+    if (slot < 0 || slot >= p.num_slots) return;
+    const int64_t blk = slot / p.B;
+    const int64_t at = (blk * p.HK * p.B + slot - blk * p.B) * D, head = (int64_t)p.B * D;
+    rows(p.k + t * p.k_stride, p.k_cache + at, head, p.HK, max(i0 - nq, 0), min(i1 - nq, nk),
+         p.k_weight);
+    // values, as they are
+    const int to = min(i1 - nq - nk, nk), heads = min(p.HK, to * RPP);
+    for (int from = max(i0 - nq - nk, 0); from < to; from += kUnroll) {
+        const int h0 = from * RPP + sub;
+        const uint16_t* in = p.v + t * p.v_stride + h0 * D + 8 * li;
+        uint4 x[kUnroll];
+#pragma unroll
+        for (int u = 0; u < kUnroll; ++u)
+            if (h0 + u * RPP < heads) x[u] = *reinterpret_cast<const uint4*>(in + u * RPP * D);
+#pragma unroll
+        for (int u = 0; u < kUnroll; ++u)
+            if (h0 + u * RPP < heads)
+                *reinterpret_cast<uint4*>(p.v_cache + at + (h0 + u * RPP) * head + 8 * li) = x[u];
     }
 }
 
@@ -391,11 +449,11 @@ pkv_status pkv_norm_rope_and_cache(void* q_out, const void* q, const void* k, co
     a.B = block_size;
     a.num_slots = num_blocks * block_size;
     a.err = err;
-    // Warps per token: enough that every SM has about 16 of them, at most one
-    // per pass of rows.
+    // Warps per token: enough that every SM has about kWarpsPerSm of them, at
+    // most one per pass of rows.
     const int rpp = 256 / head_dim;
     const int64_t passes = (num_heads + rpp - 1) / rpp + 2 * ((num_kv_heads + rpp - 1) / rpp);
-    int64_t parts = ((int64_t)sms * 16 + num_tokens - 1) / num_tokens;
+    int64_t parts = ((int64_t)sms * kWarpsPerSm + num_tokens - 1) / num_tokens;
     a.parts = (int)(parts < passes ? parts : passes);
     const int64_t warps = (int64_t)num_tokens * a.parts;
     const dim3 grid((unsigned)((warps + kWarps - 1) / kWarps));
