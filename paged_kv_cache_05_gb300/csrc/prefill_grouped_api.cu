@@ -39,7 +39,7 @@ pkv_status pkv_paged_attention_prefill_grouped(
         // the work schedule sums item costs in 64 bits: a bound far above any
         // call whose tensors fit in memory
         const double units = (double)((num_heads + 1) / 2) * num_seqs *
-                             (double)(((int64_t)max_query_len + kRows - 1) / kRows);
+                             (double)(((int64_t)max_query_len + kBM - 1) / kBM);
         const double unit_cost =
             kPairCost * ((double)max_blocks_per_seq * block_size / kBN + 1.0) + kItemCost;
         if (units * unit_cost >= 0x1p60)
@@ -98,7 +98,10 @@ pkv_status pkv_paged_attention_prefill_grouped(
     a.window = window;
     a.cap_log2 = (float)(log2e * softcap);
     a.slopes = slopes;
-    a.q_items = (max_query_len + kRows - 1) / kRows;
+    // two heads of a K/V head share its key tiles: no tile that one slot alone
+    // sees, and items half as tall (the last one of a prompt wastes less)
+    a.pack = a.G % 2 == 0;
+    a.q_items = (max_query_len + (a.pack ? kBM : kRows) - 1) / (a.pack ? kBM : kRows);
     a.num_blocks = num_blocks;
     a.err = err;
     const int kind = kGrouped | (softcap > 0.f ? kCapped : 0) | (slopes ? kBiased : 0);

@@ -422,10 +422,12 @@ struct PrefillArgs {
     int S, H, B, max_blocks, max_query_len, num_tokens;
     // the grouped kinds only
     int HK, G;                   // K/V heads, query heads per K/V head
+    int pack;                    // 1: an item's query tiles are the same 128 rows of two heads
+                                 // (of one K/V head: G is even); 0: 256 rows of one head
     int window;                  // tokens a row sees, 0: all before it
     float cap_log2;              // cap * log2(e)
     const float* slopes;         // [H]
-    int q_items;             // work items per sequence: ceil(max_query_len / kRows)
+    int q_items;             // work items per sequence: ceil(max_query_len / rows an item)
     int64_t num_blocks;
     int32_t* err;
 };
@@ -482,6 +484,7 @@ struct Item {
 struct SeqInfo {
     int q0, qlen, ctx, ni;
 };
+__device__ __forceinline__ int item_rows(const PrefillArgs& a) { return a.pack ? kBM : kRows; }
 __device__ __forceinline__ bool seq_info(const PrefillArgs& a, int s, bool whole, SeqInfo& si) {
     si.q0 = a.query_start[s];
     si.qlen = a.query_start[s + 1] - si.q0;
@@ -490,7 +493,8 @@ __device__ __forceinline__ bool seq_info(const PrefillArgs& a, int s, bool whole
     if (si.ctx < 0 || si.ctx > a.max_blocks * a.B || si.qlen < 0 || si.qlen > si.ctx ||
         si.q0 < 0 || (int64_t)si.q0 + si.qlen > a.num_tokens || (whole && si.qlen != si.ctx))
         return false;
-    const int n = (si.qlen + kRows - 1) / kRows;   // rows past the last item stay unwritten
+    const int rows = item_rows(a);
+    const int n = (si.qlen + rows - 1) / rows;     // rows past the last item stay unwritten
     si.ni = n < a.q_items ? n : a.q_items;
     return true;
 }
@@ -501,16 +505,18 @@ __device__ __forceinline__ bool seq_info(const PrefillArgs& a, int s, bool whole
 // more key tiles is served first: the group that finishes an item first (the
 // one with fewer key tiles) takes the longer tile of the next item and leads
 // it, while the other still works through its diagonal tile and output rows.
+// Packed items hold the same rows of two heads, one a slot, with the same key tiles.
 // With a window the item's key tiles begin with the one that holds the first
 // token its first row sees; both slots begin there (a slot of later rows meets
 // at most one tile that its window hides whole).
 template <int KIND>
 __device__ __forceinline__ void item_tiles(const PrefillArgs& a, const SeqInfo& si, int t,
                                            Item& it) {
-    it.q_begin = t * kRows;
-    it.sw = t & 1;
+    const bool pack = (KIND & kGrouped) != 0 && a.pack;
+    it.q_begin = t * item_rows(a);
+    it.sw = pack ? 0 : t & 1;
     for (int x = 0; x < 2; ++x) {
-        const int b = it.q_begin + (x ^ it.sw) * kBM;
+        const int b = it.q_begin + (pack ? 0 : (x ^ it.sw) * kBM);
         it.rows[x] = si.qlen - b < kBM ? (si.qlen - b > 0 ? si.qlen - b : 0) : kBM;
         it.pos0[x] = si.ctx - si.qlen + b;            // position of the tile's first query
         it.n[x] = it.rows[x] > 0 ? (it.pos0[x] + it.rows[x] - 1) / kBN + 1 : 0;
@@ -526,6 +532,16 @@ __device__ __forceinline__ void item_tiles(const PrefillArgs& a, const SeqInfo& 
     }
     it.n_kv = it.n[1] > it.n[0] ? it.n[1] : it.n[0];
     it.f = it.n[1] > it.n[0] ? 1 : 0;
+}
+
+// The head and the first row (of the sequence's new ones) of slot x.
+template <int KIND>
+__device__ __forceinline__ int slot_head(const PrefillArgs& a, const Item& it, int x) {
+    return it.h + ((KIND & kGrouped) != 0 && a.pack ? x : 0);
+}
+template <int KIND>
+__device__ __forceinline__ int slot_row(const PrefillArgs& a, const Item& it, int x) {
+    return it.q_begin + ((KIND & kGrouped) != 0 && a.pack ? 0 : (x ^ it.sw) * kBM);
 }
 
 // Estimated cost of an item, in tenths of a 128 x 128 tile product issued
@@ -554,14 +570,42 @@ __device__ __forceinline__ int item_cost(const PrefillArgs& a, const SeqInfo& si
 // at a time, item after item, each item finding in L2 the K/V tiles the one
 // before it loaded, and the two CTAs of a pair run the same item shapes side
 // by side.
+//
+// The grouped kinds deal small batches instead (few units a pair, where a run's
+// ends weigh most): the items are ranked by cost, the units follow in that
+// order, and in each round every pair takes one, the least loaded pair the
+// largest.  (16 prompts' units with 6 a pair: the fullest pair 1.5% above the
+// mean, where the runs' was 15%.)
+constexpr int kDealItems = 256;    // most items (of all sequences) of a dealt batch
+constexpr int kDealRounds = 16;    // most units a pair of it
+constexpr int kDealPairs = 96;
+
 struct Sched {
     int s, hp;         // first unit that may belong to the pair: (s, hp, last item)
     int64_t P;         // cost of the units before it
     int64_t lo, hi;    // the pair's thresholds th(k), th(k + 1)
 };
 
+// A dealt batch's schedule, in shared memory.
+struct Deal {
+    int dealt;                     // 0: runs
+    int mine;                      // units of this pair
+    int unit[kDealRounds];         // item * head groups + head group
+    int items, scan[12];
+    short seq[kDealItems], t[kDealItems], cost[kDealItems], order[kDealItems];
+    int load[kDealPairs];
+};
+
+// Heads of a unit (a CTA pair's): 2, or 4 of packed items; and how many units
+// an item has.
+__device__ __forceinline__ int unit_heads(const PrefillArgs& a) { return a.pack ? 4 : 2; }
+__device__ __forceinline__ int head_groups(const PrefillArgs& a) {
+    return (a.H + unit_heads(a) - 1) / unit_heads(a);
+}
+
 struct Walker {
-    int s, hp, ti;     // the next unit: (sequence, head pair, items from the last)
+    int s, hp, ti;     // the next unit: (sequence, head pair, items from the last);
+                       // of a dealt batch, ti units taken
     int64_t P;         // cost of the units before it
     __device__ __forceinline__ void init(const Sched& sc) {
         s = sc.s;
@@ -572,9 +616,27 @@ struct Walker {
     // the pair's next unit, as this CTA's item (its head 2 hp + rank)
     template <int KIND>
     __device__ __forceinline__ bool next(const PrefillArgs& a, const Sched& sc, bool whole,
-                                         Item& it) {
-        const int HP = (a.H + 1) >> 1;
+                                         Item& it, const Deal* deal) {
+        const int HP = head_groups(a), per = unit_heads(a);
         const int rank = (int)(blockIdx.x & 1u);
+        if constexpr ((KIND & kGrouped) != 0) {
+            if (deal->dealt) {
+                while (ti < deal->mine) {
+                    const int u = deal->unit[ti++], i = u / HP;
+                    it.h = (u - i * HP) * per + rank * (per >> 1);
+                    if (it.h >= a.H) continue;
+                    SeqInfo si;
+                    it.s = deal->seq[i];
+                    seq_info(a, it.s, whole, si);
+                    item_tiles<KIND>(a, si, deal->t[i], it);
+                    it.q0 = si.q0;
+                    it.qlen = si.qlen;
+                    it.ctx = si.ctx;
+                    return true;
+                }
+                return false;
+            }
+        }
         while (s < a.S) {
             SeqInfo si;
             seq_info(a, s, whole, si);
@@ -592,7 +654,7 @@ struct Walker {
                 s = a.S;
                 return false;
             }
-            const int h = 2 * hp + rank;
+            const int h = per * hp + rank * (per >> 1);
             const bool mine = v >= sc.lo && h < a.H;
             it.s = s;
             it.h = h;
@@ -613,12 +675,23 @@ struct Walker {
     }
 };
 
+// CTA 0 flags each sequence whose lengths are out of range, or whose rows pass
+// max_query_len (one warp).
+__device__ __forceinline__ void flag_lengths(const PrefillArgs& a, bool whole, int lane) {
+    if (blockIdx.x != 0) return;
+    for (int s = lane; s < a.S; s += 32) {
+        SeqInfo si;
+        if (!seq_info(a, s, whole, si) || si.qlen > a.max_query_len)
+            atomicOr(a.err, PKV_DEVERR_BAD_CONTEXT);
+    }
+}
+
 // Locates the pair's first unit (one warp; every CTA computes the same
 // total).  CTA 0 flags each sequence whose lengths are out of range, or
 // whose rows pass max_query_len (those rows stay unwritten).
 template <int KIND>
 __device__ __forceinline__ void plan(const PrefillArgs& a, bool whole, Sched* out, int lane) {
-    const int HP = (a.H + 1) >> 1;
+    const int HP = head_groups(a);
     long long tot = 0;
     for (int s0 = 0; s0 < a.S; s0 += 32) {
         const int s = s0 + lane;
@@ -678,6 +751,90 @@ __device__ __forceinline__ void plan(const PrefillArgs& a, bool whole, Sched* ou
     }
 }
 
+// Deals a small batch (every thread of the CTA); false, and deal->dealt 0, for
+// one that is not.
+template <int KIND>
+__device__ __forceinline__ bool deal_units(const PrefillArgs& a, Deal* d, int tid, int threads) {
+    const int lane = tid & 31, warp = tid >> 5, warps = threads >> 5;
+    const int pairs = (int)(gridDim.x >> 1), HP = head_groups(a);
+    // items before each thread's sequence
+    SeqInfo si;
+    si.ni = 0;
+    const bool few = a.S <= threads && pairs <= kDealPairs && a.S < 32768;
+    if (few && tid < a.S) seq_info(a, tid, false, si);
+    int incl = si.ni < kDealItems ? si.ni : kDealItems + 1;
+#pragma unroll
+    for (int o = 1; o < 32; o <<= 1) {
+        const int y = __shfl_up_sync(0xffffffffu, incl, o);
+        if (lane >= o) incl += y;
+    }
+    if (lane == 31) d->scan[warp] = incl;
+    if (tid == 0) d->dealt = d->mine = 0;
+    __syncthreads();
+    int total = 0;
+    for (int w = 0; w < warps; ++w) {
+        if (w == warp) incl += total;
+        total += d->scan[w];
+    }
+    const int rounds = (int)(((int64_t)total * HP + pairs - 1) / pairs);
+    if (!few || total > kDealItems || rounds > kDealRounds) return false;   // (the same for all)
+    for (int t = 0; t < si.ni; ++t) {
+        const int i = incl - si.ni + t;
+        d->seq[i] = (short)tid;
+        d->t[i] = (short)t;
+        const int cost = item_cost<KIND>(a, si, t);
+        d->cost[i] = (short)(cost < 32767 ? cost : 32767);
+        d->order[i] = (short)i;
+    }
+    if (tid == 0) d->dealt = 1;
+    const int64_t units = (int64_t)total * HP;
+    const int me = (int)(blockIdx.x >> 1);
+    if (rounds <= 1) {                     // a unit a pair at most: in any order
+        if (tid == 0 && me < units) {
+            d->unit[0] = me;
+            d->mine = 1;
+        }
+        return true;
+    }
+    for (int k = tid; k < kDealPairs; k += threads) d->load[k] = 0;
+    __syncthreads();
+    for (int i = tid; i < total; i += threads) {
+        const int c = d->cost[i];
+        int rank = 0;
+        for (int j = 0; j < total; ++j) {
+            const int o = d->cost[j];
+            rank += o > c || (o == c && j < i);
+        }
+        d->order[rank] = (short)i;
+    }
+    for (int r = 0; r < rounds; ++r) {
+        __syncthreads();
+        int rank = tid, l = 0, add = 0;
+        if (tid < pairs) {
+            l = d->load[tid];
+            if (r > 0) {
+                rank = 0;
+                for (int j = 0; j < pairs; ++j) {
+                    const int o = d->load[j];
+                    rank += o < l || (o == l && j < tid);
+                }
+            }
+            const int64_t u = (int64_t)r * pairs + rank;
+            if (u < units) {
+                const int k = (int)(u / HP), i = d->order[k];
+                add = d->cost[i];
+                if (tid == me) {
+                    d->unit[d->mine] = i * HP + (int)(u - (int64_t)k * HP);
+                    d->mine = d->mine + 1;
+                }
+            }
+        }
+        __syncthreads();
+        if (tid < pairs) d->load[tid] = l + add;
+    }
+    return true;
+}
+
 template <typename T, int D, bool FUSED, int KIND>
 __global__ void __launch_bounds__(threads_for(FUSED), 1)
     paged_prefill_tc(const __grid_constant__ CUtensorMap tm_q,
@@ -702,6 +859,7 @@ __global__ void __launch_bounds__(threads_for(FUSED), 1)
 
     const int tid = threadIdx.x, warp = tid >> 5, lane = tid & 31;
     Sched* sched = reinterpret_cast<Sched*>(gbase + C::BAR_OFF + 8 * kBarCount + 8);
+    Deal* deal = reinterpret_cast<Deal*>(gbase + C::BAR_OFF + 512);   // (grouped kinds)
 
     if (tid == 0) {
         for (int i = 0; i < kBarCount; ++i)
@@ -716,7 +874,16 @@ __global__ void __launch_bounds__(threads_for(FUSED), 1)
                      : "memory");
         asm volatile("tcgen05.relinquish_alloc_permit.cta_group::1.sync.aligned;" ::: "memory");
     }
-    if (warp == 2) plan<KIND>(a, FUSED, sched, lane);
+    if constexpr (KIND != kPlain) {
+        // launched ahead of the work before it where the grid is small
+        asm volatile("griddepcontrol.wait;" ::: "memory");
+        asm volatile("griddepcontrol.launch_dependents;" ::: "memory");
+        const bool dealt = deal_units<KIND>(a, deal, tid, threads_for(FUSED));
+        if (dealt && warp == 2) flag_lengths(a, FUSED, lane);
+        if (!dealt && warp == 2) plan<KIND>(a, FUSED, sched, lane);
+    } else {
+        if (warp == 2) plan<KIND>(a, FUSED, sched, lane);
+    }
     tc_fence_before();
     __syncthreads();
     tc_fence_after();
@@ -745,7 +912,7 @@ __global__ void __launch_bounds__(threads_for(FUSED), 1)
             Walker wk;
             wk.init(*sched);
             Item it;
-            while (ok && wk.next<KIND>(a, *sched, FUSED, it)) {
+            while (ok && wk.next<KIND>(a, *sched, FUSED, it, deal)) {
                 // slot x's query tile of the item, once the slot's last S of the
                 // previous item is done: the first-served slot's before the
                 // item's first K tile, the other's after it
@@ -755,8 +922,9 @@ __global__ void __launch_bounds__(threads_for(FUSED), 1)
                         return false;
                     mbar_expect_tx(bar(kBarQFull + x), (uint32_t)C::Q_BYTES);
                     for (int sl = 0; sl < C::SLABS; ++sl)
-                        tma_3d(sQ + x * C::Q_BYTES + sl * C::SLAB_Q, &tm_q, sl * 64, it.h,
-                               it.q0 + it.q_begin + (x ^ it.sw) * kBM, bar(kBarQFull + x));
+                        tma_3d(sQ + x * C::Q_BYTES + sl * C::SLAB_Q, &tm_q, sl * 64,
+                               slot_head<KIND>(a, it, x), it.q0 + slot_row<KIND>(a, it, x),
+                               bar(kBarQFull + x));
                     if (x) ++qn[1]; else ++qn[0];
                     return true;
                 };
@@ -839,7 +1007,7 @@ __global__ void __launch_bounds__(threads_for(FUSED), 1)
         Walker wk;
         wk.init(*sched);
         Item it;
-        while (ok && wk.next<KIND>(a, *sched, FUSED, it)) {
+        while (ok && wk.next<KIND>(a, *sched, FUSED, it, deal)) {
             const int32_t* row_tab = a.block_tables + (int64_t)it.s * a.max_blocks;
             for (int j = 0; j < it.n_kv; ++j, ++g) {
                 const int st = (int)(g % NST);
@@ -947,7 +1115,7 @@ __global__ void __launch_bounds__(threads_for(FUSED), 1)
             // between two items, when nothing is queued on the tensor pipe.
             Walker wk;
             wk.init(*sched);
-            auto next_item = [&](Item& nit) -> bool { return wk.next<KIND>(a, *sched, FUSED, nit); };
+            auto next_item = [&](Item& nit) -> bool { return wk.next<KIND>(a, *sched, FUSED, nit, deal); };
             Item nit;
             bool have = next_item(nit);
             while (ok && have) {
@@ -1060,7 +1228,7 @@ __global__ void __launch_bounds__(threads_for(FUSED), 1)
         Walker wk;
         wk.init(*sched);
         Item it;
-        while (ok && wk.next<KIND>(a, *sched, FUSED, it)) {
+        while (ok && wk.next<KIND>(a, *sched, FUSED, it, deal)) {
             const int nx = x ? it.n[1] : it.n[0];
             const int pos0 = x ? it.pos0[1] : it.pos0[0];
             const int rows = x ? it.rows[1] : it.rows[0];
@@ -1072,7 +1240,7 @@ __global__ void __launch_bounds__(threads_for(FUSED), 1)
             const int qpos = pos0 + row;             // causal limit of the row
             // first token the row's window leaves it
             const int first = KIND != kPlain && a.window > 0 ? qpos - a.window + 1 : 0;
-            const float slope = (KIND & kBiased) != 0 ? a.slopes[it.h] * 1.4426950408889634f : 0.f;
+            const float slope = (KIND & kBiased) != 0 ? a.slopes[slot_head<KIND>(a, it, x)] * 1.4426950408889634f : 0.f;
             float m = -INFINITY, l = 0.f;
             for (int j = 0; j < nx; ++j, ++gx) {
                 // S_X(j) complete (and with it the previous O_X += P_X V)
@@ -1312,7 +1480,8 @@ __global__ void __launch_bounds__(threads_for(FUSED), 1)
             tc_fence_after();
             const float inv = l > 0.f ? 1.f / l : 0.f;
             T* orow = static_cast<T*>(a.out) +
-                      ((int64_t)(it.q0 + it.q_begin + (x ^ it.sw) * kBM + row) * a.H + it.h) * D;
+                      ((int64_t)(it.q0 + slot_row<KIND>(a, it, x) + row) * a.H +
+                       slot_head<KIND>(a, it, x)) * D;
 #pragma unroll
             for (int c = 0; c < D / 32; ++c) {
                 uint32_t o[32];
@@ -1364,11 +1533,20 @@ bool make_map(CUtensorMap* m, bool bf16, uint32_t rank, const void* gaddr, const
               CU_TENSOR_MAP_FLOAT_OOB_FILL_NONE) == CUDA_SUCCESS;
 }
 
+// Dynamic shared memory of a kind: the grouped ones hold a schedule too.
+template <int D, bool SPLIT, int KIND>
+constexpr size_t smem_for() {
+    using C = PCfg<D, SPLIT>;
+    const size_t need = C::SMEM_NEED + sizeof(Deal);
+    return KIND == kPlain ? C::SMEM : need > C::SMEM ? need : C::SMEM;
+}
+
 template <typename T, int D, bool FUSED, int KIND>
 cudaError_t launch_prefill(const CUtensorMap& tq, const CUtensorMap& tk, const CUtensorMap& tv,
                            const CUtensorMap& tkin, const CUtensorMap& tvin,
                            const PrefillArgs& a, cudaStream_t stream) {
-    const size_t smem = PCfg<D, Pk<T>::kSplit>::SMEM;
+    constexpr size_t smem = smem_for<D, Pk<T>::kSplit, KIND>();
+    static_assert(smem <= 232448, "shared memory");
     cudaError_t e = cudaFuncSetAttribute(paged_prefill_tc<T, D, FUSED, KIND>,
                                          cudaFuncAttributeMaxDynamicSharedMemorySize, (int)smem);
     if (e != cudaSuccess) return e;
@@ -1388,7 +1566,8 @@ cudaError_t launch_prefill(const CUtensorMap& tq, const CUtensorMap& tk, const C
     e = cudaGetDevice(&dev);
     if (e != cudaSuccess) return e;
     // an even number of CTAs (pairs), no more than two per unit of work
-    const int64_t units = (int64_t)a.q_items * a.S * ((a.H + 1) / 2);
+    const int per = a.pack ? 4 : 2;
+    const int64_t units = (int64_t)a.q_items * a.S * ((a.H + per - 1) / per);
     const int sms = pkv::sm_count(dev);
     if (sms < 1) return cudaErrorInvalidDevice;
     const int64_t pairs = sms / 2 > 1 ? sms / 2 : 1;
@@ -1396,7 +1575,7 @@ cudaError_t launch_prefill(const CUtensorMap& tq, const CUtensorMap& tk, const C
     cfg.blockDim = dim3(threads_for(FUSED));
     cfg.dynamicSmemBytes = smem;
     cfg.stream = stream;
-    cudaLaunchAttribute attr[1];
+    cudaLaunchAttribute attr[2];
     if (cfg.gridDim.x % 2 == 0) {
         attr[0].id = cudaLaunchAttributeClusterDimension;
         attr[0].val.clusterDim.x = 2;
@@ -1404,9 +1583,15 @@ cudaError_t launch_prefill(const CUtensorMap& tq, const CUtensorMap& tk, const C
         attr[0].val.clusterDim.z = 1;
         cfg.attrs = attr;
         cfg.numAttrs = 1;
+        // a grid that leaves SMs free anyway is launched ahead
+        if (KIND != kPlain && (int)cfg.gridDim.x <= sms / 2) {
+            attr[1].id = cudaLaunchAttributeProgrammaticStreamSerialization;
+            attr[1].val.programmaticStreamSerializationAllowed = 1;
+            cfg.numAttrs = 2;
+        }
     }
     e = cudaLaunchKernelEx(&cfg, paged_prefill_tc<T, D, FUSED, KIND>, tq, tk, tv, tkin, tvin, a);
-    if (e == cudaErrorInvalidClusterSize && cfg.numAttrs == 1) {
+    if (e == cudaErrorInvalidClusterSize && cfg.numAttrs > 0) {
         // the device refused the pairing: the same kernel, CTAs placed one
         // by one
         cudaGetLastError();
