@@ -340,6 +340,12 @@ __device__ __forceinline__ uint64_t add2(uint64_t a, uint64_t b) {
     return d;
 }
 
+__device__ __forceinline__ uint64_t mul2(uint64_t a, uint64_t b) {
+    uint64_t d;
+    asm("mul.rn.f32x2 %0, %1, %2;" : "=l"(d) : "l"(a), "l"(b));
+    return d;
+}
+
 // 32 bytes to global memory in one instruction (32-byte aligned address)
 __device__ __forceinline__ void st_global_v8(void* p, const uint32_t* w) {
     asm volatile("st.global.v8.b32 [%0], {%1, %2, %3, %4, %5, %6, %7, %8};" ::"l"(p), "r"(w[0]),
@@ -1283,10 +1289,23 @@ __global__ void __launch_bounds__(threads_for(FUSED), 1)
                             // the bias grows with the key's position for a
                             // positive slope, so no bound on the raw products
                             // serves: every score is formed
+                            uint64_t bias2 = 0;
+                            float b0 = -INFINITY, b1 = -INFINITY;
 #pragma unroll
-                            for (int e = 0; e < 64; ++e)
-                                mx = fmaxf(mx, biased(__uint_as_float(r[e]),
-                                                      fmaf(slope, (float)(hh * 64 + e), at0)));
+                            for (int e = 0; e < 64; e += 2) {
+                                bias2 = e % 8 ? add2(bias2, f2(2.f * slope, 2.f * slope))
+                                              : f2(fmaf(slope, (float)(hh * 64 + e), at0),
+                                                   fmaf(slope, (float)(hh * 64 + e + 1), at0));
+                                float z0 = __uint_as_float(r[e]), z1 = __uint_as_float(r[e + 1]);
+                                if constexpr ((KIND & kCapped) != 0)
+                                    f2_split(add2(f2(capped(z0), capped(z1)), bias2), z0, z1);
+                                else
+                                    f2_split(fma2(f2(z0, z1),
+                                                  f2(sl2, sl2), bias2), z0, z1);
+                                if (e & 2) b1 = max3(b1, z0, z1);
+                                else b0 = max3(b0, z0, z1);
+                            }
+                            mx = max3(mx, b0, b1);
                             continue;
                         }
                         float e0 = pos_scale ? -INFINITY : INFINITY, e1 = e0;
@@ -1367,23 +1386,34 @@ __global__ void __launch_bounds__(threads_for(FUSED), 1)
                         }
                         uint32_t r[32];
                         tmem_ld32(tS + (uint32_t)(q * 32), r);
-                        const float at_q = fmaf(slope, (float)(q * 32), at0) - m_new;
+                        // the bias at the quarter's first key, less the max where the score
+                        // does not carry it
+                        const float at_q = fmaf(slope, (float)(q * 32), at0) -
+                                           ((KIND & kCapped) != 0 ? 0.f : m_new);
+                        uint64_t bias2 = 0;
                         uint32_t pk[16];
-                        uint32_t pr[kSplit ? 16 : 1];
+                        [[maybe_unused]] uint32_t pr[kSplit ? 16 : 1];
 #pragma unroll
                         for (int e = 0; e < 32; e += 2) {
                             float p0, p1;
-                            if constexpr ((KIND & kBiased) != 0) {
-                                p0 = biased(__uint_as_float(r[e]), fmaf(slope, (float)e, at_q));
-                                p1 = biased(__uint_as_float(r[e + 1]),
-                                            fmaf(slope, (float)(e + 1), at_q));
-                            } else if constexpr ((KIND & kCapped) != 0) {
-                                p0 = capped(__uint_as_float(r[e])) - m_new;
-                                p1 = capped(__uint_as_float(r[e + 1])) - m_new;
-                            } else {
-                                const uint64_t x2 = fma2(
-                                    f2(__uint_as_float(r[e]), __uint_as_float(r[e + 1])), sc2, nm2);
+                            // the pair's bias, formed anew every 8 keys
+                            if constexpr ((KIND & kBiased) != 0)
+                                bias2 = e % 8 ? add2(bias2, f2(2.f * slope, 2.f * slope))
+                                              : f2(fmaf(slope, (float)e, at_q),
+                                                   fmaf(slope, (float)(e + 1), at_q));
+                            if constexpr ((KIND & kCapped) != 0) {
+                                // cap (1 - 2 / (2^y + 1)) [+ bias] - m, y = raw * sl2
+                                f2_split(mul2(f2(__uint_as_float(r[e]), __uint_as_float(r[e + 1])),
+                                              sc2), p0, p1);
+                                uint64_t x2 = fma2(f2(rcp(ex2(p0) + 1.f), rcp(ex2(p1) + 1.f)),
+                                                   f2(-2.f * a.cap_log2, -2.f * a.cap_log2),
+                                                   f2(a.cap_log2 - m_new, a.cap_log2 - m_new));
+                                if constexpr ((KIND & kBiased) != 0)
+                                    x2 = add2(x2, bias2);
                                 f2_split(x2, p0, p1);
+                            } else {
+                                f2_split(fma2(f2(__uint_as_float(r[e]), __uint_as_float(r[e + 1])),
+                                              sc2, (KIND & kBiased) != 0 ? bias2 : nm2), p0, p1);
                             }
                             p0 = ex2(p0);
                             p1 = ex2(p1);
