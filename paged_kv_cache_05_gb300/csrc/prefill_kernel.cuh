@@ -867,6 +867,10 @@ __global__ void __launch_bounds__(threads_for(FUSED), 1)
     Sched* sched = reinterpret_cast<Sched*>(gbase + C::BAR_OFF + 8 * kBarCount + 8);
     Deal* deal = reinterpret_cast<Deal*>(gbase + C::BAR_OFF + 512);   // (grouped kinds)
 
+    if (KIND != kPlain && warp == 3 && lane < 3) {
+        const CUtensorMap* map = lane == 0 ? &tm_q : lane == 1 ? &tm_k : &tm_v;
+        asm volatile("prefetch.tensormap [%0];" ::"l"(reinterpret_cast<uint64_t>(map)) : "memory");
+    }
     if (tid == 0) {
         for (int i = 0; i < kBarCount; ++i)
             mbar_init(bar(i), (i == kBarPFull || i == kBarPFull + 1) ? 128u : 1u);
@@ -1243,7 +1247,9 @@ __global__ void __launch_bounds__(threads_for(FUSED), 1)
             // that tile, since its P V is issued before the other's
             const bool f_last = (it.f ? it.n[1] : it.n[0]) == it.n_kv;
             const bool zeroer = x == it.f ? f_last : !f_last;
-            const int qpos = pos0 + row;             // causal limit of the row
+            // none of this warp's rows is the tile's: they see nothing
+            const bool idle = KIND != kPlain && q4 * 32 >= rows;
+            const int qpos = idle ? -1 : pos0 + row;   // causal limit of the row
             // first token the row's window leaves it
             const int first = KIND != kPlain && a.window > 0 ? qpos - a.window + 1 : 0;
             const float slope = (KIND & kBiased) != 0 ? a.slopes[slot_head<KIND>(a, it, x)] * 1.4426950408889634f : 0.f;
