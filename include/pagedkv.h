@@ -249,7 +249,9 @@ pkv_status pkv_contiguous_attention_decode(void* out, const void* q, const void*
  * PKV_DEVERR_BAD_BLOCK and a context length out of range
  * PKV_DEVERR_BAD_CONTEXT (clamped).  num_blocks * num_kv_heads * block_size
  * must stay below 2^31 (the tiled copies address cache rows with 32-bit
- * coordinates).  The split of the work depends on the sizes and lengths alone:
+ * coordinates), max_blocks_per_seq * block_size at most 2^30.  An infinite V of a
+ * visible token gives NaN (its weight is a sum of two parts of either sign).
+ * The split of the work depends on the sizes and lengths alone:
  * results are bit-identical from call to call on one GPU.  Two launches on
  * `stream`.
  * workspace: device, >= pkv_decode_grouped_workspace_size(...) bytes, 256-byte
@@ -393,8 +395,8 @@ pkv_status pkv_paged_attention_prefill_write(void* out, const void* q, const voi
  * not looked up for it, and tokens that none sees do not matter; an infinite
  * or NaN V of a token that some row sees may show in the other rows of that
  * item too (the rows share their products).  num_blocks * num_kv_heads *
- * block_size must stay below 2^31.  Fifth-generation tensor cores, fp32
- * accumulation, one launch, no workspace.
+ * block_size must stay below 2^31, max_blocks_per_seq * block_size at most 2^30.
+ * Fifth-generation tensor cores, fp32 accumulation, one launch, no workspace.
  */
 pkv_status pkv_paged_attention_prefill_grouped(
     void* out, const void* q, const void* k_cache, const void* v_cache,

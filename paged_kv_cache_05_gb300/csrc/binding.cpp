@@ -58,6 +58,14 @@ struct Reader {
         }
         return (float)v;
     }
+    int truth(const char* name) {
+        const int v = PyObject_IsTrue(next());
+        if (v < 0) {
+            PyErr_Clear();
+            throw Refusal{PyExc_TypeError, std::string(name) + " must be a truth value"};
+        }
+        return v;
+    }
     int integer(const char* name) {
         int overflow = 0;
         const long long v = PyLong_AsLongLongAndOverflow(next(), &overflow);
@@ -159,7 +167,7 @@ pkv_status norm_rope_and_cache(Reader& r) {
     const at::Tensor* qw = r.optional("q_weight");
     const at::Tensor* kw = r.optional("k_weight");
     const float eps = r.number("eps"), scale = r.number("rope_scale");
-    const int interleaved = PyObject_IsTrue(r.next());
+    const int interleaved = r.truth("interleaved");
     const Common c(q);
     if (q.dim() != 3 || kc.dim() != 4)
         refuse("q must be [num_tokens, num_heads, head_dim], k_cache [blocks, heads, B, head_dim]");

@@ -897,8 +897,8 @@ pkv_status shape_of(const char* fn, int S, int H, int HK, int D, int B, int max_
     if (B != 8 && B != 16 && B != 32 && B != 64)
         return pkv::fail(PKV_ERR_INVALID, "%s: block_size must be 8, 16, 32 or 64", fn);
     if (max_blocks < 1) return pkv::fail(PKV_ERR_INVALID, "%s: max_blocks_per_seq must be >= 1", fn);
-    if ((int64_t)max_blocks * B >= (1LL << 31))
-        return pkv::fail(PKV_ERR_INVALID, "%s: context capacity overflows", fn);
+    if ((int64_t)max_blocks * B > (1LL << 30))
+        return pkv::fail(PKV_ERR_INVALID, "%s: context capacity above 2^30 tokens", fn);
     const int st = kStepTokens * 128 / D;
     const int64_t steps = (int64_t)S * (((int64_t)max_blocks * B + st - 1) / st);
     if (steps >= (1LL << 31))
@@ -906,6 +906,8 @@ pkv_status shape_of(const char* fn, int S, int H, int HK, int D, int B, int max_
     out->G = H / HK;
     out->heads = out->G <= 8 ? 8 : 16;
     out->chunks = (out->G + out->heads - 1) / out->heads;
+    if (steps * HK * out->chunks >= (1LL << 36))
+        return pkv::fail(PKV_ERR_INVALID, "%s: batch too large (step count overflows)", fn);
     const int64_t most = steps * HK * out->chunks / kMinSteps;
     out->ctas = (int)(most < 1 ? 1 : most < kMaxCtas ? most : kMaxCtas);
     return PKV_OK;
@@ -956,6 +958,11 @@ pkv_status pkv_paged_attention_decode_grouped(
     if (!std::isfinite(scale)) return pkv::fail(PKV_ERR_INVALID, "%s: scale is not finite", fn);
     if (!(softcap >= 0.f) || !std::isfinite(softcap))
         return pkv::fail(PKV_ERR_INVALID, "%s: softcap must be finite and not negative", fn);
+    const double log2e = 1.4426950408889634;
+    const float score = (float)(softcap > 0.f ? 2.0 * log2e * scale / softcap : log2e * scale);
+    const float cap_log2 = (float)(log2e * softcap);
+    if (!std::isfinite(score) || !std::isfinite(cap_log2))
+        return pkv::fail(PKV_ERR_INVALID, "%s: scale and softcap are too far apart", fn);
     if (window < 0) return pkv::fail(PKV_ERR_INVALID, "%s: window must not be negative", fn);
     // the tiled copies address cache rows (block, head, token) with 32-bit coordinates
     if (num_blocks < 1 || num_blocks > ((1LL << 31) - 1) / ((int64_t)num_kv_heads * block_size))
@@ -996,7 +1003,6 @@ pkv_status pkv_paged_attention_decode_grouped(
         !pkv::row_map(&tv, dtype == PKV_BF16, v_cache, rows, head_dim, box))
         return pkv::fail(PKV_ERR_CUDA, "%s: tensor map of the caches", fn);
 
-    const double log2e = 1.4426950408889634;
     char* ws = static_cast<char*>(workspace);
     Args a;
     a.out = out;
@@ -1004,8 +1010,8 @@ pkv_status pkv_paged_attention_decode_grouped(
     a.tables = block_tables;
     a.ctx = context_lens;
     a.slopes = slopes;
-    a.score = (float)(softcap > 0.f ? 2.0 * log2e * scale / softcap : log2e * scale);
-    a.cap_log2 = (float)(log2e * softcap);
+    a.score = score;
+    a.cap_log2 = cap_log2;
     a.window = window;
     a.S = num_seqs;
     a.H = num_heads;

@@ -25,8 +25,8 @@ pkv_status pkv_paged_attention_prefill_grouped(
         return pkv::fail(PKV_ERR_INVALID, "%s: block_size must be 8, 16, 32 or 64", fn);
     if (max_blocks_per_seq < 1 || max_query_len < 0 || num_query_tokens < 0)
         return pkv::fail(PKV_ERR_INVALID, "%s: bad sizes", fn);
-    if ((int64_t)max_blocks_per_seq * block_size >= (1LL << 31))
-        return pkv::fail(PKV_ERR_INVALID, "%s: context capacity overflows", fn);
+    if ((int64_t)max_blocks_per_seq * block_size > (1LL << 30))
+        return pkv::fail(PKV_ERR_INVALID, "%s: context capacity above 2^30 tokens", fn);
     // the tiled copies address cache rows (block, head, token) with 32-bit coordinates
     if (num_blocks < 1 || num_blocks > ((1LL << 31) - 1) / ((int64_t)num_kv_heads * block_size))
         return pkv::fail(PKV_ERR_INVALID,
@@ -48,6 +48,11 @@ pkv_status pkv_paged_attention_prefill_grouped(
     if (!std::isfinite(scale)) return pkv::fail(PKV_ERR_INVALID, "%s: scale is not finite", fn);
     if (!(softcap >= 0.f) || !std::isfinite(softcap))
         return pkv::fail(PKV_ERR_INVALID, "%s: softcap must be finite and not negative", fn);
+    const double log2e = 1.4426950408889634;
+    const float score = (float)(softcap > 0.f ? 2.0 * log2e * scale / softcap : log2e * scale);
+    const float cap_log2 = (float)(log2e * softcap);
+    if (!std::isfinite(score) || !std::isfinite(cap_log2))
+        return pkv::fail(PKV_ERR_INVALID, "%s: scale and softcap are too far apart", fn);
     if (window < 0) return pkv::fail(PKV_ERR_INVALID, "%s: window must not be negative", fn);
     if (num_seqs == 0 || max_query_len == 0 || num_query_tokens == 0) return PKV_OK;
     if (!out || !q || !k_cache || !v_cache || !block_tables || !context_lens || !query_start)
@@ -79,14 +84,13 @@ pkv_status pkv_paged_attention_prefill_grouped(
         !pkv::pool_map(&tv, bf16, v_cache, rows, head_dim, block_size))
         return pkv::fail(PKV_ERR_CUDA, "%s: tensor map of the caches", fn);
 
-    const double log2e = 1.4426950408889634;
     PrefillArgs a = {};
     a.out = out;
     a.out_v8 = aligned(out, 32) ? 1 : 0;
     a.block_tables = block_tables;
     a.context_lens = context_lens;
     a.query_start = query_start;
-    a.scale_log2 = (float)(softcap > 0.f ? 2.0 * log2e * scale / softcap : log2e * scale);
+    a.scale_log2 = score;
     a.S = num_seqs;
     a.H = num_heads;
     a.B = block_size;
@@ -96,7 +100,7 @@ pkv_status pkv_paged_attention_prefill_grouped(
     a.HK = num_kv_heads;
     a.G = num_heads / num_kv_heads;
     a.window = window;
-    a.cap_log2 = (float)(log2e * softcap);
+    a.cap_log2 = cap_log2;
     a.slopes = slopes;
     // two heads of a K/V head share its key tiles: no tile that one slot alone
     // sees, and items half as tall (the last one of a prompt wastes less)

@@ -364,8 +364,9 @@ pkv_status pkv_norm_rope_and_cache(void* q_out, const void* q, const void* k, co
         return pkv::fail(PKV_ERR_INVALID, "%s: head_dim must be 64 or 128", fn);
     if (block_size != 8 && block_size != 16 && block_size != 32 && block_size != 64)
         return pkv::fail(PKV_ERR_INVALID, "%s: block_size must be 8, 16, 32 or 64", fn);
-    if (num_blocks < 1 || num_blocks > (1LL << 40))
-        return pkv::fail(PKV_ERR_INVALID, "%s: num_blocks must be in [1, 2^40]", fn);
+    if (num_blocks < 1 ||
+        num_blocks > (1LL << 60) / ((int64_t)num_kv_heads * head_dim * block_size * 2))
+        return pkv::fail(PKV_ERR_INVALID, "%s: num_blocks must be >= 1 and its pool in reach", fn);
     if (dtype != PKV_F16 && dtype != PKV_BF16)
         return pkv::fail(PKV_ERR_INVALID, "%s: unknown dtype", fn);
     if (rot_dim < 0 || rot_dim > head_dim || rot_dim % 8 != 0)

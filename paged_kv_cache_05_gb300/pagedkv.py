@@ -363,6 +363,8 @@ def paged_attention_decode_grouped(out, q, k_cache, v_cache, block_tables, conte
     if workspace is None:
         S, H, D = q.shape
         HK, B = k_cache.shape[1:3]
+        if block_tables.dim() != 2:
+            raise ValueError("block_tables must be [num_seqs, max_blocks]")
         workspace = alloc_grouped_workspace(S, H, HK, D, B, block_tables.shape[1], q.device)
         if stream is not None:
             workspace.record_stream(stream)

@@ -229,3 +229,28 @@ def test_a_serving_run(pkv):
         s, pairs = bm.append_slots([0, 1, 2])
         assert len(pairs) == 0
         step(s, np.array([n + k for n in prompts], np.int32), [1, 1, 1], True)
+
+
+@pytest.mark.parametrize("S,H,HK", [(400, 2, 1), (300, 6, 2), (3, 4, 4)])
+def test_many_short_prompts_and_many_items(pkv, S, H, HK):
+    """More sequences than threads of a block, more items than a dealt batch
+    holds, more units than its rounds: the schedule by runs, packed and not."""
+    rs = np.random.default_rng(S)
+    new = [1 + i % 7 for i in range(S)] if S > 3 else [3000, 2500, 129]
+    c = make_case(rs, H, HK, 64, 8, new, [n + i % 3 for i, n in enumerate(new)], "bf16",
+                  0 if S > 3 else 40)
+    ref, slack = bounded(c, 0.125, 0.0, None)
+    check(run(pkv, c, on_device(c), 0.125), c, ref, slack)
+    assert pkv.get_device_error() == 0
+
+
+def test_rows_past_max_query_len_are_flagged(pkv):
+    from paged_kv_cache_05_gb300.pagedkv import DEVERR_BAD_CONTEXT
+    c = make_case(np.random.default_rng(12), 4, 2, 64, 16, [300, 20], [300, 20], "f16",
+                  wild=False)
+    ref, slack = bounded(c, 0.125, 0.0, None)
+    out = run(pkv, c, on_device(c), 0.125, most=128)
+    assert pkv.get_device_error() == DEVERR_BAD_CONTEXT
+    check(out[:128], c, ref[:128], slack[:128])
+    check(out[300:], c, ref[300:], slack[300:])
+    assert (out[256:300] == 7.0).all()
