@@ -490,7 +490,17 @@ struct Item {
 struct SeqInfo {
     int q0, qlen, ctx, ni;
 };
-__device__ __forceinline__ int item_rows(const PrefillArgs& a) { return a.pack ? kBM : kRows; }
+// Packed items (grouped kinds only), and the rows of an item.
+template <int KIND>
+__device__ __forceinline__ bool packed(const PrefillArgs& a) {
+    if constexpr ((KIND & kGrouped) != 0) return a.pack != 0;
+    else return false;
+}
+template <int KIND>
+__device__ __forceinline__ int item_rows(const PrefillArgs& a) {
+    return packed<KIND>(a) ? kBM : kRows;
+}
+template <int KIND>
 __device__ __forceinline__ bool seq_info(const PrefillArgs& a, int s, bool whole, SeqInfo& si) {
     si.q0 = a.query_start[s];
     si.qlen = a.query_start[s + 1] - si.q0;
@@ -499,7 +509,7 @@ __device__ __forceinline__ bool seq_info(const PrefillArgs& a, int s, bool whole
     if (si.ctx < 0 || si.ctx > a.max_blocks * a.B || si.qlen < 0 || si.qlen > si.ctx ||
         si.q0 < 0 || (int64_t)si.q0 + si.qlen > a.num_tokens || (whole && si.qlen != si.ctx))
         return false;
-    const int rows = item_rows(a);
+    const int rows = item_rows<KIND>(a);
     const int n = (si.qlen + rows - 1) / rows;     // rows past the last item stay unwritten
     si.ni = n < a.q_items ? n : a.q_items;
     return true;
@@ -518,8 +528,8 @@ __device__ __forceinline__ bool seq_info(const PrefillArgs& a, int s, bool whole
 template <int KIND>
 __device__ __forceinline__ void item_tiles(const PrefillArgs& a, const SeqInfo& si, int t,
                                            Item& it) {
-    const bool pack = (KIND & kGrouped) != 0 && a.pack;
-    it.q_begin = t * item_rows(a);
+    const bool pack = packed<KIND>(a);
+    it.q_begin = t * item_rows<KIND>(a);
     it.sw = pack ? 0 : t & 1;
     for (int x = 0; x < 2; ++x) {
         const int b = it.q_begin + (pack ? 0 : (x ^ it.sw) * kBM);
@@ -527,8 +537,8 @@ __device__ __forceinline__ void item_tiles(const PrefillArgs& a, const SeqInfo& 
         it.pos0[x] = si.ctx - si.qlen + b;            // position of the tile's first query
         it.n[x] = it.rows[x] > 0 ? (it.pos0[x] + it.rows[x] - 1) / kBN + 1 : 0;
     }
-    it.j0 = it.lo = 0;
     if constexpr ((KIND & kGrouped) != 0) {
+        it.j0 = it.lo = 0;
         const int p0 = si.ctx - si.qlen + it.q_begin;
         if (a.window > 0 && p0 >= a.window) {
             it.lo = p0 - a.window + 1;
@@ -540,14 +550,26 @@ __device__ __forceinline__ void item_tiles(const PrefillArgs& a, const SeqInfo& 
     it.f = it.n[1] > it.n[0] ? 1 : 0;
 }
 
+// The item's first key tile and first token seen.
+template <int KIND>
+__device__ __forceinline__ int tile0(const Item& it) {
+    if constexpr ((KIND & kGrouped) != 0) return it.j0;
+    else return 0;
+}
+template <int KIND>
+__device__ __forceinline__ int token0(const Item& it) {
+    if constexpr ((KIND & kGrouped) != 0) return it.lo;
+    else return 0;
+}
+
 // The head and the first row (of the sequence's new ones) of slot x.
 template <int KIND>
 __device__ __forceinline__ int slot_head(const PrefillArgs& a, const Item& it, int x) {
-    return it.h + ((KIND & kGrouped) != 0 && a.pack ? x : 0);
+    return packed<KIND>(a) ? it.h + x : it.h;
 }
 template <int KIND>
 __device__ __forceinline__ int slot_row(const PrefillArgs& a, const Item& it, int x) {
-    return it.q_begin + ((KIND & kGrouped) != 0 && a.pack ? 0 : (x ^ it.sw) * kBM);
+    return packed<KIND>(a) ? it.q_begin : it.q_begin + (x ^ it.sw) * kBM;
 }
 
 // Estimated cost of an item, in tenths of a 128 x 128 tile product issued
@@ -604,9 +626,13 @@ struct Deal {
 
 // Heads of a unit (a CTA pair's): 2, or 4 of packed items; and how many units
 // an item has.
-__device__ __forceinline__ int unit_heads(const PrefillArgs& a) { return a.pack ? 4 : 2; }
+template <int KIND>
+__device__ __forceinline__ int unit_heads(const PrefillArgs& a) {
+    return packed<KIND>(a) ? 4 : 2;
+}
+template <int KIND>
 __device__ __forceinline__ int head_groups(const PrefillArgs& a) {
-    return (a.H + unit_heads(a) - 1) / unit_heads(a);
+    return packed<KIND>(a) ? (a.H + 3) >> 2 : (a.H + 1) >> 1;
 }
 
 struct Walker {
@@ -623,7 +649,7 @@ struct Walker {
     template <int KIND>
     __device__ __forceinline__ bool next(const PrefillArgs& a, const Sched& sc, bool whole,
                                          Item& it, const Deal* deal) {
-        const int HP = head_groups(a), per = unit_heads(a);
+        const int HP = head_groups<KIND>(a), per = unit_heads<KIND>(a);
         const int rank = (int)(blockIdx.x & 1u);
         if constexpr ((KIND & kGrouped) != 0) {
             if (deal->dealt) {
@@ -633,7 +659,7 @@ struct Walker {
                     if (it.h >= a.H) continue;
                     SeqInfo si;
                     it.s = deal->seq[i];
-                    seq_info(a, it.s, whole, si);
+                    seq_info<KIND>(a, it.s, whole, si);
                     item_tiles<KIND>(a, si, deal->t[i], it);
                     it.q0 = si.q0;
                     it.qlen = si.qlen;
@@ -645,7 +671,7 @@ struct Walker {
         }
         while (s < a.S) {
             SeqInfo si;
-            seq_info(a, s, whole, si);
+            seq_info<KIND>(a, s, whole, si);
             if (si.ni == 0) {                         // no items: the next sequence
                 ++s;
                 hp = 0;
@@ -683,11 +709,12 @@ struct Walker {
 
 // CTA 0 flags each sequence whose lengths are out of range, or whose rows pass
 // max_query_len (one warp).
+template <int KIND>
 __device__ __forceinline__ void flag_lengths(const PrefillArgs& a, bool whole, int lane) {
     if (blockIdx.x != 0) return;
     for (int s = lane; s < a.S; s += 32) {
         SeqInfo si;
-        if (!seq_info(a, s, whole, si) || si.qlen > a.max_query_len)
+        if (!seq_info<KIND>(a, s, whole, si) || si.qlen > a.max_query_len)
             atomicOr(a.err, PKV_DEVERR_BAD_CONTEXT);
     }
 }
@@ -697,13 +724,13 @@ __device__ __forceinline__ void flag_lengths(const PrefillArgs& a, bool whole, i
 // whose rows pass max_query_len (those rows stay unwritten).
 template <int KIND>
 __device__ __forceinline__ void plan(const PrefillArgs& a, bool whole, Sched* out, int lane) {
-    const int HP = head_groups(a);
+    const int HP = head_groups<KIND>(a);
     long long tot = 0;
     for (int s0 = 0; s0 < a.S; s0 += 32) {
         const int s = s0 + lane;
         if (s >= a.S) break;
         SeqInfo si;
-        const bool good = seq_info(a, s, whole, si);
+        const bool good = seq_info<KIND>(a, s, whole, si);
         if (blockIdx.x == 0 && (!good || si.qlen > a.max_query_len))
             atomicOr(a.err, PKV_DEVERR_BAD_CONTEXT);
         for (int t = 0; t < si.ni; ++t) tot += item_cost<KIND>(a, si, t);
@@ -724,7 +751,7 @@ __device__ __forceinline__ void plan(const PrefillArgs& a, bool whole, Sched* ou
         long long ts = 0;
         if (s < a.S) {
             SeqInfo si;
-            seq_info(a, s, whole, si);
+            seq_info<KIND>(a, s, whole, si);
             for (int t = 0; t < si.ni; ++t) ts += item_cost<KIND>(a, si, t);
         }
         long long e = ts * HP;                        // inclusive scan of the sequences' cost
@@ -762,12 +789,12 @@ __device__ __forceinline__ void plan(const PrefillArgs& a, bool whole, Sched* ou
 template <int KIND>
 __device__ __forceinline__ bool deal_units(const PrefillArgs& a, Deal* d, int tid, int threads) {
     const int lane = tid & 31, warp = tid >> 5, warps = threads >> 5;
-    const int pairs = (int)(gridDim.x >> 1), HP = head_groups(a);
+    const int pairs = (int)(gridDim.x >> 1), HP = head_groups<KIND>(a);
     // items before each thread's sequence
     SeqInfo si;
     si.ni = 0;
     const bool few = a.S <= threads && pairs <= kDealPairs && a.S < 32768;
-    if (few && tid < a.S) seq_info(a, tid, false, si);
+    if (few && tid < a.S) seq_info<KIND>(a, tid, false, si);
     int incl = si.ni < kDealItems ? si.ni : kDealItems + 1;
 #pragma unroll
     for (int o = 1; o < 32; o <<= 1) {
@@ -889,7 +916,7 @@ __global__ void __launch_bounds__(threads_for(FUSED), 1)
         asm volatile("griddepcontrol.wait;" ::: "memory");
         asm volatile("griddepcontrol.launch_dependents;" ::: "memory");
         const bool dealt = deal_units<KIND>(a, deal, tid, threads_for(FUSED));
-        if (dealt && warp == 2) flag_lengths(a, FUSED, lane);
+        if (dealt && warp == 2) flag_lengths<KIND>(a, FUSED, lane);
         if (!dealt && warp == 2) plan<KIND>(a, FUSED, sched, lane);
     } else {
         if (warp == 2) plan<KIND>(a, FUSED, sched, lane);
@@ -970,10 +997,11 @@ __global__ void __launch_bounds__(threads_for(FUSED), 1)
                                    it.q0 + j * kBN, bar(full0 + st));
                         continue;
                     }
-                    const int tok0 = (it.j0 + j) * kBN;
+                    const int tok0 = (tile0<KIND>(it) + j) * kBN;
                     const int tok1 = min(tok0 + kBN, it.ctx);  // tokens of the tile in the context
                     // blocks before the window are not looked up
-                    const int jb0 = max(tok0, it.lo) / a.B, jb1 = (tok1 - 1) / a.B;
+                    const int jb0 = (KIND == kPlain ? tok0 : max(tok0, token0<KIND>(it))) / a.B,
+                              jb1 = (tok1 - 1) / a.B;
                     mbar_expect_tx(bar(full0 + st), (uint32_t)((jb1 - jb0 + 1) * a.B * 128 * C::SLABS));
                     for (int jb = jb0; jb <= jb1; ++jb) {
                         int64_t phys = row_tab[jb];
@@ -1261,7 +1289,7 @@ __global__ void __launch_bounds__(threads_for(FUSED), 1)
                     break;
                 }
                 tc_fence_after();
-                const int kb = (it.j0 + j) * kBN;
+                const int kb = (tile0<KIND>(it) + j) * kBN;
                 // every key visible to every row
                 const bool full = kb + kBN - 1 <= pos0 &&
                                   (KIND == kPlain || a.window <= 0 ||
@@ -1486,13 +1514,13 @@ __global__ void __launch_bounds__(threads_for(FUSED), 1)
                 // and so are V rows before every row's window, in the item's
                 // first tile (their blocks may not have been copied), by the
                 // slot served first
-                if (KIND != kPlain && j == 0 && x == it.f && it.lo > kb) {
+                if (KIND != kPlain && j == 0 && x == it.f && token0<KIND>(it) > kb) {
                     const int st = (int)(gk % NST);
                     if (!mbar_wait(bar(kBarVFull + st), (uint32_t)((gk / NST) & 1), abort_flag)) {
                         ok = false;
                         break;
                     }
-                    const int n16 = (it.lo - kb) * 8;     // 16-byte chunks per slab
+                    const int n16 = (token0<KIND>(it) - kb) * 8;     // 16-byte chunks per slab
                     unsigned char* vs = gbase + C::V_OFF + st * C::KV_BYTES;
                     for (int i = gtid; i < n16 * C::SLABS; i += 128) {
                         const int sl = i / n16, wv = i - sl * n16;
