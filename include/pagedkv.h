@@ -391,19 +391,32 @@ pkv_status pkv_paged_attention_prefill_write(void* out, const void* q, const voi
  * pkv_paged_attention_decode_grouped (scale, softcap, slopes[h] (t - p)) and
  * K/V head h / (num_heads / num_kv_heads).  Lengths, rows, limits and errors
  * are those of pkv_paged_attention_prefill; K/V are in the cache already
- * (pkv_norm_rope_and_cache).  Blocks that no row of a 256-row item sees are
- * not looked up for it, and tokens that none sees do not matter; an infinite
- * or NaN V of a token that some row sees may show in the other rows of that
- * item too (the rows share their products).  num_blocks * num_kv_heads *
+ * (pkv_norm_rope_and_cache).  Blocks that no row of an item (256 rows: up to
+ * 256 neighbouring tokens, those of several of the query heads that share a K/V
+ * head) sees are not looked up for it, and tokens that none sees do not matter;
+ * an infinite or NaN V of a token that some row sees may show in the other rows
+ * of that item too (the rows share their products).  num_blocks * num_kv_heads *
  * block_size must stay below 2^31, max_blocks_per_seq * block_size at most 2^30.
- * Fifth-generation tensor cores, fp32 accumulation, one launch, no workspace.
+ * Fifth-generation tensor cores, fp32 accumulation.
+ * workspace: NULL, or device memory of pkv_prefill_grouped_workspace_size(...)
+ * bytes (256-byte aligned, no initialisation; two calls in flight at once must
+ * not share it).  With it, batches of few query rows over long contexts (chunks
+ * of few prompts, a few new tokens a sequence) are cut along the contexts so
+ * that every SM has work, and joined by a second launch; the size is 0 where
+ * the sizes rule that out, and the workspace is then not looked at.  Without it
+ * they take one launch and the results are the same within rounding.  Either
+ * way results are bit-identical from call to call on one GPU.
  */
+pkv_status pkv_prefill_grouped_workspace_size(int num_seqs, int num_heads, int num_kv_heads,
+                                              int head_dim, int block_size, int max_blocks_per_seq,
+                                              int max_query_len, size_t* bytes);
 pkv_status pkv_paged_attention_prefill_grouped(
     void* out, const void* q, const void* k_cache, const void* v_cache,
     const int32_t* block_tables, const int32_t* context_lens, const int32_t* query_start,
     const float* slopes, float scale, float softcap, int window, int num_seqs, int num_heads,
     int num_kv_heads, int head_dim, int block_size, int max_blocks_per_seq, int64_t num_blocks,
-    int max_query_len, int num_query_tokens, pkv_dtype dtype, cudaStream_t stream);
+    int max_query_len, int num_query_tokens, pkv_dtype dtype, void* workspace,
+    size_t workspace_bytes, cudaStream_t stream);
 
 /* ------------------------------------------------------------------------ */
 /* Cache maintenance                                                         */

@@ -12,6 +12,7 @@ from .pagedkv import (BlockManager, OutOfBlocks, PagedKVError, alloc_grouped_wor
                       paged_attention_decode_noalloc, paged_attention_decode_shared,
                       norm_rope_and_cache, paged_attention_prefill,
                       paged_attention_prefill_grouped, paged_attention_prefill_write,
+                      prefill_grouped_workspace_size,
                       reshape_and_cache, rope_inv_freq, rope_phases, set_decode_wait_limit,
                       swap_blocks, version)
 
@@ -23,5 +24,6 @@ __all__ = ["BlockManager", "OutOfBlocks", "PagedKVError", "alloc_grouped_workspa
            "paged_attention_decode_noalloc", "paged_attention_decode_shared",
            "norm_rope_and_cache", "paged_attention_prefill",
            "paged_attention_prefill_grouped", "paged_attention_prefill_write",
+           "prefill_grouped_workspace_size",
            "reshape_and_cache", "rope_inv_freq", "rope_phases", "set_decode_wait_limit",
            "swap_blocks", "version"]

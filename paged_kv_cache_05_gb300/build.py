@@ -28,7 +28,8 @@ BIND_SOURCE = "binding.cpp"
 SOURCES = ["errors.cu", "cache_ops.cu", "decode_api.cu", "decode_f16.cu", "decode_bf16.cu",
            "decode_shared_f16.cu", "decode_shared_bf16.cu", "decode_append_f16.cu",
            "decode_append_bf16.cu", "decode_noalloc.cu", "decode_grouped.cu", "prefill.cu",
-           "prefill_grouped_f16.cu", "prefill_grouped_bf16.cu", "prefill_grouped_api.cu",
+           "prefill_grouped_f16.cu", "prefill_grouped_bf16.cu", "prefill_cut_f16.cu",
+           "prefill_cut_bf16.cu", "prefill_grouped_api.cu",
            "rope_cache.cu", "block_manager.cpp"]
 ARCH = ["-gencode", "arch=compute_103a,code=sm_103a"]
 

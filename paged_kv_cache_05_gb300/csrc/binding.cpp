@@ -10,6 +10,7 @@
 #include <Python.h>
 
 #include <ATen/core/Tensor.h>
+#include <ATen/ops/empty.h>
 #include <c10/cuda/CUDAGuard.h>
 #include <c10/cuda/CUDAStream.h>
 #include <torch/csrc/autograd/python_variable.h>
@@ -254,6 +255,7 @@ pkv_status prefill_grouped(Reader& r) {
     const float cap = r.number("softcap");
     const int window = r.integer("window");
     const at::Tensor* slopes = r.optional("slopes");
+    const at::Tensor* ws = r.optional("workspace");
     const Common c(q);
     if (q.dim() != 3 || kc.dim() != 4 || lens.dim() != 1)
         refuse("q must be [num_query_tokens, num_heads, head_dim], k_cache [blocks, heads, B, "
@@ -276,10 +278,23 @@ pkv_status prefill_grouped(Reader& r) {
               b = size(kc.size(2), "block_size"), width = size(tables.size(1), "max_blocks"),
               t = size(T, "num_query_tokens");
     const cudaStream_t stream = stream_of(r, c.dev);
+    // a workspace of the call's own, where one is of use: given back to the
+    // allocator when the call returns, for work queued after it on its stream
+    at::Tensor own;
+    size_t bytes = 0;
+    if (!ws && pkv_prefill_grouped_workspace_size(s, h, hk, d, b, width, most, &bytes) == PKV_OK &&
+        bytes > 0) {
+        own = at::empty({(int64_t)bytes}, q.options().dtype(at::kByte));
+        if (stream != c10::cuda::getCurrentCUDAStream((c10::DeviceIndex)c.dev).stream())
+            own.record_stream(c10::cuda::getStreamFromExternal(stream, (c10::DeviceIndex)c.dev));
+        ws = &own;
+    }
+    void* wp = ws ? c.whole(*ws, "workspace", at::kByte) : nullptr;
     return launch(c.dev, [&] {
         return pkv_paged_attention_prefill_grouped(op, qp, kp, vp, bt, cl, qs, sl, scale, cap,
                                                    window, s, h, hk, d, b, width, kc.size(0), most,
-                                                   t, c.code, stream);
+                                                   t, c.code, wp, ws ? (size_t)ws->numel() : 0,
+                                                   stream);
     });
 }
 

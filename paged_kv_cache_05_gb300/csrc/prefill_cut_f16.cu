@@ -1,0 +1,9 @@
+// The grouped kinds that may cut items along the keys, fp16.
+#include "prefill_kernel.cuh"
+
+cudaError_t pkv::launch_prefill_cut_f16(const CUtensorMap& tq, const CUtensorMap& tk,
+                                      const CUtensorMap& tv, const PrefillArgs& a, int head_dim,
+                                      int kind, cudaStream_t stream) {
+    return head_dim == 128 ? launch_grouped<__half, 128, kCut>(tq, tk, tv, a, kind, stream)
+                           : launch_grouped<__half, 64, kCut>(tq, tk, tv, a, kind, stream);
+}

@@ -5,14 +5,88 @@
 
 #include "prefill_kernel.cuh"
 
+namespace {
+
+// Heads of a query tile: of the divisors of a K/V head's G that leave at least
+// nine tenths of the tile's 128 rows used (where none does, of the one that uses
+// most), the largest whose items are few enough to be dealt quickly, else the
+// smallest above 1.  More heads a tile read the cache once for more of them and
+// fill it with fewer tokens (8 sequences of 4 new tokens, 6000 cached, G = 8: 237
+// -> 87 us against two heads an item), but a batch of many short items spends
+// more on its schedule (40 prompts of 800, G = 16: 322 us with 16, 256 with 2).
+int heads_of_tile(int G, int S, int max_query_len) {
+    int best = 1, used = 0, few = 0;
+    for (int gb = G < kBM ? G : kBM; gb >= 1; --gb) {
+        if (G % gb != 0) continue;
+        const int tb = kBM / gb, rows = tb * gb;
+        if (10 * rows >= 9 * kBM) {
+            const int64_t items = S * (((int64_t)max_query_len + 2 * tb - 1) / (2 * tb));
+            if (items <= kDealItems / 2) return gb;
+            if (gb > 1 || few == 0) few = gb;
+        }
+        if (rows > used) {
+            used = rows;
+            best = gb;
+        }
+    }
+    return few ? few : best;
+}
+
+// Most work of CTAs: the items of max_query_len new tokens by groups of heads.
+int64_t most_work(int S, int H, int gb, int max_query_len) {
+    const int tokens = 2 * (kBM / gb);
+    return (int64_t)S * (((int64_t)max_query_len + tokens - 1) / tokens) * (H / gb);
+}
+
+// Whether a batch of these sizes may have so few units that its items are cut
+// along the keys: an upper bound of their work (the lengths are on the device)
+// that would leave half of a GB300's SMs without any, and contexts of 8 key
+// tiles or more.
+bool may_split(int S, int H, int HK, int B, int max_blocks, int max_query_len) {
+    const int gb = heads_of_tile(H / HK, S, max_query_len);
+    return S <= kSplitItems && (int64_t)max_blocks * B >= 8 * kBN &&
+           most_work(S, H, gb, max_query_len) <= kSplitParts / 4;
+}
+
+struct SplitLayout {
+    size_t units, ml, acc, total;
+};
+SplitLayout split_layout(int D) {
+    SplitLayout l;
+    const size_t rows = (size_t)kSplitParts * 2 * kBM;
+    l.units = 256;
+    l.ml = pkv::align_up(l.units + sizeof(SplitUnit) * kSplitParts, 256);
+    l.acc = l.ml + 8 * rows;
+    l.total = l.acc + 4 * rows * (size_t)D;
+    return l;
+}
+
+}  // namespace
+
 extern "C" {
+
+pkv_status pkv_prefill_grouped_workspace_size(int num_seqs, int num_heads, int num_kv_heads,
+                                              int head_dim, int block_size, int max_blocks_per_seq,
+                                              int max_query_len, size_t* bytes) {
+    const char* fn = "pkv_prefill_grouped_workspace_size";
+    if (!bytes) return pkv::fail(PKV_ERR_INVALID, "%s: bytes is NULL", fn);
+    if (num_seqs < 0 || num_heads < 1 || num_kv_heads < 1 || num_heads % num_kv_heads != 0 ||
+        (head_dim != 64 && head_dim != 128) || block_size < 1 || max_blocks_per_seq < 1 ||
+        max_query_len < 0)
+        return pkv::fail(PKV_ERR_INVALID, "%s: bad sizes", fn);
+    *bytes = may_split(num_seqs, num_heads, num_kv_heads, block_size, max_blocks_per_seq,
+                       max_query_len)
+                 ? split_layout(head_dim).total : 0;
+    return PKV_OK;
+}
 
 pkv_status pkv_paged_attention_prefill_grouped(
     void* out, const void* q, const void* k_cache, const void* v_cache,
     const int32_t* block_tables, const int32_t* context_lens, const int32_t* query_start,
     const float* slopes, float scale, float softcap, int window, int num_seqs, int num_heads,
     int num_kv_heads, int head_dim, int block_size, int max_blocks_per_seq, int64_t num_blocks,
-    int max_query_len, int num_query_tokens, pkv_dtype dtype, cudaStream_t stream) {
+    int max_query_len, int num_query_tokens, pkv_dtype dtype, void* workspace,
+    size_t workspace_bytes, cudaStream_t stream) {
     const char* fn = "pkv_paged_attention_prefill_grouped";
     if (num_seqs < 0 || num_seqs > 65535)
         return pkv::fail(PKV_ERR_INVALID, "%s: num_seqs must be in [0, 65535]", fn);
@@ -35,11 +109,12 @@ pkv_status pkv_paged_attention_prefill_grouped(
                          fn);
     if (dtype != PKV_F16 && dtype != PKV_BF16)
         return pkv::fail(PKV_ERR_INVALID, "%s: unknown dtype", fn);
+    const int gb = heads_of_tile(num_heads / num_kv_heads, num_seqs, max_query_len);
     {
         // the work schedule sums item costs in 64 bits: a bound far above any
         // call whose tensors fit in memory
-        const double units = (double)((num_heads + 1) / 2) * num_seqs *
-                             (double)(((int64_t)max_query_len + kBM - 1) / kBM);
+        const double units =
+            (double)most_work(num_seqs, num_heads, gb, max_query_len);
         const double unit_cost =
             kPairCost * ((double)max_blocks_per_seq * block_size / kBN + 1.0) + kItemCost;
         if (units * unit_cost >= 0x1p60)
@@ -65,17 +140,25 @@ pkv_status pkv_paged_attention_prefill_grouped(
                          "%s: block_tables, context_lens, query_start and slopes must be 4-byte "
                          "aligned",
                          fn);
+    const bool split = workspace && may_split(num_seqs, num_heads, num_kv_heads, block_size,
+                                              max_blocks_per_seq, max_query_len);
+    const SplitLayout lay = split_layout(head_dim);
+    if (split && !aligned(workspace, 256))
+        return pkv::fail(PKV_ERR_INVALID, "%s: workspace must be 256-byte aligned", fn);
+    if (split && workspace_bytes < lay.total)
+        return pkv::fail(PKV_ERR_INVALID, "%s: workspace too small (%zu < %zu bytes)", fn,
+                         workspace_bytes, lay.total);
     int32_t* err = pkv::device_error_word();
     if (!err) return pkv::fail(PKV_ERR_CUDA, "%s: no CUDA device", fn);
 
     const bool bf16 = dtype == PKV_BF16;
     CUtensorMap tq, tk, tv;
     {
-        // q: [tokens][heads][D], one box = 128 tokens x 64 elements of one head
+        // q: [tokens][heads][D], one box = tb tokens x gb heads x 64 elements
         const cuuint64_t D = (cuuint64_t)head_dim;
         const cuuint64_t dims[3] = {D, (cuuint64_t)num_heads, (cuuint64_t)num_query_tokens};
         const cuuint64_t strides[2] = {D * 2, (cuuint64_t)num_heads * D * 2};
-        const cuuint32_t box[3] = {64, 1, (cuuint32_t)kBM};
+        const cuuint32_t box[3] = {64, (cuuint32_t)gb, (cuuint32_t)(kBM / gb)};
         if (!make_map(&tq, bf16, 3, q, dims, strides, box))
             return pkv::fail(PKV_ERR_CUDA, "%s: tensor map of q", fn);
     }
@@ -102,16 +185,26 @@ pkv_status pkv_paged_attention_prefill_grouped(
     a.window = window;
     a.cap_log2 = cap_log2;
     a.slopes = slopes;
-    // two heads of a K/V head share its key tiles: no tile that one slot alone
-    // sees, and items half as tall (the last one of a prompt wastes less)
-    a.pack = a.G % 2 == 0;
-    a.q_items = (max_query_len + (a.pack ? kBM : kRows) - 1) / (a.pack ? kBM : kRows);
+    a.gb = gb;
+    a.tb = kBM / gb;
+    a.head_units = num_heads / gb;
+    a.units_per_kv = a.G / gb;
+    a.per = a.head_units % 2 == 0 ? 2 : 1;
+    a.q_items = (int)(((int64_t)max_query_len + 2 * a.tb - 1) / (2 * a.tb));
     a.num_blocks = num_blocks;
+    if (split) {
+        char* ws = static_cast<char*>(workspace);
+        a.split = reinterpret_cast<SplitHead*>(ws);
+        a.split_units = reinterpret_cast<SplitUnit*>(ws + lay.units);
+        a.split_ml = reinterpret_cast<float2*>(ws + lay.ml);
+        a.split_acc = reinterpret_cast<float*>(ws + lay.acc);
+    }
     a.err = err;
     const int kind = kGrouped | (softcap > 0.f ? kCapped : 0) | (slopes ? kBiased : 0);
-    const cudaError_t e =
-        bf16 ? pkv::launch_prefill_grouped_bf16(tq, tk, tv, a, head_dim, kind, stream)
-             : pkv::launch_prefill_grouped_f16(tq, tk, tv, a, head_dim, kind, stream);
+    pkv::LaunchGrouped* const launch =
+        split ? (bf16 ? pkv::launch_prefill_cut_bf16 : pkv::launch_prefill_cut_f16)
+              : (bf16 ? pkv::launch_prefill_grouped_bf16 : pkv::launch_prefill_grouped_f16);
+    const cudaError_t e = launch(tq, tk, tv, a, head_dim, kind, stream);
     if (e != cudaSuccess) return pkv::cuda_fail(e, fn);
     return PKV_OK;
 }

@@ -428,28 +428,51 @@ struct PrefillArgs {
     int S, H, B, max_blocks, max_query_len, num_tokens;
     // the grouped kinds only
     int HK, G;                   // K/V heads, query heads per K/V head
-    int pack;                    // 1: an item's query tiles are the same 128 rows of two heads
-                                 // (of one K/V head: G is even); 0: 256 rows of one head
+    // a query tile holds tb tokens of gb heads of one K/V head (token by token);
+    // the H / gb groups of heads take the place of the heads in the schedule
+    int gb, tb, head_units, units_per_kv;
+    int per;                     // CTAs of a unit of work: 2, or 1 of an odd head_units
     int window;                  // tokens a row sees, 0: all before it
     float cap_log2;              // cap * log2(e)
     const float* slopes;         // [H]
+    // split items (null: none): what a workspace holds, see SplitHead
+    struct SplitHead* split;
+    struct SplitUnit* split_units;   // [kSplitParts]
+    float2* split_ml;                // [kSplitParts][2][128]: running max (log2), sum
+    float* split_acc;                // [kSplitParts][2][128][D]: unnormalised output
     int q_items;             // work items per sequence: ceil(max_query_len / rows an item)
     int64_t num_blocks;
     int32_t* err;
 };
 
+// A batch of few units over long caches cuts its items along the keys, so that
+// every SM has work; the parts of an item are joined by a second kernel.  Unit u's
+// CTA r (of its `per`) leaves its part at per u + r.
+constexpr int kSplitParts = 320;   // most parts of such a batch
+constexpr int kMaxParts = 32;      // most parts of an item
+struct SplitHead {
+    int units, groups;             // units (0: nothing was split); units of an item part
+};
+struct SplitUnit {
+    int parts, part;               // parts of its item, which one
+    int head;                      // the first of its gb heads
+    int rows[2];                   // live tile rows of each slot
+    int row[2];                    // its first token's row of q and out
+};
+
 // Kinds of a kernel, bits: query heads that share K/V heads and an optional
 // sliding window; scores capped by cap tanh(z / cap); scores biased by
 // slope[h] (t - p).  0 is the plain kernel.
-enum : int { kPlain = 0, kGrouped = 1, kCapped = 2, kBiased = 4 };
+// kCut: of a batch whose items may be cut along the keys (a workspace is given).
+enum : int { kPlain = 0, kGrouped = 1, kCapped = 2, kBiased = 4, kCut = 8 };
 
-// Launch of a grouped kind (kind has kGrouped set) on 16-bit elements of one type.
-cudaError_t launch_prefill_grouped_f16(const CUtensorMap& tq, const CUtensorMap& tk,
-                                       const CUtensorMap& tv, const PrefillArgs& a, int head_dim,
-                                       int kind, cudaStream_t stream);
-cudaError_t launch_prefill_grouped_bf16(const CUtensorMap& tq, const CUtensorMap& tk,
-                                        const CUtensorMap& tv, const PrefillArgs& a, int head_dim,
-                                        int kind, cudaStream_t stream);
+// Launch of a grouped kind on 16-bit elements of one type; the _cut ones of a
+// kind with kCut.
+using LaunchGrouped = cudaError_t(const CUtensorMap& tq, const CUtensorMap& tk,
+                                  const CUtensorMap& tv, const PrefillArgs& a, int head_dim,
+                                  int kind, cudaStream_t stream);
+LaunchGrouped launch_prefill_grouped_f16, launch_prefill_grouped_bf16, launch_prefill_cut_f16,
+    launch_prefill_cut_bf16;
 
 }  // namespace pkv
 
@@ -482,6 +505,7 @@ struct Item {
     int n_kv;                        // key tiles loaded: the larger of n[0], n[1]
     int j0, lo;                      // the item's first key tile (its tiles count from it)
                                      // and first token seen: 0 without a window
+    int unit, part, parts;           // of a cut item: its place, which of how many parts
     int f;                           // the slot served first at each key tile
 };
 
@@ -490,15 +514,42 @@ struct Item {
 struct SeqInfo {
     int q0, qlen, ctx, ni;
 };
-// Packed items (grouped kinds only), and the rows of an item.
+// Tokens and heads of a query tile, and how many heads (groups of them) there
+// are to schedule.
 template <int KIND>
-__device__ __forceinline__ bool packed(const PrefillArgs& a) {
-    if constexpr ((KIND & kGrouped) != 0) return a.pack != 0;
-    else return false;
+__device__ __forceinline__ int tile_tokens(const PrefillArgs& a) {
+    if constexpr ((KIND & kGrouped) != 0) return a.tb;
+    else return kBM;
 }
 template <int KIND>
-__device__ __forceinline__ int item_rows(const PrefillArgs& a) {
-    return packed<KIND>(a) ? kBM : kRows;
+__device__ __forceinline__ int tile_heads(const PrefillArgs& a) {
+    if constexpr ((KIND & kGrouped) != 0) return a.gb;
+    else return 1;
+}
+template <int KIND>
+__device__ __forceinline__ int head_units(const PrefillArgs& a) {
+    if constexpr ((KIND & kGrouped) != 0) return a.head_units;
+    else return a.H;
+}
+
+// The CTAs that take a unit side by side, this one's place among them, the
+// group of CTAs it is in and how many of those there are.
+template <int KIND>
+__device__ __forceinline__ int unit_ctas(const PrefillArgs& a) {
+    if constexpr ((KIND & kGrouped) != 0) return a.per;
+    else return 2;
+}
+template <int KIND>
+__device__ __forceinline__ int unit_rank(const PrefillArgs& a) {
+    return (int)blockIdx.x & (unit_ctas<KIND>(a) - 1);
+}
+template <int KIND>
+__device__ __forceinline__ int my_group(const PrefillArgs& a) {
+    return (int)(blockIdx.x >> (unit_ctas<KIND>(a) - 1));
+}
+template <int KIND>
+__device__ __forceinline__ int cta_groups(const PrefillArgs& a) {
+    return (int)(gridDim.x >> (unit_ctas<KIND>(a) - 1));
 }
 template <int KIND>
 __device__ __forceinline__ bool seq_info(const PrefillArgs& a, int s, bool whole, SeqInfo& si) {
@@ -509,7 +560,7 @@ __device__ __forceinline__ bool seq_info(const PrefillArgs& a, int s, bool whole
     if (si.ctx < 0 || si.ctx > a.max_blocks * a.B || si.qlen < 0 || si.qlen > si.ctx ||
         si.q0 < 0 || (int64_t)si.q0 + si.qlen > a.num_tokens || (whole && si.qlen != si.ctx))
         return false;
-    const int rows = item_rows<KIND>(a);
+    const int rows = 2 * tile_tokens<KIND>(a);
     const int n = (si.qlen + rows - 1) / rows;     // rows past the last item stay unwritten
     si.ni = n < a.q_items ? n : a.q_items;
     return true;
@@ -521,21 +572,21 @@ __device__ __forceinline__ bool seq_info(const PrefillArgs& a, int s, bool whole
 // more key tiles is served first: the group that finishes an item first (the
 // one with fewer key tiles) takes the longer tile of the next item and leads
 // it, while the other still works through its diagonal tile and output rows.
-// Packed items hold the same rows of two heads, one a slot, with the same key tiles.
 // With a window the item's key tiles begin with the one that holds the first
 // token its first row sees; both slots begin there (a slot of later rows meets
 // at most one tile that its window hides whole).
 template <int KIND>
 __device__ __forceinline__ void item_tiles(const PrefillArgs& a, const SeqInfo& si, int t,
                                            Item& it) {
-    const bool pack = packed<KIND>(a);
-    it.q_begin = t * item_rows<KIND>(a);
-    it.sw = pack ? 0 : t & 1;
+    const int tokens = tile_tokens<KIND>(a);
+    it.q_begin = t * 2 * tokens;
+    it.sw = t & 1;
     for (int x = 0; x < 2; ++x) {
-        const int b = it.q_begin + (pack ? 0 : (x ^ it.sw) * kBM);
-        it.rows[x] = si.qlen - b < kBM ? (si.qlen - b > 0 ? si.qlen - b : 0) : kBM;
+        const int b = it.q_begin + (x ^ it.sw) * tokens;
+        const int live = si.qlen - b < tokens ? (si.qlen - b > 0 ? si.qlen - b : 0) : tokens;
+        it.rows[x] = live * tile_heads<KIND>(a);
         it.pos0[x] = si.ctx - si.qlen + b;            // position of the tile's first query
-        it.n[x] = it.rows[x] > 0 ? (it.pos0[x] + it.rows[x] - 1) / kBN + 1 : 0;
+        it.n[x] = live > 0 ? (it.pos0[x] + live - 1) / kBN + 1 : 0;
     }
     if constexpr ((KIND & kGrouped) != 0) {
         it.j0 = it.lo = 0;
@@ -562,14 +613,10 @@ __device__ __forceinline__ int token0(const Item& it) {
     else return 0;
 }
 
-// The head and the first row (of the sequence's new ones) of slot x.
-template <int KIND>
-__device__ __forceinline__ int slot_head(const PrefillArgs& a, const Item& it, int x) {
-    return packed<KIND>(a) ? it.h + x : it.h;
-}
+// The first row (of the sequence's new ones) of slot x.
 template <int KIND>
 __device__ __forceinline__ int slot_row(const PrefillArgs& a, const Item& it, int x) {
-    return packed<KIND>(a) ? it.q_begin : it.q_begin + (x ^ it.sw) * kBM;
+    return it.q_begin + (x ^ it.sw) * tile_tokens<KIND>(a);
 }
 
 // Estimated cost of an item, in tenths of a 128 x 128 tile product issued
@@ -599,14 +646,18 @@ __device__ __forceinline__ int item_cost(const PrefillArgs& a, const SeqInfo& si
 // before it loaded, and the two CTAs of a pair run the same item shapes side
 // by side.
 //
-// The grouped kinds deal small batches instead (few units a pair, where a run's
+// The grouped kinds put several heads of a K/V head in a query tile, so that a
+// few new tokens fill it and the K/V tiles are read once for them, and deal
+// small batches instead (few units a pair, where a run's
 // ends weigh most): the items are ranked by cost, the units follow in that
 // order, and in each round every pair takes one, the least loaded pair the
 // largest.  (16 prompts' units with 6 a pair: the fullest pair 1.5% above the
 // mean, where the runs' was 15%.)
 constexpr int kDealItems = 256;    // most items (of all sequences) of a dealt batch
 constexpr int kDealRounds = 16;    // most units a pair of it
-constexpr int kDealPairs = 96;
+constexpr int kDealGroups = 192;   // most CTAs, or pairs of them
+constexpr int kSplitItems = 64;    // most items of a batch whose items may be cut
+constexpr int kMinTiles = 3;       // fewest key tiles of a part
 
 struct Sched {
     int s, hp;         // first unit that may belong to the pair: (s, hp, last item)
@@ -619,20 +670,28 @@ struct Deal {
     int dealt;                     // 0: runs
     int mine;                      // units of this pair
     int unit[kDealRounds];         // item * head groups + head group
-    int items, scan[12];
+    Item item[kDealRounds];        // as this CTA's items
+    int cut;                       // the items are parts (part, parts) of the batch's
+    int scan[12];
     short seq[kDealItems], t[kDealItems], cost[kDealItems], order[kDealItems];
-    int load[kDealPairs];
+    unsigned char part[kDealItems], parts[kDealItems];
+    int load[kDealGroups];
+    // the batch's items before they are cut
+    short seq0[kSplitItems], t0[kSplitItems], tiles0[kSplitItems];
+    int at0[kSplitItems + 1];
 };
 
-// Heads of a unit (a CTA pair's): 2, or 4 of packed items; and how many units
-// an item has.
-template <int KIND>
-__device__ __forceinline__ int unit_heads(const PrefillArgs& a) {
-    return packed<KIND>(a) ? 4 : 2;
-}
+// Units of an item: pairs of heads, or of groups of heads, or such groups where
+// their number is odd.
 template <int KIND>
 __device__ __forceinline__ int head_groups(const PrefillArgs& a) {
-    return packed<KIND>(a) ? (a.H + 3) >> 2 : (a.H + 1) >> 1;
+    if constexpr ((KIND & kGrouped) != 0) return a.head_units >> (a.per - 1);
+    else return (a.H + 1) >> 1;
+}
+
+// First of n key tiles of part k of `parts`.
+__device__ __forceinline__ int part_begin(int n, int k, int parts) {
+    return n * k / parts;                  // (n below 2^23, parts at most 32)
 }
 
 struct Walker {
@@ -649,24 +708,13 @@ struct Walker {
     template <int KIND>
     __device__ __forceinline__ bool next(const PrefillArgs& a, const Sched& sc, bool whole,
                                          Item& it, const Deal* deal) {
-        const int HP = head_groups<KIND>(a), per = unit_heads<KIND>(a);
-        const int rank = (int)(blockIdx.x & 1u);
+        const int HP = head_groups<KIND>(a);
+        const int rank = unit_rank<KIND>(a);
         if constexpr ((KIND & kGrouped) != 0) {
             if (deal->dealt) {
-                while (ti < deal->mine) {
-                    const int u = deal->unit[ti++], i = u / HP;
-                    it.h = (u - i * HP) * per + rank * (per >> 1);
-                    if (it.h >= a.H) continue;
-                    SeqInfo si;
-                    it.s = deal->seq[i];
-                    seq_info<KIND>(a, it.s, whole, si);
-                    item_tiles<KIND>(a, si, deal->t[i], it);
-                    it.q0 = si.q0;
-                    it.qlen = si.qlen;
-                    it.ctx = si.ctx;
-                    return true;
-                }
-                return false;
+                if (ti >= deal->mine) return false;
+                it = deal->item[ti++];
+                return true;
             }
         }
         while (s < a.S) {
@@ -686,8 +734,8 @@ struct Walker {
                 s = a.S;
                 return false;
             }
-            const int h = per * hp + rank * (per >> 1);
-            const bool mine = v >= sc.lo && h < a.H;
+            const int h = unit_ctas<KIND>(a) * hp + rank;
+            const bool mine = v >= sc.lo && h < head_units<KIND>(a);
             it.s = s;
             it.h = h;
             it.q0 = si.q0;
@@ -738,7 +786,7 @@ __device__ __forceinline__ void plan(const PrefillArgs& a, bool whole, Sched* ou
 #pragma unroll
     for (int o = 16; o > 0; o >>= 1) tot += __shfl_xor_sync(0xffffffffu, tot, o);
     tot *= HP;
-    const int64_t np = gridDim.x >> 1, k = blockIdx.x >> 1;
+    const int64_t np = cta_groups<KIND>(a), k = my_group<KIND>(a);
     const int64_t A = 2 * (int64_t)tot;
     const int64_t lo = k * (A / np) + (k * (A % np)) / np;
     const int64_t hi = (k + 1) * (A / np) + ((k + 1) * (A % np)) / np;
@@ -784,16 +832,129 @@ __device__ __forceinline__ void plan(const PrefillArgs& a, bool whole, Sched* ou
     }
 }
 
+// This CTA's item of the pair's unit u.
+template <int KIND>
+__device__ __forceinline__ Item unit_item(const PrefillArgs& a, const Deal* d, int u) {
+    const int HP = head_groups<KIND>(a);
+    const int i = u / HP;
+    Item it;
+    it.h = a.per * (u - i * HP) + unit_rank<KIND>(a);
+    SeqInfo si;
+    it.s = d->seq[i];
+    seq_info<KIND>(a, it.s, false, si);
+    item_tiles<KIND>(a, si, d->t[i], it);
+    it.q0 = si.q0;
+    it.qlen = si.qlen;
+    it.ctx = si.ctx;
+    it.unit = u;
+    it.part = 0;
+    it.parts = 1;
+    if ((KIND & kCut) != 0 && d->cut && d->parts[i] > 1) {   // key tiles [b, e) of the item's
+        it.part = d->part[i];
+        it.parts = d->parts[i];
+        const int b = part_begin(it.n_kv, it.part, it.parts);
+        const int e = part_begin(it.n_kv, it.part + 1, it.parts);
+        for (int x = 0; x < 2; ++x) {
+            const int n = it.n[x] < e ? it.n[x] : e;
+            it.n[x] = n > b ? n - b : 0;
+        }
+        it.j0 += b;
+        it.n_kv = it.n[1] > it.n[0] ? it.n[1] : it.n[0];
+        it.f = it.n[1] > it.n[0] ? 1 : 0;
+    }
+    return it;
+}
+
+// Cuts the items of a batch of few units along their keys, where that is
+// estimated to shorten it (every thread; false: not cut).  `first`: the items
+// before this thread's sequence; total: the items, then their parts.
+// The estimate, in key tiles with 1.5 for an item's fixed work: with at most a
+// unit a CTA the largest part, else the mean load and half a part; the join
+// costs about 3.
+template <int KIND>
+__device__ __forceinline__ bool cut_items(const PrefillArgs& a, Deal* d, const SeqInfo& si,
+                                          int first, int& total, int tid) {
+    const int groups = cta_groups<KIND>(a), HP = head_groups<KIND>(a), lane = tid & 31;
+    const int most_parts = kSplitParts >> (a.per - 1);
+    if (total == 0 || total > kSplitItems || total * HP > most_parts) return false;
+    for (int t = 0; t < si.ni; ++t) {
+        Item it;
+        item_tiles<KIND>(a, si, t, it);
+        d->seq0[first + t] = (short)tid;
+        d->t0[first + t] = (short)t;
+        d->tiles0[first + t] = (short)(it.n_kv < 32767 ? it.n_kv : 32767);
+    }
+    __syncthreads();
+    if (tid < 32) {
+        // lane L tries parts of the largest item's tiles / (L + 1)
+        int most = 0;
+        for (int i = lane; i < total; i += 32) most = max(most, (int)d->tiles0[i]);
+        most = __reduce_max_sync(0xffffffffu, most);
+        const int size = max((most + lane) / (lane + 1), kMinTiles);
+        int n = 0, tiles = 0;
+        for (int i = 0; i < total; ++i) {
+            n += (d->tiles0[i] + size - 1) / size;
+            tiles += d->tiles0[i];
+        }
+        const float mean = ((float)tiles + 1.5f * (float)n) * (float)HP / (float)groups;
+        float est = n * HP <= groups ? fmaxf((float)min(size, most) + 1.5f, mean)
+                                    : mean + 0.5f * (float)size;
+        if (n > total) est += 3.f;
+        if (n * HP > most_parts || n > kDealItems) est = INFINITY;
+        float best = est;
+#pragma unroll
+        for (int o = 16; o > 0; o >>= 1) best = fminf(best, __shfl_xor_sync(0xffffffffu, best, o));
+        const int win = __ffs(__ballot_sync(0xffffffffu, est == best)) - 1;
+        const int take = __shfl_sync(0xffffffffu, size, win);
+        const bool cut = __shfl_sync(0xffffffffu, n, win) > total;
+        // parts of items 2 lane and 2 lane + 1, and those before them
+        int p[2], sum = 0;
+        for (int k = 0; k < 2; ++k) {
+            const int i = 2 * lane + k;
+            p[k] = i < total ? (d->tiles0[i] + take - 1) / take : 0;
+            sum += p[k];
+        }
+        int incl = sum;
+#pragma unroll
+        for (int o = 1; o < 32; o <<= 1) {
+            const int y = __shfl_up_sync(0xffffffffu, incl, o);
+            if (lane >= o) incl += y;
+        }
+        d->at0[2 * lane] = incl - sum;
+        d->at0[2 * lane + 1] = incl - p[1];
+        if (lane == 31) d->at0[kSplitItems] = cut ? incl : 0;
+    }
+    __syncthreads();
+    const int parts = d->at0[kSplitItems];
+    if (parts == 0) return false;
+    if (tid < total) {
+        const int i0 = d->at0[tid], i1 = tid + 1 < total ? d->at0[tid + 1] : parts;
+        for (int i = i0; i < i1; ++i) {
+            const int n = part_begin(d->tiles0[tid], i - i0 + 1, i1 - i0) -
+                          part_begin(d->tiles0[tid], i - i0, i1 - i0);
+            d->seq[i] = d->seq0[tid];
+            d->t[i] = d->t0[tid];
+            d->part[i] = (unsigned char)(i - i0);
+            d->parts[i] = (unsigned char)(i1 - i0);
+            const int cost = kPairCost * n + kItemCost;
+            d->cost[i] = (short)(cost < 32767 ? cost : 32767);
+            d->order[i] = (short)i;
+        }
+    }
+    total = parts;
+    return true;
+}
+
 // Deals a small batch (every thread of the CTA); false, and deal->dealt 0, for
 // one that is not.
 template <int KIND>
 __device__ __forceinline__ bool deal_units(const PrefillArgs& a, Deal* d, int tid, int threads) {
     const int lane = tid & 31, warp = tid >> 5, warps = threads >> 5;
-    const int pairs = (int)(gridDim.x >> 1), HP = head_groups<KIND>(a);
+    const int groups = cta_groups<KIND>(a), HP = head_groups<KIND>(a);
     // items before each thread's sequence
     SeqInfo si;
     si.ni = 0;
-    const bool few = a.S <= threads && pairs <= kDealPairs && a.S < 32768;
+    const bool few = a.S <= threads && groups <= kDealGroups && a.S < 32768;
     if (few && tid < a.S) seq_info<KIND>(a, tid, false, si);
     int incl = si.ni < kDealItems ? si.ni : kDealItems + 1;
 #pragma unroll
@@ -809,9 +970,19 @@ __device__ __forceinline__ bool deal_units(const PrefillArgs& a, Deal* d, int ti
         if (w == warp) incl += total;
         total += d->scan[w];
     }
-    const int rounds = (int)(((int64_t)total * HP + pairs - 1) / pairs);
-    if (!few || total > kDealItems || rounds > kDealRounds) return false;   // (the same for all)
-    for (int t = 0; t < si.ni; ++t) {
+    const bool teller = (KIND & kCut) != 0 && blockIdx.x == 0 && tid == 0;
+    if (teller) a.split->units = 0;
+    if (!few || total > kDealItems) return false;     // (the same for all)
+    bool cut = false;
+    if constexpr ((KIND & kCut) != 0) cut = cut_items<KIND>(a, d, si, incl - si.ni, total, tid);
+    const int rounds = (int)(((int64_t)total * HP + groups - 1) / groups);
+    if (rounds > kDealRounds) return false;
+    if (cut && teller) {
+        a.split->units = total * HP;
+        a.split->groups = HP;
+    }
+    if (tid == 0) d->cut = cut;
+    for (int t = 0; t < si.ni && !cut; ++t) {
         const int i = incl - si.ni + t;
         d->seq[i] = (short)tid;
         d->t[i] = (short)t;
@@ -821,15 +992,17 @@ __device__ __forceinline__ bool deal_units(const PrefillArgs& a, Deal* d, int ti
     }
     if (tid == 0) d->dealt = 1;
     const int64_t units = (int64_t)total * HP;
-    const int me = (int)(blockIdx.x >> 1);
-    if (rounds <= 1) {                     // a unit a pair at most: in any order
+    const int me = my_group<KIND>(a);
+    if (rounds <= 1) {                     // a unit a CTA at most: in any order
         if (tid == 0 && me < units) {
             d->unit[0] = me;
             d->mine = 1;
         }
+        __syncthreads();
+        if (tid < d->mine) d->item[tid] = unit_item<KIND>(a, d, d->unit[tid]);
         return true;
     }
-    for (int k = tid; k < kDealPairs; k += threads) d->load[k] = 0;
+    for (int k = tid; k < kDealGroups; k += threads) d->load[k] = 0;
     __syncthreads();
     for (int i = tid; i < total; i += threads) {
         const int c = d->cost[i];
@@ -843,16 +1016,16 @@ __device__ __forceinline__ bool deal_units(const PrefillArgs& a, Deal* d, int ti
     for (int r = 0; r < rounds; ++r) {
         __syncthreads();
         int rank = tid, l = 0, add = 0;
-        if (tid < pairs) {
+        if (tid < groups) {
             l = d->load[tid];
             if (r > 0) {
                 rank = 0;
-                for (int j = 0; j < pairs; ++j) {
+                for (int j = 0; j < groups; ++j) {
                     const int o = d->load[j];
                     rank += o < l || (o == l && j < tid);
                 }
             }
-            const int64_t u = (int64_t)r * pairs + rank;
+            const int64_t u = (int64_t)r * groups + rank;
             if (u < units) {
                 const int k = (int)(u / HP), i = d->order[k];
                 add = d->cost[i];
@@ -863,8 +1036,10 @@ __device__ __forceinline__ bool deal_units(const PrefillArgs& a, Deal* d, int ti
             }
         }
         __syncthreads();
-        if (tid < pairs) d->load[tid] = l + add;
+        if (tid < groups) d->load[tid] = l + add;
     }
+    __syncthreads();
+    if (tid < d->mine) d->item[tid] = unit_item<KIND>(a, d, d->unit[tid]);
     return true;
 }
 
@@ -936,7 +1111,99 @@ __global__ void __launch_bounds__(threads_for(FUSED), 1)
         // (separate warps: a lane waiting on a barrier would hold up the
         // other's issue).  Both walk the same items and the same global
         // key-tile sequence g; tile g uses stage g % NST of its ring.
-        if (lane == 0) {
+        if constexpr (KIND != kPlain) {
+            // One lane a cache block: the table entries of the next tile are
+            // fetched before the wait for its stage and the lanes issue
+            // their copies side by side (2 prompts of 512 over 4000 cached
+            // tokens: 90.0 us, 96.1 with one lane for all blocks).
+            const bool kq = warp == 0;
+            const CUtensorMap* map = kq ? &tm_k : &tm_v;
+            const uint32_t ring = kq ? sK : sV;
+            const int full0 = kq ? kBarKFull : kBarVFull, empty0 = kq ? kBarKEmpty : kBarVEmpty;
+            int64_t g = 0;
+            int qn[2] = {0, 0};               // query tiles loaded, per slot
+            bool ok = true;
+            Walker wk;
+            wk.init(*sched);
+            Item it;
+            while (ok && wk.next<KIND>(a, *sched, FUSED, it, deal)) {
+                // lane 0: slot x's query tile, as below
+                auto load_q = [&](int x) -> bool {
+                    const int n = x ? qn[1] : qn[0];
+                    if (n > 0 && !mbar_wait(bar(kBarQEmpty + x), (uint32_t)((n - 1) & 1), abort_flag))
+                        return false;
+                    mbar_expect_tx(bar(kBarQFull + x), (uint32_t)(a.gb * a.tb * 128 * C::SLABS));
+                    for (int sl = 0; sl < C::SLABS; ++sl)
+                        tma_3d(sQ + x * C::Q_BYTES + sl * C::SLAB_Q, &tm_q, sl * 64, it.h * a.gb,
+                               it.q0 + slot_row<KIND>(a, it, x), bar(kBarQFull + x));
+                    if (x) ++qn[1]; else ++qn[0];
+                    return true;
+                };
+                const int32_t* row_tab = a.block_tables + (int64_t)it.s * a.max_blocks;
+                const int head = it.h / a.units_per_kv;
+                // the lane's block of key tile j (at most 16 a tile; blocks
+                // before the window are not looked up); false: none
+                int jb = 0;
+                auto block = [&](int j) -> bool {
+                    const int tok0 = (tile0<KIND>(it) + j) * kBN;
+                    const int tok1 = min(tok0 + kBN, it.ctx);
+                    jb = max(tok0, token0<KIND>(it)) / a.B + lane;
+                    return j < it.n_kv && jb <= (tok1 - 1) / a.B;
+                };
+                bool has = block(0);
+                int phys = has ? row_tab[jb] : 0;
+                for (int j = 0; j < it.n_kv; ++j, ++g) {
+                    const int st = (int)(g % NST);
+                    const bool now = has;
+                    const int jb_now = jb;
+                    int ph = phys;
+                    has = block(j + 1);
+                    if (has) phys = row_tab[jb];
+                    const int blocks = __popc(__ballot_sync(0xffffffffu, now));
+                    int got = 1;
+                    if (lane == 0) {
+                        if (kq && j <= 1) got = load_q(j ? 1 - it.f : it.f);
+                        if (got && g >= NST)
+                            got = mbar_wait(bar(empty0 + st), (uint32_t)((g / NST - 1) & 1),
+                                            abort_flag);
+                        if (got)
+                            mbar_expect_tx(bar(full0 + st),
+                                           (uint32_t)(blocks * a.B * 128 * C::SLABS));
+                    }
+                    __syncwarp();
+                    ok = __shfl_sync(0xffffffffu, got, 0) != 0;
+                    if (!ok) break;
+                    if (now) {
+                        if (ph < 0 || ph >= a.num_blocks) {
+                            if (kq) atomicOr(a.err, PKV_DEVERR_BAD_BLOCK);
+                            ph = 0;                             // keeps the byte count; flagged
+                        }
+                        const int y = (int)(((int64_t)ph * a.HK + head) * a.B);
+                        const uint32_t koff =
+                            (uint32_t)(jb_now * a.B - (tile0<KIND>(it) + j) * kBN) * 128u;
+                        for (int sl = 0; sl < C::SLABS; ++sl)
+                            tma_2d(ring + st * C::KV_BYTES + sl * C::SLAB_KV + koff, map, sl * 64,
+                                   y, bar(full0 + st));
+                    }
+                    __syncwarp();
+                }
+                if (ok && kq && it.n_kv == 1) {
+                    int got = 1;
+                    if (lane == 0) got = load_q(1 - it.f);
+                    ok = __shfl_sync(0xffffffffu, got, 0) != 0;
+                }
+            }
+            if (lane == 0) {
+                if (!ok) fail();
+                // every copy lands before the CTA can exit, as below
+                for (int x = 0; kq && x < 2; ++x)
+                    if (qn[x] > 0)
+                        mbar_wait(bar(kBarQFull + x), (uint32_t)((qn[x] - 1) & 1), nullptr);
+                for (int64_t t = g - NST < 0 ? 0 : g - NST; t < g; ++t)
+                    mbar_wait(bar(full0 + (int)(t % NST)), (uint32_t)((t / NST) & 1), nullptr);
+            }
+            __syncwarp();
+        } else if (lane == 0) {
             const bool kq = warp == 0;
             const CUtensorMap* map = kq ? &tm_k : &tm_v;
             const CUtensorMap* in_map = kq ? &tm_kin : &tm_vin;
@@ -960,7 +1227,7 @@ __global__ void __launch_bounds__(threads_for(FUSED), 1)
                     mbar_expect_tx(bar(kBarQFull + x), (uint32_t)C::Q_BYTES);
                     for (int sl = 0; sl < C::SLABS; ++sl)
                         tma_3d(sQ + x * C::Q_BYTES + sl * C::SLAB_Q, &tm_q, sl * 64,
-                               slot_head<KIND>(a, it, x), it.q0 + slot_row<KIND>(a, it, x),
+                               it.h * tile_heads<KIND>(a), it.q0 + slot_row<KIND>(a, it, x),
                                bar(kBarQFull + x));
                     if (x) ++qn[1]; else ++qn[0];
                     return true;
@@ -999,9 +1266,7 @@ __global__ void __launch_bounds__(threads_for(FUSED), 1)
                     }
                     const int tok0 = (tile0<KIND>(it) + j) * kBN;
                     const int tok1 = min(tok0 + kBN, it.ctx);  // tokens of the tile in the context
-                    // blocks before the window are not looked up
-                    const int jb0 = (KIND == kPlain ? tok0 : max(tok0, token0<KIND>(it))) / a.B,
-                              jb1 = (tok1 - 1) / a.B;
+                    const int jb0 = tok0 / a.B, jb1 = (tok1 - 1) / a.B;
                     mbar_expect_tx(bar(full0 + st), (uint32_t)((jb1 - jb0 + 1) * a.B * 128 * C::SLABS));
                     for (int jb = jb0; jb <= jb1; ++jb) {
                         int64_t phys = row_tab[jb];
@@ -1009,9 +1274,7 @@ __global__ void __launch_bounds__(threads_for(FUSED), 1)
                             if (kq) atomicOr(a.err, PKV_DEVERR_BAD_BLOCK);
                             phys = 0;                           // keeps the byte count; flagged
                         }
-                        const int y = KIND == kPlain
-                                          ? (int)((phys * a.H + it.h) * a.B)
-                                          : (int)((phys * a.HK + it.h / a.G) * a.B);
+                        const int y = (int)((phys * a.H + it.h) * a.B);
                         const uint32_t koff = (uint32_t)(jb * a.B - tok0) * 128u;
                         for (int sl = 0; sl < C::SLABS; ++sl)
                             tma_2d(ring + st * C::KV_BYTES + sl * C::SLAB_KV + koff, map, sl * 64,
@@ -1254,6 +1517,7 @@ __global__ void __launch_bounds__(threads_for(FUSED), 1)
         const int q4 = warp & 3;                     // this warp's lane quarter
         const int row = q4 * 32 + lane;              // row of the tile = TMEM lane
         const int gtid = (warp - 2 - 4 * x) * 32 + lane;   // 0..127 within the group
+        const int tok = KIND == kPlain ? row : row / a.gb;  // the row's token of the tile
         const uint32_t tl = tmem + ((uint32_t)(q4 * 32) << 16);
         const uint32_t tS = tl + (uint32_t)(x * kBN);      // S_X, then P_X over it
         const uint32_t tO = tl + kColO + (uint32_t)(x * D);
@@ -1277,10 +1541,12 @@ __global__ void __launch_bounds__(threads_for(FUSED), 1)
             const bool zeroer = x == it.f ? f_last : !f_last;
             // none of this warp's rows is the tile's: they see nothing
             const bool idle = KIND != kPlain && q4 * 32 >= rows;
-            const int qpos = idle ? -1 : pos0 + row;   // causal limit of the row
+            const int qpos = idle ? -1 : pos0 + tok;   // causal limit of the row
             // first token the row's window leaves it
             const int first = KIND != kPlain && a.window > 0 ? qpos - a.window + 1 : 0;
-            const float slope = (KIND & kBiased) != 0 ? a.slopes[slot_head<KIND>(a, it, x)] * 1.4426950408889634f : 0.f;
+            const float slope = (KIND & kBiased) != 0 ? a.slopes[it.h * a.gb + row - tok * a.gb] *
+                                                               1.4426950408889634f
+                                                         : 0.f;
             float m = -INFINITY, l = 0.f;
             for (int j = 0; j < nx; ++j, ++gx) {
                 // S_X(j) complete (and with it the previous O_X += P_X V)
@@ -1293,7 +1559,7 @@ __global__ void __launch_bounds__(threads_for(FUSED), 1)
                 // every key visible to every row
                 const bool full = kb + kBN - 1 <= pos0 &&
                                   (KIND == kPlain || a.window <= 0 ||
-                                   kb >= pos0 + kBM - a.window);
+                                   kb >= pos0 + a.tb - a.window);
                 // the score of raw product v with key e of the tile (log2 units)
                 auto capped = [&](float v) {
                     return a.cap_log2 * (1.f - 2.f * rcp(ex2(v * sl2) + 1.f));
@@ -1534,6 +1800,29 @@ __global__ void __launch_bounds__(threads_for(FUSED), 1)
             }
             if (!ok) break;
             g += it.n_kv;
+            // a part of a cut item: its rows' statistics and unnormalised output
+            bool part = false;
+            int64_t place = 0;
+            if constexpr ((KIND & kCut) != 0) {
+                if (deal->dealt && deal->cut) {
+                    // (read again here: nothing of it stays in registers meanwhile)
+                    const Item& done = deal->item[wk.ti - 1];
+                    const int at = a.per * done.unit + unit_rank<KIND>(a);
+                    if (gtid == 0) {
+                        SplitUnit& u = a.split_units[at];
+                        u.rows[x] = rows;
+                        u.row[x] = it.q0 + slot_row<KIND>(a, it, x);
+                        if (x == 0) {
+                            u.parts = done.parts;
+                            u.part = done.part;
+                            u.head = it.h * a.gb;
+                        }
+                    }
+                    part = done.parts > 1;
+                    place = ((int64_t)at * 2 + x) * kBM + row;
+                    if (part) a.split_ml[place] = make_float2(m, l);
+                }
+            }
             if (nx == 0) continue;
             // the item's output rows of this tile, once its last P V is done
             if (!mbar_wait(bar(kBarPvDone + x), (uint32_t)(items & 1), abort_flag)) {
@@ -1544,13 +1833,20 @@ __global__ void __launch_bounds__(threads_for(FUSED), 1)
             tc_fence_after();
             const float inv = l > 0.f ? 1.f / l : 0.f;
             T* orow = static_cast<T*>(a.out) +
-                      ((int64_t)(it.q0 + slot_row<KIND>(a, it, x) + row) * a.H +
-                       slot_head<KIND>(a, it, x)) * D;
+                      (KIND == kPlain
+                           ? (int64_t)(it.q0 + slot_row<KIND>(a, it, x) + row) * a.H + it.h
+                           : (int64_t)(it.q0 + slot_row<KIND>(a, it, x) + tok) * a.H +
+                                 it.h * a.gb + row - tok * a.gb) * D;
 #pragma unroll
             for (int c = 0; c < D / 32; ++c) {
                 uint32_t o[32];
                 tmem_ld32(tO + c * 32, o);
-                if (row < rows) {
+                if ((KIND & kCut) != 0 && part) {
+                    if (row < rows)
+#pragma unroll
+                        for (int e = 0; e < 4; ++e)
+                            st_global_v8(a.split_acc + place * D + c * 32 + e * 8, o + 8 * e);
+                } else if (row < rows) {
                     uint32_t wv[16];
 #pragma unroll
                     for (int e = 0; e < 16; ++e)
@@ -1581,6 +1877,71 @@ __global__ void __launch_bounds__(threads_for(FUSED), 1)
         asm volatile("tcgen05.dealloc.cta_group::1.sync.aligned.b32 %0, %1;" ::"r"(tmem),
                      "r"(kTmemCols)
                      : "memory");
+    }
+}
+
+// Joins the parts of the items that were cut: with M the largest running max,
+//   out = sum_k 2^(m_k - M) acc_k / sum_k 2^(m_k - M) l_k
+// over the parts that saw a key of the row.  blockIdx.x: a unit's CTA,
+// blockIdx.y: its slot, blockIdx.z: a quarter of its rows, whose weights are
+// formed first; then each thread sums four elements of a row at a time.
+constexpr int kJoinThreads = 256;
+constexpr int kJoinRows = kBM / 4;
+
+template <typename T, int D>
+__global__ void __launch_bounds__(kJoinThreads) prefill_join(const PrefillArgs a) {
+    asm volatile("griddepcontrol.wait;" ::: "memory");
+    asm volatile("griddepcontrol.launch_dependents;" ::: "memory");
+    __shared__ float weight[kMaxParts][kJoinRows];    // of a part, over the row's sum
+    const SplitHead head = *a.split;
+    const int unit = (int)(blockIdx.x >> (a.per - 1));
+    if (unit >= head.units) return;
+    const int x = blockIdx.y, tid = threadIdx.x;
+    const SplitUnit u = a.split_units[blockIdx.x];
+    if (u.parts <= 1 || u.part != 0) return;
+    // what a kernel that gave up left may be anything: nothing out of range
+    const int row0 = u.row[x];
+    if (u.parts > kMaxParts || unit + (u.parts - 1) * head.groups >= head.units || u.rows[x] < 0 ||
+        u.rows[x] > a.gb * a.tb || row0 < 0 ||
+        row0 > a.num_tokens - (u.rows[x] + a.gb - 1) / a.gb || u.head < 0 || u.head > a.H - a.gb)
+        return;
+    const int r0 = blockIdx.z * kJoinRows, rows = min(u.rows[x] - r0, kJoinRows);
+    if (rows <= 0) return;
+    auto at = [&](int k, int r) -> int64_t {
+        return ((int64_t)(blockIdx.x + a.per * k * head.groups) * 2 + x) * kBM + r0 + r;
+    };
+    if (tid < rows) {
+        float M = -INFINITY, L = 0.f;
+        for (int k = 0; k < u.parts; ++k) M = fmaxf(M, a.split_ml[at(k, tid)].x);
+        for (int k = 0; k < u.parts; ++k) {
+            const float2 ml = a.split_ml[at(k, tid)];
+            // a part without a key of the row: nothing, whatever its output holds
+            const float f = ml.x == -INFINITY && ml.y == 0.f ? 0.f : ex2(ml.x - M);
+            weight[k][tid] = f;
+            L += f * ml.y;
+        }
+        const float inv = L > 0.f ? 1.f / L : L;      // (NaN stays NaN)
+        for (int k = 0; k < u.parts; ++k) weight[k][tid] *= inv;
+    }
+    __syncthreads();
+    for (int e = tid; e < rows * (D / 4); e += kJoinThreads) {
+        const int r = e / (D / 4), d = e - r * (D / 4);
+        float4 o = make_float4(0.f, 0.f, 0.f, 0.f);
+#pragma unroll 8
+        for (int k = 0; k < u.parts; ++k) {
+            const float f = weight[k][r];
+            float4 v = make_float4(0.f, 0.f, 0.f, 0.f);
+            if (f != 0.f) v = reinterpret_cast<const float4*>(a.split_acc + at(k, r) * D)[d];
+            o.x += f * v.x;
+            o.y += f * v.y;
+            o.z += f * v.z;
+            o.w += f * v.w;
+        }
+        const int tok = (r0 + r) / a.gb;
+        reinterpret_cast<uint2*>(static_cast<T*>(a.out) +
+                                 ((int64_t)(row0 + tok) * a.H + u.head + r0 + r - tok * a.gb) *
+                                     D)[d] =
+            make_uint2(Pk<T>::pack_out(o.x, o.y), Pk<T>::pack_out(o.z, o.w));
     }
 }
 
@@ -1629,13 +1990,13 @@ cudaError_t launch_prefill(const CUtensorMap& tq, const CUtensorMap& tk, const C
     int dev = 0;
     e = cudaGetDevice(&dev);
     if (e != cudaSuccess) return e;
-    // an even number of CTAs (pairs), no more than two per unit of work
-    const int per = a.pack ? 4 : 2;
-    const int64_t units = (int64_t)a.q_items * a.S * ((a.H + per - 1) / per);
+    // an even number of CTAs (pairs), no more than the units of work can use
+    const int64_t units =
+        (int64_t)a.q_items * a.S * (KIND == kPlain ? (a.H + 1) / 2 : (a.head_units + 1) / 2);
     const int sms = pkv::sm_count(dev);
     if (sms < 1) return cudaErrorInvalidDevice;
     const int64_t pairs = sms / 2 > 1 ? sms / 2 : 1;
-    cfg.gridDim = dim3((unsigned)(2 * (units < pairs ? units : pairs)));
+    cfg.gridDim = dim3((unsigned)(2 * (units < pairs && (KIND & kCut) == 0 ? units : pairs)));
     cfg.blockDim = dim3(threads_for(FUSED));
     cfg.dynamicSmemBytes = smem;
     cfg.stream = stream;
@@ -1663,24 +2024,38 @@ cudaError_t launch_prefill(const CUtensorMap& tq, const CUtensorMap& tk, const C
         e = cudaLaunchKernelEx(&cfg, paged_prefill_tc<T, D, FUSED, KIND>, tq, tk, tv, tkin, tvin, a);
     }
     if (e != cudaSuccess) return e;
+    if constexpr ((KIND & kCut) != 0) {
+        cudaLaunchConfig_t jc = {};
+        jc.gridDim = dim3(kSplitParts, 2, kBM / kJoinRows);
+        jc.blockDim = dim3(kJoinThreads);
+        jc.stream = stream;
+        attr[0].id = cudaLaunchAttributeProgrammaticStreamSerialization;
+        attr[0].val.programmaticStreamSerializationAllowed = 1;
+        jc.attrs = attr;
+        jc.numAttrs = 1;
+        e = cudaLaunchKernelEx(&jc, prefill_join<T, D>, a);
+        if (e != cudaSuccess) return e;
+    }
     return cudaGetLastError();
 }
 
 bool aligned(const void* p, uintptr_t al) { return (reinterpret_cast<uintptr_t>(p) & (al - 1)) == 0; }
 
-template <typename T, int D>
+// CUT: kCut or 0
+template <typename T, int D, int CUT>
 cudaError_t launch_grouped(const CUtensorMap& tq, const CUtensorMap& tk, const CUtensorMap& tv,
                            const PrefillArgs& a, int kind, cudaStream_t stream) {
-    switch (kind) {
-        case kGrouped:
-            return launch_prefill<T, D, false, kGrouped>(tq, tk, tv, tq, tq, a, stream);
-        case kGrouped | kCapped:
-            return launch_prefill<T, D, false, kGrouped | kCapped>(tq, tk, tv, tq, tq, a, stream);
-        case kGrouped | kBiased:
-            return launch_prefill<T, D, false, kGrouped | kBiased>(tq, tk, tv, tq, tq, a, stream);
+    constexpr int G = kGrouped | CUT;
+    switch (kind & (kCapped | kBiased)) {
+        case 0:
+            return launch_prefill<T, D, false, G>(tq, tk, tv, tq, tq, a, stream);
+        case kCapped:
+            return launch_prefill<T, D, false, G | kCapped>(tq, tk, tv, tq, tq, a, stream);
+        case kBiased:
+            return launch_prefill<T, D, false, G | kBiased>(tq, tk, tv, tq, tq, a, stream);
         default:
-            return launch_prefill<T, D, false, kGrouped | kCapped | kBiased>(tq, tk, tv, tq, tq, a,
-                                                                             stream);
+            return launch_prefill<T, D, false, G | kCapped | kBiased>(tq, tk, tv, tq, tq, a,
+                                                                      stream);
     }
 }
 

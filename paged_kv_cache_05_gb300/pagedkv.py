@@ -80,7 +80,9 @@ def lib():
                                                     i32, i32, i32, i32, i64, i32, P, sz, P], i32),
             "pkv_paged_attention_prefill_grouped": ([P, P, P, P, P, P, P, P, f32, f32, i32, i32,
                                                      i32, i32, i32, i32, i32, i64, i32, i32, i32,
-                                                     P], i32),
+                                                     P, sz, P], i32),
+            "pkv_prefill_grouped_workspace_size": ([i32, i32, i32, i32, i32, i32, i32,
+                                                    ctypes.POINTER(sz)], i32),
             "pkv_rope_inv_freq": ([i32, ctypes.c_double, i32, ctypes.c_double, i32,
                                    ctypes.c_double, ctypes.c_double, P, ctypes.POINTER(f32)],
                                   i32),
@@ -431,17 +433,28 @@ def paged_attention_prefill_write(out, q, k, v, k_cache, v_cache, block_tables, 
     return out
 
 
+def prefill_grouped_workspace_size(num_seqs, num_heads, num_kv_heads, head_dim, block_size,
+                                   max_blocks_per_seq, max_query_len) -> int:
+    """Bytes of the workspace paged_attention_prefill_grouped can use (0: none)."""
+    out = ctypes.c_size_t(0)
+    _check("pkv_prefill_grouped_workspace_size",
+           lib().pkv_prefill_grouped_workspace_size(num_seqs, num_heads, num_kv_heads, head_dim,
+                                                    block_size, max_blocks_per_seq, max_query_len,
+                                                    ctypes.byref(out)))
+    return out.value
+
+
 def paged_attention_prefill_grouped(out, q, k_cache, v_cache, block_tables, context_lens,
                                     query_start, scale, max_query_len, softcap=0.0, window=0,
-                                    slopes=None, stream=None):
+                                    slopes=None, workspace=None, stream=None):
     """paged_attention_prefill for H query heads over HK shared K/V heads (H a
     multiple of HK): q, out [T, H, D], caches [blocks, HK, B, D]; scores capped
     by softcap * tanh(z / softcap), limited to the last `window` tokens and
-    biased by slopes[h] * (t - p), where given."""
-    torch = _torch()
+    biased by slopes[h] * (t - p), where given.  workspace: a uint8 CUDA tensor of
+    prefill_grouped_workspace_size() bytes; None takes one for the call."""
     st = (_bind or _binding()).paged_attention_prefill_grouped(
         out, q, k_cache, v_cache, block_tables, context_lens, query_start, scale, max_query_len,
-        softcap, window, slopes, None if stream is None else stream.cuda_stream)
+        softcap, window, slopes, workspace, None if stream is None else stream.cuda_stream)
     if st:
         _check("pkv_paged_attention_prefill_grouped", st)
     return out

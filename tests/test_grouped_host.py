@@ -56,8 +56,9 @@ def test_prefill_rejects_bad_arguments_before_any_gpu_call(pkv):
     L = pkv.lib()
     f = 1 << 20
     names = ["out", "q", "k", "v", "bt", "cl", "qs", "sl", "scale", "cap", "win", "S", "H", "HK",
-             "D", "B", "maxb", "nb", "most", "T", "dtype", "stream"]
-    base = [f, f, f, f, f, f, f, None, 0.125, 0.0, 0, 4, 8, 2, 64, 16, 4, 64, 10, 40, 0, None]
+             "D", "B", "maxb", "nb", "most", "T", "dtype", "ws", "wsb", "stream"]
+    base = [f, f, f, f, f, f, f, None, 0.125, 0.0, 0, 4, 8, 2, 64, 16, 4, 64, 10, 40, 0, None, 0,
+            None]
 
     def call(**kw):
         a = list(base)
@@ -73,6 +74,17 @@ def test_prefill_rejects_bad_arguments_before_any_gpu_call(pkv):
         assert call(**kw) == 1, kw
         assert "grouped" in pkv.pagedkv.last_error()
     assert call(S=0) == 0 and call(T=0) == 0 and call(most=0) == 0
+    # a workspace is looked at where the sizes may have use for it
+    need = pkv.prefill_grouped_workspace_size(4, 8, 2, 64, 16, 64, 10)
+    assert need > 0
+    assert call(maxb=64, ws=f * 256, wsb=need - 1) == 1 and "small" in pkv.pagedkv.last_error()
+    assert call(maxb=64, ws=f * 256 + 16, wsb=need) == 1
+    for none in [(4, 8, 2, 64, 16, 4, 10), (4, 8, 2, 64, 16, 64, 100000), (4, 64, 2, 64, 16, 64, 500),
+                 (1000, 8, 2, 64, 16, 64, 10)]:
+        assert pkv.prefill_grouped_workspace_size(*none) == 0
+    for bad in [(4, 7, 2, 64, 16, 64, 10), (4, 8, 2, 96, 16, 64, 10), (-1, 8, 2, 64, 16, 64, 10)]:
+        with pytest.raises(pkv.PagedKVError):
+            pkv.prefill_grouped_workspace_size(*bad)
 
 
 def test_binding_refuses_host_tensors_and_other_objects(pkv):
