@@ -68,7 +68,7 @@ def kernel_source_digest(files=("decode_kernel.cuh", "decode_api.cu", "pkv_inter
     return h.hexdigest()[:16]
 
 
-PREFILL_SOURCES = ("prefill.cu", "pkv_internal.h")
+PREFILL_SOURCES = ("prefill_kernel.cuh", "prefill.cu", "pkv_internal.h")
 
 
 def profiled_traffic(workload: str, profile: str = None, sources=None):

@@ -250,7 +250,8 @@ pkv_status pkv_contiguous_attention_decode(void* out, const void* q, const void*
  * PKV_DEVERR_BAD_CONTEXT (clamped).  num_blocks * num_kv_heads * block_size
  * must stay below 2^31 (the tiled copies address cache rows with 32-bit
  * coordinates), max_blocks_per_seq * block_size at most 2^30.  An infinite V of a
- * visible token gives NaN (its weight is a sum of two parts of either sign).
+ * visible token gives NaN (its weight is a sum of two parts of either sign); a
+ * visible token whose score is not finite in fp32 may give NaN too.
  * The split of the work depends on the sizes and lengths alone:
  * results are bit-identical from call to call on one GPU.  Two launches on
  * `stream`.
@@ -395,7 +396,8 @@ pkv_status pkv_paged_attention_prefill_write(void* out, const void* q, const voi
  * 256 neighbouring tokens, those of several of the query heads that share a K/V
  * head) sees are not looked up for it, and tokens that none sees do not matter;
  * an infinite or NaN V of a token that some row sees may show in the other rows
- * of that item too (the rows share their products).  num_blocks * num_kv_heads *
+ * of that item too (the rows share their products), and a visible token whose
+ * score is not finite in fp32 may give NaN.  num_blocks * num_kv_heads *
  * block_size must stay below 2^31, max_blocks_per_seq * block_size at most 2^30.
  * Fifth-generation tensor cores, fp32 accumulation.
  * workspace: NULL, or device memory of pkv_prefill_grouped_workspace_size(...)
@@ -442,6 +444,8 @@ pkv_status pkv_reshape_and_cache(const void* k, const void* v, void* k_cache, vo
  * For token t and head row x of its queries or keys, in fp32 and rounded once
  * at the end:
  *   x <- x / sqrt(mean(x^2) + eps) * weight     when that kind's weight is given
+ *     (a bf16 row whose sum of squares passes the fp32 range, elements of about
+ *     10^18, becomes 0 or NaN)
  *   pair i of x turns by the angle positions[t] * f_i:
  *     (a, b) <- rope_scale * (a cos - b sin, b cos + a sin)
  * Pair i, i < rot_dim / 2, is (x[i], x[i + rot_dim / 2]) or, with interleaved
