@@ -40,6 +40,14 @@
 // share leave one part in each, and a second kernel joins them.  All joins are
 // in range order, so results do not vary from call to call.
 //
+// Measured (GB300, us a call, both kernels, and the share of the measured 6.8
+// TB/s copy rate that the visible K and V come at): 8 sequences of 8192-32768
+// tokens, 32/8 heads x 128, bf16, 111 us, 0.93; 64 of 1-2048, 40/8 x 128, fp16,
+// capped, 49.6 us, 0.80; 33 of 17-8191, 16/1 x 64, bf16, window 1000, biased, 10.7 us; one
+// of 500, 6.9 us.  About 7 us of a call do not shrink with the bytes: the ranges'
+// start (lengths, tables, queries, the first copies, one behind the other) and
+// the second kernel.
+//
 // Masked tokens (before the window, past the context) are excluded by
 // selection in S, and their V rows are zeroed in shared memory, so what the
 // pool holds there never matters; blocks without a visible token are neither

@@ -13,7 +13,7 @@ namespace {
 // smallest above 1.  More heads a tile read the cache once for more of them and
 // fill it with fewer tokens (8 sequences of 4 new tokens, 6000 cached, G = 8: 237
 // -> 87 us against two heads an item), but a batch of many short items spends
-// more on its schedule (40 prompts of 800, G = 16: 322 us with 16, 256 with 2).
+// more on its schedule (40 prompts of 800, G = 16: 322 us with 16, 239 with 2).
 int heads_of_tile(int G, int S, int max_query_len) {
     int best = 1, used = 0, few = 0;
     for (int gb = G < kBM ? G : kBM; gb >= 1; --gb) {

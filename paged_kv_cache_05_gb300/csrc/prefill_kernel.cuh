@@ -47,6 +47,20 @@
 // chunk c of row r at chunk c ^ (r % 8)); V the same bytes read as an
 // MN-major operand (N = head dimension); P in tensor memory, row = lane, keys
 // 32 q + 2c and 32 q + 2c + 1 in column 32 q + c (bf16 residuals 16 further).
+//
+// The grouped kinds (query heads that share K/V heads, an optional window, cap
+// and distance bias) put the rows of several heads of a K/V head in a tile, deal
+// small batches' items by cost, start at the tile of the first row's window, and
+// cut the items of batches too small for the device along the keys.  Bound: the
+// same chain of softmax and products per tile as the plain kind's, plus what a
+// score costs more (the cap two more operations of the special unit and a
+// reciprocal's worth of arithmetic, the bias a max over formed scores).
+// Measured (GB300, us a call and the share of the matrix unit's time): 4 prompts
+// of 1900-2048 tokens, 32/8 heads x 128, fp16, 146.5 us, 895 TFLOP/s, tensor pipe
+// 41% busy; 4 chunks of 301-1024 behind 5000 tokens, window 1024, capped, 16/4 x
+// 128, bf16, 53.6 us, 24%; 8 biased prompts of 100-1100, 24/6 x 64, fp16, 33.5
+// us, 11%; one prompt of 61 tokens 9.8 us, of which the start-up and the chain of
+// one tile are nearly all.
 #pragma once
 
 #include <cuda.h>
@@ -497,7 +511,8 @@ enum : int {
     kBarCount = 35
 };
 
-// One work item: 256 query rows (two query tiles) of one (sequence, head).
+// One work item: 256 query rows (two query tiles) of one (sequence, head), or of
+// gb heads and 2 tb tokens.
 struct Item {
     int s, h, q0, qlen, ctx, q_begin;
     int sw;                          // slot x holds rows (x ^ sw) * 128 .. + 127 of the item
