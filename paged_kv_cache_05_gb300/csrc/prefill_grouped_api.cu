@@ -39,13 +39,19 @@ int64_t most_work(int S, int H, int gb, int max_query_len) {
 }
 
 // Whether a batch of these sizes may have so few units that its items are cut
-// along the keys: an upper bound of their work (the lengths are on the device)
-// that would leave half of a GB300's SMs without any, and contexts of 8 key
-// tiles or more.
-bool may_split(int S, int H, int HK, int B, int max_blocks, int max_query_len) {
+// along the keys.  The lengths are on the device: this goes by upper bounds of the
+// work (items by groups of heads) and of an item's key tiles.  A batch that turns
+// out not to be cut pays for the second launch and the estimate (about 5 us), so
+// work for half of the SMs or less asks for 8 tiles, for all of them 16 (4 prompts
+// of 2-194 over 3798, 40/8 heads x 64: 92 -> 63 us; 2 of 512 over 4000, which are
+// not cut: 91 -> 96).
+bool may_split(int S, int H, int HK, int B, int max_blocks, int max_query_len, int window) {
     const int gb = heads_of_tile(H / HK, S, max_query_len);
-    return S <= kSplitItems && (int64_t)max_blocks * B >= 8 * kBN &&
-           most_work(S, H, gb, max_query_len) <= kSplitParts / 4;
+    int64_t keys = (int64_t)max_blocks * B;
+    if (window > 0 && keys > (int64_t)window + 2 * (kBM / gb)) keys = window + 2 * (kBM / gb);
+    const int64_t work = most_work(S, H, gb, max_query_len);
+    return S <= kSplitItems && (work <= kSplitParts / 4 ? keys >= 8 * kBN
+                                                       : work <= kSplitParts / 2 && keys >= 16 * kBN);
 }
 
 struct SplitLayout {
@@ -54,7 +60,7 @@ struct SplitLayout {
 SplitLayout split_layout(int D) {
     SplitLayout l;
     const size_t rows = (size_t)kSplitParts * 2 * kBM;
-    l.units = 256;
+    l.units = pkv::align_up(sizeof(SplitHead), 256);
     l.ml = pkv::align_up(l.units + sizeof(SplitUnit) * kSplitParts, 256);
     l.acc = l.ml + 8 * rows;
     l.total = l.acc + 4 * rows * (size_t)D;
@@ -75,7 +81,7 @@ pkv_status pkv_prefill_grouped_workspace_size(int num_seqs, int num_heads, int n
         max_query_len < 0)
         return pkv::fail(PKV_ERR_INVALID, "%s: bad sizes", fn);
     *bytes = may_split(num_seqs, num_heads, num_kv_heads, block_size, max_blocks_per_seq,
-                       max_query_len)
+                       max_query_len, 0)
                  ? split_layout(head_dim).total : 0;
     return PKV_OK;
 }
@@ -141,7 +147,7 @@ pkv_status pkv_paged_attention_prefill_grouped(
                          "aligned",
                          fn);
     const bool split = workspace && may_split(num_seqs, num_heads, num_kv_heads, block_size,
-                                              max_blocks_per_seq, max_query_len);
+                                              max_blocks_per_seq, max_query_len, window);
     const SplitLayout lay = split_layout(head_dim);
     if (split && !aligned(workspace, 256))
         return pkv::fail(PKV_ERR_INVALID, "%s: workspace must be 256-byte aligned", fn);
@@ -193,6 +199,7 @@ pkv_status pkv_paged_attention_prefill_grouped(
     a.q_items = (int)(((int64_t)max_query_len + 2 * a.tb - 1) / (2 * a.tb));
     a.num_blocks = num_blocks;
     if (split) {
+        a.most_work = (int)most_work(num_seqs, num_heads, gb, max_query_len);
         char* ws = static_cast<char*>(workspace);
         a.split = reinterpret_cast<SplitHead*>(ws);
         a.split_units = reinterpret_cast<SplitUnit*>(ws + lay.units);

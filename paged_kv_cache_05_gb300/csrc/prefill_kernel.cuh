@@ -446,6 +446,7 @@ struct PrefillArgs {
     // the H / gb groups of heads take the place of the heads in the schedule
     int gb, tb, head_units, units_per_kv;
     int per;                     // CTAs of a unit of work: 2, or 1 of an odd head_units
+    int most_work;               // work of CTAs, at most: items by groups of heads
     int window;                  // tokens a row sees, 0: all before it
     float cap_log2;              // cap * log2(e)
     const float* slopes;         // [H]
@@ -464,8 +465,10 @@ struct PrefillArgs {
 // CTA r (of its `per`) leaves its part at per u + r.
 constexpr int kSplitParts = 320;   // most parts of such a batch
 constexpr int kMaxParts = 32;      // most parts of an item
+constexpr int kSplitItems = 64;    // most items of it before they are cut
 struct SplitHead {
-    int units, groups;             // units (0: nothing was split); units of an item part
+    int items, parts;              // items (0: none was cut) and the parts of all of them
+    int first[kSplitItems];        // an item's first part
 };
 struct SplitUnit {
     int parts, part;               // parts of its item, which one
@@ -671,8 +674,7 @@ __device__ __forceinline__ int item_cost(const PrefillArgs& a, const SeqInfo& si
 constexpr int kDealItems = 256;    // most items (of all sequences) of a dealt batch
 constexpr int kDealRounds = 16;    // most units a pair of it
 constexpr int kDealGroups = 192;   // most CTAs, or pairs of them
-constexpr int kSplitItems = 64;    // most items of a batch whose items may be cut
-constexpr int kMinTiles = 3;       // fewest key tiles of a part
+constexpr float kJoinCost = 2.f, kJoinRowCost = 0.05f / 256.f;   // in key tiles, see cut_items
 
 struct Sched {
     int s, hp;         // first unit that may belong to the pair: (s, hp, last item)
@@ -692,7 +694,7 @@ struct Deal {
     unsigned char part[kDealItems], parts[kDealItems];
     int load[kDealGroups];
     // the batch's items before they are cut
-    short seq0[kSplitItems], t0[kSplitItems], tiles0[kSplitItems];
+    short seq0[kSplitItems], t0[kSplitItems], tiles0[kSplitItems], rows0[kSplitItems];
     int at0[kSplitItems + 1];
 };
 
@@ -884,8 +886,7 @@ __device__ __forceinline__ Item unit_item(const PrefillArgs& a, const Deal* d, i
 // estimated to shorten it (every thread; false: not cut).  `first`: the items
 // before this thread's sequence; total: the items, then their parts.
 // The estimate, in key tiles with 1.5 for an item's fixed work: with at most a
-// unit a CTA the largest part, else the mean load and half a part; the join
-// costs about 3.
+// unit a CTA the largest part, else the mean load and half a part, and the join.
 template <int KIND>
 __device__ __forceinline__ bool cut_items(const PrefillArgs& a, Deal* d, const SeqInfo& si,
                                           int first, int& total, int tid) {
@@ -898,6 +899,7 @@ __device__ __forceinline__ bool cut_items(const PrefillArgs& a, Deal* d, const S
         d->seq0[first + t] = (short)tid;
         d->t0[first + t] = (short)t;
         d->tiles0[first + t] = (short)(it.n_kv < 32767 ? it.n_kv : 32767);
+        d->rows0[first + t] = (short)(it.rows[0] + it.rows[1]);
     }
     __syncthreads();
     if (tid < 32) {
@@ -905,16 +907,18 @@ __device__ __forceinline__ bool cut_items(const PrefillArgs& a, Deal* d, const S
         int most = 0;
         for (int i = lane; i < total; i += 32) most = max(most, (int)d->tiles0[i]);
         most = __reduce_max_sync(0xffffffffu, most);
-        const int size = max((most + lane) / (lane + 1), kMinTiles);
-        int n = 0, tiles = 0;
+        const int size = max((most + lane) / (lane + 1), 1);
+        int n = 0, tiles = 0, rows = 0;     // rows: left by all parts
         for (int i = 0; i < total; ++i) {
-            n += (d->tiles0[i] + size - 1) / size;
+            const int parts = (d->tiles0[i] + size - 1) / size;
+            n += parts;
             tiles += d->tiles0[i];
+            rows += parts * d->rows0[i];
         }
         const float mean = ((float)tiles + 1.5f * (float)n) * (float)HP / (float)groups;
         float est = n * HP <= groups ? fmaxf((float)min(size, most) + 1.5f, mean)
                                     : mean + 0.5f * (float)size;
-        if (n > total) est += 3.f;
+        if (n > total) est += kJoinCost + kJoinRowCost * (float)(rows * HP * a.per);
         if (n * HP > most_parts || n > kDealItems) est = INFINITY;
         float best = est;
 #pragma unroll
@@ -986,15 +990,19 @@ __device__ __forceinline__ bool deal_units(const PrefillArgs& a, Deal* d, int ti
         total += d->scan[w];
     }
     const bool teller = (KIND & kCut) != 0 && blockIdx.x == 0 && tid == 0;
-    if (teller) a.split->units = 0;
+    if (teller) a.split->items = 0;
     if (!few || total > kDealItems) return false;     // (the same for all)
     bool cut = false;
+    const int items = total;
     if constexpr ((KIND & kCut) != 0) cut = cut_items<KIND>(a, d, si, incl - si.ni, total, tid);
     const int rounds = (int)(((int64_t)total * HP + groups - 1) / groups);
     if (rounds > kDealRounds) return false;
-    if (cut && teller) {
-        a.split->units = total * HP;
-        a.split->groups = HP;
+    if ((KIND & kCut) != 0 && cut && blockIdx.x == 0) {
+        if (tid < items) a.split->first[tid] = d->at0[tid];
+        if (teller) {
+            a.split->items = items;
+            a.split->parts = total;
+        }
     }
     if (tid == 0) d->cut = cut;
     for (int t = 0; t < si.ni && !cut; ++t) {
@@ -1897,33 +1905,40 @@ __global__ void __launch_bounds__(threads_for(FUSED), 1)
 
 // Joins the parts of the items that were cut: with M the largest running max,
 //   out = sum_k 2^(m_k - M) acc_k / sum_k 2^(m_k - M) l_k
-// over the parts that saw a key of the row.  blockIdx.x: a unit's CTA,
-// blockIdx.y: its slot, blockIdx.z: a quarter of its rows, whose weights are
+// over the parts that saw a key of the row.  blockIdx.x: an item of a group of
+// heads, blockIdx.y: its slot, blockIdx.z: a slice of its rows, whose weights are
 // formed first; then each thread sums four elements of a row at a time.
 constexpr int kJoinThreads = 256;
-constexpr int kJoinRows = kBM / 4;
+constexpr int kJoinRows = kBM / 4;         // most rows of a block
+constexpr int kMaxSlices = 16;             // most blocks of a slot's rows
+constexpr int kJoinSpread = 160 << 10;     // unused shared memory of an SM's blocks
 
 template <typename T, int D>
 __global__ void __launch_bounds__(kJoinThreads) prefill_join(const PrefillArgs a) {
     asm volatile("griddepcontrol.wait;" ::: "memory");
     asm volatile("griddepcontrol.launch_dependents;" ::: "memory");
     __shared__ float weight[kMaxParts][kJoinRows];    // of a part, over the row's sum
-    const SplitHead head = *a.split;
-    const int unit = (int)(blockIdx.x >> (a.per - 1));
-    if (unit >= head.units) return;
+    const int item = (int)blockIdx.x / a.head_units, h = (int)blockIdx.x - item * a.head_units;
+    if (item >= kSplitItems) return;
+    // (loaded together: none waits for another)
+    const int items = a.split->items, parts = a.split->parts, first = a.split->first[item];
+    // group h of the item's part k is its head_units (first + k) + h'th
+    const int unit0 = first * a.head_units + h;
     const int x = blockIdx.y, tid = threadIdx.x;
-    const SplitUnit u = a.split_units[blockIdx.x];
-    if (u.parts <= 1 || u.part != 0) return;
+    if (item >= items || first < 0 || first >= parts || parts * a.head_units > kSplitParts) return;
+    const SplitUnit u = a.split_units[unit0];
+    if (u.parts <= 1) return;
     // what a kernel that gave up left may be anything: nothing out of range
     const int row0 = u.row[x];
-    if (u.parts > kMaxParts || unit + (u.parts - 1) * head.groups >= head.units || u.rows[x] < 0 ||
+    if (u.parts > kMaxParts || first + u.parts > parts || u.rows[x] < 0 ||
         u.rows[x] > a.gb * a.tb || row0 < 0 ||
         row0 > a.num_tokens - (u.rows[x] + a.gb - 1) / a.gb || u.head < 0 || u.head > a.H - a.gb)
         return;
-    const int r0 = blockIdx.z * kJoinRows, rows = min(u.rows[x] - r0, kJoinRows);
+    const int slice = kBM / (int)gridDim.z, r0 = (int)blockIdx.z * slice;
+    const int rows = min(u.rows[x] - r0, slice);
     if (rows <= 0) return;
     auto at = [&](int k, int r) -> int64_t {
-        return ((int64_t)(blockIdx.x + a.per * k * head.groups) * 2 + x) * kBM + r0 + r;
+        return ((int64_t)(unit0 + k * a.head_units) * 2 + x) * kBM + r0 + r;
     };
     if (tid < rows) {
         float M = -INFINITY, L = 0.f;
@@ -2040,9 +2055,21 @@ cudaError_t launch_prefill(const CUtensorMap& tq, const CUtensorMap& tk, const C
     }
     if (e != cudaSuccess) return e;
     if constexpr ((KIND & kCut) != 0) {
+        // A few blocks an SM.  Launched ahead, they settle on the SMs that the kernel
+        // before leaves first, as many as fit: shared memory that is not used
+        // spreads them over all (one chunk of 300 over 6000: 34.5 us with 80 blocks
+        // where they fall, 33.2 spread, 25.7 with 320).
+        int slices = kBM / kJoinRows;
+        while (slices < kMaxSlices && (int64_t)a.most_work * 4 * slices <= 8 * sms) slices *= 2;
+        const int64_t blocks = (int64_t)a.most_work * 2 * slices;
+        const int each = (int)((blocks + sms - 1) / sms);
         cudaLaunchConfig_t jc = {};
-        jc.gridDim = dim3(kSplitParts, 2, kBM / kJoinRows);
+        jc.gridDim = dim3((unsigned)a.most_work, 2, (unsigned)slices);
         jc.blockDim = dim3(kJoinThreads);
+        jc.dynamicSmemBytes = each < 8 ? (size_t)kJoinSpread / each : 0;
+        e = cudaFuncSetAttribute(prefill_join<T, D>, cudaFuncAttributeMaxDynamicSharedMemorySize,
+                                 kJoinSpread);
+        if (e != cudaSuccess) return e;
         jc.stream = stream;
         attr[0].id = cudaLaunchAttributeProgrammaticStreamSerialization;
         attr[0].val.programmaticStreamSerializationAllowed = 1;

@@ -41,6 +41,8 @@ CASES = [
     (1, 1, 64, 64, "bf16", [1], 20001, 0, 8.0, False),
     (67, 1, 64, 16, "f16", [2], 1300, 0, 0.0, False),
     (2, 1, 128, 16, "f16", [4], 1024, 5, 0.0, False),
+    (40, 8, 64, 8, "bf16", [2, 60, 101, 33], 2600, 0, 0.0, True),
+    (12, 2, 128, 32, "f16", [20, 1, 17], 1200, 900, 0.0, False),
 ]
 
 
