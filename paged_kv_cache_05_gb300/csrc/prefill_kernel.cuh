@@ -908,9 +908,12 @@ __device__ __forceinline__ bool cut_items(const PrefillArgs& a, Deal* d, const S
         for (int i = lane; i < total; i += 32) most = max(most, (int)d->tiles0[i]);
         most = __reduce_max_sync(0xffffffffu, most);
         const int size = max((most + lane) / (lane + 1), 1);
+        const float inv = __fdividef(1.f, (float)size);
         int n = 0, tiles = 0, rows = 0;     // rows: left by all parts
+#pragma unroll 4
         for (int i = 0; i < total; ++i) {
-            const int parts = (d->tiles0[i] + size - 1) / size;
+            // (one off at times: an estimate)
+            const int parts = (int)(((float)d->tiles0[i] - 0.5f) * inv) + 1;
             n += parts;
             tiles += d->tiles0[i];
             rows += parts * d->rows0[i];
@@ -941,7 +944,9 @@ __device__ __forceinline__ bool cut_items(const PrefillArgs& a, Deal* d, const S
         }
         d->at0[2 * lane] = incl - sum;
         d->at0[2 * lane + 1] = incl - p[1];
-        if (lane == 31) d->at0[kSplitItems] = cut ? incl : 0;
+        if (lane == 31)
+            d->at0[kSplitItems] =
+                cut && incl > total && incl * HP <= most_parts && incl <= kDealItems ? incl : 0;
     }
     __syncthreads();
     const int parts = d->at0[kSplitItems];
