@@ -59,7 +59,7 @@
 // of 1900-2048 tokens, 32/8 heads x 128, fp16, 146.5 us, 895 TFLOP/s, tensor pipe
 // 41% busy; 4 chunks of 301-1024 behind 5000 tokens, window 1024, capped, 16/4 x
 // 128, bf16, 53.6 us, 24%; 8 biased prompts of 100-1100, 24/6 x 64, fp16, 33.5
-// us, 11%; one prompt of 61 tokens 9.8 us, of which the start-up and the chain of
+// us, 11%; one prompt of 61 tokens 9.1 us, of which the start-up and the chain of
 // one tile are nearly all.
 #pragma once
 
@@ -446,6 +446,7 @@ struct PrefillArgs {
     // the H / gb groups of heads take the place of the heads in the schedule
     int gb, tb, head_units, units_per_kv;
     int per;                     // CTAs of a unit of work: 2, or 1 of an odd head_units
+    int item_tokens;             // 2 tb, or tb: items of one tile, in slot 0
     int most_work;               // work of CTAs, at most: items by groups of heads
     int window;                  // tokens a row sees, 0: all before it
     float cap_log2;              // cap * log2(e)
@@ -515,7 +516,7 @@ enum : int {
 };
 
 // One work item: 256 query rows (two query tiles) of one (sequence, head), or of
-// gb heads and 2 tb tokens.
+// gb heads and 2 tb tokens (or tb).
 struct Item {
     int s, h, q0, qlen, ctx, q_begin;
     int sw;                          // slot x holds rows (x ^ sw) * 128 .. + 127 of the item
@@ -538,6 +539,12 @@ template <int KIND>
 __device__ __forceinline__ int tile_tokens(const PrefillArgs& a) {
     if constexpr ((KIND & kGrouped) != 0) return a.tb;
     else return kBM;
+}
+// and of an item
+template <int KIND>
+__device__ __forceinline__ int item_tokens(const PrefillArgs& a) {
+    if constexpr ((KIND & kGrouped) != 0) return a.item_tokens;
+    else return 2 * kBM;
 }
 template <int KIND>
 __device__ __forceinline__ int tile_heads(const PrefillArgs& a) {
@@ -578,7 +585,7 @@ __device__ __forceinline__ bool seq_info(const PrefillArgs& a, int s, bool whole
     if (si.ctx < 0 || si.ctx > a.max_blocks * a.B || si.qlen < 0 || si.qlen > si.ctx ||
         si.q0 < 0 || (int64_t)si.q0 + si.qlen > a.num_tokens || (whole && si.qlen != si.ctx))
         return false;
-    const int rows = 2 * tile_tokens<KIND>(a);
+    const int rows = item_tokens<KIND>(a);
     const int n = (si.qlen + rows - 1) / rows;     // rows past the last item stay unwritten
     si.ni = n < a.q_items ? n : a.q_items;
     return true;
@@ -597,11 +604,17 @@ template <int KIND>
 __device__ __forceinline__ void item_tiles(const PrefillArgs& a, const SeqInfo& si, int t,
                                            Item& it) {
     const int tokens = tile_tokens<KIND>(a);
-    it.q_begin = t * 2 * tokens;
+    it.q_begin = t * item_tokens<KIND>(a);
     it.sw = t & 1;
+    int end = si.qlen;
+    if constexpr ((KIND & kGrouped) != 0)
+        if (a.item_tokens == tokens) {             // one tile: in slot 0
+            it.sw = 0;
+            end = min(end, it.q_begin + tokens);
+        }
     for (int x = 0; x < 2; ++x) {
         const int b = it.q_begin + (x ^ it.sw) * tokens;
-        const int live = si.qlen - b < tokens ? (si.qlen - b > 0 ? si.qlen - b : 0) : tokens;
+        const int live = end - b < tokens ? (end - b > 0 ? end - b : 0) : tokens;
         it.rows[x] = live * tile_heads<KIND>(a);
         it.pos0[x] = si.ctx - si.qlen + b;            // position of the tile's first query
         it.n[x] = live > 0 ? (it.pos0[x] + live - 1) / kBN + 1 : 0;
