@@ -162,3 +162,64 @@ def test_tiles_of_fewer_heads(pkv, S, H, HK, new):  # noqa: F811
     ref, slack = bounded(c, 0.125, 0.0, None)
     check(run(pkv, c, on_device(c), 0.125), c, ref, slack)
     assert pkv.get_device_error() == 0
+
+
+PAIRS = [
+    # items of two tiles: more tiles than SMs
+    (16, 4, 128, 16, "bf16", [200, 131, 64, 257, 90], 300, 100, 20.0, True),
+    (24, 24, 64, 32, "f16", [300, 290, 129, 257], 200, 129, 0.0, False),
+    (32, 8, 64, 8, "bf16", [300, 1, 255, 170], 77, 0, 0.0, True),
+    (40, 8, 128, 64, "f16", [260, 130, 77], 0, 64, 30.0, False),
+]
+
+
+@pytest.mark.parametrize("case", PAIRS, ids=lambda c: "%dx%d-D%d-B%d-%s-new%d-past%d-w%d-c%g-%d" % (
+    c[0], c[1], c[2], c[3], c[4], max(c[5]), c[6], c[7], c[8], c[9]))
+def test_items_of_two_tiles(pkv, case):  # noqa: F811
+    H, HK, D, B, dtype, new, past, window, cap, biased = case
+    rs = np.random.default_rng(H + D + B + past + window)
+    c = make_case(rs, H, HK, D, B, new, [n + max(past - 31 * i, 0) for i, n in enumerate(new)],
+                  dtype, window, 6.0 if cap else 1.0)
+    slopes = alibi(H) if biased else None
+    scale = 1 / math.sqrt(D)
+    ref, slack = bounded(c, scale, cap, slopes)
+    check(run(pkv, c, on_device(c), scale, cap, slopes), c, ref, slack)
+    assert pkv.get_device_error() == 0
+
+
+@pytest.mark.parametrize("new,past", [([3, 6], 2000), ([40, 70], 0), ([200, 190, 180, 170], 0)])
+def test_rows_behind_the_last_sequence(pkv, new, past):  # noqa: F811
+    """A padded batch: q and out have more rows than the sequences."""
+    import torch
+    c = make_case(np.random.default_rng(21), 16, 4, 64, 16, new, [n + past for n in new], "bf16")
+    ref, slack = bounded(c, 0.125, 0.0, None)
+    d = on_device(c)
+    rows = sum(new)
+    q = torch.full((rows + 70, 16, 64), float("nan"), dtype=d["q"].dtype, device="cuda")
+    q[:rows] = d["q"]
+    out = torch.full_like(q, 7.0)
+    pkv.paged_attention_prefill_grouped(out, q, d["kc"], d["vc"], d["bt"], d["cl"], d["qs"], 0.125,
+                                        max(new))
+    assert pkv.get_device_error() == 0
+    assert (out[rows:] == 7.0).all()
+    check(out[:rows], c, ref, slack * 1.25)
+
+
+def test_a_call_of_its_own_workspace_on_another_stream(pkv):  # noqa: F811
+    """The workspace that a call takes is not given to others before it is done."""
+    import torch
+    c = make_case(np.random.default_rng(23), 8, 2, 128, 16, [6, 9], [2600, 1900], "f16", wild=False)
+    d = on_device(c)
+    ref, slack = bounded(c, 0.09, 0.0, None)
+    n = space(pkv, c, d)[1]
+    side = torch.cuda.Stream()
+    outs = [torch.empty_like(d["q"]) for _ in range(6)]
+    torch.cuda.synchronize()
+    for out in outs:
+        pkv.paged_attention_prefill_grouped(out, d["q"], d["kc"], d["vc"], d["bt"], d["cl"], d["qs"],
+                                            0.09, 9, stream=side)
+        torch.full((n,), 0xFF, dtype=torch.uint8, device="cuda")
+    torch.cuda.synchronize()
+    assert pkv.get_device_error() == 0
+    for out in outs:
+        check(out, c, ref, slack * 1.25)
