@@ -69,6 +69,10 @@ constexpr int kStepTokens = 16;             // tokens a step at head_dim 128, tw
 constexpr int kMaxCtas = 512;
 constexpr int kMinSteps = 2;                // fewest steps of a CTA
 constexpr float kRaiseLog2 = 8.f;           // raise the running max only past this growth
+// Largest cap whose scores are formed as cap (1 - 2 / (2^y + 1)), which is off by
+// up to 2^-20 of the CAP: up to here 2^-14 in the score, below the outputs'
+// rounding.  Above it tanhf, whose error goes with the score.
+constexpr float kDirectCap = 64.f;
 constexpr float kLog2e = 1.4426950408889634f;
 
 __device__ __forceinline__ float ex2(float x) {
@@ -136,8 +140,9 @@ struct Args {
     const int32_t* tables;
     const int32_t* ctx;
     const float* slopes;
-    float score;           // without a cap: scale * log2(e), else 2 log2(e) scale / cap
+    float score;           // scale * log2(e); with a cap 2 log2(e) scale / cap, past kDirectCap scale
     float cap_log2;        // cap * log2(e); 0: no cap
+    float cap_inv;         // 1 / cap past kDirectCap, else 0
     int window, S, H, HK, G, chunks, max_blocks, cap_tokens, lgB, tpc, num_blocks;
     int ctas;              // of the grid
     uint64_t wait_ns;
@@ -474,7 +479,9 @@ __device__ __forceinline__ void walk(const Args& a, const Batch& b, Cursor<Geo<D
                                 f(z[u][v][2 * i + e], t0 + u * 16 + v * 8 + 2 * kq + e, i);
             };
             each([&](float& y, int, int) { y *= a.score; });
-            if (a.cap_log2 > 0.f)           // cap tanh(y) = cap (1 - 2 / (2^(2 log2(e) y) + 1))
+            if (a.cap_inv > 0.f)
+                each([&](float& y, int, int) { y = a.cap_log2 * tanhf(y * a.cap_inv); });
+            else if (a.cap_log2 > 0.f)      // cap tanh(y) = cap (1 - 2 / (2^(2 log2(e) y) + 1))
                 each([&](float& y, int, int) {
                     y = a.cap_log2 * (1.f - __fdividef(2.f, ex2(y) + 1.f));
                 });
@@ -971,6 +978,7 @@ pkv_status pkv_paged_attention_decode_grouped(
     const float cap_log2 = (float)(log2e * softcap);
     if (!std::isfinite(score) || !std::isfinite(cap_log2))
         return pkv::fail(PKV_ERR_INVALID, "%s: scale and softcap are too far apart", fn);
+    const bool large_cap = softcap > kDirectCap;
     if (window < 0) return pkv::fail(PKV_ERR_INVALID, "%s: window must not be negative", fn);
     // the tiled copies address cache rows (block, head, token) with 32-bit coordinates
     if (num_blocks < 1 || num_blocks > ((1LL << 31) - 1) / ((int64_t)num_kv_heads * block_size))
@@ -1018,8 +1026,9 @@ pkv_status pkv_paged_attention_decode_grouped(
     a.tables = block_tables;
     a.ctx = context_lens;
     a.slopes = slopes;
-    a.score = score;
+    a.score = large_cap ? scale : score;
     a.cap_log2 = cap_log2;
+    a.cap_inv = large_cap ? (float)(1.0 / softcap) : 0.f;
     a.window = window;
     a.S = num_seqs;
     a.H = num_heads;
