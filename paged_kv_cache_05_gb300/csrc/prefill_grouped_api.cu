@@ -135,6 +135,7 @@ pkv_status pkv_paged_attention_prefill_grouped(
     const float cap_log2 = (float)(log2e * softcap);
     if (!std::isfinite(score) || !std::isfinite(cap_log2))
         return pkv::fail(PKV_ERR_INVALID, "%s: scale and softcap are too far apart", fn);
+    const bool large_cap = softcap > kDirectCap;
     if (window < 0) return pkv::fail(PKV_ERR_INVALID, "%s: window must not be negative", fn);
     if (num_seqs == 0 || max_query_len == 0 || num_query_tokens == 0) return PKV_OK;
     if (!out || !q || !k_cache || !v_cache || !block_tables || !context_lens || !query_start)
@@ -180,7 +181,7 @@ pkv_status pkv_paged_attention_prefill_grouped(
     a.block_tables = block_tables;
     a.context_lens = context_lens;
     a.query_start = query_start;
-    a.scale_log2 = score;
+    a.scale_log2 = large_cap ? 1.f : score;
     a.S = num_seqs;
     a.H = num_heads;
     a.B = block_size;
@@ -191,6 +192,8 @@ pkv_status pkv_paged_attention_prefill_grouped(
     a.G = num_heads / num_kv_heads;
     a.window = window;
     a.cap_log2 = cap_log2;
+    a.cap_scale = scale;
+    a.cap_inv = large_cap ? (float)(1.0 / softcap) : 0.f;
     a.slopes = slopes;
     a.gb = gb;
     a.tb = kBM / gb;
@@ -217,7 +220,8 @@ pkv_status pkv_paged_attention_prefill_grouped(
         a.split_acc = reinterpret_cast<float*>(ws + lay.acc);
     }
     a.err = err;
-    const int kind = kGrouped | (softcap > 0.f ? kCapped : 0) | (slopes ? kBiased : 0);
+    const int kind = kGrouped | (softcap > 0.f && !large_cap ? kCapped : 0) |
+                     (slopes || large_cap ? kBiased : 0);
     pkv::LaunchGrouped* const launch =
         split ? (bf16 ? pkv::launch_prefill_cut_bf16 : pkv::launch_prefill_cut_f16)
               : (bf16 ? pkv::launch_prefill_grouped_bf16 : pkv::launch_prefill_grouped_f16);

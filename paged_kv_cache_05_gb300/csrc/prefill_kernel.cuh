@@ -450,7 +450,8 @@ struct PrefillArgs {
     int most_work;               // work of CTAs, at most: items by groups of heads
     int window;                  // tokens a row sees, 0: all before it
     float cap_log2;              // cap * log2(e)
-    const float* slopes;         // [H]
+    float cap_scale, cap_inv;    // a large cap: scale and 1 / cap (else 0), and scale_log2 1
+    const float* slopes;         // [H]; null: none
     // split items (null: none): what a workspace holds, see SplitHead
     struct SplitHead* split;
     struct SplitUnit* split_units;   // [kSplitParts]
@@ -480,7 +481,13 @@ struct SplitUnit {
 
 // Kinds of a kernel, bits: query heads that share K/V heads and an optional
 // sliding window; scores capped by cap tanh(z / cap); scores biased by
-// slope[h] (t - p).  0 is the plain kernel.
+// slope[h] (t - p).  0 is the plain kernel.  kCapped forms the capped score as
+// cap (1 - 2 / (2^y + 1)), which is off by up to 2^-20 of the CAP: for caps up to
+// kDirectCap 2^-14 in the score, below the outputs' rounding.  Larger caps take
+// kBiased alone, slopes or not, whose scores a pass over the tile replaces first
+// (cap_inv > 0; in the kind with neither that branch costs 3%: 4 prompts of
+// 1900-2048 tokens 147.4 -> 151.6 us).
+constexpr float kDirectCap = 64.f;
 // kCut: of a batch whose items may be cut along the keys (a workspace is given).
 enum : int { kPlain = 0, kGrouped = 1, kCapped = 2, kBiased = 4, kCut = 8 };
 
@@ -1084,6 +1091,21 @@ __device__ __forceinline__ bool deal_units(const PrefillArgs& a, Deal* d, int ti
     return true;
 }
 
+// A large cap: this warp's rows of a score tile, raw products, become capped scores
+// in log2 units, by a tanh whose error goes with the score (one warp; out of line:
+// few calls take it).
+__device__ __noinline__ void cap_scores(uint32_t ts, float scale, float inv, float cap_log2) {
+#pragma unroll 1
+    for (int q = 0; q < kBN / 32; ++q) {
+        uint32_t r[32];
+        tmem_ld32(ts + (uint32_t)(q * 32), r);
+#pragma unroll
+        for (int e = 0; e < 32; ++e)
+            r[e] = __float_as_uint(cap_log2 * tanhf(__uint_as_float(r[e]) * scale * inv));
+        tmem_st32(ts + (uint32_t)(q * 32), r);
+    }
+}
+
 template <typename T, int D, bool FUSED, int KIND>
 __global__ void __launch_bounds__(threads_for(FUSED), 1)
     paged_prefill_tc(const __grid_constant__ CUtensorMap tm_q,
@@ -1585,9 +1607,10 @@ __global__ void __launch_bounds__(threads_for(FUSED), 1)
             const int qpos = idle ? -1 : pos0 + tok;   // causal limit of the row
             // first token the row's window leaves it
             const int first = KIND != kPlain && a.window > 0 ? qpos - a.window + 1 : 0;
-            const float slope = (KIND & kBiased) != 0 ? a.slopes[it.h * a.gb + row - tok * a.gb] *
-                                                               1.4426950408889634f
-                                                         : 0.f;
+            float slope = 0.f;                       // (log2 units; a large cap may have none)
+            if constexpr ((KIND & kBiased) != 0)
+                if (a.slopes)
+                    slope = a.slopes[it.h * a.gb + row - tok * a.gb] * 1.4426950408889634f;
             float m = -INFINITY, l = 0.f;
             for (int j = 0; j < nx; ++j, ++gx) {
                 // S_X(j) complete (and with it the previous O_X += P_X V)
@@ -1617,6 +1640,8 @@ __global__ void __launch_bounds__(threads_for(FUSED), 1)
                 // instruction cache every time): a rolled loop over the 32-key
                 // quarters, skipping those no row of the warp sees.
                 float mx = -INFINITY;
+                if constexpr ((KIND & (kCapped | kBiased)) == kBiased)
+                    if (a.cap_inv > 0.f) cap_scores(tS, a.cap_scale, a.cap_inv, a.cap_log2);
                 if (full) {
                     uint32_t rr[2][64];
                     tmem_ld64_nw(tS, rr[0]);

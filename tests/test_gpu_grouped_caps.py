@@ -85,3 +85,40 @@ def test_decode_cap_of_the_score_range_is_no_cap(pkv):
                                            1 / math.sqrt(128), softcap=cap)
         outs.append(out.float())
     assert torch.allclose(*outs, rtol=2.0 ** -10, atol=2.0 ** -16)
+
+
+@pytest.mark.parametrize("cap", CAPS)
+@pytest.mark.parametrize("H,HK,D,dtype,new,past,biased,window,scale", [
+    (4, 2, 64, "f16", [300, 1, 64], 333, False, 0, 0.125),
+    (3, 1, 128, "bf16", [200, 131], 90, True, 150, 0.09),
+    (8, 1, 128, "f16", [140], 500, True, 0, -0.3),
+    (5, 5, 64, "bf16", [260, 40], 0, False, 100, 0.125)])
+def test_prompts(pkv, cap, H, HK, D, dtype, new, past, biased, window, scale):
+    prompts(pkv, H, HK, D, dtype, new, past, biased, window, scale, cap)
+
+
+@pytest.mark.parametrize("cap", CAPS)
+@pytest.mark.parametrize("dtype,D,biased", [("f16", 128, False), ("bf16", 64, True)])
+def test_prompts_cut_along_the_keys(pkv, cap, dtype, D, biased):
+    assert pkv.prefill_grouped_workspace_size(1, 8, 2, D, 16, 300, 6) > 0
+    prompts(pkv, 8, 2, D, dtype, [6], 4700, biased, 0, 0.09, cap)
+
+
+def prompts(pkv, H, HK, D, dtype, new, past, biased, window, scale, cap):
+    """fp16 weights keep 11 bits here: 2^-11 of sum p |v| / sum p more (slack is at
+    least 2^-16 of that sum), and 2^-25 of the largest |v| a token at most."""
+    import torch
+    c = make_case(np.random.default_rng(H + D), H, HK, D, 16, new, [n + past for n in new], dtype,
+                  window, 4.0)
+    slopes = slopes_of(H, biased)
+    ref, slack = reference(c, scale, cap, slopes)
+    slack = slack * direct(cap)
+    if dtype == "f16":
+        slack = slack * (1 + 2.0 ** 5) + max(c["ctx"]) * 2.0 ** -25 * 6
+    d = on_device(c)
+    out = torch.empty_like(d["q"])
+    pkv.paged_attention_prefill_grouped(out, d["q"], d["kc"], d["vc"], d["bt"], d["cl"], d["qs"],
+                                        scale, max(new), softcap=cap, window=window,
+                                        slopes=tensor(slopes))
+    assert pkv.get_device_error() == 0
+    check(out, c, ref, slack, "cap %g" % cap)
