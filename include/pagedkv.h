@@ -238,7 +238,8 @@ pkv_status pkv_contiguous_attention_decode(void* out, const void* q, const void*
  *   z_t = z_t + slopes[h] * (t - p)              when slopes is not NULL
  *   out[s][h] = sum_t softmax_t(z) V_s[t][h / G],   lo <= t < n,
  * lo = max(0, n - window) when window > 0, else 0.  fp32 arithmetic (weights
- * keep at least 16 bits in the products with V), one rounding at the end.  Any cap
+ * keep at least 16 bits in the products with V; with fp16 storage those below 2^-20
+ * of the row's largest are held to 2^-36 of it), one rounding at the end.  Any cap
  * whose product with log2(e) is finite in fp32 will do: up to 64 the capped score
  * is off by at most 2^-20 of the cap, above it by a few 2^-24 of itself.
  * context_lens[s] == 0 gives a zero row.

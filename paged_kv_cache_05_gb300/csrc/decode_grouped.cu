@@ -30,10 +30,10 @@
 //   online softmax in log2 units, a row's statistics in the four lanes that
 //   hold it; P goes straight from S's registers to the operand of O += P V.
 //   P is split into a 16-bit high part and the 16-bit residual, so weights keep
-//   at least 16 bits.  With up to 8 heads, rows 8-15 of the product are free:
-//   the residual takes them, and O is the sum of row r and row r + 8 at the
-//   end, at no further product.  With 9 to 16 heads the residual is a second
-//   product.
+//   at least 16 bits (fp16: those above 2^-20 of the row's largest).  With up to 8
+//   heads, rows 8-15 of the product are free: the residual takes them, and O is the
+//   sum of row r and row r + 8 at the end, at no further product.  With 9 to 16
+//   heads the residual is a second product.
 // A warp ends with at most two partial rows (running max, sum, unnormalised
 // output), of a row that began before its range and one that goes on after it,
 // left in shared memory; the CTA joins those of the same row.  Rows that CTAs
@@ -68,7 +68,21 @@ constexpr int kStages = 2;                  // ring stages per warp
 constexpr int kStepTokens = 16;             // tokens a step at head_dim 128, twice that at 64
 constexpr int kMaxCtas = 512;
 constexpr int kMinSteps = 2;                // fewest steps of a CTA
-constexpr float kRaiseLog2 = 8.f;           // raise the running max only past this growth
+// Weights are formed as 2^(z - max + kLift), and the running max is raised only past
+// a growth of kRaise (log2).  fp16 has 2^-24 as its smallest step: without the lift
+// weights below 2^-25 of the largest would vanish from the product with V and stay in
+// the sum of weights, which tens of thousands of them beside a large one show (32768
+// of 2^-25.2: up to 0.6 of what they add to the output, 2^-11 of the values, was
+// lost).  Lifted by 2^11, at most 2^15 within a raise of 4 (the roundings below keep
+// that bound for scores of any size), they are held to 2^-36 of the row's largest.
+template <typename T>
+struct Weight {
+    static constexpr float kLift = 0.f, kRaise = 8.f;
+};
+template <>
+struct Weight<__half> {
+    static constexpr float kLift = 11.f, kRaise = 4.f;
+};
 // Largest cap whose scores are formed as cap (1 - 2 / (2^y + 1)), which is off by
 // up to 2^-20 of the CAP: up to here 2^-14 in the score, below the outputs'
 // rounding.  Above it tanhf, whose error goes with the score.
@@ -500,7 +514,7 @@ __device__ __forceinline__ void walk(const Args& a, const Batch& b, Cursor<Geo<D
             for (int i = 0; i < NH; ++i) {
                 mx[i] = fmaxf(mx[i], __shfl_xor_sync(kFull, mx[i], 1));
                 mx[i] = fmaxf(mx[i], __shfl_xor_sync(kFull, mx[i], 2));
-                const bool up = mx[i] > m[i] + kRaiseLog2 || m[i] == -INFINITY;
+                const bool up = mx[i] > __fadd_rd(m[i], Weight<T>::kRaise) || m[i] == -INFINITY;
                 alpha[i] = up ? ex2(m[i] - mx[i]) : 1.f;
                 if (up) m[i] = mx[i];
                 raised |= up;
@@ -516,7 +530,10 @@ __device__ __forceinline__ void walk(const Args& a, const Batch& b, Cursor<Geo<D
                     acc[i][3] *= alpha[NH - 1];
                 }
             }
-            each([&](float& y, int, int i) { y = ex2(y - m[i]); });
+            float top[NH];
+#pragma unroll
+            for (int i = 0; i < NH; ++i) top[i] = __fadd_ru(m[i], -Weight<T>::kLift);
+            each([&](float& y, int, int i) { y = ex2(y - top[i]); });
             if (edge)                       // (m is -infinity where every visible score is)
                 each([&](float& y, int t, int) {
                     if (t < cc.q.lo || t >= cc.q.n) y = 0.f;
