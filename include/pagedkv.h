@@ -402,7 +402,12 @@ pkv_status pkv_paged_attention_prefill_write(void* out, const void* q, const voi
  * of that item too (the rows share their products), and a visible token whose
  * score is not finite in fp32 may give NaN.  num_blocks * num_kv_heads *
  * block_size must stay below 2^31, max_blocks_per_seq * block_size at most 2^30.
- * Fifth-generation tensor cores, fp32 accumulation.
+ * Fifth-generation tensor cores, fp32 accumulation.  In the products with V,
+ * weights keep about 16 bits with bf16 storage; with fp16 they are rounded to 11
+ * bits, those below 2^-23 of the row's largest to 2^-34 of it.  (Calls that
+ * pkv_paged_attention_prefill could answer -- num_kv_heads == num_heads, no cap,
+ * slopes or window -- over at most 8192 tokens of capacity have its results, bit for
+ * bit where they are not cut: fp16 weights below 2^-14 of the largest to 2^-25.)
  * workspace: NULL, or device memory of pkv_prefill_grouped_workspace_size(...)
  * bytes (256-byte aligned, no initialisation; two calls in flight at once must
  * not share it).  With it, batches of few query rows over long contexts (chunks

@@ -195,6 +195,11 @@ pkv_status pkv_paged_attention_prefill_grouped(
     a.cap_scale = scale;
     a.cap_inv = large_cap ? (float)(1.0 / softcap) : 0.f;
     a.slopes = slopes;
+    const bool lifted =
+        a.G > 1 || window > 0 || max_blocks_per_seq * block_size > kPlainTokens;
+    a.lift = lifted ? kLift : 0.f;
+    a.rescale = lifted ? kLiftRescale : kRescaleLog2;
+    a.up = lifted ? kLiftUp : 0.f;
     a.gb = gb;
     a.tb = kBM / gb;
     a.head_units = num_heads / gb;

@@ -89,6 +89,18 @@ constexpr uint32_t kTmemCols = 512;
 // their bf16 residuals in 32 q + 16 .. + 31
 constexpr uint32_t kColO = 2 * kBN;
 constexpr float kRescaleLog2 = 8.f;  // raise the running max only past this growth
+// fp16 weights are rounded to 11 bits (a residual as bf16's would be half as many
+// products with V again, for an error that is half an output's rounding), and end at
+// 2^-24: below 2^-25 of the row's largest they would vanish from the product with V
+// and stay in the sum of weights, which tens of thousands of them beside a large one
+// show.  So the grouped kinds form them as 2^(z - max + kLift) and raise the max past
+// a growth of kLiftRescale: at most 2^13, held to 2^-34 of the row's largest.  The max
+// is raised to a little more than the largest score (kLiftUp of it), so that its
+// rounding, for scores of any size, takes no weight past fp16's range.
+constexpr float kLift = 9.f, kLiftRescale = 4.f, kLiftUp = 0x1p-22f;
+// What the plain kernel computes too, over at most so many tokens, is not lifted and
+// has that kernel's bits: what could vanish is 2^-12 of the largest value.
+constexpr int kPlainTokens = 8192;
 constexpr uint64_t kWaitLimitNs = 1000000000ull;
 constexpr uint32_t kWaitLimitIters = 1u << 26;
 
@@ -452,6 +464,8 @@ struct PrefillArgs {
     float cap_log2;              // cap * log2(e)
     float cap_scale, cap_inv;    // a large cap: scale and 1 / cap (else 0), and scale_log2 1
     const float* slopes;         // [H]; null: none
+    float lift, rescale, up;     // of fp16 weights without a cap or a bias: kLift,
+                                 // kLiftRescale and kLiftUp, or 0, kRescaleLog2 and 0
     // split items (null: none): what a workspace holds, see SplitHead
     struct SplitHead* split;
     struct SplitUnit* split_units;   // [kSplitParts]
@@ -1723,7 +1737,17 @@ __global__ void __launch_bounds__(threads_for(FUSED), 1)
                         if (mx > -INFINITY) mx = a.cap_log2 * (1.f - 2.f * rcp(ex2(mx) + 1.f));
                 }
                 float m_new = m;
-                if (mx > m + kRescaleLog2 || (m == -INFINITY && mx > -INFINITY)) m_new = mx;
+                constexpr bool kMayLift = KIND != kPlain && std::is_same<T, __half>::value;
+                constexpr bool kLifts = (KIND & (kCapped | kBiased)) != 0;   // always
+                if constexpr (kMayLift) {
+                    const float most = __fadd_rd(m, kLifts ? kLiftRescale : a.rescale);
+                    if (mx > most || (m == -INFINITY && mx > -INFINITY))
+                        m_new = fmaf(fabsf(mx), kLifts ? kLiftUp : a.up, mx);
+                } else {
+                    if (mx > m + kRescaleLog2 || (m == -INFINITY && mx > -INFINITY)) m_new = mx;
+                }
+                // weights are 2^(z - top)
+                const float top = kMayLift ? __fadd_ru(m_new, kLifts ? -kLift : -a.lift) : m_new;
                 const bool rescale = j > 0 && m_new != m;
                 const float alpha = rescale ? ex2(m - m_new) : 1.f;
                 // weights, packed in pairs over S, a quarter of 32 keys at a
@@ -1731,7 +1755,7 @@ __global__ void __launch_bounds__(threads_for(FUSED), 1)
                 // parts) and + 16 .. + 31 (bf16 residuals), which held that
                 // quarter's scores, read again here
                 uint64_t rs2 = f2(0.f, 0.f);
-                const uint64_t sc2 = f2(sl2, sl2), nm2 = f2(-m_new, -m_new);
+                const uint64_t sc2 = f2(sl2, sl2), nm2 = f2(-top, -top);
                 // The full-tile loop carries no mask code and is unrolled; the
                 // diagonal one compares each key with the row's last visible
                 // key, is rolled (small code, as for the max), and writes zero
@@ -1755,7 +1779,7 @@ __global__ void __launch_bounds__(threads_for(FUSED), 1)
                         // the bias at the quarter's first key, less the max where the score
                         // does not carry it
                         const float at_q = fmaf(slope, (float)(q * 32), at0) -
-                                           ((KIND & kCapped) != 0 ? 0.f : m_new);
+                                           ((KIND & kCapped) != 0 ? 0.f : top);
                         uint64_t bias2 = 0;
                         uint32_t pk[16];
                         [[maybe_unused]] uint32_t pr[kSplit ? 16 : 1];
@@ -1768,12 +1792,12 @@ __global__ void __launch_bounds__(threads_for(FUSED), 1)
                                               : f2(fmaf(slope, (float)e, at_q),
                                                    fmaf(slope, (float)(e + 1), at_q));
                             if constexpr ((KIND & kCapped) != 0) {
-                                // cap (1 - 2 / (2^y + 1)) [+ bias] - m, y = raw * sl2
+                                // cap (1 - 2 / (2^y + 1)) [+ bias] - top, y = raw * sl2
                                 f2_split(mul2(f2(__uint_as_float(r[e]), __uint_as_float(r[e + 1])),
                                               sc2), p0, p1);
                                 uint64_t x2 = fma2(f2(rcp(ex2(p0) + 1.f), rcp(ex2(p1) + 1.f)),
                                                    f2(-2.f * a.cap_log2, -2.f * a.cap_log2),
-                                                   f2(a.cap_log2 - m_new, a.cap_log2 - m_new));
+                                                   f2(a.cap_log2 - top, a.cap_log2 - top));
                                 if constexpr ((KIND & kBiased) != 0)
                                     x2 = add2(x2, bias2);
                                 f2_split(x2, p0, p1);

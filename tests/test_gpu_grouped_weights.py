@@ -81,3 +81,27 @@ def test_decode(pkv, S, H, HK, cap, dtype):
     assert pkv.get_device_error() == 0
     want, w = expected(v, n, cap)
     check(out, want, w, 2.0 ** -36 if dtype == torch.float16 else 2.0 ** -60, n)
+
+
+@pytest.mark.parametrize("dtype", ["float16", "bfloat16"])
+@pytest.mark.parametrize("cap,biased", [(0.0, False), (40.0, False), (0.0, True), (40.0, True)])
+@pytest.mark.parametrize("H,HK,D,cut", [(4, 1, 64, False), (2, 2, 128, False), (8, 2, 128, True)])
+def test_prompts(pkv, H, HK, D, cut, cap, biased, dtype):
+    import torch
+    dtype = getattr(torch, dtype)
+    n, m, B = 40000, 3, 64
+    kc, vc, table, v = pool(n, HK, D, B, dtype, 4)
+    q = torch.zeros((m, H, D), dtype=dtype, device="cuda")
+    q[:, :, 0] = 1.0
+    out = torch.empty_like(q)
+    size = pkv.prefill_grouped_workspace_size(1, H, HK, D, B, table.shape[1], m)
+    assert size > 0
+    space = torch.empty(size if cut else 0, dtype=torch.uint8, device="cuda")
+    t = lambda *a: torch.tensor(a, dtype=torch.int32, device="cuda")  # noqa: E731
+    pkv.paged_attention_prefill_grouped(
+        out, q, kc, vc, table.contiguous(), t(n), t(0, m), Z0 * math.log(2.0), m, softcap=cap,
+        slopes=torch.zeros(H, device="cuda") if biased else None, workspace=space)
+    assert pkv.get_device_error() == 0
+    for i in range(m):
+        want, w = expected(v, n - m + 1 + i, cap)
+        check(out[i:i + 1], want, w, 2.0 ** -34 if dtype == torch.float16 else 2.0 ** -60, n)
