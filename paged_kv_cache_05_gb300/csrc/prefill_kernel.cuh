@@ -545,6 +545,7 @@ struct Item {
     int n_kv;                        // key tiles loaded: the larger of n[0], n[1]
     int j0, lo;                      // the item's first key tile (its tiles count from it)
                                      // and first token seen: 0 without a window
+    int end;                         // past the last token that a row of the item sees
     int unit, part, parts;           // of a cut item: its place, which of how many parts
     int f;                           // the slot served first at each key tile
 };
@@ -642,6 +643,7 @@ __device__ __forceinline__ void item_tiles(const PrefillArgs& a, const SeqInfo& 
     }
     if constexpr ((KIND & kGrouped) != 0) {
         it.j0 = it.lo = 0;
+        it.end = si.ctx - si.qlen + min(end, it.q_begin + 2 * tokens);
         const int p0 = si.ctx - si.qlen + it.q_begin;
         if (a.window > 0 && p0 >= a.window) {
             it.lo = p0 - a.window + 1;
@@ -653,7 +655,7 @@ __device__ __forceinline__ void item_tiles(const PrefillArgs& a, const SeqInfo& 
     it.f = it.n[1] > it.n[0] ? 1 : 0;
 }
 
-// The item's first key tile and first token seen.
+// The item's first key tile, first token seen and the token past the last.
 template <int KIND>
 __device__ __forceinline__ int tile0(const Item& it) {
     if constexpr ((KIND & kGrouped) != 0) return it.j0;
@@ -663,6 +665,11 @@ template <int KIND>
 __device__ __forceinline__ int token0(const Item& it) {
     if constexpr ((KIND & kGrouped) != 0) return it.lo;
     else return 0;
+}
+template <int KIND>
+__device__ __forceinline__ int token_end(const Item& it) {
+    if constexpr ((KIND & kGrouped) != 0) return it.end;
+    else return it.ctx;
 }
 
 // The first row (of the sequence's new ones) of slot x.
@@ -1219,11 +1226,11 @@ __global__ void __launch_bounds__(threads_for(FUSED), 1)
                 const int32_t* row_tab = a.block_tables + (int64_t)it.s * a.max_blocks;
                 const int head = it.h / a.units_per_kv;
                 // the lane's block of key tile j (at most 16 a tile; blocks
-                // before the window are not looked up); false: none
+                // that no row sees are not looked up); false: none
                 int jb = 0;
                 auto block = [&](int j) -> bool {
                     const int tok0 = (tile0<KIND>(it) + j) * kBN;
-                    const int tok1 = min(tok0 + kBN, it.ctx);
+                    const int tok1 = min(tok0 + kBN, token_end<KIND>(it));
                     jb = max(tok0, token0<KIND>(it)) / a.B + lane;
                     return j < it.n_kv && jb <= (tok1 - 1) / a.B;
                 };
@@ -1611,7 +1618,7 @@ __global__ void __launch_bounds__(threads_for(FUSED), 1)
             const int nx = x ? it.n[1] : it.n[0];
             const int pos0 = x ? it.pos0[1] : it.pos0[0];
             const int rows = x ? it.rows[1] : it.rows[0];
-            // the group that zeroes V rows past the context (only the item's
+            // the group that zeroes V rows past the last one seen (only the item's
             // last key tile has any): the first slot served whose rows reach
             // that tile, since its P V is issued before the other's
             const bool f_last = (it.f ? it.n[1] : it.n[0]) == it.n_kv;
@@ -1848,16 +1855,17 @@ __global__ void __launch_bounds__(threads_for(FUSED), 1)
                         tmem_st32(tO + c * 32, o);
                     }
                 }
-                // V rows past the context (partial last block, blocks never
-                // loaded) are zeroed: their weights are 0, but 0 * NaN would not be
+                // V rows past the context (grouped kinds: past the last token that
+                // a row of the item sees; partial last block, blocks never loaded)
+                // are zeroed: their weights are 0, but 0 * NaN would not be
                 const int64_t gk = g + j;
-                if (zeroer && kb + kBN > it.ctx) {
+                if (zeroer && kb + kBN > token_end<KIND>(it)) {
                     const int st = (int)(gk % NST);
                     if (!mbar_wait(bar(kBarVFull + st), (uint32_t)((gk / NST) & 1), abort_flag)) {
                         ok = false;
                         break;
                     }
-                    const int z0 = it.ctx - kb > 0 ? it.ctx - kb : 0;
+                    const int z0 = token_end<KIND>(it) - kb > 0 ? token_end<KIND>(it) - kb : 0;
                     const int n16 = (kBN - z0) * 8;       // 16-byte chunks per slab
                     unsigned char* vs = gbase + C::V_OFF + st * C::KV_BYTES;
                     for (int i = gtid; i < n16 * C::SLABS; i += 128) {
