@@ -278,15 +278,18 @@ pkv_status prefill_grouped(Reader& r) {
               b = size(kc.size(2), "block_size"), width = size(tables.size(1), "max_blocks"),
               t = size(T, "num_query_tokens");
     const cudaStream_t stream = stream_of(r, c.dev);
-    // a workspace of the call's own, where one is of use: given back to the
-    // allocator when the call returns, for work queued after it on its stream
+    // a workspace of the call's own, where one is of use: taken from the allocator
+    // as its stream's memory (another stream's may have work pending on it) and
+    // given back when the call returns, for work queued after it on that stream
     at::Tensor own;
     size_t bytes = 0;
     if (!ws && pkv_prefill_grouped_workspace_size(s, h, hk, d, b, width, most, &bytes) == PKV_OK &&
         bytes > 0) {
+        const auto dev = (c10::DeviceIndex)c.dev;
+        c10::cuda::OptionalCUDAStreamGuard on;
+        if (stream != c10::cuda::getCurrentCUDAStream(dev).stream())
+            on.reset_stream(c10::cuda::getStreamFromExternal(stream, dev));
         own = at::empty({(int64_t)bytes}, q.options().dtype(at::kByte));
-        if (stream != c10::cuda::getCurrentCUDAStream((c10::DeviceIndex)c.dev).stream())
-            own.record_stream(c10::cuda::getStreamFromExternal(stream, (c10::DeviceIndex)c.dev));
         ws = &own;
     }
     void* wp = ws ? c.whole(*ws, "workspace", at::kByte) : nullptr;

@@ -180,6 +180,19 @@ def _dev(t, name, dtype=None, ndim=None):
     return t.data_ptr()
 
 
+def _own_workspace(num_bytes, device, stream):
+    """A workspace that a call on `stream` takes for itself.  The allocator hands out
+    memory that the current stream has given back with work still pending on it, so
+    it is taken, and given back, as memory of the stream that uses it."""
+    torch = _torch()
+    if stream is None:
+        return torch.empty(num_bytes, dtype=torch.uint8, device=device)
+    if not isinstance(stream, torch.cuda.Stream):
+        stream = torch.cuda.ExternalStream(stream.cuda_stream, device=device)
+    with torch.cuda.stream(stream):
+        return torch.empty(num_bytes, dtype=torch.uint8, device=device)
+
+
 def decode_workspace_size(num_seqs, num_heads, head_dim, block_size, max_blocks_per_seq,
                           partition_size=0) -> int:
     out = ctypes.c_size_t(0)
@@ -361,15 +374,13 @@ def paged_attention_decode_grouped(out, q, k_cache, v_cache, block_tables, conte
     of HK): q, out [S, H, D], caches [blocks, HK, B, D]; scores capped by
     softcap * tanh(z / softcap), limited to the last `window` tokens and biased
     by slopes[h] * (t - p), where given."""
-    torch = _torch()
     if workspace is None:
         S, H, D = q.shape
         HK, B = k_cache.shape[1:3]
         if block_tables.dim() != 2:
             raise ValueError("block_tables must be [num_seqs, max_blocks]")
-        workspace = alloc_grouped_workspace(S, H, HK, D, B, block_tables.shape[1], q.device)
-        if stream is not None:
-            workspace.record_stream(stream)
+        workspace = _own_workspace(
+            decode_grouped_workspace_size(S, H, HK, D, B, block_tables.shape[1]), q.device, stream)
     st = (_bind or _binding()).paged_attention_decode_grouped(
         out, q, k_cache, v_cache, block_tables, context_lens, scale, softcap, window, slopes,
         workspace, None if stream is None else stream.cuda_stream)
