@@ -225,8 +225,8 @@ def paged_attention_decode(out, q, k_cache, v_cache, block_tables, context_lens,
     if block_tables.dim() != 2 or block_tables.shape[0] != S:
         raise ValueError("block_tables must be [num_seqs, max_blocks]")
     if workspace is None:
-        workspace = alloc_workspace(S, H, D, B, block_tables.shape[1], partition_size,
-                                    q.device)
+        n = decode_workspace_size(S, H, D, B, block_tables.shape[1], partition_size)
+        workspace = _own_workspace(max(n, 256), q.device, stream)
     ptrs = [_dev(out, "out"), _dev(q, "q"), _dev(k_cache, "k_cache"), _dev(v_cache, "v_cache"),
             _dev(block_tables, "block_tables", torch.int32),
             _dev(context_lens, "context_lens", torch.int32, 1)]
@@ -259,8 +259,8 @@ def paged_attention_decode_append(out, q, k_new, v_new, k_cache, v_cache, block_
     if block_tables.dim() != 2 or block_tables.shape[0] != S:
         raise ValueError("block_tables must be [num_seqs, max_blocks]")
     if workspace is None:
-        workspace = alloc_workspace(S, H, D, B, block_tables.shape[1], partition_size,
-                                    q.device)
+        n = decode_workspace_size(S, H, D, B, block_tables.shape[1], partition_size)
+        workspace = _own_workspace(max(n, 256), q.device, stream)
     ptrs = [_dev(out, "out"), _dev(q, "q"), _dev(k_new, "k_new"), _dev(v_new, "v_new"),
             _dev(k_cache, "k_cache"), _dev(v_cache, "v_cache"),
             _dev(block_tables, "block_tables", torch.int32),
@@ -300,7 +300,7 @@ def paged_attention_decode_shared(out, q, k_cache, v_cache, block_tables, contex
         raise ValueError("block_tables must be [num_seqs, max_blocks]")
     if workspace is None:
         n = decode_shared_workspace_size(S, H, D, B, block_tables.shape[1], partition_size)
-        workspace = torch.empty(max(n, 256), dtype=torch.uint8, device=q.device)
+        workspace = _own_workspace(max(n, 256), q.device, stream)
     ptrs = [_dev(out, "out"), _dev(q, "q"), _dev(k_cache, "k_cache"), _dev(v_cache, "v_cache"),
             _dev(block_tables, "block_tables", torch.int32),
             _dev(context_lens, "context_lens", torch.int32, 1)]
@@ -338,7 +338,7 @@ def contiguous_attention_decode(out, q, k, v, context_lens, scale, partition_siz
     T = k.shape[2]
     if workspace is None:
         n = contiguous_workspace_size(S, H, D, T, partition_size)
-        workspace = torch.empty(max(n, 256), dtype=torch.uint8, device=q.device)
+        workspace = _own_workspace(max(n, 256), q.device, stream)
     _check("pkv_contiguous_attention_decode",
            lib().pkv_contiguous_attention_decode(
                _dev(out, "out"), _dev(q, "q"), _dev(k, "k"), _dev(v, "v"),

@@ -81,3 +81,34 @@ def test_grouped_decode(pkv):
     assert (kept == 0x5A).all()
     check(out, c, ref, slack)
     assert pkv.get_device_error() == 0
+
+
+@pytest.mark.parametrize("which", ["decode", "append", "shared", "contiguous"])
+def test_decode_calls(pkv, which):
+    """The calls for one K/V head per query head."""
+    import torch
+    H, D, B, n, S = 4, 128, 16, 4000, 2
+    c, d, ref, slack = batch(H, H, D, [1] * S, [n] * S)
+    mb = c["bt"].shape[1]
+    out = torch.empty_like(d["q"])
+    if which == "shared":
+        size = pkv.decode_shared_workspace_size(S, H, D, B, mb)
+        call = lambda s: pkv.paged_attention_decode_shared(  # noqa: E731
+            out, d["q"], d["kc"], d["vc"], d["bt"], d["cl"], 0.09, stream=s)
+    elif which == "contiguous":
+        k, v = (p[d["bt"][:, :n // B].long()].transpose(1, 2).reshape(S, H, n, D).contiguous()
+                for p in (d["kc"], d["vc"]))
+        size = pkv.contiguous_workspace_size(S, H, D, n)
+        call = lambda s: pkv.contiguous_attention_decode(  # noqa: E731
+            out, d["q"], k, v, d["cl"], 0.09, stream=s)
+    else:
+        size = pkv.decode_workspace_size(S, H, D, B, mb)
+        at = (d["bt"][:, (n - 1) // B].long(), slice(None), (n - 1) % B)
+        new = [d[p][at].contiguous() for p in ("kc", "vc")] if which == "append" else []
+        f = pkv.paged_attention_decode_append if new else pkv.paged_attention_decode
+        call = lambda s: f(out, d["q"], *new, d["kc"], d["vc"], d["bt"], d["cl"], 0.09,  # noqa: E731
+                           stream=s)
+    kept = pending(max(size, 256), call)
+    assert (kept == 0x5A).all()
+    check(out, c, ref, slack)
+    assert pkv.get_device_error() == 0
