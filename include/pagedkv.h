@@ -284,7 +284,8 @@ pkv_status pkv_paged_attention_decode_grouped(
  * runs out sets PKV_DEVERR_TIMEOUT; the CTA then stops issuing copies, its
  * other waits give up at once, its results for the call are not valid, and it
  * returns after every copy it issued has landed (those waits always keep the
- * 1 s bound, so no copy lands in a CTA that has ended).  The next call starts
+ * 1 s bound, so no copy lands in a CTA that has ended).  (In the _grouped form
+ * each other wait runs to its own limit.)  The next call starts
  * afresh.  A short limit exists to exercise that path (tests); 0 gives up on
  * the first check that finds a phase incomplete.  *previous (may be NULL)
  * receives the limit it replaces.  Host only; touches no GPU.
