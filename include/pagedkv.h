@@ -284,8 +284,8 @@ pkv_status pkv_paged_attention_decode_grouped(
  * runs out sets PKV_DEVERR_TIMEOUT; the CTA then stops issuing copies, its
  * other waits give up at once, its results for the call are not valid, and it
  * returns after every copy it issued has landed (those waits always keep the
- * 1 s bound, so no copy lands in a CTA that has ended).  (In the _grouped form
- * each other wait runs to its own limit.)  The next call starts
+ * 1 s bound, so no copy lands in a CTA that has ended).  (In the
+ * _grouped form each other wait runs to its own limit.)  The next call starts
  * afresh.  A short limit exists to exercise that path (tests); 0 gives up on
  * the first check that finds a phase incomplete.  *previous (may be NULL)
  * receives the limit it replaces.  Host only; touches no GPU.
@@ -352,7 +352,9 @@ pkv_status pkv_paged_attention_decode_noalloc(void* out, const void* q, const vo
  * tensors fit in memory).
  * Fifth-generation tensor cores (tcgen05, accumulators in tensor memory, TMA
  * tiled copies through the block table), fp32 accumulation, one launch, no
- * workspace.
+ * workspace.  In the products with V, weights keep about 16 bits with bf16 storage;
+ * with fp16 they are rounded to 11 bits, those below 2^-14 of the row's largest to
+ * 2^-25 of it (many thousands of such weights beside a large one are lost).
  */
 pkv_status pkv_paged_attention_prefill(void* out, const void* q, const void* k_cache,
                                        const void* v_cache, const int32_t* block_tables,
@@ -415,7 +417,10 @@ pkv_status pkv_paged_attention_prefill_write(void* out, const void* q, const voi
  * of few prompts, a few new tokens a sequence) are cut along the contexts so
  * that every SM has work, and joined by a second launch; the size is 0 where
  * the sizes rule that out, and the workspace is then not looked at.  Without it
- * they take one launch and the results are the same within rounding.  Either
+ * they take one launch and the results are the same within rounding.  The sizes
+ * are max_query_len and the table's width, not the lengths: a call that is not cut
+ * after all (short prompts in a table of 1024 tokens or more) takes some 5 us
+ * longer with a workspace than without.  Either
  * way results are bit-identical from call to call on one GPU.
  */
 pkv_status pkv_prefill_grouped_workspace_size(int num_seqs, int num_heads, int num_kv_heads,
@@ -453,8 +458,8 @@ pkv_status pkv_reshape_and_cache(const void* k, const void* v, void* k_cache, vo
  * For token t and head row x of its queries or keys, in fp32 and rounded once
  * at the end:
  *   x <- x / sqrt(mean(x^2) + eps) * weight     when that kind's weight is given
- *     (a bf16 row whose sum of squares passes the fp32 range, elements of about
- *     10^18, becomes 0 or NaN)
+ *     (a bf16 row whose sum of squares leaves the fp32 range, elements of about
+ *     10^18 or, with eps 0, of 10^-20, becomes 0, infinite or NaN)
  *   pair i of x turns by the angle positions[t] * f_i:
  *     (a, b) <- rope_scale * (a cos - b sin, b cos + a sin)
  * Pair i, i < rot_dim / 2, is (x[i], x[i + rot_dim / 2]) or, with interleaved
@@ -493,12 +498,15 @@ pkv_status pkv_norm_rope_and_cache(void* q_out, const void* q, const void* k, co
  * / 2], radians per position, and the factor to pass as rope_scale:
  *   PKV_ROPE_PLAIN     f_i = base^(-2i / rot_dim), factor 1
  *   PKV_ROPE_LINEAR    f_i / factor: positions squeezed into the trained length
+ *                      (position interpolation, Chen et al., 2023)
  *   PKV_ROPE_BASE      base replaced by base * factor^(rot_dim / (rot_dim - 2)):
  *                      the slowest pair is slowed by factor, the fastest kept
  *   PKV_ROPE_BY_PARTS  pairs that make more than beta_fast turns over
  *                      original_len positions kept, those that make fewer than
  *                      beta_slow slowed by factor, a linear ramp over the pairs
  *                      between; rope_scale = 0.1 ln(factor) + 1
+ *                      (YaRN, Peng et al., 2023, with its rounding of the ramp's
+ *                      ends to whole pairs)
  * (original_len and the betas are read for BY_PARTS only; factor >= 1 for all
  * but PLAIN).  pkv_rope_phases turns n frequencies into the fixed-point form
  * that pkv_norm_rope_and_cache reads (copy them to the device once).

@@ -43,8 +43,8 @@
 // Measured (GB300, us a call, both kernels, and the share of the measured 6.8
 // TB/s copy rate that the visible K and V come at): 8 sequences of 8192-32768
 // tokens, 32/8 heads x 128, bf16, 111 us, 0.93; 64 of 1-2048, 40/8 x 128, fp16,
-// capped, 49.6 us, 0.80; 33 of 17-8191, 16/1 x 64, bf16, window 1000, biased, 10.7 us; one
-// of 500, 6.9 us.  About 7 us of a call do not shrink with the bytes: the ranges'
+// capped, 50.0 us, 0.79; 33 of 17-8191, 16/1 x 64, bf16, window 1000, biased, 10.8 us; one
+// of 500, 7.0 us.  About 7 us of a call do not shrink with the bytes: the ranges'
 // start (lengths, tables, queries, the first copies, one behind the other) and
 // the second kernel.
 //

@@ -45,7 +45,9 @@ int64_t most_work(int S, int H, int gb, int max_query_len, int tiles) {
 // out not to be cut pays for the second launch and the estimate (about 5 us), so
 // work for half of the SMs or less asks for 8 tiles, for all of them 16 (4 prompts
 // of 2-194 over 3798, 40/8 heads x 64: 92 -> 63 us; 2 of 512 over 4000, which are
-// not cut: 91 -> 96).
+// not cut: 91 -> 96).  The capacity is the table's, so short prompts in a server's
+// wide table pay it too (one of 61 tokens, 32/8 x 128: 9.3 us in a table of under
+// 1024 tokens or without a workspace, 13.6 with one): their callers give none.
 bool may_split(int S, int H, int HK, int B, int max_blocks, int max_query_len, int window) {
     const int gb = heads_of_tile(H / HK, S, max_query_len);
     int64_t keys = (int64_t)max_blocks * B;
@@ -207,7 +209,7 @@ pkv_status pkv_paged_attention_prefill_grouped(
     a.per = a.head_units % 2 == 0 ? 2 : 1;
     // Items of one tile where every such item can have an SM of its own: the two of
     // an item would share one (one prompt, 32/8 heads x 128, bf16: of 61 tokens 9.85 ->
-    // 9.1 us, of 125 11.4 -> 9.8).
+    // 9.1 us, of 125 11.4 -> 9.8).  Not in the cut kind, whose bounds count items of two.
     int dev = 0;
     const cudaError_t de = cudaGetDevice(&dev);
     if (de != cudaSuccess) return pkv::cuda_fail(de, fn);

@@ -308,7 +308,10 @@ pkv_status pkv_rope_inv_freq(int rot_dim, double base, pkv_rope_scaling scaling,
                              "%s: scaling by parts needs original_len >= 1 and "
                              "0 < beta_slow < beta_fast",
                              fn);
-        // the (fractional) pair that makes `turns` turns over the original length
+        // YaRN (Peng, Quesnelle, Fan, Shippole, 2023): a ramp between the pairs that
+        // make beta_fast and beta_slow turns over the original length, its ends on
+        // whole pairs, never empty, and attention scaled by 0.1 ln(factor) + 1.
+        // The (fractional) pair that makes `turns` turns:
         auto pair_of = [&](double turns) {
             return rot_dim * std::log(original_len / (turns * 6.283185307179586)) /
                    (2.0 * std::log(base));
