@@ -57,7 +57,7 @@
 // reciprocal's worth of arithmetic, the bias a max over formed scores).
 // Measured (GB300, us a call and the share of the matrix unit's time): 4 prompts
 // of 1900-2048 tokens, 32/8 heads x 128, fp16, 148 us, 886 TFLOP/s, tensor pipe
-// 41% busy; 4 chunks of 301-1024 behind 5000 tokens, window 1024, capped, 16/4 x
+// 40% busy; 4 chunks of 301-1024 behind 5000 tokens, window 1024, capped, 16/4 x
 // 128, bf16, 53.8 us, 24%; 8 biased prompts of 100-1100, 24/6 x 64, fp16, 34.5
 // us, 11%; one prompt of 61 tokens 9.15 us (in a table of under 1024 tokens, or
 // without a workspace), of which the start-up and the chain of one tile are nearly
