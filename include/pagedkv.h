@@ -556,6 +556,122 @@ pkv_status pkv_swap_blocks(void* dst_k_cache, void* dst_v_cache, const void* src
                            int64_t dst_num_blocks, pkv_dtype dtype, cudaStream_t stream);
 
 /* ------------------------------------------------------------------------ */
+/* Latent attention                                                          */
+/* ------------------------------------------------------------------------ */
+
+/*
+ * Models with latent attention keep one row a token: a latent vector c of
+ * latent_dim elements, from which each head's key and value would be formed
+ * (k_h = U_h c, v_h = W_h c), and a rotated key part r of rope_dim elements that
+ * all heads share.  The score of query head h, of parts q_n and q_r, is
+ *   z = scale (q_n . U_h c + q_r . r)
+ * The expanded form computes k_h and v_h (prompts: few products a pair of tokens);
+ * the absorbed form takes the query into the latent space instead, q_n . U_h c =
+ * (U_h^T q_n) . c, attends the cached rows themselves and applies W_h to the
+ * result (new tokens over a long cache: no head's keys are formed or read).  The
+ * products with U and W are the caller's.
+ *   cache   [num_blocks][block_size][latent_dim + rope_dim], one pool
+ * latent_dim 256 or 512, rope_dim 64, fp16 or bf16 storage, block_size 8, 16, 32
+ * or 64; block tables, context lengths, slots and errors as above.
+ */
+
+/*
+ * The new tokens' way into a latent cache in one pass.  For token t, in fp32 and
+ * rounded once:
+ *   row = (norm(latent[t]), turn(k_rope[t]))   to slot slot_mapping[t] of the cache
+ *   q_out[t][h] = turn(q[t][h])                the rotary part of query head h
+ * norm is x / sqrt(mean(x^2) + eps) * weight when weight (fp32 [latent_dim],
+ * device) is given, else x; turn, phases (uint64 [rope_dim / 2]), interleaved,
+ * rope_scale, positions, slots (negative: not written; past the pool: skipped,
+ * PKV_DEVERR_BAD_SLOT, its queries are still written) and what a bf16 row of very
+ * large elements gives are those of pkv_norm_rope_and_cache.
+ * Strides are in elements, multiples of 8: row t of a tensor at t * stride, its head
+ * h h * head_stride further, so that slices of joint projections are taken as they
+ * are, and q_out may be the last rope_dim elements of absorbed queries
+ * [num_tokens][num_heads][latent_dim + rope_dim].  q_out may be q (same address and
+ * strides); otherwise the span of its rows shares no memory with the inputs, nor does
+ * the cache with any (PKV_ERR_INVALID).  All but positions, slots and phases 16-byte
+ * aligned.  One launch, no workspace; num_tokens == 0 launches nothing.
+ */
+pkv_status pkv_latent_norm_rope_and_cache(
+    void* q_out, int64_t q_out_stride, int64_t q_out_head_stride, const void* q, int64_t q_stride,
+    int64_t q_head_stride, const void* latent, int64_t latent_stride, const void* k_rope,
+    int64_t k_rope_stride, void* cache, const int64_t* slot_mapping, const int32_t* positions,
+    const uint64_t* phases, int interleaved, float rope_scale, const float* weight, float eps,
+    int num_tokens, int num_heads, int latent_dim, int rope_dim, int block_size,
+    int64_t num_blocks, pkv_dtype dtype, cudaStream_t stream);
+
+/*
+ * The cached rows of each sequence's first tokens, contiguous: row key_start[s] + t
+ * of rows [num_rows][latent_dim + rope_dim] is token t's, for t < key_start[s + 1] -
+ * key_start[s] (int32 [num_seqs + 1], device, not decreasing, key_start[num_seqs] <=
+ * num_rows; rows of no sequence are left as they are).  A chunk of a prompt forms
+ * the keys and values of the tokens before it from them.  A token past the table
+ * (PKV_DEVERR_BAD_CONTEXT) or in a block past the pool (PKV_DEVERR_BAD_BLOCK) is not
+ * copied.  A bit copy; one launch, no workspace.
+ */
+pkv_status pkv_gather_latent(void* rows, const void* cache, const int32_t* block_tables,
+                             const int32_t* key_start, int num_seqs, int latent_dim, int rope_dim,
+                             int block_size, int max_blocks_per_seq, int64_t num_blocks,
+                             int num_rows, pkv_dtype dtype, cudaStream_t stream);
+
+/*
+ * Prompts in the expanded form.  Sequence s has query rows query_start[s] ..
+ * query_start[s + 1] - 1 and keys key_start[s] .. key_start[s + 1] - 1, its new
+ * tokens' keys the last of them: row i attends keys t <= klen - qlen + i,
+ *   out[row][h] = sum_t softmax_t(scale (q[row][h][0 .. N) . k[t][h] +
+ *                                       q[row][h][N .. N + 64) . k_rope[t])) v[t][h]
+ *   q       [num_query_tokens][num_heads][N + 64]   N = head_dim, 64 or 128
+ *   k, v    [num_key_tokens][num_heads][N]
+ *   k_rope  [num_key_tokens][64]
+ *   out     [num_query_tokens][num_heads][N], contiguous
+ * Strides in elements, multiples of 8 (k and v may be halves of one up-projection's
+ * output, k_rope the ends of gathered rows); all tensors 16-byte aligned; out shares
+ * no memory with the others.  A sequence whose rows leave the tensors, with more
+ * than max_query_len rows or max_key_len keys, or with fewer keys than rows is
+ * skipped (PKV_DEVERR_BAD_CONTEXT).  Rows of no sequence are left as they are.
+ */
+pkv_status pkv_latent_attention_prefill(
+    void* out, const void* q, int64_t q_stride, int64_t q_head_stride, const void* k,
+    int64_t k_stride, int64_t k_head_stride, const void* k_rope, int64_t k_rope_stride,
+    const void* v, int64_t v_stride, int64_t v_head_stride, const int32_t* query_start,
+    const int32_t* key_start, float scale, int num_seqs, int num_heads, int head_dim, int rope_dim,
+    int max_query_len, int max_key_len, int num_query_tokens, int num_key_tokens, pkv_dtype dtype,
+    cudaStream_t stream);
+
+/*
+ * New tokens over the cache, in the absorbed form.  Sequence s holds
+ * context_lens[s] tokens, its qlen = query_start[s + 1] - query_start[s] new ones
+ * the last of them (already written); row query_start[s] + i attends, with the
+ * cached rows as keys and their latent parts as values,
+ *   out[row][h] = sum_t softmax_t(scale q[row][h] . row_t) row_t[0 .. latent_dim)
+ * without ancestors: the tokens t <= ctx - qlen + i (a chain);
+ * with ancestors (int64 [num_query_tokens], device, qlen <= 64): the tokens before
+ * the new ones, and new token j when bit j of ancestors[row] is set -- a tree of
+ * drafted tokens, whose rows carry the bits of their path and their own.  Bits from
+ * qlen on are ignored; a row that attends nothing is 0.
+ *   q    [num_query_tokens][num_heads][latent_dim + 64], out [..][..][latent_dim],
+ *        contiguous, 16-byte aligned
+ *   query_start  int32 [num_seqs + 1], device, or NULL: one row a sequence
+ *        (num_query_tokens == num_seqs)
+ * A sequence with ctx == 0 has rows of 0 (an empty place of a padded batch).  One
+ * with ctx < 0 or past the table, 0 < ctx < qlen, qlen past max_query_len or rows
+ * outside [0, num_query_tokens) is skipped (PKV_DEVERR_BAD_CONTEXT); a block past
+ * the pool is left out (PKV_DEVERR_BAD_BLOCK).  Rows of no sequence are left as they
+ * are.  num_blocks * block_size must stay below 2^31.
+ * workspace: device memory of pkv_latent_decode_workspace_size(...) bytes, 256-byte
+ * aligned, no initialisation; two calls in flight at once must not share it.
+ */
+pkv_status pkv_latent_decode_workspace_size(int num_seqs, int num_heads, int latent_dim,
+                                            int max_query_len, size_t* bytes);
+pkv_status pkv_latent_attention_decode(
+    void* out, const void* q, const void* cache, const int32_t* block_tables,
+    const int32_t* context_lens, const int32_t* query_start, const int64_t* ancestors, float scale,
+    int num_seqs, int num_heads, int latent_dim, int rope_dim, int block_size,
+    int max_blocks_per_seq, int64_t num_blocks, int max_query_len, int num_query_tokens,
+    pkv_dtype dtype, void* workspace, size_t workspace_bytes, cudaStream_t stream);
+
+/* ------------------------------------------------------------------------ */
 /* Errors                                                                    */
 /* ------------------------------------------------------------------------ */
 

@@ -2,7 +2,7 @@
 
 Each translation unit compiles in parallel; the objects are linked into
 ``paged_kv_cache_05_gb300/libpagedkv.so`` against the shared CUDA runtime.
-``_pkvbind.so`` beside it is the Python module of the grouped entry points
+``_pkvbind.so`` beside it is the Python module of the grouped and latent entry points
 (g++ against the installed torch's headers).
 Usage: ``python -m paged_kv_cache_05_gb300.build [--force] [--verbose]``.
 """
@@ -30,7 +30,8 @@ SOURCES = ["errors.cu", "cache_ops.cu", "decode_api.cu", "decode_f16.cu", "decod
            "decode_append_bf16.cu", "decode_noalloc.cu", "decode_grouped.cu", "prefill.cu",
            "prefill_grouped_f16.cu", "prefill_grouped_bf16.cu", "prefill_cut_f16.cu",
            "prefill_cut_bf16.cu", "prefill_grouped_api.cu",
-           "rope_cache.cu", "block_manager.cpp"]
+           "rope_cache.cu", "latent_cache.cu", "latent_decode.cu", "latent_prefill.cu",
+           "block_manager.cpp"]
 ARCH = ["-gencode", "arch=compute_103a,code=sm_103a"]
 
 

@@ -30,12 +30,14 @@
 #include <cuda_runtime.h>
 
 #include <cmath>
-#include <type_traits>
 
 #include "launch.cuh"
 #include "pkv_internal.h"
+#include "rows16.cuh"
 
 namespace {
+
+using namespace pkv::rows16;
 
 constexpr int kThreads = 128;
 constexpr int kWarps = kThreads / 32;
@@ -62,48 +64,6 @@ struct RopeArgs {
     int64_t num_slots;
     int32_t* err;
 };
-
-template <typename T>
-__device__ __forceinline__ float2 unpack2(uint32_t w) {
-    if constexpr (std::is_same<T, __half>::value)
-        return __half22float2(*reinterpret_cast<const __half2*>(&w));
-    else
-        return make_float2(__uint_as_float(w << 16), __uint_as_float(w & 0xffff0000u));
-}
-
-template <typename T>
-__device__ __forceinline__ uint32_t pack2(float lo, float hi) {
-    if constexpr (std::is_same<T, __half>::value) {
-        const __half2 h = __floats2half2_rn(lo, hi);
-        return *reinterpret_cast<const uint32_t*>(&h);
-    } else {
-        const __nv_bfloat162 h = __floats2bfloat162_rn(lo, hi);
-        return *reinterpret_cast<const uint32_t*>(&h);
-    }
-}
-
-// Pairs of fp32 values in one 64-bit register, and the packed operations that
-// work on both at once.
-__device__ __forceinline__ uint64_t two(float a, float b) {
-    uint64_t r;
-    asm("mov.b64 %0, {%1, %2};" : "=l"(r) : "f"(a), "f"(b));
-    return r;
-}
-__device__ __forceinline__ float2 split(uint64_t v) {
-    float2 r;
-    asm("mov.b64 {%0, %1}, %2;" : "=f"(r.x), "=f"(r.y) : "l"(v));
-    return r;
-}
-__device__ __forceinline__ uint64_t mul2(uint64_t a, uint64_t b) {
-    uint64_t d;
-    asm("mul.rn.f32x2 %0, %1, %2;" : "=l"(d) : "l"(a), "l"(b));
-    return d;
-}
-__device__ __forceinline__ uint64_t fma2(uint64_t a, uint64_t b, uint64_t c) {
-    uint64_t d;
-    asm("fma.rn.f32x2 %0, %1, %2, %3;" : "=l"(d) : "l"(a), "l"(b), "l"(c));
-    return d;
-}
 
 template <typename T, int D, bool INTERLEAVED>
 __global__ void __launch_bounds__(kThreads, kResident) norm_rope_and_cache_kernel(const RopeArgs p) {
@@ -271,14 +231,6 @@ cudaError_t launch(const RopeArgs& a, int D, bool interleaved, dim3 grid, cudaSt
                              : (interleaved ? (Kernel)norm_rope_and_cache_kernel<T, 128, true>
                                             : (Kernel)norm_rope_and_cache_kernel<T, 128, false>);
     return pkv::launch_pdl(k, grid, dim3(kThreads), stream, a);
-}
-
-bool aligned(const void* p, uintptr_t n) { return (reinterpret_cast<uintptr_t>(p) & (n - 1)) == 0; }
-
-// Bytes [a, a + an) and [b, b + bn) share a byte.
-bool overlap(const void* a, int64_t an, const void* b, int64_t bn) {
-    const uintptr_t x = reinterpret_cast<uintptr_t>(a), y = reinterpret_cast<uintptr_t>(b);
-    return x < y + (uintptr_t)bn && y < x + (uintptr_t)an;
 }
 
 }  // namespace

@@ -89,6 +89,16 @@ def lib():
             "pkv_rope_phases": ([P, i32, P], i32),
             "pkv_norm_rope_and_cache": ([P, P, P, P, i64, i64, i64, P, P, P, P, P, i32, i32, f32,
                                          P, P, f32, i32, i32, i32, i32, i32, i64, i32, P], i32),
+            "pkv_latent_norm_rope_and_cache": ([P, i64, i64, P, i64, i64, P, i64, P, i64, P, P, P,
+                                                P, i32, f32, P, f32, i32, i32, i32, i32, i32, i64,
+                                                i32, P], i32),
+            "pkv_gather_latent": ([P, P, P, P, i32, i32, i32, i32, i32, i64, i32, i32, P], i32),
+            "pkv_latent_attention_prefill": ([P, P, i64, i64, P, i64, i64, P, i64, P, i64, i64, P,
+                                              P, f32, i32, i32, i32, i32, i32, i32, i32, i32, i32,
+                                              P], i32),
+            "pkv_latent_decode_workspace_size": ([i32, i32, i32, i32, ctypes.POINTER(sz)], i32),
+            "pkv_latent_attention_decode": ([P, P, P, P, P, P, P, f32, i32, i32, i32, i32, i32, i32,
+                                             i64, i32, i32, i32, P, sz, P], i32),
             "pkv_copy_blocks": ([P, P, P, i32, i32, i32, i32, i64, i32, P], i32),
             "pkv_swap_blocks": ([P, P, P, P, P, i32, i32, i32, i32, i64, i64, i32, P], i32),
             "pkv_get_device_error": ([ctypes.POINTER(ctypes.c_int32), i32, P], i32),
@@ -554,7 +564,7 @@ _bind = None
 
 
 def _binding():
-    """The compiled binding of the grouped entry points (_pkvbind.so, built with
+    """The compiled binding of the grouped and latent entry points (_pkvbind.so, built with
     the library): their tensors are checked and described to the C ABI there,
     which costs a few tenths of a microsecond instead of eight."""
     global _bind
@@ -584,6 +594,79 @@ def norm_rope_and_cache(q_out, q, k, v, k_cache, v_cache, slot_mapping, position
     if st:
         _check("pkv_norm_rope_and_cache", st)
     return q_out
+
+
+def latent_norm_rope_and_cache(q_out, q, latent, k_rope, cache, slot_mapping, positions, phases,
+                               weight=None, eps=1e-6, rope_scale=1.0, interleaved=False,
+                               stream=None):
+    """The new tokens' way into a latent cache [blocks, B, R + 64] in one pass: the
+    latent rows [T, R], normed where a fp32 weight [R] is given, and the shared key
+    part k_rope [T, 64], turned, to their slots; the queries' rotary parts q
+    [T, H, 64], turned, to q_out (which may be q, or the ends of absorbed queries
+    [T, H, R + 64]).  All four may be slices.  phases: rope_phases() of 32
+    frequencies."""
+    st = (_bind or _binding()).latent_norm_rope_and_cache(
+        q_out, q, latent, k_rope, cache, slot_mapping, positions, phases, weight, eps, rope_scale,
+        interleaved, None if stream is None else stream.cuda_stream)
+    if st:
+        _check("pkv_latent_norm_rope_and_cache", st)
+    return q_out
+
+
+def gather_latent(rows, cache, block_tables, key_start, stream=None):
+    """Cached rows, contiguous: rows[key_start[s] + t] is token t of sequence s, for
+    the first key_start[s + 1] - key_start[s] tokens of each; rows [T, R + 64]."""
+    st = (_bind or _binding()).gather_latent(rows, cache, block_tables, key_start, 64,
+                                             None if stream is None else stream.cuda_stream)
+    if st:
+        _check("pkv_gather_latent", st)
+    return rows
+
+
+def latent_attention_prefill(out, q, k, k_rope, v, query_start, key_start, scale, max_query_len,
+                             max_key_len, stream=None):
+    """Causal attention of prompts in the expanded form: q [Tq, H, N + 64], per-head
+    keys and values k, v [Tk, H, N], the shared key part k_rope [Tk, 64] (all may be
+    slices), ragged by query_start and key_start [S + 1]; a sequence's rows are the
+    last of its keys.  out [Tq, H, N]."""
+    st = (_bind or _binding()).latent_attention_prefill(
+        out, q, k, k_rope, v, query_start, key_start, scale, max_query_len, max_key_len,
+        None if stream is None else stream.cuda_stream)
+    if st:
+        _check("pkv_latent_attention_prefill", st)
+    return out
+
+
+def latent_decode_workspace_size(num_seqs, num_heads, latent_dim, max_query_len=1) -> int:
+    """Bytes of workspace latent_attention_decode takes for these sizes."""
+    n = ctypes.c_size_t(0)
+    _check("pkv_latent_decode_workspace_size",
+           lib().pkv_latent_decode_workspace_size(int(num_seqs), int(num_heads), int(latent_dim),
+                                                  int(max_query_len), ctypes.byref(n)))
+    return n.value
+
+
+def alloc_latent_workspace(num_seqs, num_heads, latent_dim, max_query_len=1, device="cuda"):
+    """A workspace for latent_attention_decode, to be kept between calls."""
+    torch = _torch()
+    return torch.empty(latent_decode_workspace_size(num_seqs, num_heads, latent_dim, max_query_len),
+                       dtype=torch.uint8, device=device)
+
+
+def latent_attention_decode(out, q, cache, block_tables, context_lens, scale, query_start=None,
+                            max_query_len=1, ancestors=None, workspace=None, stream=None):
+    """New tokens over a latent cache [blocks, B, R + 64], in the absorbed form: q
+    [T, H, R + 64] attends the cached rows of its sequence, out [T, H, R] sums their
+    latent parts.  One row a sequence, or rows query_start[s] .. query_start[s + 1] of
+    each (at most max_query_len), which are its last tokens: a chain, or with ancestors
+    (int64 [T]) a tree of at most 64 drafted tokens, row i seeing those whose bits it
+    has set.  workspace: alloc_latent_workspace(), or memory of the call's own."""
+    st = (_bind or _binding()).latent_attention_decode(
+        out, q, cache, block_tables, context_lens, scale, query_start, max_query_len, ancestors,
+        workspace, None if stream is None else stream.cuda_stream)
+    if st:
+        _check("pkv_latent_attention_decode", st)
+    return out
 
 
 def copy_blocks(k_cache, v_cache, pairs, stream=None):
