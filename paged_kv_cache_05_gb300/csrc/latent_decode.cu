@@ -1,114 +1,857 @@
 // Attention of new tokens over a latent cache, in the absorbed form: the cache rows
-// are the keys of every head and their first R elements the values.
+// (W = R + 64 elements) are the keys of every head and their first R elements the
+// values.  Per (token, head) row, over the tokens t it sees:
+//   z_t = scale q . row_t,   out = sum_t 2^(z_t - m) row_t[0 .. R) / sum_t 2^(z_t - m)
+// in log2 units, with the running max and sum of the softmax (one pass over the cache).
 //
-// A first version: a block a (token, head) row, a warp a token at a time, the running
-// maximum and sum of the softmax per warp, the warps joined at the end.
+// Every head of a token attends the same rows, so a tile is 128 (token, head) rows of
+// one sequence, 128 cached tokens a step, and both products are matrix products:
+// 2 x 128 x 128 x (W + R) operations on 128 x 2 W bytes, at 128 heads 242 a byte, near
+// the 284 at which the tensor cores and the memory take the same time.  An output of
+// 128 x 512 in fp32 is all of an SM's tensor memory, and 128 query rows and a tile of
+// tokens exceed its shared memory, so a tile is a pair of CTAs' (cluster of two, one
+// product by both, cta_group::2):
+//   S = Q K^T      each CTA holds 64 query rows (A) and 64 of the tile's tokens (half
+//                  of B's columns), and gets 64 x 128 scores in 64 columns: lanes 0-63
+//                  its rows against tokens 0-63, lanes 64-127 against tokens 64-127
+//   O += P V       each CTA holds its rows' weights P (A) and half of the values' R
+//                  elements of all 128 tokens (half of B's columns)
+// A token's row thus comes to each CTA of the pair in part as a key and in part as a
+// value, 17/9 of its bytes in all: the copies' rate into the SMs (10-11 TB/s of boxes
+// of 8 rows, measured) bounds long contexts at 5.8 TB/s of the cache.
+//
+// Eight warps a CTA:
+//   warp 0      queries and keys: boxes of 8 rows x KC chunks of 64 elements, one lane
+//               a box, rings of KS slots of KC chunks of the tile's 64 tokens, freed
+//               chunk by chunk as S is formed
+//   warp 6      values: boxes of 8 rows x R / 128 chunks, rings of VS slots of 32 tokens
+//   warp 1      (of the first CTA) issues the products from one thread
+//   warps 2-5   softmax: a thread a row and half of the tile's tokens; the two halves
+//               of a row meet in shared memory.  The max is raised only past a growth of
+//               kRescale, so that most steps leave O alone.
+// S is double-buffered: S of step j + 1 is formed while the softmax of step j runs.
+//
+// The steps of all (sequence, row tile)s are dealt to the pairs in equal runs.  A run
+// that holds all steps of one writes its output rows; parts of one are left in the
+// workspace (fp32 output, max and sum), and a second kernel joins them.
+#include <cuda.h>
 #include <cuda_bf16.h>
 #include <cuda_fp16.h>
 #include <cuda_runtime.h>
 
 #include <cmath>
 
-#include "launch.cuh"
 #include "pkv_internal.h"
 #include "rows16.cuh"
+#include "tc_ptx.cuh"
+#include "tensor_map.h"
 
 namespace {
 
-using namespace pkv::rows16;
+using namespace pkv::tc;
+using pkv::rows16::aligned;
+using pkv::rows16::overlap;
+using pkv::rows16::pack2;
 
 constexpr int kP = 64;
+constexpr int kRows = 128;            // rows of a pair's tile
+constexpr int kTok = 128;             // tokens of a step
+constexpr int kThreads = 256;
+constexpr int kMaxPairs = 96;
+constexpr uint32_t kColO = 128;       // tensor memory: S at 0 and 64, O from here
+
+template <int R>
+struct Cfg {
+    static constexpr int W = R + kP;
+    static constexpr int CH = W / 64;                 // chunks of a row
+    static constexpr int VCH = R / 128;               // chunks of a CTA's half of the values
+    static constexpr int KC = R == 512 ? 3 : 5;       // chunks of a key slot
+    static constexpr int KSUB = CH / KC;              // slots of a step
+    static constexpr int KS = R == 512 ? 3 : 2;
+    static constexpr int VS = R == 512 ? 4 : 8;
+    static constexpr int K_SLOT = KC * 8192;
+    static constexpr int V_GROUP = VCH * 1024;        // 8 tokens
+    static constexpr int V_SLOT = 4 * V_GROUP;
+    static constexpr int Q_BYTES = CH * 8192;
+    static constexpr int Q_OFF = 0;
+    static constexpr int K_OFF = Q_OFF + Q_BYTES;
+    static constexpr int V_OFF = K_OFF + KS * K_SLOT;
+    static constexpr int P_OFF = V_OFF + VS * V_SLOT;
+    static constexpr int SMEM = P_OFF + 16384 + 1024; // 1 KiB of alignment slack
+    static_assert(SMEM + 2048 <= 232448, "shared memory");
+    static_assert(KSUB * KC == CH, "chunks");
+};
+
+enum : int {
+    kKFull = 0,      // + slot (up to 3): both CTAs' keys are there (first CTA's barrier)
+    kKEmpty = 3,     // + slot
+    kVFull = 6,      // + slot (up to 8)
+    kVEmpty = 14,    // + slot
+    kSFull = 22,     // + buffer
+    kPFull = 24,     // weights written by all softmax warps (first CTA's)
+    kPvDone = 25,    // O += P V of a step completed
+    kQFull = 26,
+    kQEmpty = 27,    // a segment's last S formed
+    kORead = 28,     // a segment's output read from tensor memory (first CTA's)
+    kSpare = 29,
+    kBars = 30
+};
 
 struct Args {
     uint16_t* out;
-    const uint16_t *q, *cache;
+    const uint16_t* cache;
     const int32_t *tables, *ctx, *q_start;
     const int64_t* ancestors;
     float scale_log2;
     int S, H, B, max_blocks, max_qlen, T;
     int64_t num_blocks;
+    int pairs, slot_rows;             // rows of a part in the workspace
+    int out_v8;                       // out is 32-byte aligned: 32-byte stores
+    struct Rec* rec;                  // [pairs]
+    float2* ml;                       // [2 pairs][slot_rows]
+    float* acc;                       // [2 pairs][slot_rows][R]
     int32_t* err;
 };
 
+// What is left to join: rows of the output whose parts lie in `parts` slots: `slot`,
+// then the first of each following pair.
+struct Rec {
+    int row0, rows, slot, parts;
+};
+
+struct Seq {
+    int q0, qlen, ctx;
+    int nt, nr;                       // steps of a row tile, row tiles (0: nothing to do)
+    __device__ __forceinline__ bool load(const Args& a, int s) {
+        q0 = a.q_start ? a.q_start[s] : s;
+        qlen = a.q_start ? a.q_start[s + 1] - q0 : 1;
+        ctx = a.ctx[s];
+        nt = nr = 0;
+        if (ctx < 0 || (int64_t)ctx > (int64_t)a.max_blocks * a.B || qlen < 0 ||
+            qlen > a.max_qlen || q0 < 0 || (int64_t)q0 + qlen > a.T || (ctx > 0 && qlen > ctx))
+            return false;
+        if (qlen > 0 && ctx > 0) {
+            nt = (ctx + kTok - 1) / kTok;
+            nr = (int)(((int64_t)qlen * a.H + kRows - 1) / kRows);
+        }
+        return true;
+    }
+    __device__ __forceinline__ int64_t steps() const { return (int64_t)nt * nr; }
+};
+
+// Where a pair's run begins.
+struct Start {
+    int s;
+    int64_t off, n;                   // steps before it in the sequence, steps of the run
+};
+
+// A run of steps of one row tile.
+struct Seg {
+    int s, q0, qlen, ctx;
+    int row;                          // first row of the tile among the sequence's
+    int rows;                         // live rows of the tile
+    int j0, j1;                       // steps
+    bool whole;
+    int slot;                         // of a part: 0 the run's first, 1 another
+};
+
+struct Walker {
+    Seq q, next;
+    int s;
+    int64_t off, left;
+    bool first;
+    __device__ __forceinline__ void init(const Args& a, const Start& st) {
+        s = st.s;
+        off = st.off;
+        left = st.n;
+        first = true;
+        if (left > 0) {
+            q.load(a, s);
+            if (s + 1 < a.S) next.load(a, s + 1);
+        }
+    }
+    __device__ __forceinline__ bool get(const Args& a, Seg& g) {
+        if (left <= 0) return false;
+        while (off >= q.steps()) {
+            if (++s >= a.S) return false;
+            off = 0;
+            q = next;
+            if (s + 1 < a.S) next.load(a, s + 1);
+        }
+        const int rt = (int)(off / q.nt);
+        g.s = s;
+        g.q0 = q.q0;
+        g.qlen = q.qlen;
+        g.ctx = q.ctx;
+        g.row = rt * kRows;
+        g.rows = min(kRows, q.qlen * a.H - g.row);
+        g.j0 = (int)(off - (int64_t)rt * q.nt);
+        g.j1 = (int)min((int64_t)q.nt, g.j0 + left);
+        g.whole = g.j0 == 0 && g.j1 == q.nt;
+        g.slot = first ? 0 : 1;
+        first = false;
+        off += g.j1 - g.j0;
+        left -= g.j1 - g.j0;
+        return true;
+    }
+};
+
+// The block of a sequence's token and the cache row of it, or -1.
+__device__ __forceinline__ int cache_row(const Args& a, const Seg& g, int t) {
+    if (t >= g.ctx) return -1;
+    const int b = t / a.B;
+    const int id = a.tables[(int64_t)g.s * a.max_blocks + b];
+    if (id < 0 || id >= a.num_blocks) return -1;
+    return id * a.B + (t - b * a.B);
+}
+
 template <typename T, int R>
-__global__ void __launch_bounds__(128) latent_decode_simple(const Args a) {
-    pkv::pdl_wait_then_release();
-    constexpr int W = R + kP, E = W / 64;   // pairs of elements a lane
-    __shared__ float s_m[4], s_l[4], s_o[4][R];
-    const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
-    const int s = blockIdx.z, i = blockIdx.y, h = blockIdx.x;
-    const int q0 = a.q_start ? a.q_start[s] : s;
-    const int qlen = a.q_start ? a.q_start[s + 1] - q0 : 1, ctx = a.ctx[s];
-    const bool bad = ctx < 0 || (int64_t)ctx > (int64_t)a.max_blocks * a.B || qlen < 0 ||
-                     qlen > a.max_qlen || q0 < 0 || (int64_t)q0 + qlen > a.T ||
-                     (ctx > 0 && qlen > ctx);
-    if (bad) {
-        if (threadIdx.x == 0 && i == 0 && h == 0) atomicOr(a.err, PKV_DEVERR_BAD_CONTEXT);
-        return;
-    }
-    if (i >= qlen) return;
-    const int64_t row = (int64_t)(q0 + i) * a.H + h;
-    const uint32_t* q = reinterpret_cast<const uint32_t*>(a.q + row * W);
-    float2 qv[E], o[E];
-#pragma unroll
-    for (int e = 0; e < E; ++e) {
-        qv[e] = unpack2<T>(q[32 * e + lane]);
-        o[e] = make_float2(0.f, 0.f);
-    }
-    float m = -INFINITY, l = 0.f;
-    const int base = ctx - qlen;
-    const uint64_t seen = a.ancestors ? (uint64_t)a.ancestors[q0 + i] : ~0ull;
-    for (int t = warp; t < ctx; t += 4) {
-        const int j = t - base;
-        if (j >= 0 && (a.ancestors ? !(seen >> j & 1) : j > i)) continue;
-        const int blk = a.tables[(int64_t)s * a.max_blocks + t / a.B];
-        if (blk < 0 || blk >= a.num_blocks) {
-            if (lane == 0) atomicOr(a.err, PKV_DEVERR_BAD_BLOCK);
-            continue;
+__global__ void __launch_bounds__(kThreads, 1)
+    latent_decode_pair(const __grid_constant__ CUtensorMap tm_q,
+                       const __grid_constant__ CUtensorMap tm_k,
+                       const __grid_constant__ CUtensorMap tm_v, const Args a) {
+    using C = Cfg<R>;
+    extern __shared__ __align__(1024) uint8_t smem_raw[];
+    __shared__ __align__(8) uint64_t bars[kBars];
+    __shared__ uint32_t s_tmem;
+    __shared__ int s_abort;
+    __shared__ Start s_start;
+    __shared__ int64_t s_scan[8];
+    __shared__ int64_t s_total;                  // steps of all
+    __shared__ float s_x[2][2][64];              // a row's maxima (or sums) by halves
+
+    const int tid = threadIdx.x, warp = tid >> 5, lane = tid & 31;
+    const uint32_t rank = cluster_rank();
+    const int pair = (int)(blockIdx.x >> 1);
+    volatile int* const abort_flag = &s_abort;
+    const uint32_t base = (smem_u32(smem_raw) + 1023) & ~1023u;
+    const uint32_t sQ = base + C::Q_OFF, sK = base + C::K_OFF, sV = base + C::V_OFF,
+                   sP = base + C::P_OFF;
+    auto bar = [&](int i) { return smem_u32(&bars[i]); };
+
+    if (warp == 1) {
+        if (lane == 0) {
+            for (int i = 0; i < kBars; ++i) {
+                const bool two = i < kKEmpty || (i >= kVFull && i < kVEmpty) || i == kQFull;
+                mbar_init(bar(i), two ? 2 : i == kPFull || i == kORead ? 8 : 1);
+            }
+            mbar_init_fence();
+            s_abort = 0;
         }
-        const uint32_t* k = reinterpret_cast<const uint32_t*>(
-            a.cache + ((int64_t)blk * a.B + t % a.B) * W);
-        float2 kv[E];
-        float z = 0.f;
-#pragma unroll
-        for (int e = 0; e < E; ++e) {
-            kv[e] = unpack2<T>(k[32 * e + lane]);
-            z = fmaf(qv[e].x, kv[e].x, fmaf(qv[e].y, kv[e].y, z));
+        __syncwarp();
+        alloc_pair(smem_u32(&s_tmem));
+    } else if (warp == 0 && lane == 0) {
+        prefetch_map(&tm_q);
+        prefetch_map(&tm_k);
+        prefetch_map(&tm_v);
+    }
+    asm volatile("griddepcontrol.wait;" ::: "memory");
+    asm volatile("griddepcontrol.launch_dependents;" ::: "memory");
+
+    // the pair's run of the steps: [b, e) of all
+    {
+        int64_t mine = 0;
+        for (int s = tid; s < a.S; s += kThreads) {
+            Seq q;
+            if (!q.load(a, s) && blockIdx.x == 0) atomicOr(a.err, PKV_DEVERR_BAD_CONTEXT);
+            mine += q.steps();
         }
 #pragma unroll
-        for (int x = 16; x > 0; x >>= 1) z += __shfl_xor_sync(0xffffffffu, z, x);
-        z *= a.scale_log2;
-        const float mn = fmaxf(m, z), c = exp2f(m - mn), p = exp2f(z - mn);
-        m = mn;
-        l = l * c + p;
+        for (int o = 16; o > 0; o >>= 1) mine += __shfl_xor_sync(0xffffffffu, mine, o);
+        if (lane == 0) s_scan[warp] = mine;
+        __syncthreads();
+        int64_t total = 0;
+        for (int w = 0; w < 8; ++w) total += s_scan[w];
+        const int64_t np = min((int64_t)a.pairs, total);
+        const int64_t b = pair < np ? total * pair / np : 0;
+        const int64_t e = pair < np ? total * (pair + 1) / np : 0;
+        if (tid == 0) {
+            s_start.s = 0;
+            s_start.off = 0;
+            s_start.n = e - b;
+            s_total = total;
+        }
+        int64_t before = 0;
+        for (int s0 = 0; s0 < a.S && e > b; s0 += kThreads) {
+            const int s = s0 + tid;
+            Seq q;
+            q.nt = q.nr = 0;
+            if (s < a.S) q.load(a, s);
+            const int64_t n = q.steps();
+            int64_t incl = n;
 #pragma unroll
-        for (int e = 0; e < E; ++e)
-            o[e] = make_float2(fmaf(o[e].x, c, p * kv[e].x), fmaf(o[e].y, c, p * kv[e].y));
+            for (int o = 1; o < 32; o <<= 1) {
+                const int64_t y = __shfl_up_sync(0xffffffffu, incl, o);
+                if (lane >= o) incl += y;
+            }
+            __syncthreads();
+            if (lane == 31) s_scan[warp] = incl;
+            __syncthreads();
+            incl += before;
+            for (int w = 0; w < 8; ++w) {
+                if (w < warp) incl += s_scan[w];
+                before += s_scan[w];
+            }
+            if (n > 0 && incl > b && incl - n <= b) {
+                s_start.s = s;
+                s_start.off = b - (incl - n);
+            }
+            if (before > b) break;
+        }
+        // (nothing to join, until a part is left)
+        if (tid == 0 && rank == 0) a.rec[pair] = Rec{0, 0, 0, 0};
     }
-    if (lane == 0) {
-        s_m[warp] = m;
-        s_l[warp] = l;
-    }
-#pragma unroll
-    for (int e = 0; e < R / 64; ++e) {
-        s_o[warp][2 * (32 * e + lane)] = o[e].x;
-        s_o[warp][2 * (32 * e + lane) + 1] = o[e].y;
-    }
+    fence_before();
     __syncthreads();
-    float M = -INFINITY, L = 0.f;
-    for (int x = 0; x < 4; ++x) M = fmaxf(M, s_m[x]);
-    for (int x = 0; x < 4; ++x) L += M == -INFINITY ? 0.f : s_l[x] * exp2f(s_m[x] - M);
-    uint32_t* out = reinterpret_cast<uint32_t*>(a.out + row * R);
-    for (int d = threadIdx.x; d < R / 2; d += 128) {
-        float x = 0.f, y = 0.f;
-        for (int w = 0; w < 4; ++w) {
-            const float f = s_m[w] == -INFINITY ? 0.f : exp2f(s_m[w] - M);
-            x = fmaf(f, s_o[w][2 * d], x);
-            y = fmaf(f, s_o[w][2 * d + 1], y);
+    cluster_sync();
+    fence_after();
+    const uint32_t tmem = s_tmem;
+    const Start start = s_start;
+    bool ok = true;
+    auto fail = [&]() {
+        if (!*abort_flag) atomicOr(a.err, PKV_DEVERR_TIMEOUT);
+        *abort_flag = 1;
+    };
+
+    if (warp == 0) {
+        // ================================================= queries and keys
+        Walker wk;
+        wk.init(a, start);
+        Seg g;
+        int kc = 0, segs = 0;
+        const uint32_t qfull = at_rank(bar(kQFull), 0);
+        const int none = (int)min(a.num_blocks * a.B, (int64_t)0x7fffffff);   // past the pool: zeros
+        while (ok && wk.get(a, g)) {
+            auto row_of = [&](int j) {
+                return lane < 8 ? cache_row(a, g, j * kTok + 64 * (int)rank + 8 * lane) : -1;
+            };
+            int y = row_of(g.j0);
+            if (segs > 0 && !warp_wait(bar(kQEmpty), (uint32_t)((segs - 1) & 1), abort_flag)) {
+                ok = false;
+                break;
+            }
+            const bool live = g.rows > 64 * (int)rank;
+            if (lane == 0) mbar_expect_tx_cluster(qfull, live ? C::Q_BYTES : 0);
+            __syncwarp();
+            if (live && lane < C::CH)
+                tma_2d_pair(sQ + lane * 8192, &tm_q, lane * 64,
+                            g.q0 * a.H + g.row + 64 * (int)rank, qfull);
+            for (int j = g.j0; j < g.j1; ++j) {
+                const int yn = j + 1 < g.j1 ? row_of(j + 1) : -1;
+                for (int u = 0; u < C::KSUB; ++u, ++kc) {
+                    const int st = kc % C::KS, n = kc / C::KS;
+                    if (n > 0 && !warp_wait(bar(kKEmpty + st), (uint32_t)((n - 1) & 1), abort_flag)) {
+                        ok = false;
+                        break;
+                    }
+                    const uint32_t full = at_rank(bar(kKFull + st), 0);
+                    if (lane == 0) mbar_expect_tx_cluster(full, C::K_SLOT);
+                    __syncwarp();
+                    if (lane < 8)
+                        tma_3d_pair(sK + st * C::K_SLOT + lane * C::KC * 1024, &tm_k, 0,
+                                    y < 0 ? none : y, u * C::KC, full);
+                }
+                if (!ok) break;
+                y = yn;
+            }
+            ++segs;
         }
-        const float inv = L > 0.f ? 1.f / L : 0.f;
-        out[d] = pack2<T>(x * inv, y * inv);
+        if (!ok) fail();
+    } else if (warp == 6) {
+        // ================================================= values
+        Walker wk;
+        wk.init(a, start);
+        Seg g;
+        int vc = 0;
+        const int none = (int)min(a.num_blocks * a.B, (int64_t)0x7fffffff);
+        while (ok && wk.get(a, g)) {
+            auto row_of = [&](int j) {
+                return lane < 16 ? cache_row(a, g, j * kTok + 8 * lane) : -1;
+            };
+            int y = row_of(g.j0);
+            for (int j = g.j0; j < g.j1; ++j) {
+                const int yn = j + 1 < g.j1 ? row_of(j + 1) : -1;
+                const int left = g.ctx - j * kTok;           // tokens of the step and after
+                const int subs = left >= kTok ? 4 : (left + 31) / 32;
+                // a block past the pool is left out
+                if (lane < 16 && y < 0 && 8 * lane < left && rank == 0)
+                    atomicOr(a.err, PKV_DEVERR_BAD_BLOCK);
+                // the group that holds the last token and places behind it, whose
+                // values may be anything: copied by the warp, zeros behind the last
+                const int tail = left < kTok && (left & 7) ? left >> 3 : -1;
+                for (int v = 0; v < subs; ++v, ++vc) {
+                    const int st = vc % C::VS, n = vc / C::VS;
+                    if (n > 0 && !warp_wait(bar(kVEmpty + st), (uint32_t)((n - 1) & 1), abort_flag)) {
+                        ok = false;
+                        break;
+                    }
+                    const uint32_t full = at_rank(bar(kVFull + st), 0);
+                    const uint32_t slot = sV + st * C::V_SLOT;
+                    const bool has_tail = (tail >> 2) == v;
+                    if (has_tail) {
+                        const int yt = __shfl_sync(0xffffffffu, y, tail & 15);
+                        const uint32_t to = slot + (tail & 3) * C::V_GROUP;
+                        for (int i = lane; i < C::VCH * 64; i += 32) {
+                            const int r = i / (C::VCH * 8), c = i - r * (C::VCH * 8);
+                            uint4 w = make_uint4(0u, 0u, 0u, 0u);
+                            if (yt >= 0 && r < (left & 7))
+                                w = *reinterpret_cast<const uint4*>(
+                                    a.cache + (int64_t)(yt + r) * C::W + (int)rank * (R / 2) + c * 8);
+                            st_shared_v4(to + (c >> 3) * 1024 + r * 128 + (((c & 7) ^ r) << 4), w.x,
+                                         w.y, w.z, w.w);
+                        }
+                        fence_async_smem();
+                        __syncwarp();
+                    }
+                    if (lane == 0)
+                        mbar_expect_tx_cluster(full, has_tail ? 3 * C::V_GROUP : C::V_SLOT);
+                    __syncwarp();
+                    if ((lane >> 2) == v && lane != tail)
+                        tma_3d_pair(slot + (lane & 3) * C::V_GROUP, &tm_v, 0, y < 0 ? none : y,
+                                    (int)rank * C::VCH, full);
+                }
+                if (!ok) break;
+                y = yn;
+            }
+        }
+        if (!ok) fail();
+    } else if (warp == 1) {
+        // ================================================= products
+        if (rank == 0 && lane == 0) {
+            constexpr uint32_t ID_S = idesc(El<T>::kType, false, kTok, kRows);
+            constexpr uint32_t ID_PV = idesc(El<T>::kType, true, 256, kRows);
+            const uint64_t dQ = sdesc(sQ, 16, 1024), dK = sdesc(sK, 16, C::KC * 1024),
+                           dV = sdesc(sV, 1024, C::V_GROUP), dP = sdesc(sP, 16, 1024);
+            Walker wk;
+            wk.init(a, start);
+            Seg g;
+            int kc = 0, vc = 0, sc = 0, pc = 0, segs = 0;
+            bool have = wk.get(a, g);
+            while (ok && have) {
+                const Seg cur = g;
+                have = wk.get(a, g);
+                auto pv = [&](int j) {
+                    if (!mbar_wait<false>(bar(kPFull), (uint32_t)(pc & 1), abort_flag)) return false;
+                    if (j == cur.j0 && segs > 0 &&
+                        !mbar_wait<false>(bar(kORead), (uint32_t)((segs - 1) & 1), abort_flag))
+                        return false;
+                    const int left = cur.ctx - j * kTok;
+                    const int subs = left >= kTok ? 4 : (left + 31) / 32;
+                    for (int v = 0; v < subs; ++v, ++vc) {
+                        const int st = vc % C::VS;
+                        if (!mbar_wait<false>(bar(kVFull + st), (uint32_t)((vc / C::VS) & 1),
+                                              abort_flag))
+                            return false;
+                        fence_after();
+#pragma unroll
+                        for (int k = 0; k < 2; ++k) {
+                            const uint64_t da = dP + (uint64_t)(((v >> 1) * 8192 + (v & 1) * 64 + k * 32) >> 4);
+#pragma unroll
+                            for (int n = 0; n < R / 256; ++n) {
+                                const uint64_t db = dV + (uint64_t)((st * C::V_SLOT + k * 2 * C::V_GROUP +
+                                                                     n * 2048) >> 4);
+                                umma_pair(tmem + kColO + n * 128, da, db, ID_PV,
+                                          j > cur.j0 || v > 0 || k > 0);
+                            }
+                        }
+                        commit_pair(bar(kVEmpty + st));
+                    }
+                    commit_pair(bar(kPvDone));
+                    ++pc;
+                    return true;
+                };
+                if (!mbar_wait<false>(bar(kQFull), (uint32_t)(segs & 1), abort_flag)) {
+                    ok = false;
+                    break;
+                }
+                for (int j = cur.j0; ok && j < cur.j1; ++j) {
+                    for (int u = 0; u < C::KSUB; ++u, ++kc) {
+                        const int st = kc % C::KS;
+                        if (!mbar_wait<false>(bar(kKFull + st), (uint32_t)((kc / C::KS) & 1),
+                                              abort_flag)) {
+                            ok = false;
+                            break;
+                        }
+                        fence_after();
+#pragma unroll
+                        for (int i = 0; i < C::KC * 4; ++i) {
+                            const int c = i >> 2, k = i & 3;
+                            umma_pair(tmem + (sc & 1) * 64,
+                                      dQ + (uint64_t)(((u * C::KC + c) * 8192 + k * 32) >> 4),
+                                      dK + (uint64_t)((st * C::K_SLOT + c * 1024 + k * 32) >> 4), ID_S,
+                                      u > 0 || i > 0);
+                        }
+                        commit_pair(bar(kKEmpty + st));
+                    }
+                    if (!ok) break;
+                    commit_pair(bar(kSFull + (sc & 1)));
+                    ++sc;
+                    if (j == cur.j1 - 1) commit_pair(bar(kQEmpty));
+                    if (j > cur.j0 && !pv(j - 1)) ok = false;
+                }
+                if (ok && !pv(cur.j1 - 1)) ok = false;
+                ++segs;
+            }
+            if (!ok) {
+                fail();
+                // what was issued completes before the tensor memory goes
+                volatile int never = 0;
+                commit_pair(bar(kSpare));
+                mbar_wait(bar(kSpare), 0, &never);
+            }
+        }
+        __syncwarp();
+    } else if (warp >= 2 && warp < 6) {
+        // ================================================= softmax
+        const int quad = warp & 3, half = quad >> 1;
+        const int rl = (quad & 1) * 32 + lane;               // row of this CTA's 64
+        const uint32_t lanes = (uint32_t)(quad * 32) << 16;
+        const uint32_t pfull = at_rank(bar(kPFull), 0), oread = at_rank(bar(kORead), 0);
+        // sequences without a token: rows of zero
+        for (int s = pair * 2 + (int)rank; s < a.S; s += 2 * a.pairs) {
+            Seq q;
+            if (!q.load(a, s) || q.ctx != 0 || q.qlen == 0) continue;
+            uint4* o = reinterpret_cast<uint4*>(a.out + (int64_t)q.q0 * a.H * R);
+            const int64_t n = (int64_t)q.qlen * a.H * R / 8;
+            for (int64_t i = tid - 64; i < n; i += 128) o[i] = make_uint4(0u, 0u, 0u, 0u);
+        }
+        Walker wk;
+        wk.init(a, start);
+        Seg g;
+        int sc = 0, par = 0;
+        const uint64_t scale2 = f2(a.scale_log2, a.scale_log2);
+        while (wk.get(a, g)) {
+            const int row = 64 * (int)rank + rl;             // of the tile
+            const bool live = 64 * (int)rank + (quad & 1) * 32 < g.rows;   // the warp's
+            const int i = (g.row + min(row, g.rows - 1)) / a.H;            // its token
+            const int first = g.ctx - g.qlen;                // tokens that every row sees
+            // the new tokens that the row sees, by bits (a chain's row i: the first i + 1)
+            uint64_t bits = 0;
+            int sees = first + i + 1;
+            if (a.ancestors) {
+                sees = first;
+                bits = (uint64_t)a.ancestors[g.q0 + i];
+                if (g.qlen < 64) bits &= (1ull << g.qlen) - 1;
+            }
+            float m = -INFINITY;
+            uint64_t l2 = 0;                                 // two partial sums
+            for (int j = g.j0; j < g.j1; ++j, ++sc) {
+                const int t0 = j * kTok + 64 * half;         // the thread's first token
+                const int t_group = t0 + 8 * (lane & 7);
+                // groups of 8 tokens whose block is in the pool
+                uint32_t groups = 0xffu;
+                if (live) {
+                    const bool in = t_group >= g.ctx || cache_row(a, g, t_group) >= 0;
+                    groups = __ballot_sync(0xffffffffu, in) & 0xffu;
+                }
+                ok = ok && warp_wait(bar(kSFull + (sc & 1)), (uint32_t)((sc >> 1) & 1), abort_flag);
+                fence_after();
+                uint32_t w[32];
+                float alpha = 1.f;
+                if (live) {
+                    uint32_t z[64];
+                    ld64(tmem + lanes + (uint32_t)((sc & 1) * 64), z);
+                    ld_wait(z);
+#pragma unroll
+                    for (int e = 0; e < 32; ++e) {
+                        float x, y;
+                        f2_split(mul2(f2(__uint_as_float(z[2 * e]), __uint_as_float(z[2 * e + 1])),
+                                      scale2),
+                                 x, y);
+                        z[2 * e] = __float_as_uint(x);
+                        z[2 * e + 1] = __float_as_uint(y);
+                    }
+                    if (t0 + 64 > first || groups != 0xffu) {
+                        const int n = sees - t0;             // tokens seen without bits
+                        uint64_t see = n >= 64 ? ~0ull : n > 0 ? (1ull << n) - 1 : 0ull;
+                        if (bits) see |= n >= 64 ? 0ull : n >= 0 ? bits << n : n > -64 ? bits >> -n : 0ull;
+                        uint32_t lo = (uint32_t)see, hi = (uint32_t)(see >> 32);
+                        if (groups != 0xffu) {
+#pragma unroll
+                            for (int k = 0; k < 4; ++k) {
+                                if (!(groups >> k & 1)) lo &= ~(0xffu << 8 * k);
+                                if (!(groups >> (k + 4) & 1)) hi &= ~(0xffu << 8 * k);
+                            }
+                        }
+#pragma unroll
+                        for (int e = 0; e < 64; ++e)
+                            if (!((e < 32 ? lo >> e : hi >> (e - 32)) & 1))
+                                z[e] = __float_as_uint(-INFINITY);
+                    }
+                    float top = __uint_as_float(z[0]);
+#pragma unroll
+                    for (int e = 1; e < 63; e += 2)
+                        top = max3(top, __uint_as_float(z[e]), __uint_as_float(z[e + 1]));
+                    top = fmaxf(top, __uint_as_float(z[63]));
+                    s_x[par][half][rl] = top;
+                    named_sync(1 + (quad & 1), 64);
+                    top = fmaxf(top, s_x[par][1 - half][rl]);
+                    par ^= 1;
+                    if (top > m + El<T>::kRescale || m == -INFINITY) {
+                        // raised a little past the largest for lifted weights, so that
+                        // scores' rounding, whatever their size, takes none past fp16
+                        const float mn = El<T>::kLift > 0.f && top > -INFINITY
+                                             ? fmaf(fabsf(top), 0x1p-22f, top) : top;
+                        if (mn > m) {
+                            alpha = ex2(m - mn);
+                            m = mn;
+                        }
+                    }
+                    const float minus = m == -INFINITY ? 0.f : El<T>::kLift - m;
+                    const uint64_t minus2 = f2(minus, minus);
+                    uint64_t sum[2] = {0, 0};
+#pragma unroll
+                    for (int e = 0; e < 32; ++e) {
+                        float x, y;
+                        f2_split(add2(f2(__uint_as_float(z[2 * e]), __uint_as_float(z[2 * e + 1])),
+                                      minus2),
+                                 x, y);
+                        w[e] = El<T>::pack(ex2(x), ex2(y));
+                        sum[e & 1] = add2(sum[e & 1], El<T>::unpack(w[e]));
+                    }
+                    l2 = fma2(l2, f2(alpha, alpha), add2(sum[0], sum[1]));
+                }
+                // the step before has read its weights and written O
+                ok = ok && (sc == 0 || warp_wait(bar(kPvDone), (uint32_t)((sc - 1) & 1), abort_flag));
+                fence_after();
+                if (live) {
+                    if (j > g.j0 && __any_sync(0xffffffffu, alpha != 1.f)) {
+                        const uint64_t al2 = f2(alpha, alpha);
+#pragma unroll 1
+                        for (int c = 0; c < R / 2; c += 32) {
+                            uint32_t o[32];
+                            ld32(tmem + lanes + kColO + c, o);
+                            ld_wait(o);
+#pragma unroll
+                            for (int e = 0; e < 16; ++e) {
+                                float x, y;
+                                f2_split(mul2(f2(__uint_as_float(o[2 * e]),
+                                                 __uint_as_float(o[2 * e + 1])),
+                                              al2),
+                                         x, y);
+                                o[2 * e] = __float_as_uint(x);
+                                o[2 * e + 1] = __float_as_uint(y);
+                            }
+                            st32(tmem + lanes + kColO + c, o);
+                        }
+                        st_wait();
+                    }
+                    // row rl of the half's 64 tokens: 128 bytes, 16-byte piece c at c ^ (rl % 8)
+                    const uint32_t p = sP + half * 8192 + rl * 128;
+#pragma unroll
+                    for (int c = 0; c < 8; ++c)
+                        st_shared_v4(p + ((c ^ (rl & 7)) << 4), w[4 * c], w[4 * c + 1], w[4 * c + 2],
+                                     w[4 * c + 3]);
+                    fence_async_smem();
+                }
+                fence_before();
+                __syncwarp();
+                if (lane == 0) mbar_arrive_cluster(pfull);
+            }
+            // the tile's output
+            ok = ok && warp_wait(bar(kPvDone), (uint32_t)((sc - 1) & 1), abort_flag);
+            fence_after();
+            if (live) {
+                float x, y;
+                f2_split(l2, x, y);
+                float l = x + y;
+                s_x[par][half][rl] = l;
+                named_sync(1 + (quad & 1), 64);
+                l += s_x[par][1 - half][rl];
+                par ^= 1;
+                const bool mine = row < g.rows && ok;
+                const int64_t at = (int64_t)(pair * 2 + g.slot) * a.slot_rows + row;
+                if (mine && !g.whole && half == 0) a.ml[at] = make_float2(m, l);
+                const float inv = l > 0.f ? 1.f / l : l;     // (NaN stays NaN)
+                uint16_t* orow = a.out + ((int64_t)g.q0 * a.H + g.row + row) * R + half * (R / 2);
+                float* prow = a.acc + at * R + half * (R / 2);
+#pragma unroll 1
+                for (int c = 0; c < R / 2; c += 32) {
+                    uint32_t o[32];
+                    ld32(tmem + lanes + kColO + c, o);
+                    ld_wait(o);
+                    if (!mine) continue;
+                    if (g.whole) {
+                        uint32_t p[16];
+#pragma unroll
+                        for (int e = 0; e < 16; ++e)
+                            p[e] = inv != 0.f ? El<T>::pack(__uint_as_float(o[2 * e]) * inv,
+                                                            __uint_as_float(o[2 * e + 1]) * inv)
+                                              : 0u;
+                        if (a.out_v8) {
+                            st_global_v8(orow + c, p);
+                            st_global_v8(orow + c + 16, p + 8);
+                        } else {
+#pragma unroll
+                            for (int e = 0; e < 4; ++e)
+                                *reinterpret_cast<uint4*>(orow + c + 8 * e) =
+                                    make_uint4(p[4 * e], p[4 * e + 1], p[4 * e + 2], p[4 * e + 3]);
+                        }
+                    } else {
+#pragma unroll
+                        for (int e = 0; e < 4; ++e) st_global_v8(prow + c + 8 * e, o + 8 * e);
+                    }
+                }
+            }
+            fence_before();
+            __syncwarp();
+            if (lane == 0) mbar_arrive_cluster(oread);
+            // the first part of a tile that goes on in the next pairs' runs
+            if (!g.whole && g.j0 == 0 && rank == 0 && warp == 2 && lane == 0) {
+                // steps of the tile from this run's end on, and the runs they fall in
+                const int64_t total = s_total, np = min((int64_t)a.pairs, total);
+                const int64_t e = total * (pair + 1) / np;   // first step after this run
+                const int64_t z = e + (wk.q.nt - g.j1) - 1;  // the tile's last
+                int64_t last = z * np / total;               // the run that holds it
+                while (last + 1 < np && total * (last + 1) / np <= z) ++last;
+                while (total * last / np > z) --last;
+                a.rec[pair] = Rec{g.q0 * a.H + g.row, ok ? g.rows : 0, pair * 2 + g.slot,
+                                  (int)(last - pair) + 1};
+            }
+        }
+        if (!ok && lane == 0) fail();
     }
+
+    __syncwarp();
+    if (*abort_flag) {
+        // copies in flight end before the CTA does
+        const uint64_t t = global_ns();
+        while (global_ns() - t < 200000ull) __nanosleep(1000);
+    }
+    fence_before();
+    __syncthreads();
+    cluster_sync();
+    if (warp == 1) {
+        fence_after();
+        dealloc_pair(tmem);
+    }
+}
+
+// Joins the parts of a row tile: with M the largest running max,
+//   out = sum_k 2^(m_k - M) acc_k / sum_k 2^(m_k - M) l_k.
+// blockIdx.x: the pair that left the first part; a block takes kJoinRows rows, R / 4
+// threads a row.
+constexpr int kJoinRows = 4;
+
+template <typename T, int R>
+__global__ void __launch_bounds__(R / 4) latent_decode_join(const Args a) {
+    asm volatile("griddepcontrol.wait;" ::: "memory");
+    asm volatile("griddepcontrol.launch_dependents;" ::: "memory");
+    __shared__ float weight[2 * kMaxPairs];
+    __shared__ float red[2][R / 128];
+    const Rec rec = a.rec[blockIdx.x];
+    // what a kernel that gave up left may be anything: nothing out of range
+    if (rec.rows <= 0 || rec.rows > a.slot_rows || rec.parts < 1 || rec.slot < 0 ||
+        rec.slot / 2 + rec.parts > a.pairs || rec.row0 < 0 ||
+        (int64_t)rec.row0 + rec.rows > (int64_t)a.T * a.H)
+        return;
+    const int d = threadIdx.x, warp = d >> 5, lane = d & 31;
+    for (int r = blockIdx.y * kJoinRows; r < min(rec.rows, (int)(blockIdx.y + 1) * kJoinRows); ++r) {
+        auto slot = [&](int k) -> int64_t {
+            return (int64_t)(k == 0 ? rec.slot : (rec.slot / 2 + k) * 2) * a.slot_rows + r;
+        };
+        // thread k: part k's max and sum (parts <= kMaxPairs; R / 4 threads are 64 or 128)
+        float M = -INFINITY;
+        for (int k = d; k < rec.parts; k += R / 4) {
+            weight[k] = a.ml[slot(k)].x;
+            weight[kMaxPairs + k] = a.ml[slot(k)].y;
+            M = fmaxf(M, weight[k]);
+        }
+#pragma unroll
+        for (int o = 16; o > 0; o >>= 1) M = fmaxf(M, __shfl_xor_sync(0xffffffffu, M, o));
+        if (lane == 0) red[0][warp] = M;
+        __syncthreads();
+        for (int w = 0; w < R / 128; ++w) M = fmaxf(M, red[0][w]);
+        float L = 0.f;
+        for (int k = d; k < rec.parts; k += R / 4) {
+            // a part without a token that the row sees: nothing, whatever its output holds
+            const float f = weight[k] == -INFINITY && weight[kMaxPairs + k] == 0.f
+                                ? 0.f : ex2(weight[k] - M);
+            weight[k] = f;
+            L += f * weight[kMaxPairs + k];
+        }
+#pragma unroll
+        for (int o = 16; o > 0; o >>= 1) L += __shfl_xor_sync(0xffffffffu, L, o);
+        if (lane == 0) red[1][warp] = L;
+        __syncthreads();
+        L = 0.f;
+        for (int w = 0; w < R / 128; ++w) L += red[1][w];
+        const float inv = L > 0.f ? 1.f / L : L;      // (NaN stays NaN)
+        float4 o = make_float4(0.f, 0.f, 0.f, 0.f);
+#pragma unroll 8
+        for (int k = 0; k < rec.parts; ++k) {
+            const float f = weight[k];
+            float4 v = make_float4(0.f, 0.f, 0.f, 0.f);
+            if (f != 0.f) v = reinterpret_cast<const float4*>(a.acc + slot(k) * R)[d];
+            o.x = fmaf(f, v.x, o.x);
+            o.y = fmaf(f, v.y, o.y);
+            o.z = fmaf(f, v.z, o.z);
+            o.w = fmaf(f, v.w, o.w);
+        }
+        reinterpret_cast<uint2*>(a.out + ((int64_t)rec.row0 + r) * R)[d] =
+            make_uint2(pack2<T>(o.x * inv, o.y * inv), pack2<T>(o.z * inv, o.w * inv));
+        __syncthreads();
+    }
+}
+
+// ------------------------------------------------------------ host side
+struct Layout {
+    size_t ml, acc, total;
+    int rows;
+};
+Layout layout(int H, int R, int max_qlen) {
+    Layout l;
+    const int64_t rows = (int64_t)H * (max_qlen > 0 ? max_qlen : 1);
+    l.rows = (int)(rows < kRows ? rows : kRows);
+    l.ml = pkv::align_up(sizeof(Rec) * kMaxPairs, 256);
+    l.acc = pkv::align_up(l.ml + 8 * (size_t)(2 * kMaxPairs) * l.rows, 256);
+    l.total = l.acc + 4 * (size_t)(2 * kMaxPairs) * l.rows * R;
+    return l;
+}
+
+// Rows of `row` elements in chunks of 64: boxes of `chunks` chunks of 8 rows.
+bool chunk_map(CUtensorMap* m, bool bf16, const void* at, int64_t rows, int row, int chunks) {
+    const PFN_cuTensorMapEncodeTiled_v12000 fn = pkv::map_encoder();
+    if (!fn) return false;
+    const cuuint64_t dims[3] = {64, (cuuint64_t)rows, (cuuint64_t)(row / 64)};
+    const cuuint64_t strides[2] = {(cuuint64_t)row * 2, 128};
+    const cuuint32_t box[3] = {64, 8, (cuuint32_t)chunks};
+    const cuuint32_t estr[3] = {1, 1, 1};
+    return fn(m, bf16 ? CU_TENSOR_MAP_DATA_TYPE_BFLOAT16 : CU_TENSOR_MAP_DATA_TYPE_FLOAT16, 3,
+              const_cast<void*>(at), dims, strides, box, estr, CU_TENSOR_MAP_INTERLEAVE_NONE,
+              CU_TENSOR_MAP_SWIZZLE_128B, CU_TENSOR_MAP_L2_PROMOTION_L2_256B,
+              CU_TENSOR_MAP_FLOAT_OOB_FILL_NONE) == CUDA_SUCCESS;
+}
+
+template <typename T, int R>
+cudaError_t launch(const CUtensorMap& tq, const CUtensorMap& tk, const CUtensorMap& tv,
+                   const Args& a, cudaStream_t stream) {
+    cudaError_t e = cudaFuncSetAttribute(latent_decode_pair<T, R>,
+                                         cudaFuncAttributeMaxDynamicSharedMemorySize, Cfg<R>::SMEM);
+    if (e != cudaSuccess) return e;
+    cudaLaunchConfig_t cfg = {};
+    cfg.gridDim = dim3((unsigned)(2 * a.pairs));
+    cfg.blockDim = dim3(kThreads);
+    cfg.dynamicSmemBytes = Cfg<R>::SMEM;
+    cfg.stream = stream;
+    cudaLaunchAttribute attr[2];
+    attr[0].id = cudaLaunchAttributeClusterDimension;
+    attr[0].val.clusterDim.x = 2;
+    attr[0].val.clusterDim.y = 1;
+    attr[0].val.clusterDim.z = 1;
+    attr[1].id = cudaLaunchAttributeProgrammaticStreamSerialization;
+    attr[1].val.programmaticStreamSerializationAllowed = 1;
+    cfg.attrs = attr;
+    cfg.numAttrs = 1;
+    e = cudaLaunchKernelEx(&cfg, latent_decode_pair<T, R>, tq, tk, tv, a);
+    if (e != cudaSuccess) return e;
+    cudaLaunchConfig_t jc = {};
+    jc.gridDim = dim3((unsigned)a.pairs, (unsigned)((a.slot_rows + kJoinRows - 1) / kJoinRows));
+    jc.blockDim = dim3(R / 4);
+    jc.stream = stream;
+    jc.attrs = attr + 1;
+    jc.numAttrs = 1;
+    return cudaLaunchKernelEx(&jc, latent_decode_join<T, R>, a);
 }
 
 }  // namespace
@@ -122,7 +865,7 @@ pkv_status pkv_latent_decode_workspace_size(int num_seqs, int num_heads, int lat
     if (num_seqs < 0 || num_heads < 1 || (latent_dim != 256 && latent_dim != 512) ||
         max_query_len < 0)
         return pkv::fail(PKV_ERR_INVALID, "%s: bad sizes", fn);
-    *bytes = 256;
+    *bytes = layout(num_heads, latent_dim, max_query_len).total;
     return PKV_OK;
 }
 
@@ -146,9 +889,14 @@ pkv_status pkv_latent_attention_decode(
         return pkv::fail(PKV_ERR_INVALID, "%s: bad sizes", fn);
     if ((int64_t)max_blocks_per_seq * block_size > (1LL << 30))
         return pkv::fail(PKV_ERR_INVALID, "%s: context capacity above 2^30 tokens", fn);
-    if (num_blocks < 1 || num_blocks > ((1LL << 31) - 1) / block_size)
+    // the tiled copies address cache rows and query rows with 32-bit coordinates
+    if (num_blocks < 1 || num_blocks > ((1LL << 31) - 65) / block_size)
         return pkv::fail(PKV_ERR_INVALID,
-                         "%s: num_blocks must be >= 1, and num_blocks * block_size below 2^31", fn);
+                         "%s: num_blocks must be >= 1, and num_blocks * block_size below 2^31 - 64",
+                         fn);
+    if ((int64_t)num_query_tokens * num_heads > (1LL << 31) - 256)
+        return pkv::fail(PKV_ERR_INVALID, "%s: num_query_tokens * num_heads must be below 2^31 - 256",
+                         fn);
     if (dtype != PKV_F16 && dtype != PKV_BF16)
         return pkv::fail(PKV_ERR_INVALID, "%s: unknown dtype", fn);
     const float scale_log2 = (float)(1.4426950408889634 * scale);
@@ -163,21 +911,84 @@ pkv_status pkv_latent_attention_decode(
         return pkv::fail(PKV_ERR_INVALID, "%s: NULL pointer", fn);
     if (!aligned(out, 16) || !aligned(q, 16) || !aligned(cache, 16))
         return pkv::fail(PKV_ERR_INVALID, "%s: out, q and the cache must be 16-byte aligned", fn);
+    if (!aligned(block_tables, 4) || !aligned(context_lens, 4) || !aligned(query_start, 4) ||
+        !aligned(ancestors, 8))
+        return pkv::fail(PKV_ERR_INVALID,
+                         "%s: misaligned block_tables, context_lens, query_start or ancestors", fn);
+    if (!aligned(workspace, 256))
+        return pkv::fail(PKV_ERR_INVALID, "%s: workspace must be 256-byte aligned", fn);
+    const Layout l = layout(num_heads, latent_dim, max_query_len);
+    if (workspace_bytes < l.total)
+        return pkv::fail(PKV_ERR_INVALID, "%s: workspace too small (%zu < %zu bytes)", fn,
+                         workspace_bytes, l.total);
+    const int W = latent_dim + kP;
+    const int64_t rows = (int64_t)num_query_tokens * num_heads;
+    if (overlap(out, rows * latent_dim * 2, q, rows * W * 2) ||
+        overlap(out, rows * latent_dim * 2, cache, num_blocks * block_size * W * 2) ||
+        overlap(out, rows * latent_dim * 2, workspace, (int64_t)l.total))
+        return pkv::fail(PKV_ERR_INVALID, "%s: out overlaps an input or the workspace", fn);
     int32_t* err = pkv::device_error_word();
     if (!err) return pkv::fail(PKV_ERR_CUDA, "%s: no CUDA device", fn);
-    Args a = {static_cast<uint16_t*>(out), static_cast<const uint16_t*>(q),
-              static_cast<const uint16_t*>(cache), block_tables, context_lens, query_start,
-              ancestors, scale_log2, num_seqs, num_heads, block_size, max_blocks_per_seq,
-              max_query_len, num_query_tokens, num_blocks, err};
-    using Kernel = void (*)(Args);
-    const Kernel k = dtype == PKV_F16
-                         ? (latent_dim == 256 ? (Kernel)latent_decode_simple<__half, 256>
-                                              : (Kernel)latent_decode_simple<__half, 512>)
-                         : (latent_dim == 256 ? (Kernel)latent_decode_simple<__nv_bfloat16, 256>
-                                              : (Kernel)latent_decode_simple<__nv_bfloat16, 512>);
-    const cudaError_t e = pkv::launch_pdl(
-        k, dim3((unsigned)num_heads, (unsigned)max_query_len, (unsigned)num_seqs), dim3(128),
-        stream, a);
+    int dev = 0;
+    cudaError_t e = cudaGetDevice(&dev);
+    if (e != cudaSuccess) return pkv::cuda_fail(e, fn);
+    const int sms = pkv::sm_count(dev);
+    if (sms < 2) return pkv::fail(PKV_ERR_CUDA, "%s: no multiprocessors", fn);
+
+    const bool bf16 = dtype == PKV_BF16;
+    CUtensorMap tq, tk, tv;
+    {
+        // a CTA's 64 query rows, a box a chunk of 64 elements
+        const PFN_cuTensorMapEncodeTiled_v12000 enc = pkv::map_encoder();
+        const cuuint64_t dims[2] = {(cuuint64_t)W, (cuuint64_t)rows};
+        const cuuint64_t strides[1] = {(cuuint64_t)W * 2};
+        const cuuint32_t box[2] = {64, 64}, estr[2] = {1, 1};
+        if (!enc || enc(&tq, bf16 ? CU_TENSOR_MAP_DATA_TYPE_BFLOAT16 : CU_TENSOR_MAP_DATA_TYPE_FLOAT16,
+                        2, const_cast<void*>(q), dims, strides, box, estr,
+                        CU_TENSOR_MAP_INTERLEAVE_NONE, CU_TENSOR_MAP_SWIZZLE_128B,
+                        CU_TENSOR_MAP_L2_PROMOTION_L2_256B,
+                        CU_TENSOR_MAP_FLOAT_OOB_FILL_NONE) != CUDA_SUCCESS)
+            return pkv::fail(PKV_ERR_CUDA, "%s: tensor map of q", fn);
+    }
+    const int64_t places = num_blocks * block_size;
+    if (!chunk_map(&tk, bf16, cache, places, W, latent_dim == 512 ? Cfg<512>::KC : Cfg<256>::KC) ||
+        !chunk_map(&tv, bf16, cache, places, W, latent_dim / 128))
+        return pkv::fail(PKV_ERR_CUDA, "%s: tensor map of the cache", fn);
+
+    Args a = {};
+    a.out = static_cast<uint16_t*>(out);
+    a.cache = static_cast<const uint16_t*>(cache);
+    a.tables = block_tables;
+    a.ctx = context_lens;
+    a.q_start = query_start;
+    a.ancestors = ancestors;
+    a.scale_log2 = scale_log2;
+    a.S = num_seqs;
+    a.H = num_heads;
+    a.B = block_size;
+    a.max_blocks = max_blocks_per_seq;
+    a.max_qlen = max_query_len;
+    a.T = num_query_tokens;
+    a.num_blocks = num_blocks;
+    a.slot_rows = l.rows;
+    a.out_v8 = aligned(out, 32) ? 1 : 0;
+    // pairs: no more than there can be steps
+    int64_t pairs = sms / 2 < kMaxPairs ? sms / 2 : kMaxPairs;
+    const int64_t per_seq = (((int64_t)max_blocks_per_seq * block_size + kTok - 1) / kTok) *
+                            (((int64_t)max_query_len * num_heads + kRows - 1) / kRows);
+    if (per_seq < pairs && per_seq * num_seqs < pairs) pairs = per_seq * num_seqs;
+    a.pairs = (int)pairs;
+    char* ws = static_cast<char*>(workspace);
+    a.rec = reinterpret_cast<Rec*>(ws);
+    a.ml = reinterpret_cast<float2*>(ws + l.ml);
+    a.acc = reinterpret_cast<float*>(ws + l.acc);
+    a.err = err;
+    if (bf16)
+        e = latent_dim == 512 ? launch<__nv_bfloat16, 512>(tq, tk, tv, a, stream)
+                              : launch<__nv_bfloat16, 256>(tq, tk, tv, a, stream);
+    else
+        e = latent_dim == 512 ? launch<__half, 512>(tq, tk, tv, a, stream)
+                              : launch<__half, 256>(tq, tk, tv, a, stream);
     if (e != cudaSuccess) return pkv::cuda_fail(e, fn);
     return PKV_OK;
 }
