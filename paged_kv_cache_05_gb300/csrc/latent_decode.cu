@@ -21,11 +21,12 @@
 // of 8 rows, measured) bounds long contexts at 5.8 TB/s of the cache.
 //
 // Eight warps a CTA:
-//   warp 0      queries and keys: boxes of 8 rows x KC chunks of 64 elements, one lane
-//               a box, rings of KS slots of KC chunks of the tile's 64 tokens, freed
-//               chunk by chunk as S is formed
-//   warp 6      values: boxes of 8 rows x R / 128 chunks, rings of VS slots of 32 tokens
-//   warp 1      (of the first CTA) issues the products from one thread
+//   warp 0      keys: boxes of 8 rows x KC chunks of 64 elements, one lane a box, a ring
+//               of KS slots of KC chunks of the tile's 64 tokens, freed slot by slot as S
+//               is formed
+//   warp 6      values: boxes of 8 rows x R / 128 chunks, a ring of VS slots of 32 tokens
+//   warp 7      queries
+//   warp 1      (of the first CTA) issues the products
 //   warps 2-5   softmax: a thread a row and half of the tile's tokens; the two halves
 //               of a row meet in shared memory.  The max is raised only past a growth of
 //               kRescale, so that most steps leave O alone.
@@ -109,7 +110,7 @@ struct Args {
     int out_v8;                       // out is 32-byte aligned: 32-byte stores
     struct Rec* rec;                  // [pairs]
     float2* ml;                       // [2 pairs][slot_rows]
-    float* acc;                       // [2 pairs][slot_rows][R]
+    float* acc;                       // [2 pairs][R / 8][slot_rows][8]
     int32_t* err;
 };
 
@@ -142,7 +143,9 @@ struct Seq {
 // Where a pair's run begins.
 struct Start {
     int s;
+    Seq q;
     int64_t off, n;                   // steps before it in the sequence, steps of the run
+    int64_t total;                    // steps of all
 };
 
 // A run of steps of one row tile.
@@ -165,10 +168,8 @@ struct Walker {
         off = st.off;
         left = st.n;
         first = true;
-        if (left > 0) {
-            q.load(a, s);
-            if (s + 1 < a.S) next.load(a, s + 1);
-        }
+        q = st.q;
+        if (left > 0 && s + 1 < a.S) next.load(a, s + 1);
     }
     __device__ __forceinline__ bool get(const Args& a, Seg& g) {
         if (left <= 0) return false;
@@ -216,8 +217,7 @@ __global__ void __launch_bounds__(kThreads, 1)
     __shared__ uint32_t s_tmem;
     __shared__ int s_abort;
     __shared__ Start s_start;
-    __shared__ int64_t s_scan[8];
-    __shared__ int64_t s_total;                  // steps of all
+    __shared__ int64_t s_scan[2][8];
     __shared__ float s_x[2][2][64];              // a row's maxima (or sums) by halves
 
     const int tid = threadIdx.x, warp = tid >> 5, lane = tid & 31;
@@ -229,6 +229,14 @@ __global__ void __launch_bounds__(kThreads, 1)
                    sP = base + C::P_OFF;
     auto bar = [&](int i) { return smem_u32(&bars[i]); };
 
+    asm volatile("griddepcontrol.wait;" ::: "memory");
+    asm volatile("griddepcontrol.launch_dependents;" ::: "memory");
+
+    // the pair's run of the steps: [b, e) of all (the lengths are loaded once where
+    // there is a thread a sequence, and on their way while the barriers are made)
+    Seq mine;
+    mine.nt = mine.nr = 0;
+    bool good = tid >= a.S || mine.load(a, tid);
     if (warp == 1) {
         if (lane == 0) {
             for (int i = 0; i < kBars; ++i) {
@@ -245,65 +253,69 @@ __global__ void __launch_bounds__(kThreads, 1)
         prefetch_map(&tm_k);
         prefetch_map(&tm_v);
     }
-    asm volatile("griddepcontrol.wait;" ::: "memory");
-    asm volatile("griddepcontrol.launch_dependents;" ::: "memory");
-
-    // the pair's run of the steps: [b, e) of all
     {
-        int64_t mine = 0;
-        for (int s = tid; s < a.S; s += kThreads) {
+        // this thread's steps, and those of the threads before it in the warp
+        int64_t n = mine.steps(), incl = n, rest = 0;
+        for (int s = tid + kThreads; s < a.S; s += kThreads) {
             Seq q;
-            if (!q.load(a, s) && blockIdx.x == 0) atomicOr(a.err, PKV_DEVERR_BAD_CONTEXT);
-            mine += q.steps();
+            good &= q.load(a, s);
+            rest += q.steps();
         }
+        if (!good && blockIdx.x == 0) atomicOr(a.err, PKV_DEVERR_BAD_CONTEXT);
 #pragma unroll
-        for (int o = 16; o > 0; o >>= 1) mine += __shfl_xor_sync(0xffffffffu, mine, o);
-        if (lane == 0) s_scan[warp] = mine;
+        for (int o = 1; o < 32; o <<= 1) {
+            const int64_t y = __shfl_up_sync(0xffffffffu, incl, o);
+            if (lane >= o) incl += y;
+        }
+        if (a.S > kThreads) {
+#pragma unroll
+            for (int o = 16; o > 0; o >>= 1) rest += __shfl_xor_sync(0xffffffffu, rest, o);
+        }
+        if (lane == 31) {
+            s_scan[0][warp] = incl;
+            s_scan[1][warp] = rest;
+        }
+        if (tid == 0) s_start.n = 0;
+        fence_before();
         __syncthreads();
-        int64_t total = 0;
-        for (int w = 0; w < 8; ++w) total += s_scan[w];
+        asm volatile("barrier.cluster.arrive.release.aligned;" ::: "memory");
+        int64_t total = 0, before = 0;
+        for (int w = 0; w < 8; ++w) {
+            if (w < warp) incl += s_scan[0][w];
+            before += s_scan[0][w];
+            total += s_scan[0][w] + s_scan[1][w];
+        }
         const int64_t np = min((int64_t)a.pairs, total);
         const int64_t b = pair < np ? total * pair / np : 0;
         const int64_t e = pair < np ? total * (pair + 1) / np : 0;
-        if (tid == 0) {
-            s_start.s = 0;
-            s_start.off = 0;
-            s_start.n = e - b;
-            s_total = total;
-        }
-        int64_t before = 0;
-        for (int s0 = 0; s0 < a.S && e > b; s0 += kThreads) {
-            const int s = s0 + tid;
-            Seq q;
-            q.nt = q.nr = 0;
-            if (s < a.S) q.load(a, s);
-            const int64_t n = q.steps();
-            int64_t incl = n;
+        auto found = [&](int s) {                // the sequence that holds step b
+            if (e > b && incl > b && incl - n <= b) s_start = Start{s, mine, b - (incl - n), e - b, total};
+        };
+        found(tid);
+        for (int s0 = kThreads; s0 < a.S && before <= b && e > b; s0 += kThreads) {
+            mine.nt = mine.nr = 0;
+            if (s0 + tid < a.S) mine.load(a, s0 + tid);
+            n = incl = mine.steps();
 #pragma unroll
             for (int o = 1; o < 32; o <<= 1) {
                 const int64_t y = __shfl_up_sync(0xffffffffu, incl, o);
                 if (lane >= o) incl += y;
             }
             __syncthreads();
-            if (lane == 31) s_scan[warp] = incl;
+            if (lane == 31) s_scan[0][warp] = incl;
             __syncthreads();
             incl += before;
             for (int w = 0; w < 8; ++w) {
-                if (w < warp) incl += s_scan[w];
-                before += s_scan[w];
+                if (w < warp) incl += s_scan[0][w];
+                before += s_scan[0][w];
             }
-            if (n > 0 && incl > b && incl - n <= b) {
-                s_start.s = s;
-                s_start.off = b - (incl - n);
-            }
-            if (before > b) break;
+            found(s0 + tid);
         }
         // (nothing to join, until a part is left)
         if (tid == 0 && rank == 0) a.rec[pair] = Rec{0, 0, 0, 0};
     }
-    fence_before();
     __syncthreads();
-    cluster_sync();
+    asm volatile("barrier.cluster.wait.acquire.aligned;" ::: "memory");
     fence_after();
     const uint32_t tmem = s_tmem;
     const Start start = s_start;
@@ -314,28 +326,17 @@ __global__ void __launch_bounds__(kThreads, 1)
     };
 
     if (warp == 0) {
-        // ================================================= queries and keys
+        // ================================================= keys
         Walker wk;
         wk.init(a, start);
         Seg g;
-        int kc = 0, segs = 0;
-        const uint32_t qfull = at_rank(bar(kQFull), 0);
+        int kc = 0;
         const int none = (int)min(a.num_blocks * a.B, (int64_t)0x7fffffff);   // past the pool: zeros
         while (ok && wk.get(a, g)) {
             auto row_of = [&](int j) {
                 return lane < 8 ? cache_row(a, g, j * kTok + 64 * (int)rank + 8 * lane) : -1;
             };
             int y = row_of(g.j0);
-            if (segs > 0 && !warp_wait(bar(kQEmpty), (uint32_t)((segs - 1) & 1), abort_flag)) {
-                ok = false;
-                break;
-            }
-            const bool live = g.rows > 64 * (int)rank;
-            if (lane == 0) mbar_expect_tx_cluster(qfull, live ? C::Q_BYTES : 0);
-            __syncwarp();
-            if (live && lane < C::CH)
-                tma_2d_pair(sQ + lane * 8192, &tm_q, lane * 64,
-                            g.q0 * a.H + g.row + 64 * (int)rank, qfull);
             for (int j = g.j0; j < g.j1; ++j) {
                 const int yn = j + 1 < g.j1 ? row_of(j + 1) : -1;
                 for (int u = 0; u < C::KSUB; ++u, ++kc) {
@@ -354,9 +355,26 @@ __global__ void __launch_bounds__(kThreads, 1)
                 if (!ok) break;
                 y = yn;
             }
-            ++segs;
         }
         if (!ok) fail();
+    } else if (warp == 7) {
+        // ================================================= queries
+        Walker wk;
+        wk.init(a, start);
+        Seg g;
+        const uint32_t qfull = at_rank(bar(kQFull), 0);
+        for (int segs = 0; wk.get(a, g); ++segs) {
+            if (segs > 0 && !warp_wait(bar(kQEmpty), (uint32_t)((segs - 1) & 1), abort_flag)) {
+                fail();
+                break;
+            }
+            const bool live = g.rows > 64 * (int)rank;
+            if (lane == 0) mbar_expect_tx_cluster(qfull, live ? C::Q_BYTES : 0);
+            __syncwarp();
+            if (live && lane < 8)
+                tma_3d_pair(sQ + lane * C::CH * 1024, &tm_q, 0,
+                            g.q0 * a.H + g.row + 64 * (int)rank + 8 * lane, 0, qfull);
+        }
     } else if (warp == 6) {
         // ================================================= values
         Walker wk;
@@ -417,15 +435,19 @@ __global__ void __launch_bounds__(kThreads, 1)
         if (!ok) fail();
     } else if (warp == 1) {
         // ================================================= products
-        if (rank == 0 && lane == 0) {
+        if (rank == 0 && elect_one()) {
             constexpr uint32_t ID_S = idesc(El<T>::kType, false, kTok, kRows);
             constexpr uint32_t ID_PV = idesc(El<T>::kType, true, 256, kRows);
-            const uint64_t dQ = sdesc(sQ, 16, 1024), dK = sdesc(sK, 16, C::KC * 1024),
+            const uint64_t dQ = sdesc(sQ, 16, C::CH * 1024), dK = sdesc(sK, 16, C::KC * 1024),
                            dV = sdesc(sV, 1024, C::V_GROUP), dP = sdesc(sP, 16, 1024);
             Walker wk;
             wk.init(a, start);
             Seg g;
             int kc = 0, vc = 0, sc = 0, pc = 0, segs = 0;
+            auto k_full = [&](int k) { return bar(kKFull + k % C::KS); };
+            auto k_par = [&](int k) { return (uint32_t)((k / C::KS) & 1); };
+            auto v_full = [&](int v) { return bar(kVFull + v % C::VS); };
+            auto v_par = [&](int v) { return (uint32_t)((v / C::VS) & 1); };
             bool have = wk.get(a, g);
             while (ok && have) {
                 const Seg cur = g;
@@ -438,23 +460,19 @@ __global__ void __launch_bounds__(kThreads, 1)
                     const int left = cur.ctx - j * kTok;
                     const int subs = left >= kTok ? 4 : (left + 31) / 32;
                     for (int v = 0; v < subs; ++v, ++vc) {
-                        const int st = vc % C::VS;
-                        if (!mbar_wait<false>(bar(kVFull + st), (uint32_t)((vc / C::VS) & 1),
-                                              abort_flag))
-                            return false;
+                        if (!mbar_wait<false>(v_full(vc), v_par(vc), abort_flag)) return false;
                         fence_after();
+                        const uint64_t da = dP + (uint64_t)(((v >> 1) * 8192 + (v & 1) * 64) >> 4);
+                        const uint64_t db = dV + (uint64_t)(((vc % C::VS) * C::V_SLOT) >> 4);
 #pragma unroll
                         for (int k = 0; k < 2; ++k) {
-                            const uint64_t da = dP + (uint64_t)(((v >> 1) * 8192 + (v & 1) * 64 + k * 32) >> 4);
 #pragma unroll
-                            for (int n = 0; n < R / 256; ++n) {
-                                const uint64_t db = dV + (uint64_t)((st * C::V_SLOT + k * 2 * C::V_GROUP +
-                                                                     n * 2048) >> 4);
-                                umma_pair(tmem + kColO + n * 128, da, db, ID_PV,
+                            for (int n = 0; n < R / 256; ++n)
+                                umma_pair(tmem + kColO + n * 128, da + 2 * k,
+                                          db + ((k * 2 * C::V_GROUP + n * 2048) >> 4), ID_PV,
                                           j > cur.j0 || v > 0 || k > 0);
-                            }
                         }
-                        commit_pair(bar(kVEmpty + st));
+                        commit_pair(bar(kVEmpty + vc % C::VS));
                     }
                     commit_pair(bar(kPvDone));
                     ++pc;
@@ -466,22 +484,20 @@ __global__ void __launch_bounds__(kThreads, 1)
                 }
                 for (int j = cur.j0; ok && j < cur.j1; ++j) {
                     for (int u = 0; u < C::KSUB; ++u, ++kc) {
-                        const int st = kc % C::KS;
-                        if (!mbar_wait<false>(bar(kKFull + st), (uint32_t)((kc / C::KS) & 1),
-                                              abort_flag)) {
+                        if (!mbar_wait<false>(k_full(kc), k_par(kc), abort_flag)) {
                             ok = false;
                             break;
                         }
                         fence_after();
+                        const uint64_t da = dQ + (uint64_t)((u * C::KC * 1024) >> 4);
+                        const uint64_t db = dK + (uint64_t)(((kc % C::KS) * C::K_SLOT) >> 4);
 #pragma unroll
                         for (int i = 0; i < C::KC * 4; ++i) {
                             const int c = i >> 2, k = i & 3;
-                            umma_pair(tmem + (sc & 1) * 64,
-                                      dQ + (uint64_t)(((u * C::KC + c) * 8192 + k * 32) >> 4),
-                                      dK + (uint64_t)((st * C::K_SLOT + c * 1024 + k * 32) >> 4), ID_S,
-                                      u > 0 || i > 0);
+                            umma_pair(tmem + (sc & 1) * 64, da + ((c * 1024 + k * 32) >> 4),
+                                      db + ((c * 1024 + k * 32) >> 4), ID_S, u > 0 || i > 0);
                         }
-                        commit_pair(bar(kKEmpty + st));
+                        commit_pair(bar(kKEmpty + kc % C::KS));
                     }
                     if (!ok) break;
                     commit_pair(bar(kSFull + (sc & 1)));
@@ -660,16 +676,21 @@ __global__ void __launch_bounds__(kThreads, 1)
                 l += s_x[par][1 - half][rl];
                 par ^= 1;
                 const bool mine = row < g.rows && ok;
-                const int64_t at = (int64_t)(pair * 2 + g.slot) * a.slot_rows + row;
-                if (mine && !g.whole && half == 0) a.ml[at] = make_float2(m, l);
+                const int64_t slot = pair * 2 + g.slot;
+                if (mine && !g.whole && half == 0)
+                    a.ml[slot * a.slot_rows + row] = make_float2(m, l);
                 const float inv = l > 0.f ? 1.f / l : l;     // (NaN stays NaN)
                 uint16_t* orow = a.out + ((int64_t)g.q0 * a.H + g.row + row) * R + half * (R / 2);
-                float* prow = a.acc + at * R + half * (R / 2);
+                float* prow = a.acc + ((slot * (R / 8) + half * (R / 16)) * a.slot_rows + row) * 8;
+                uint32_t next[32];
+                ld32(tmem + lanes + kColO, next);
 #pragma unroll 1
                 for (int c = 0; c < R / 2; c += 32) {
                     uint32_t o[32];
-                    ld32(tmem + lanes + kColO + c, o);
-                    ld_wait(o);
+                    ld_wait(next);
+#pragma unroll
+                    for (int e = 0; e < 32; ++e) o[e] = next[e];
+                    if (c + 32 < R / 2) ld32(tmem + lanes + kColO + c + 32, next);
                     if (!mine) continue;
                     if (g.whole) {
                         uint32_t p[16];
@@ -689,7 +710,8 @@ __global__ void __launch_bounds__(kThreads, 1)
                         }
                     } else {
 #pragma unroll
-                        for (int e = 0; e < 4; ++e) st_global_v8(prow + c + 8 * e, o + 8 * e);
+                        for (int e = 0; e < 4; ++e)
+                            st_global_v8(prow + (int64_t)(c / 8 + e) * a.slot_rows * 8, o + 8 * e);
                     }
                 }
             }
@@ -699,7 +721,7 @@ __global__ void __launch_bounds__(kThreads, 1)
             // the first part of a tile that goes on in the next pairs' runs
             if (!g.whole && g.j0 == 0 && rank == 0 && warp == 2 && lane == 0) {
                 // steps of the tile from this run's end on, and the runs they fall in
-                const int64_t total = s_total, np = min((int64_t)a.pairs, total);
+                const int64_t total = start.total, np = min((int64_t)a.pairs, total);
                 const int64_t e = total * (pair + 1) / np;   // first step after this run
                 const int64_t z = e + (wk.q.nt - g.j1) - 1;  // the tile's last
                 int64_t last = z * np / total;               // the run that holds it
@@ -729,69 +751,65 @@ __global__ void __launch_bounds__(kThreads, 1)
 
 // Joins the parts of a row tile: with M the largest running max,
 //   out = sum_k 2^(m_k - M) acc_k / sum_k 2^(m_k - M) l_k.
-// blockIdx.x: the pair that left the first part; a block takes kJoinRows rows, R / 4
-// threads a row.
-constexpr int kJoinRows = 4;
+// blockIdx.x: the pair that left the first part; a block takes 8 rows and 256 elements,
+// a thread 8 elements of a row, in one pass over the parts, kJoinParts of them loaded
+// at a time.
+constexpr int kJoinThreads = 256;
+constexpr int kJoinParts = 4;
 
 template <typename T, int R>
-__global__ void __launch_bounds__(R / 4) latent_decode_join(const Args a) {
+__global__ void __launch_bounds__(kJoinThreads) latent_decode_join(const Args a) {
     asm volatile("griddepcontrol.wait;" ::: "memory");
     asm volatile("griddepcontrol.launch_dependents;" ::: "memory");
-    __shared__ float weight[2 * kMaxPairs];
-    __shared__ float red[2][R / 128];
     const Rec rec = a.rec[blockIdx.x];
+    const int r = blockIdx.y * 8 + (threadIdx.x & 7);
+    const int d = blockIdx.z * 32 + (threadIdx.x >> 3);      // eight elements
     // what a kernel that gave up left may be anything: nothing out of range
-    if (rec.rows <= 0 || rec.rows > a.slot_rows || rec.parts < 1 || rec.slot < 0 ||
+    if (r >= rec.rows || rec.rows > a.slot_rows || rec.parts < 1 || rec.slot < 0 ||
         rec.slot / 2 + rec.parts > a.pairs || rec.row0 < 0 ||
         (int64_t)rec.row0 + rec.rows > (int64_t)a.T * a.H)
         return;
-    const int d = threadIdx.x, warp = d >> 5, lane = d & 31;
-    for (int r = blockIdx.y * kJoinRows; r < min(rec.rows, (int)(blockIdx.y + 1) * kJoinRows); ++r) {
-        auto slot = [&](int k) -> int64_t {
-            return (int64_t)(k == 0 ? rec.slot : (rec.slot / 2 + k) * 2) * a.slot_rows + r;
-        };
-        // thread k: part k's max and sum (parts <= kMaxPairs; R / 4 threads are 64 or 128)
-        float M = -INFINITY;
-        for (int k = d; k < rec.parts; k += R / 4) {
-            weight[k] = a.ml[slot(k)].x;
-            weight[kMaxPairs + k] = a.ml[slot(k)].y;
-            M = fmaxf(M, weight[k]);
-        }
+    float M = -INFINITY, L = 0.f;
+    float o[8] = {};
+    for (int k0 = 0; k0 < rec.parts; k0 += kJoinParts) {
+        float2 ml[kJoinParts];
+        float4 v[kJoinParts][2];
 #pragma unroll
-        for (int o = 16; o > 0; o >>= 1) M = fmaxf(M, __shfl_xor_sync(0xffffffffu, M, o));
-        if (lane == 0) red[0][warp] = M;
-        __syncthreads();
-        for (int w = 0; w < R / 128; ++w) M = fmaxf(M, red[0][w]);
-        float L = 0.f;
-        for (int k = d; k < rec.parts; k += R / 4) {
+        for (int k = 0; k < kJoinParts; ++k) {
+            ml[k] = make_float2(-INFINITY, 0.f);
+            if (k0 + k < rec.parts) {
+                const int64_t slot = k0 + k == 0 ? rec.slot : (rec.slot / 2 + k0 + k) * 2;
+                ml[k] = a.ml[slot * a.slot_rows + r];
+                const float4* p = reinterpret_cast<const float4*>(
+                    a.acc + ((slot * (R / 8) + d) * a.slot_rows + r) * 8);
+                v[k][0] = p[0];
+                v[k][1] = p[1];
+            }
+        }
+        float top = M;
+#pragma unroll
+        for (int k = 0; k < kJoinParts; ++k) top = fmaxf(top, ml[k].x);
+        const float f0 = M == -INFINITY ? 0.f : ex2(M - top);
+        M = top;
+        L *= f0;
+#pragma unroll
+        for (int e = 0; e < 8; ++e) o[e] *= f0;
+#pragma unroll
+        for (int k = 0; k < kJoinParts; ++k) {
             // a part without a token that the row sees: nothing, whatever its output holds
-            const float f = weight[k] == -INFINITY && weight[kMaxPairs + k] == 0.f
-                                ? 0.f : ex2(weight[k] - M);
-            weight[k] = f;
-            L += f * weight[kMaxPairs + k];
-        }
+            if (ml[k].x == -INFINITY && ml[k].y == 0.f) continue;
+            const float f = ex2(ml[k].x - M);
+            L = fmaf(f, ml[k].y, L);
+            const float x[8] = {v[k][0].x, v[k][0].y, v[k][0].z, v[k][0].w,
+                                v[k][1].x, v[k][1].y, v[k][1].z, v[k][1].w};
 #pragma unroll
-        for (int o = 16; o > 0; o >>= 1) L += __shfl_xor_sync(0xffffffffu, L, o);
-        if (lane == 0) red[1][warp] = L;
-        __syncthreads();
-        L = 0.f;
-        for (int w = 0; w < R / 128; ++w) L += red[1][w];
-        const float inv = L > 0.f ? 1.f / L : L;      // (NaN stays NaN)
-        float4 o = make_float4(0.f, 0.f, 0.f, 0.f);
-#pragma unroll 8
-        for (int k = 0; k < rec.parts; ++k) {
-            const float f = weight[k];
-            float4 v = make_float4(0.f, 0.f, 0.f, 0.f);
-            if (f != 0.f) v = reinterpret_cast<const float4*>(a.acc + slot(k) * R)[d];
-            o.x = fmaf(f, v.x, o.x);
-            o.y = fmaf(f, v.y, o.y);
-            o.z = fmaf(f, v.z, o.z);
-            o.w = fmaf(f, v.w, o.w);
+            for (int e = 0; e < 8; ++e) o[e] = fmaf(f, x[e], o[e]);
         }
-        reinterpret_cast<uint2*>(a.out + ((int64_t)rec.row0 + r) * R)[d] =
-            make_uint2(pack2<T>(o.x * inv, o.y * inv), pack2<T>(o.z * inv, o.w * inv));
-        __syncthreads();
     }
+    const float inv = L > 0.f ? 1.f / L : L;          // (NaN stays NaN)
+    reinterpret_cast<uint4*>(a.out + ((int64_t)rec.row0 + r) * R)[d] =
+        make_uint4(pack2<T>(o[0] * inv, o[1] * inv), pack2<T>(o[2] * inv, o[3] * inv),
+                   pack2<T>(o[4] * inv, o[5] * inv), pack2<T>(o[6] * inv, o[7] * inv));
 }
 
 // ------------------------------------------------------------ host side
@@ -842,12 +860,17 @@ cudaError_t launch(const CUtensorMap& tq, const CUtensorMap& tk, const CUtensorM
     attr[1].id = cudaLaunchAttributeProgrammaticStreamSerialization;
     attr[1].val.programmaticStreamSerializationAllowed = 1;
     cfg.attrs = attr;
-    cfg.numAttrs = 1;
+    cfg.numAttrs = 2;
     e = cudaLaunchKernelEx(&cfg, latent_decode_pair<T, R>, tq, tk, tv, a);
     if (e != cudaSuccess) return e;
+    // (the same split of the SMs' memory as the kernel before: no change of it between)
+    e = cudaFuncSetAttribute(latent_decode_join<T, R>,
+                             cudaFuncAttributePreferredSharedMemoryCarveout,
+                             cudaSharedmemCarveoutMaxShared);
+    if (e != cudaSuccess) return e;
     cudaLaunchConfig_t jc = {};
-    jc.gridDim = dim3((unsigned)a.pairs, (unsigned)((a.slot_rows + kJoinRows - 1) / kJoinRows));
-    jc.blockDim = dim3(R / 4);
+    jc.gridDim = dim3((unsigned)a.pairs, (unsigned)((a.slot_rows + 7) / 8), R / 256);
+    jc.blockDim = dim3(kJoinThreads);
     jc.stream = stream;
     jc.attrs = attr + 1;
     jc.numAttrs = 1;
@@ -937,20 +960,9 @@ pkv_status pkv_latent_attention_decode(
 
     const bool bf16 = dtype == PKV_BF16;
     CUtensorMap tq, tk, tv;
-    {
-        // a CTA's 64 query rows, a box a chunk of 64 elements
-        const PFN_cuTensorMapEncodeTiled_v12000 enc = pkv::map_encoder();
-        const cuuint64_t dims[2] = {(cuuint64_t)W, (cuuint64_t)rows};
-        const cuuint64_t strides[1] = {(cuuint64_t)W * 2};
-        const cuuint32_t box[2] = {64, 64}, estr[2] = {1, 1};
-        if (!enc || enc(&tq, bf16 ? CU_TENSOR_MAP_DATA_TYPE_BFLOAT16 : CU_TENSOR_MAP_DATA_TYPE_FLOAT16,
-                        2, const_cast<void*>(q), dims, strides, box, estr,
-                        CU_TENSOR_MAP_INTERLEAVE_NONE, CU_TENSOR_MAP_SWIZZLE_128B,
-                        CU_TENSOR_MAP_L2_PROMOTION_L2_256B,
-                        CU_TENSOR_MAP_FLOAT_OOB_FILL_NONE) != CUDA_SUCCESS)
-            return pkv::fail(PKV_ERR_CUDA, "%s: tensor map of q", fn);
-    }
     const int64_t places = num_blocks * block_size;
+    if (!chunk_map(&tq, bf16, q, rows, W, W / 64))
+        return pkv::fail(PKV_ERR_CUDA, "%s: tensor map of q", fn);
     if (!chunk_map(&tk, bf16, cache, places, W, latent_dim == 512 ? Cfg<512>::KC : Cfg<256>::KC) ||
         !chunk_map(&tv, bf16, cache, places, W, latent_dim / 128))
         return pkv::fail(PKV_ERR_CUDA, "%s: tensor map of the cache", fn);

@@ -40,14 +40,14 @@ __device__ __forceinline__ uint32_t at_rank(uint32_t addr, uint32_t rank) {
     asm("mapa.shared::cluster.u32 %0, %1, %2;" : "=r"(r) : "r"(addr), "r"(rank));
     return r;
 }
-// Arrivals on a barrier of either CTA of the cluster (at_rank).
+// Arrivals on a barrier of either CTA of the cluster (at_rank).  What they order went
+// through fence_async_smem and is read by the tensor cores: a release at cluster scope
+// would be a fence of all of the thread's memory, about 1000 cycles each.
 __device__ __forceinline__ void mbar_arrive_cluster(uint32_t bar) {
-    asm volatile("mbarrier.arrive.release.cluster.shared::cluster.b64 _, [%0];" ::"r"(bar)
-                 : "memory");
+    asm volatile("mbarrier.arrive.shared::cluster.b64 _, [%0];" ::"r"(bar) : "memory");
 }
 __device__ __forceinline__ void mbar_expect_tx_cluster(uint32_t bar, uint32_t bytes) {
-    asm volatile("mbarrier.arrive.expect_tx.release.cluster.shared::cluster.b64 _, [%0], %1;" ::"r"(bar),
-                 "r"(bytes)
+    asm volatile("mbarrier.arrive.expect_tx.shared::cluster.b64 _, [%0], %1;" ::"r"(bar), "r"(bytes)
                  : "memory");
 }
 
@@ -60,7 +60,7 @@ __device__ __forceinline__ bool mbar_try(uint32_t bar, uint32_t parity) {
     if (SUSPEND)
         asm volatile(
             "{\n\t.reg .pred p;\n\t"
-            "mbarrier.try_wait.parity.acquire.cluster.shared::cta.b64 p, [%1], %2, %3;\n\t"
+            "mbarrier.try_wait.parity.shared::cta.b64 p, [%1], %2, %3;\n\t"
             "selp.u32 %0, 1, 0, p;\n\t}"
             : "=r"(done)
             : "r"(bar), "r"(parity), "r"(1000000u)
@@ -68,7 +68,7 @@ __device__ __forceinline__ bool mbar_try(uint32_t bar, uint32_t parity) {
     else
         asm volatile(
             "{\n\t.reg .pred p;\n\t"
-            "mbarrier.test_wait.parity.acquire.cluster.shared::cta.b64 p, [%1], %2;\n\t"
+            "mbarrier.test_wait.parity.shared::cta.b64 p, [%1], %2;\n\t"
             "selp.u32 %0, 1, 0, p;\n\t}"
             : "=r"(done)
             : "r"(bar), "r"(parity)
@@ -164,6 +164,20 @@ __device__ __forceinline__ void tma_3d_pair(uint32_t dst, const CUtensorMap* map
 }
 
 // ------------------------------------------------------------ products
+// Products and commits are issued by one thread, the one that elect_one chooses: the
+// compiler then knows that the region has a single thread and keeps the operands in the
+// uniform registers that the instructions read.  (A pair's products of N = 256, four and
+// a commit at a time behind a barrier: 66 cycles each, 64 the tensor cores'; from
+// `lane == 0` 131, by a whole warp with an election a product 89.)
+__device__ __forceinline__ bool elect_one() {
+    uint32_t r;
+    asm volatile(
+        "{\n\t.reg .pred p;\n\t"
+        "elect.sync _|p, 0xffffffff;\n\t"
+        "selp.u32 %0, 1, 0, p;\n\t}"
+        : "=r"(r));
+    return r != 0;
+}
 // Shared-memory matrix descriptor: start address, leading and stride byte offsets
 // (16-byte units), the fixed version bit 46, 128-byte swizzle.
 __device__ __forceinline__ uint64_t sdesc(uint32_t addr, uint32_t lbo, uint32_t sbo) {
