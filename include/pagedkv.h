@@ -630,14 +630,21 @@ pkv_status pkv_gather_latent(void* rows, const void* cache, const int32_t* block
  * no memory with the others.  A sequence whose rows leave the tensors, with more
  * than max_query_len rows or max_key_len keys, or with fewer keys than rows is
  * skipped (PKV_DEVERR_BAD_CONTEXT).  Rows of no sequence are left as they are.
+ * Values behind a sequence's last key do not reach its rows; a visible token whose
+ * score or value is not finite may show in the other rows of its step.
+ * workspace: device memory of pkv_latent_prefill_workspace_size(...) bytes, 256-byte
+ * aligned, no initialisation; two calls in flight at once must not share it.  0 bytes
+ * (NULL) where max_key_len is at most 512.
  */
+pkv_status pkv_latent_prefill_workspace_size(int head_dim, int max_query_len, int max_key_len,
+                                             size_t* bytes);
 pkv_status pkv_latent_attention_prefill(
     void* out, const void* q, int64_t q_stride, int64_t q_head_stride, const void* k,
     int64_t k_stride, int64_t k_head_stride, const void* k_rope, int64_t k_rope_stride,
     const void* v, int64_t v_stride, int64_t v_head_stride, const int32_t* query_start,
     const int32_t* key_start, float scale, int num_seqs, int num_heads, int head_dim, int rope_dim,
     int max_query_len, int max_key_len, int num_query_tokens, int num_key_tokens, pkv_dtype dtype,
-    cudaStream_t stream);
+    void* workspace, size_t workspace_bytes, cudaStream_t stream);
 
 /*
  * New tokens over the cache, in the absorbed form.  Sequence s holds

@@ -10,7 +10,8 @@ from .pagedkv import (BlockManager, OutOfBlocks, PagedKVError, alloc_grouped_wor
                       decode_grouped_workspace_size,
                       decode_shared_workspace_size, decode_workspace_size, gather_latent, get_device_error,
                       latent_attention_decode, latent_attention_prefill,
-                      latent_decode_workspace_size, latent_norm_rope_and_cache, lib,
+                      latent_decode_workspace_size, latent_norm_rope_and_cache,
+                      latent_prefill_workspace_size, lib,
                       paged_attention_decode, paged_attention_decode_append, paged_attention_decode_grouped,
                       paged_attention_decode_noalloc, paged_attention_decode_shared,
                       norm_rope_and_cache, paged_attention_prefill,
@@ -25,7 +26,7 @@ __all__ = ["BlockManager", "OutOfBlocks", "PagedKVError", "alloc_grouped_workspa
            "decode_grouped_workspace_size",
            "decode_shared_workspace_size", "decode_workspace_size", "gather_latent", "get_device_error",
            "latent_attention_decode", "latent_attention_prefill", "latent_decode_workspace_size",
-           "latent_norm_rope_and_cache", "lib", "paged_attention_decode",
+           "latent_norm_rope_and_cache", "latent_prefill_workspace_size", "lib", "paged_attention_decode",
            "paged_attention_decode_append", "paged_attention_decode_grouped",
            "paged_attention_decode_noalloc", "paged_attention_decode_shared",
            "norm_rope_and_cache", "paged_attention_prefill",

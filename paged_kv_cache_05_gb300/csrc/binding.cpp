@@ -399,6 +399,7 @@ pkv_status latent_prefill(Reader& r) {
     const at::Tensor& ks = r.tensor("key_start");
     const float scale = r.number("scale");
     const int most_q = r.integer("max_query_len"), most_k = r.integer("max_key_len");
+    const at::Tensor* ws = r.optional("workspace");
     const Common c(q);
     if (q.dim() != 3 || k.dim() != 3 || rope.dim() != 2 || qs.dim() != 1 || qs.size(0) < 1)
         refuse("q must be [num_query_tokens, num_heads, head_dim + rope_dim], k [num_key_tokens, "
@@ -417,11 +418,18 @@ pkv_status latent_prefill(Reader& r) {
               n = size(N, "head_dim"), d = size(P, "rope_dim"), tq = size(Tq, "num_query_tokens"),
               tk = size(Tk, "num_key_tokens");
     const cudaStream_t stream = stream_of(r, c.dev);
+    at::Tensor own;
+    size_t bytes = 0;
+    if (!ws && pkv_latent_prefill_workspace_size(n, most_q, most_k, &bytes) == PKV_OK && bytes > 0) {
+        own = own_workspace(q, c.dev, stream, bytes);
+        ws = &own;
+    }
+    void* wp = ws ? c.whole(*ws, "workspace", at::kByte) : nullptr;
     return launch(c.dev, [&] {
         return pkv_latent_attention_prefill(op, qv.at, qv.token, qv.head, kv.at, kv.token, kv.head,
                                             rv.at, rv.token, vv.at, vv.token, vv.head, qp, kp,
-                                            scale, s, h, n, d, most_q, most_k, tq, tk, c.code,
-                                            stream);
+                                            scale, s, h, n, d, most_q, most_k, tq, tk, c.code, wp,
+                                            ws ? (size_t)ws->numel() : 0, stream);
     });
 }
 

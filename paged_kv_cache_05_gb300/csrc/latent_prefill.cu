@@ -1,109 +1,867 @@
 // Attention of prompts in the expanded form of latent attention: a head's keys are N
-// elements of its own and 64 that all heads share, its values N elements.
+// elements of its own and 64 that all heads share, its values N elements.  Query row i
+// of a sequence (of qlen rows and klen keys) sees the keys t <= klen - qlen + i:
+//   z_t = scale (q[0 .. N) . k_t + q[N ..) . r_t),
+//   out = sum_t 2^(z_t - m) v_t / sum_t 2^(z_t - m)
+// in log2 units, with the running max and sum of the softmax (one pass over the keys).
 //
-// A first version: a block a (token, head) row, a warp a key at a time, the running
-// maximum and sum of the softmax per warp, the warps joined at the end.
+// Bound: the tensor cores: 2 (2 N + 64) operations a (row, key) pair of a head, against
+// one exponential.  An item is 512 query rows of one head, its steps 128 keys each.  The
+// products are pairs' (clusters of two CTAs, cta_group::2, M = 256): each CTA holds 128
+// rows of each of two slots (rows 0-255 and 256-511 of the item) and half of a step's
+// keys and values (64 keys; N / 2 elements of every value), so that a step's 80 KB come
+// to the SMs once for 512 rows.  (One CTA with 256 rows alone would need 31 bytes a
+// cycle of them, of the 36 that the copies reach, and read 128 bytes a cycle of its
+// shared memory, all there are: 96 here.)
+//
+// Twelve warps a CTA: keys, products (the first CTA's), values and queries a warp each,
+// then four of softmax a slot, a thread a row.  The slots take turns: while one's
+// softmax runs, the tensor cores work for the other.  Weights P are written over the
+// scores S in tensor memory, in halves, so that P V begins on the first.  Products
+// complete in order: S of a slot's step means that P V of its step before is done.  The
+// max is raised only past a growth of kRescale, so that most steps leave O alone.
+//
+// The steps of all items are dealt to the pairs in equal runs; parts of an item are left
+// in the workspace and joined by a second kernel.  Where no item has more than
+// kWholeSteps steps, items stay whole and there is no second kernel.
+#include <cuda.h>
 #include <cuda_bf16.h>
 #include <cuda_fp16.h>
 #include <cuda_runtime.h>
 
+#include <cfloat>
 #include <cmath>
 
-#include "launch.cuh"
 #include "pkv_internal.h"
 #include "rows16.cuh"
+#include "tc_ptx.cuh"
+#include "tensor_map.h"
 
 namespace {
 
-using namespace pkv::rows16;
+using namespace pkv::tc;
+using pkv::rows16::aligned;
+using pkv::rows16::overlap;
+using pkv::rows16::pack2;
 
 constexpr int kP = 64;
+constexpr int kRows = 512;            // rows of an item: two slots of a pair's 256
+constexpr int kKeys = 128;            // keys of a step
+constexpr int kThreads = 384;
+constexpr int kMaxPairs = 96;
+constexpr int kWholeSteps = 4;
+constexpr int kBoxRows = 16;          // keys, or values, of a box
+constexpr int kQBoxRows = 32;
+constexpr uint32_t kColO = 256;       // tensor memory: S (and P over it) at 0 and 128, O from here
+
+template <int N>
+struct Cfg {
+    static constexpr int CH = (N + kP) / 64;          // chunks of 64 elements of a key
+    static constexpr int KS = N == 128 ? 3 : 4;       // stages
+    static constexpr int VS = N == 128 ? 3 : 4;
+    static constexpr int Q_CHUNK = 128 * 128;         // a slot's rows of a chunk
+    static constexpr int Q_SLOT = CH * Q_CHUNK;
+    static constexpr int K_CHUNK = 64 * 128;          // a CTA's keys of a chunk
+    static constexpr int K_STAGE = CH * K_CHUNK;
+    static constexpr int V_STAGE = kKeys * 128;       // 64 elements (N = 64: 32 and zeros)
+    static constexpr int Q_OFF = 0;
+    static constexpr int K_OFF = 2 * Q_SLOT;
+    static constexpr int V_OFF = K_OFF + KS * K_STAGE;
+    static constexpr int SMEM = V_OFF + VS * V_STAGE + 1024;   // 1 KiB of alignment slack
+    static_assert(SMEM + 1024 <= 232448, "shared memory");
+};
+
+enum : int {
+    kQFull = 0,      // + slot: its rows are there (first CTA's barrier)
+    kQEmpty = 2,     // + slot: an item's last S formed
+    kKFull = 4,      // + stage (up to 4)
+    kKEmpty = 8,     // + stage
+    kVFull = 12,     // + stage
+    kVEmpty = 16,    // + stage
+    kSFull = 20,     // + slot: S formed, every earlier product done
+    kPFull = 22,     // + 2 slot + half: weights written, O rescaled (first CTA's)
+    kODone = 26,     // + slot: an item's last P V done
+    kORead = 28,     // + slot: its output read from tensor memory (first CTA's)
+    kSpare = 30,
+    kBars = 31
+};
 
 struct Args {
     uint16_t* out;
-    const uint16_t *q, *k, *k_rope, *v;
-    int64_t q_stride, q_head, k_stride, k_head, r_stride, v_stride, v_head;
+    const uint16_t* v;
+    int64_t v_stride, v_head;
     const int32_t *q_start, *k_start;
     float scale_log2;
     int S, H, max_q, max_k, Tq, Tk;
+    int pairs, slot_rows;             // rows of a part in the workspace
+    int out_v8;                       // out is 32-byte aligned: 32-byte stores
+    int whole;                        // items stay whole
+    struct Rec* rec;                  // [pairs]
+    float2* ml;                       // [2 pairs][slot_rows]
+    float* acc;                       // [2 pairs][N / 8][slot_rows][8]
     int32_t* err;
 };
 
+// What is left to join: rows of the output of a head whose parts lie in `parts` slots:
+// `slot`, then the first of each following pair.
+struct Rec {
+    int row0, rows, head, slot, parts, pad[3];
+};
+
+struct Seq {
+    int q0, k0, qlen, klen;           // qlen 0: nothing to do
+    __device__ __forceinline__ bool load(const Args& a, int s) {
+        q0 = a.q_start[s];
+        qlen = a.q_start[s + 1] - q0;
+        k0 = a.k_start[s];
+        klen = a.k_start[s + 1] - k0;
+        if (qlen < 0 || qlen > a.max_q || q0 < 0 || (int64_t)q0 + qlen > a.Tq || klen < qlen ||
+            klen > a.max_k || k0 < 0 || (int64_t)k0 + klen > a.Tk) {
+            qlen = 0;
+            return false;
+        }
+        return true;
+    }
+    __device__ __forceinline__ int items() const { return (qlen + kRows - 1) / kRows; }
+    // steps of item t: to the key of its last row
+    __device__ __forceinline__ int steps(int t) const {
+        return (klen - qlen + min(qlen, (t + 1) * kRows) + kKeys - 1) / kKeys;
+    }
+    __device__ __forceinline__ int64_t head_steps() const {
+        int64_t n = 0;
+        for (int t = 0; t < items(); ++t) n += steps(t);
+        return n;
+    }
+};
+
+// Where a pair's run begins.
+struct Start {
+    int s;
+    Seq q;
+    int64_t off, n;                   // steps before it in the sequence, steps of the run
+    int64_t total;                    // steps of all
+};
+
+// Steps [j0, j1) of an item.
+struct Item {
+    int q0, k0, klen, h;              // first row of all, first key of all
+    int off;                          // the last key that its row 0 sees
+    int rows;
+    int n[2];                         // steps of each slot's rows
+    int j0, j1, steps;
+    int slot;                         // of a part: 0 the run's first, 1 another
+    __device__ __forceinline__ bool whole() const { return j0 == 0 && j1 == steps; }
+    __device__ __forceinline__ bool active(int x) const { return n[x] > j0; }
+    __device__ __forceinline__ int end(int x) const { return min(n[x], j1); }
+};
+
+struct Walker {
+    Seq q, next;
+    int s, h, t, j;
+    int64_t left;
+    bool first;
+    __device__ __forceinline__ void init(const Args& a, const Start& st) {
+        s = st.s;
+        q = st.q;
+        left = st.n;
+        first = true;
+        h = t = j = 0;
+        if (left <= 0) return;
+        if (s + 1 < a.S) next.load(a, s + 1);
+        const int64_t per = q.head_steps();
+        h = (int)(st.off / per);
+        int64_t rest = st.off - h * per;
+        while (rest >= q.steps(t)) rest -= q.steps(t++);
+        j = (int)rest;
+        if (a.whole && j > 0) {                       // the run's items are those that begin in it
+            left -= q.steps(t) - j;
+            j = 0;
+            ++t;
+        }
+    }
+    __device__ __forceinline__ bool get(const Args& a, Item& it) {
+        if (left <= 0) return false;
+        while (t >= q.items()) {
+            t = 0;
+            if (q.qlen > 0 && ++h < a.H) break;
+            h = 0;
+            if (++s >= a.S) return false;
+            q = next;
+            if (s + 1 < a.S) next.load(a, s + 1);
+        }
+        it.q0 = q.q0 + t * kRows;
+        it.k0 = q.k0;
+        it.klen = q.klen;
+        it.h = h;
+        it.off = q.klen - q.qlen + t * kRows;
+        it.rows = min(kRows, q.qlen - t * kRows);
+        it.steps = q.steps(t);
+        it.n[0] = (it.off + min(it.rows, kRows / 2) + kKeys - 1) / kKeys;
+        it.n[1] = it.rows > kRows / 2 ? it.steps : 0;
+        it.j0 = j;
+        it.j1 = a.whole ? it.steps : (int)min((int64_t)it.steps, j + left);
+        it.slot = first ? 0 : 1;
+        first = false;
+        left -= it.j1 - it.j0;
+        j = 0;
+        if (it.j1 == it.steps) ++t;
+        return true;
+    }
+};
+
 template <typename T, int N>
-__global__ void __launch_bounds__(128) latent_prefill_simple(const Args a) {
-    pkv::pdl_wait_then_release();
-    constexpr int E = (N + kP) / 64, V = N / 64;
-    __shared__ float s_m[4], s_l[4], s_o[4][N];
-    const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
-    const int s = blockIdx.z, h = blockIdx.y, i = blockIdx.x;
-    const int q0 = a.q_start[s], k0 = a.k_start[s];
-    const int qlen = a.q_start[s + 1] - q0, klen = a.k_start[s + 1] - k0;
-    if (qlen < 0 || qlen > a.max_q || q0 < 0 || (int64_t)q0 + qlen > a.Tq || klen < qlen ||
-        klen > a.max_k || k0 < 0 || (int64_t)k0 + klen > a.Tk) {
-        if (threadIdx.x == 0 && i == 0 && h == 0) atomicOr(a.err, PKV_DEVERR_BAD_CONTEXT);
-        return;
-    }
-    if (i >= qlen) return;
-    const int64_t row = q0 + i;
-    const uint32_t* q = reinterpret_cast<const uint32_t*>(a.q + row * a.q_stride + h * a.q_head);
-    float2 qv[E], o[V];
-#pragma unroll
-    for (int e = 0; e < E; ++e) qv[e] = unpack2<T>(q[32 * e + lane]);
-#pragma unroll
-    for (int e = 0; e < V; ++e) o[e] = make_float2(0.f, 0.f);
-    float m = -INFINITY, l = 0.f;
-    const int end = klen - qlen + i + 1;
-    for (int t = warp; t < end; t += 4) {
-        const int64_t at = k0 + t;
-        const uint32_t* k = reinterpret_cast<const uint32_t*>(a.k + at * a.k_stride + h * a.k_head);
-        const uint32_t* r = reinterpret_cast<const uint32_t*>(a.k_rope + at * a.r_stride);
-        const uint32_t* v = reinterpret_cast<const uint32_t*>(a.v + at * a.v_stride + h * a.v_head);
-        float z = 0.f;
-#pragma unroll
-        for (int e = 0; e < E; ++e) {
-            const float2 x = unpack2<T>(e < V ? k[32 * e + lane] : r[lane]);
-            z = fmaf(qv[e].x, x.x, fmaf(qv[e].y, x.y, z));
+__global__ void __launch_bounds__(kThreads, 1)
+    latent_prefill_pair(const __grid_constant__ CUtensorMap tm_q,
+                        const __grid_constant__ CUtensorMap tm_k,
+                        const __grid_constant__ CUtensorMap tm_r,
+                        const __grid_constant__ CUtensorMap tm_v, const Args a) {
+    using C = Cfg<N>;
+    extern __shared__ __align__(1024) uint8_t smem_raw[];
+    __shared__ __align__(8) uint64_t bars[kBars];
+    __shared__ uint32_t s_tmem;
+    __shared__ int s_abort;
+    __shared__ Start s_start;
+    __shared__ int64_t s_scan[2][kThreads / 32];
+
+    const int tid = threadIdx.x, warp = tid >> 5, lane = tid & 31;
+    const uint32_t rank = cluster_rank();
+    const int pair = (int)(blockIdx.x >> 1);
+    volatile int* const abort_flag = &s_abort;
+    const uint32_t base = (smem_u32(smem_raw) + 1023) & ~1023u;
+    const uint32_t sQ = base + C::Q_OFF, sK = base + C::K_OFF, sV = base + C::V_OFF;
+    auto bar = [&](int i) { return smem_u32(&bars[i]); };
+
+    asm volatile("griddepcontrol.wait;" ::: "memory");
+    asm volatile("griddepcontrol.launch_dependents;" ::: "memory");
+
+    // the pair's run of the steps: [b, e) of all (the lengths are loaded once where
+    // there is a thread a sequence, and on their way while the barriers are made)
+    Seq mine;
+    mine.qlen = 0;
+    bool good = tid >= a.S || mine.load(a, tid);
+    if (warp == 1) {
+        if (lane == 0) {
+            for (int i = 0; i < kBars; ++i) {
+                const bool two = i < kQEmpty || (i >= kKFull && i < kKEmpty) ||
+                                 (i >= kVFull && i < kVEmpty);
+                const bool warps = (i >= kPFull && i < kODone) || (i >= kORead && i < kSpare);
+                mbar_init(bar(i), two ? 2 : warps ? 8 : 1);
+            }
+            mbar_init_fence();
+            s_abort = 0;
         }
-#pragma unroll
-        for (int x = 16; x > 0; x >>= 1) z += __shfl_xor_sync(0xffffffffu, z, x);
-        z *= a.scale_log2;
-        const float mn = fmaxf(m, z), c = exp2f(m - mn), p = exp2f(z - mn);
-        m = mn;
-        l = l * c + p;
-#pragma unroll
-        for (int e = 0; e < V; ++e) {
-            const float2 x = unpack2<T>(v[32 * e + lane]);
-            o[e] = make_float2(fmaf(o[e].x, c, p * x.x), fmaf(o[e].y, c, p * x.y));
+        __syncwarp();
+        alloc_pair(smem_u32(&s_tmem));
+    } else if (warp == 0 && lane == 0) {
+        prefetch_map(&tm_q);
+        prefetch_map(&tm_k);
+        prefetch_map(&tm_r);
+        prefetch_map(&tm_v);
+    }
+    {
+        constexpr int kWarps = kThreads / 32;
+        // this thread's steps, and those of the threads before it in the warp
+        int64_t n = mine.head_steps() * a.H, incl = n, rest = 0;
+        for (int s = tid + kThreads; s < a.S; s += kThreads) {
+            Seq q;
+            good &= q.load(a, s);
+            rest += q.head_steps() * a.H;
         }
-    }
-    if (lane == 0) {
-        s_m[warp] = m;
-        s_l[warp] = l;
-    }
+        if (!good && blockIdx.x == 0) atomicOr(a.err, PKV_DEVERR_BAD_CONTEXT);
 #pragma unroll
-    for (int e = 0; e < V; ++e) {
-        s_o[warp][2 * (32 * e + lane)] = o[e].x;
-        s_o[warp][2 * (32 * e + lane) + 1] = o[e].y;
+        for (int o = 1; o < 32; o <<= 1) {
+            const int64_t y = __shfl_up_sync(0xffffffffu, incl, o);
+            if (lane >= o) incl += y;
+        }
+        if (a.S > kThreads) {
+#pragma unroll
+            for (int o = 16; o > 0; o >>= 1) rest += __shfl_xor_sync(0xffffffffu, rest, o);
+        }
+        if (lane == 31) {
+            s_scan[0][warp] = incl;
+            s_scan[1][warp] = rest;
+        }
+        if (tid == 0) s_start.n = 0;
+        fence_before();
+        __syncthreads();
+        asm volatile("barrier.cluster.arrive.release.aligned;" ::: "memory");
+        int64_t total = 0, before = 0;
+        for (int w = 0; w < kWarps; ++w) {
+            if (w < warp) incl += s_scan[0][w];
+            before += s_scan[0][w];
+            total += s_scan[0][w] + s_scan[1][w];
+        }
+        const int64_t np = min((int64_t)a.pairs, total);
+        const int64_t b = pair < np ? total * pair / np : 0;
+        const int64_t e = pair < np ? total * (pair + 1) / np : 0;
+        auto found = [&](int s) {                // the sequence that holds step b
+            if (e > b && incl > b && incl - n <= b)
+                s_start = Start{s, mine, b - (incl - n), e - b, total};
+        };
+        found(tid);
+        for (int s0 = kThreads; s0 < a.S && before <= b && e > b; s0 += kThreads) {
+            mine.qlen = 0;
+            if (s0 + tid < a.S) mine.load(a, s0 + tid);
+            n = incl = mine.head_steps() * a.H;
+#pragma unroll
+            for (int o = 1; o < 32; o <<= 1) {
+                const int64_t y = __shfl_up_sync(0xffffffffu, incl, o);
+                if (lane >= o) incl += y;
+            }
+            __syncthreads();
+            if (lane == 31) s_scan[0][warp] = incl;
+            __syncthreads();
+            incl += before;
+            for (int w = 0; w < kWarps; ++w) {
+                if (w < warp) incl += s_scan[0][w];
+                before += s_scan[0][w];
+            }
+            found(s0 + tid);
+        }
+        // (nothing to join, until a part is left)
+        if (tid == 0 && rank == 0 && !a.whole) a.rec[pair].rows = 0;
     }
     __syncthreads();
-    float M = -INFINITY, L = 0.f;
-    for (int x = 0; x < 4; ++x) M = fmaxf(M, s_m[x]);
-    for (int x = 0; x < 4; ++x) L += M == -INFINITY ? 0.f : s_l[x] * exp2f(s_m[x] - M);
-    uint32_t* out = reinterpret_cast<uint32_t*>(a.out + (row * a.H + h) * N);
-    for (int d = threadIdx.x; d < N / 2; d += 128) {
-        float x = 0.f, y = 0.f;
-        for (int w = 0; w < 4; ++w) {
-            const float f = s_m[w] == -INFINITY ? 0.f : exp2f(s_m[w] - M);
-            x = fmaf(f, s_o[w][2 * d], x);
-            y = fmaf(f, s_o[w][2 * d + 1], y);
+    asm volatile("barrier.cluster.wait.acquire.aligned;" ::: "memory");
+    fence_after();
+    const uint32_t tmem = s_tmem;
+    const Start start = s_start;
+    bool ok = true;
+    auto fail = [&]() {
+        if (!*abort_flag) atomicOr(a.err, PKV_DEVERR_TIMEOUT);
+        *abort_flag = 1;
+    };
+
+    if (warp == 0) {
+        // ================================================= keys
+        Walker wk;
+        wk.init(a, start);
+        Item it;
+        int kc = 0;
+        constexpr int BOXES = 64 / kBoxRows;
+        const int c = lane / BOXES, r = (lane - c * BOXES) * kBoxRows;   // a lane's box
+        while (ok && wk.get(a, it)) {
+            for (int j = it.j0; j < it.j1; ++j, ++kc) {
+                const int st = kc % C::KS, n = kc / C::KS;
+                if (n > 0 && !warp_wait(bar(kKEmpty + st), (uint32_t)((n - 1) & 1), abort_flag)) {
+                    ok = false;
+                    break;
+                }
+                const uint32_t full = at_rank(bar(kKFull + st), 0);
+                if (lane == 0) mbar_expect_tx_cluster(full, C::K_STAGE);
+                __syncwarp();
+                const uint32_t to = sK + st * C::K_STAGE + c * C::K_CHUNK + r * 128;
+                const int key = it.k0 + j * kKeys + 64 * (int)rank + r;
+                if (c < C::CH - 1) tma_3d_pair(to, &tm_k, c * 64, it.h, key, full);
+                else if (c == C::CH - 1) tma_3d_pair(to, &tm_r, 0, 0, key, full);
+            }
         }
-        out[d] = pack2<T>(x / L, y / L);
+        if (!ok) fail();
+    } else if (warp == 2) {
+        // ================================================= values
+        Walker wk;
+        wk.init(a, start);
+        Item it;
+        int vc = 0;
+        constexpr int BOXES = kKeys / kBoxRows;
+        while (ok && wk.get(a, it)) {
+            for (int j = it.j0; j < it.j1; ++j, ++vc) {
+                const int st = vc % C::VS, n = vc / C::VS;
+                if (n > 0 && !warp_wait(bar(kVEmpty + st), (uint32_t)((n - 1) & 1), abort_flag)) {
+                    ok = false;
+                    break;
+                }
+                const uint32_t full = at_rank(bar(kVFull + st), 0);
+                const uint32_t stage = sV + st * C::V_STAGE;
+                const int left = it.klen - j * kKeys;        // keys of the step and after
+                // the box that holds the sequence's last key and others' rows behind it,
+                // which may be anything: copied by the warp, zeros behind the last
+                const int tail = left < kKeys && left % kBoxRows ? left / kBoxRows : -1;
+                if (tail >= 0) {
+                    const uint16_t* from = a.v + (int64_t)(it.k0 + j * kKeys + tail * kBoxRows) * a.v_stride +
+                                           it.h * a.v_head + (int)rank * (N / 2);
+                    for (int i = lane; i < kBoxRows * 8; i += 32) {
+                        const int r = i >> 3, p = i & 7;
+                        uint4 w = make_uint4(0u, 0u, 0u, 0u);
+                        if (r < left % kBoxRows && p < N / 16)
+                            w = *reinterpret_cast<const uint4*>(from + r * a.v_stride + p * 8);
+                        st_shared_v4(stage + (tail * kBoxRows + r) * 128 + ((p ^ (r & 7)) << 4), w.x,
+                                     w.y, w.z, w.w);
+                    }
+                    fence_async_smem();
+                    __syncwarp();
+                }
+                if (lane == 0)
+                    mbar_expect_tx_cluster(full, C::V_STAGE - (tail >= 0 ? kBoxRows * 128 : 0));
+                __syncwarp();
+                // boxes behind the last key: past the tensor's end, zeros
+                if (lane < BOXES && lane != tail)
+                    tma_3d_pair(stage + lane * kBoxRows * 128, &tm_v, (int)rank * (N / 2), it.h,
+                                lane * kBoxRows < left ? it.k0 + j * kKeys + lane * kBoxRows : a.Tk,
+                                full);
+            }
+        }
+        if (!ok) fail();
+    } else if (warp == 3) {
+        // ================================================= queries
+        Walker wk;
+        wk.init(a, start);
+        Item it;
+        int count[2] = {0, 0};
+        constexpr int BOXES = 128 / kQBoxRows;
+        const int c = lane / BOXES, r = (lane - c * BOXES) * kQBoxRows;
+        while (ok && wk.get(a, it)) {
+            for (int x = 0; x < 2; ++x) {
+                if (!it.active(x)) continue;
+                const int n = count[x]++;
+                if (n > 0 && !warp_wait(bar(kQEmpty + x), (uint32_t)((n - 1) & 1), abort_flag)) {
+                    ok = false;
+                    break;
+                }
+                const uint32_t full = at_rank(bar(kQFull + x), 0);
+                if (lane == 0) mbar_expect_tx_cluster(full, C::Q_SLOT);
+                __syncwarp();
+                if (c < C::CH)
+                    tma_3d_pair(sQ + x * C::Q_SLOT + c * C::Q_CHUNK + r * 128, &tm_q, c * 64, it.h,
+                                it.q0 + x * 256 + 128 * (int)rank + r, full);
+            }
+        }
+        if (!ok) fail();
+    } else if (warp == 1) {
+        // ================================================= products
+        if (rank == 0 && elect_one()) {
+            constexpr uint32_t ID_S = idesc(El<T>::kType, false, kKeys, 256);
+            constexpr uint32_t ID_PV = idesc(El<T>::kType, true, N, 256);
+            const uint64_t dQ = sdesc(sQ, 16, 1024), dK = sdesc(sK, 16, 1024),
+                           dV = sdesc(sV, 1024, 1024);
+            Walker wk;
+            wk.init(a, start);
+            Item it, nit;
+            int kc = 0, vc = 0;
+            int qs[2] = {0, 0}, ps[2] = {0, 0}, os[2] = {0, 0};
+            // S of slot x for step j of item i from the keys in stage kc
+            auto form_s = [&](int x, const Item& i, int j) {
+                if (j == i.j0 && !mbar_wait<false>(bar(kQFull + x), (uint32_t)(qs[x]++ & 1), abort_flag))
+                    return false;
+                fence_after();
+                const uint64_t da = dQ + (uint64_t)((x * C::Q_SLOT) >> 4);
+                const uint64_t db = dK + (uint64_t)(((kc % C::KS) * C::K_STAGE) >> 4);
+#pragma unroll
+                for (int e = 0; e < C::CH * 4; ++e)
+                    umma_pair(tmem + x * 128, da + (((e >> 2) * C::Q_CHUNK + (e & 3) * 32) >> 4),
+                              db + (((e >> 2) * C::K_CHUNK + (e & 3) * 32) >> 4), ID_S, e > 0);
+                commit_pair(bar(kSFull + x));
+                if (j == i.end(x) - 1) commit_pair(bar(kQEmpty + x));
+                return true;
+            };
+            auto keys = [&]() {
+                return mbar_wait<false>(bar(kKFull + kc % C::KS), (uint32_t)((kc / C::KS) & 1), abort_flag);
+            };
+            bool have = wk.get(a, nit);
+            int j = 0;
+            if (have) {
+                it = nit;
+                j = it.j0;
+                ok = keys();
+                for (int x = 0; ok && x < 2; ++x)
+                    if (j < it.end(x)) ok = form_s(x, it, j);
+                commit_pair(bar(kKEmpty + kc % C::KS));
+                ++kc;
+            }
+            while (ok && have) {
+                // the step after this one
+                const bool same = j + 1 < it.j1;
+                const int nj = same ? j + 1 : 0;
+                bool more = same;
+                if (!same) more = wk.get(a, nit);
+                const int nextj = same ? nj : nit.j0;
+                bool got_k = false, got_v = false;
+                for (int x = 0; ok && x < 2; ++x) {
+                    if (j < it.end(x)) {
+                        const uint64_t db = dV + (uint64_t)(((vc % C::VS) * C::V_STAGE) >> 4);
+                        for (int half = 0; ok && half < 2; ++half) {
+                            ok = mbar_wait<false>(bar(kPFull + 2 * x + half), (uint32_t)(ps[x] & 1), abort_flag);
+                            if (ok && half == 0 && j == it.j0 && os[x] > 0)
+                                ok = mbar_wait<false>(bar(kORead + x), (uint32_t)((os[x] - 1) & 1), abort_flag);
+                            if (ok && !got_v)
+                                ok = got_v = mbar_wait<false>(bar(kVFull + vc % C::VS),
+                                                              (uint32_t)((vc / C::VS) & 1), abort_flag);
+                            if (!ok) break;
+                            fence_after();
+#pragma unroll
+                            for (int e = 0; e < 4; ++e)
+                                umma_ts_pair(tmem + kColO + x * N, tmem + x * 128 + half * 32 + e * 8,
+                                             db + ((half * 8192 + e * 2048) >> 4), ID_PV,
+                                             j > it.j0 || half > 0 || e > 0);
+                        }
+                        ++ps[x];
+                        if (ok && j == it.end(x) - 1) {
+                            commit_pair(bar(kODone + x));
+                            ++os[x];
+                        }
+                    }
+                    if (ok && more && nextj < (same ? it.end(x) : nit.end(x))) {
+                        if (!got_k) ok = got_k = keys();
+                        if (ok) ok = form_s(x, same ? it : nit, nextj);
+                    }
+                }
+                if (!ok) break;
+                commit_pair(bar(kVEmpty + vc % C::VS));
+                ++vc;
+                if (more) {
+                    commit_pair(bar(kKEmpty + kc % C::KS));
+                    ++kc;
+                }
+                if (!same) it = nit;
+                j = nextj;
+                have = more;
+            }
+            if (!ok) {
+                fail();
+                // what was issued completes before the tensor memory goes
+                volatile int never = 0;
+                commit_pair(bar(kSpare));
+                mbar_wait(bar(kSpare), 0, &never);
+            }
+        }
+        __syncwarp();
+    } else {
+        // ================================================= softmax
+        const int x = warp >= 8, quad = warp & 3;
+        const uint32_t lanes = (uint32_t)(quad * 32) << 16;
+        const uint32_t tS = tmem + lanes + x * 128, tO = tmem + lanes + kColO + x * N;
+        const uint32_t pfull = at_rank(bar(kPFull + 2 * x), 0), oread = at_rank(bar(kORead + x), 0);
+        const int rw = x * 256 + (int)rank * 128 + quad * 32;     // the warp's first row of an item
+        const int row = rw + lane;
+        Walker wk;
+        wk.init(a, start);
+        Item it;
+        int sc = 0, oc = 0;
+        const float scale = a.scale_log2;
+        const uint64_t scale2 = f2(scale, scale);
+        while (wk.get(a, it)) {
+            const bool live = rw < it.rows;                  // the warp has rows
+            const int64_t slot = pair * 2 + it.slot;
+            const bool whole = it.whole();
+            float m = -INFINITY;
+            uint64_t l2 = 0;                                 // two partial sums
+            for (int j = it.j0; j < it.end(x); ++j, ++sc) {
+                ok = ok && warp_wait(bar(kSFull + x), (uint32_t)(sc & 1), abort_flag);
+                fence_after();
+                if (live) {
+                    uint32_t z[2][64];
+                    ld64(tS, z[0]);
+                    ld64(tS + 64, z[1]);
+                    ld_wait(z[0]);
+                    ld_wait(z[1]);
+                    const int n = it.off + row + 1 - j * kKeys;   // keys of the step that it sees
+                    if (it.off + rw + 1 - j * kKeys < kKeys) {
+                        // a hidden key's score: lowest of the scaled ones
+                        const float hide = scale < 0.f ? INFINITY : -INFINITY;
+#pragma unroll
+                        for (int e = 0; e < 128; ++e)
+                            if (e >= n) z[e >> 6][e & 63] = __float_as_uint(hide);
+                    }
+                    float top = __uint_as_float(z[0][0]);
+                    if (scale >= 0.f) {
+                        float t1 = __uint_as_float(z[1][0]);
+#pragma unroll
+                        for (int e = 1; e < 63; e += 2) {
+                            top = max3(top, __uint_as_float(z[0][e]), __uint_as_float(z[0][e + 1]));
+                            t1 = max3(t1, __uint_as_float(z[1][e]), __uint_as_float(z[1][e + 1]));
+                        }
+                        top = fmaxf(max3(top, __uint_as_float(z[0][63]), __uint_as_float(z[1][63])), t1);
+                    } else {
+#pragma unroll
+                        for (int e = 1; e < 128; ++e) top = fminf(top, __uint_as_float(z[e >> 6][e & 63]));
+                    }
+                    // (a row whose scores are all hidden has none: scale 0 times infinity)
+                    top = fabsf(top) == INFINITY ? -INFINITY : top * scale;
+                    float alpha = 1.f;
+                    if (top > m + El<T>::kRescale || m == -INFINITY) {
+                        // raised a little past the largest for lifted weights, so that
+                        // scores' rounding, whatever their size, takes none past fp16
+                        const float mn = El<T>::kLift > 0.f && top > -INFINITY
+                                             ? fmaf(fabsf(top), 0x1p-22f, top) : top;
+                        if (mn > m) {
+                            alpha = ex2(m - mn);
+                            m = mn;
+                        }
+                    }
+                    if (j > it.j0 && __any_sync(0xffffffffu, alpha != 1.f)) {
+                        const uint64_t al2 = f2(alpha, alpha);
+#pragma unroll 1
+                        for (int c = 0; c < N; c += 16) {
+                            uint32_t o[16];
+                            ld16(tO + c, o);
+                            ld_wait(o);
+#pragma unroll
+                            for (int e = 0; e < 8; ++e) {
+                                float p, q;
+                                f2_split(mul2(f2(__uint_as_float(o[2 * e]), __uint_as_float(o[2 * e + 1])),
+                                              al2),
+                                         p, q);
+                                o[2 * e] = __float_as_uint(p);
+                                o[2 * e + 1] = __float_as_uint(q);
+                            }
+                            st16(tO + c, o);
+                        }
+                    }
+                    const float minus = m == -INFINITY ? 0.f : El<T>::kLift - m;
+                    const uint64_t minus2 = f2(minus, minus);
+                    uint64_t sum[2] = {0, 0};
+#pragma unroll
+                    for (int half = 0; half < 2; ++half) {
+                        uint32_t w[32];
+#pragma unroll
+                        for (int e = 0; e < 32; ++e) {
+                            float p, q;
+                            f2_split(fma2(f2(__uint_as_float(z[half][2 * e]),
+                                             __uint_as_float(z[half][2 * e + 1])),
+                                          scale2, minus2),
+                                     p, q);
+                            w[e] = El<T>::pack(ex2(p), ex2(q));
+                            sum[e & 1] = add2(sum[e & 1], El<T>::unpack(w[e]));
+                        }
+                        st32(tS + half * 32, w);
+                        st_wait();
+                        fence_before();
+                        __syncwarp();
+                        if (lane == 0) mbar_arrive_cluster(pfull + half * 8);
+                    }
+                    l2 = fma2(l2, f2(alpha, alpha), add2(sum[0], sum[1]));
+                } else {
+                    fence_before();
+                    __syncwarp();
+                    if (lane == 0) {
+                        mbar_arrive_cluster(pfull);
+                        mbar_arrive_cluster(pfull + 8);
+                    }
+                }
+            }
+            // the slot's output
+            float p, q;
+            f2_split(l2, p, q);
+            const float l = p + q;
+            const bool mine = row < it.rows && ok;
+            if (mine && !whole) a.ml[slot * a.slot_rows + row] = make_float2(m, l);
+            if (it.active(x)) {
+                ok = ok && warp_wait(bar(kODone + x), (uint32_t)(oc++ & 1), abort_flag);
+                fence_after();
+                if (live) {
+                    const float inv = 1.f / l;
+                    uint16_t* orow = a.out + ((int64_t)(it.q0 + row) * a.H + it.h) * N;
+                    float* prow = a.acc + (slot * (N / 8) * a.slot_rows + row) * 8;
+                    uint32_t next[32];
+                    ld32(tO, next);
+#pragma unroll 1
+                    for (int c = 0; c < N; c += 32) {
+                        uint32_t o[32];
+                        ld_wait(next);
+#pragma unroll
+                        for (int e = 0; e < 32; ++e) o[e] = next[e];
+                        if (c + 32 < N) ld32(tO + c + 32, next);
+                        if (!mine) continue;
+                        if (whole) {
+                            uint32_t w[16];
+#pragma unroll
+                            for (int e = 0; e < 16; ++e)
+                                w[e] = El<T>::pack(__uint_as_float(o[2 * e]) * inv,
+                                                   __uint_as_float(o[2 * e + 1]) * inv);
+                            if (a.out_v8) {
+                                st_global_v8(orow + c, w);
+                                st_global_v8(orow + c + 16, w + 8);
+                            } else {
+#pragma unroll
+                                for (int e = 0; e < 4; ++e)
+                                    *reinterpret_cast<uint4*>(orow + c + 8 * e) =
+                                        make_uint4(w[4 * e], w[4 * e + 1], w[4 * e + 2], w[4 * e + 3]);
+                            }
+                        } else {
+#pragma unroll
+                            for (int e = 0; e < 4; ++e)
+                                st_global_v8(prow + (int64_t)(c / 8 + e) * a.slot_rows * 8, o + 8 * e);
+                        }
+                    }
+                }
+                fence_before();
+                __syncwarp();
+                if (lane == 0) mbar_arrive_cluster(oread);
+            }
+            // the first part of an item that goes on in the next pairs' runs
+            if (!whole && it.j0 == 0 && rank == 0 && warp == 4 && lane == 0) {
+                const int64_t total = start.total, np = min((int64_t)a.pairs, total);
+                const int64_t e = total * (pair + 1) / np;   // first step after this run
+                const int64_t z = e + (it.steps - it.j1) - 1;    // the item's last
+                int64_t last = z * np / total;               // the run that holds it
+                while (last + 1 < np && total * (last + 1) / np <= z) ++last;
+                while (total * last / np > z) --last;
+                a.rec[pair] = Rec{it.q0, ok ? it.rows : 0, it.h, pair * 2 + it.slot,
+                                  (int)(last - pair) + 1, {0, 0, 0}};
+            }
+        }
+        if (!ok && lane == 0) fail();
     }
+
+    __syncwarp();
+    if (*abort_flag) {
+        // copies in flight end before the CTA does
+        const uint64_t t = global_ns();
+        while (global_ns() - t < 200000ull) __nanosleep(1000);
+    }
+    fence_before();
+    __syncthreads();
+    cluster_sync();
+    if (warp == 1) {
+        fence_after();
+        dealloc_pair(tmem);
+    }
+}
+
+// Joins the parts of an item: with M the largest running max,
+//   out = sum_k 2^(m_k - M) acc_k / sum_k 2^(m_k - M) l_k.
+// blockIdx.x: the pair that left the first part; a block takes 8 rows and 256 / 8
+// eights of elements (N = 64: 32 rows), a thread 8 elements of a row, in one pass over
+// the parts, kJoinParts of them loaded at a time.
+constexpr int kJoinThreads = 256;
+constexpr int kJoinParts = 4;
+
+template <typename T, int N>
+__global__ void __launch_bounds__(kJoinThreads) latent_prefill_join(const Args a) {
+    asm volatile("griddepcontrol.wait;" ::: "memory");
+    asm volatile("griddepcontrol.launch_dependents;" ::: "memory");
+    constexpr int kRowsAtOnce = kJoinThreads / (N / 8);
+    const Rec rec = a.rec[blockIdx.x];
+    const int r = blockIdx.y * kRowsAtOnce + (int)threadIdx.x % kRowsAtOnce;
+    const int d = threadIdx.x / kRowsAtOnce;                 // eight elements
+    // what a kernel that gave up left may be anything: nothing out of range
+    if (r >= rec.rows || rec.rows > a.slot_rows || rec.parts < 1 || rec.slot < 0 ||
+        rec.slot / 2 + rec.parts > a.pairs || rec.row0 < 0 || rec.head < 0 || rec.head >= a.H ||
+        (int64_t)rec.row0 + rec.rows > a.Tq)
+        return;
+    float M = -INFINITY, L = 0.f;
+    float o[8] = {};
+    for (int k0 = 0; k0 < rec.parts; k0 += kJoinParts) {
+        float2 ml[kJoinParts];
+        float4 v[kJoinParts][2];
+#pragma unroll
+        for (int k = 0; k < kJoinParts; ++k) {
+            ml[k] = make_float2(-INFINITY, 0.f);
+            if (k0 + k < rec.parts) {
+                const int64_t slot = k0 + k == 0 ? rec.slot : (rec.slot / 2 + k0 + k) * 2;
+                ml[k] = a.ml[slot * a.slot_rows + r];
+                const float4* p = reinterpret_cast<const float4*>(
+                    a.acc + ((slot * (N / 8) + d) * a.slot_rows + r) * 8);
+                v[k][0] = p[0];
+                v[k][1] = p[1];
+            }
+        }
+        float top = M;
+#pragma unroll
+        for (int k = 0; k < kJoinParts; ++k) top = fmaxf(top, ml[k].x);
+        const float f0 = M == -INFINITY ? 0.f : ex2(M - top);
+        M = top;
+        L *= f0;
+#pragma unroll
+        for (int e = 0; e < 8; ++e) o[e] *= f0;
+#pragma unroll
+        for (int k = 0; k < kJoinParts; ++k) {
+            // a part without a key that the row sees: nothing, whatever its output holds
+            if (ml[k].x == -INFINITY && ml[k].y == 0.f) continue;
+            const float f = ex2(ml[k].x - M);
+            L = fmaf(f, ml[k].y, L);
+            const float x[8] = {v[k][0].x, v[k][0].y, v[k][0].z, v[k][0].w,
+                                v[k][1].x, v[k][1].y, v[k][1].z, v[k][1].w};
+#pragma unroll
+            for (int e = 0; e < 8; ++e) o[e] = fmaf(f, x[e], o[e]);
+        }
+    }
+    const float inv = 1.f / L;
+    reinterpret_cast<uint4*>(a.out + (((int64_t)rec.row0 + r) * a.H + rec.head) * N)[d] =
+        make_uint4(pack2<T>(o[0] * inv, o[1] * inv), pack2<T>(o[2] * inv, o[3] * inv),
+                   pack2<T>(o[4] * inv, o[5] * inv), pack2<T>(o[6] * inv, o[7] * inv));
+}
+
+// ------------------------------------------------------------ host side
+struct Layout {
+    size_t ml, acc, total;
+    int rows;
+};
+Layout layout(int N, int max_q, int max_k) {
+    Layout l = {};
+    if (max_k <= kWholeSteps * kKeys) return l;       // items stay whole
+    l.rows = max_q < kRows ? (max_q > 0 ? max_q : 1) : kRows;
+    l.ml = pkv::align_up(sizeof(Rec) * kMaxPairs, 256);
+    l.acc = pkv::align_up(l.ml + 8 * (size_t)(2 * kMaxPairs) * l.rows, 256);
+    l.total = l.acc + 4 * (size_t)(2 * kMaxPairs) * l.rows * N;
+    return l;
+}
+
+// Tokens of heads of `row` elements, as boxes of 64 elements of box_rows tokens of a head.
+bool head_map(CUtensorMap* m, bool bf16, const void* at, int row, int heads, int64_t tokens,
+              int64_t token_stride, int64_t head_stride, int box_rows) {
+    const PFN_cuTensorMapEncodeTiled_v12000 fn = pkv::map_encoder();
+    if (!fn) return false;
+    const cuuint64_t dims[3] = {(cuuint64_t)row, (cuuint64_t)heads, (cuuint64_t)tokens};
+    const cuuint64_t strides[2] = {(cuuint64_t)head_stride * 2, (cuuint64_t)token_stride * 2};
+    const cuuint32_t box[3] = {64, 1, (cuuint32_t)box_rows};
+    const cuuint32_t estr[3] = {1, 1, 1};
+    return fn(m, bf16 ? CU_TENSOR_MAP_DATA_TYPE_BFLOAT16 : CU_TENSOR_MAP_DATA_TYPE_FLOAT16, 3,
+              const_cast<void*>(at), dims, strides, box, estr, CU_TENSOR_MAP_INTERLEAVE_NONE,
+              CU_TENSOR_MAP_SWIZZLE_128B, CU_TENSOR_MAP_L2_PROMOTION_L2_128B,
+              CU_TENSOR_MAP_FLOAT_OOB_FILL_NONE) == CUDA_SUCCESS;
+}
+
+template <typename T, int N>
+cudaError_t launch(const CUtensorMap& tq, const CUtensorMap& tk, const CUtensorMap& tr,
+                   const CUtensorMap& tv, const Args& a, cudaStream_t stream) {
+    cudaError_t e = cudaFuncSetAttribute(latent_prefill_pair<T, N>,
+                                         cudaFuncAttributeMaxDynamicSharedMemorySize, Cfg<N>::SMEM);
+    if (e != cudaSuccess) return e;
+    cudaLaunchConfig_t cfg = {};
+    cfg.gridDim = dim3((unsigned)(2 * a.pairs));
+    cfg.blockDim = dim3(kThreads);
+    cfg.dynamicSmemBytes = Cfg<N>::SMEM;
+    cfg.stream = stream;
+    cudaLaunchAttribute attr[2];
+    attr[0].id = cudaLaunchAttributeClusterDimension;
+    attr[0].val.clusterDim.x = 2;
+    attr[0].val.clusterDim.y = 1;
+    attr[0].val.clusterDim.z = 1;
+    attr[1].id = cudaLaunchAttributeProgrammaticStreamSerialization;
+    attr[1].val.programmaticStreamSerializationAllowed = 1;
+    cfg.attrs = attr;
+    cfg.numAttrs = 2;
+    e = cudaLaunchKernelEx(&cfg, latent_prefill_pair<T, N>, tq, tk, tr, tv, a);
+    if (e != cudaSuccess || a.whole) return e;
+    // (the same split of the SMs' memory as the kernel before: no change of it between)
+    e = cudaFuncSetAttribute(latent_prefill_join<T, N>,
+                             cudaFuncAttributePreferredSharedMemoryCarveout,
+                             cudaSharedmemCarveoutMaxShared);
+    if (e != cudaSuccess) return e;
+    cudaLaunchConfig_t jc = {};
+    constexpr int kRowsAtOnce = kJoinThreads / (N / 8);
+    jc.gridDim = dim3((unsigned)a.pairs, (unsigned)((a.slot_rows + kRowsAtOnce - 1) / kRowsAtOnce));
+    jc.blockDim = dim3(kJoinThreads);
+    jc.stream = stream;
+    jc.attrs = attr + 1;
+    jc.numAttrs = 1;
+    return cudaLaunchKernelEx(&jc, latent_prefill_join<T, N>, a);
 }
 
 }  // namespace
 
 extern "C" {
+
+pkv_status pkv_latent_prefill_workspace_size(int head_dim, int max_query_len, int max_key_len,
+                                             size_t* bytes) {
+    const char* fn = "pkv_latent_prefill_workspace_size";
+    if (!bytes) return pkv::fail(PKV_ERR_INVALID, "%s: bytes is NULL", fn);
+    if ((head_dim != 64 && head_dim != 128) || max_query_len < 0 || max_key_len < 0)
+        return pkv::fail(PKV_ERR_INVALID, "%s: bad sizes", fn);
+    *bytes = layout(head_dim, max_query_len, max_key_len).total;
+    return PKV_OK;
+}
 
 pkv_status pkv_latent_attention_prefill(
     void* out, const void* q, int64_t q_stride, int64_t q_head_stride, const void* k,
@@ -111,7 +869,7 @@ pkv_status pkv_latent_attention_prefill(
     const void* v, int64_t v_stride, int64_t v_head_stride, const int32_t* query_start,
     const int32_t* key_start, float scale, int num_seqs, int num_heads, int head_dim, int rope_dim,
     int max_query_len, int max_key_len, int num_query_tokens, int num_key_tokens, pkv_dtype dtype,
-    cudaStream_t stream) {
+    void* workspace, size_t workspace_bytes, cudaStream_t stream) {
     const char* fn = "pkv_latent_attention_prefill";
     if (num_seqs < 0 || num_seqs > 65535)
         return pkv::fail(PKV_ERR_INVALID, "%s: num_seqs must be in [0, 65535]", fn);
@@ -122,19 +880,23 @@ pkv_status pkv_latent_attention_prefill(
     if (rope_dim != kP) return pkv::fail(PKV_ERR_INVALID, "%s: rope_dim must be 64", fn);
     if (max_query_len < 0 || max_key_len < 0 || num_query_tokens < 0 || num_key_tokens < 0)
         return pkv::fail(PKV_ERR_INVALID, "%s: bad sizes", fn);
+    // the tiled copies address tokens with 32-bit coordinates
+    if (num_query_tokens > (1 << 30) || num_key_tokens > (1 << 30))
+        return pkv::fail(PKV_ERR_INVALID, "%s: at most 2^30 tokens", fn);
     if (dtype != PKV_F16 && dtype != PKV_BF16)
         return pkv::fail(PKV_ERR_INVALID, "%s: unknown dtype", fn);
     const float scale_log2 = (float)(1.4426950408889634 * scale);
     if (!std::isfinite(scale_log2))
         return pkv::fail(PKV_ERR_INVALID, "%s: scale is not finite", fn);
     const struct {
-        int64_t token, head, row;
+        const void* at;
+        int64_t token, head, row, heads, tokens;
         const char* name;
-    } st[4] = {{q_stride, q_head_stride, head_dim + kP, "q"},
-               {k_stride, k_head_stride, head_dim, "k"},
-               {k_rope_stride, kP, kP, "k_rope"},
-               {v_stride, v_head_stride, head_dim, "v"}};
-    for (const auto& x : st)
+    } in[4] = {{q, q_stride, q_head_stride, head_dim + kP, num_heads, num_query_tokens, "q"},
+               {k, k_stride, k_head_stride, head_dim, num_heads, num_key_tokens, "k"},
+               {k_rope, k_rope_stride, kP, kP, 1, num_key_tokens, "k_rope"},
+               {v, v_stride, v_head_stride, head_dim, num_heads, num_key_tokens, "v"}};
+    for (const auto& x : in)
         if (x.token < x.row || x.head < x.row || x.token % 8 != 0 || x.head % 8 != 0 ||
             x.token > (1LL << 32) || x.head > (1LL << 32))
             return pkv::fail(PKV_ERR_INVALID,
@@ -150,22 +912,76 @@ pkv_status pkv_latent_attention_prefill(
                          fn);
     if (!aligned(query_start, 4) || !aligned(key_start, 4))
         return pkv::fail(PKV_ERR_INVALID, "%s: misaligned query_start or key_start", fn);
+    const int64_t out_bytes = (int64_t)num_query_tokens * num_heads * head_dim * 2;
+    if (num_key_tokens == 0) return PKV_OK;           // no sequence has a row
+    for (const auto& x : in)
+        if (overlap(out, out_bytes, x.at,
+                    ((x.tokens - 1) * x.token + (x.heads - 1) * x.head + x.row) * 2))
+            return pkv::fail(PKV_ERR_INVALID, "%s: out overlaps %s", fn, x.name);
+    const Layout l = layout(head_dim, max_query_len, max_key_len);
+    if (l.total > 0) {
+        if (!workspace || !aligned(workspace, 256))
+            return pkv::fail(PKV_ERR_INVALID, "%s: workspace must be 256-byte aligned, not NULL", fn);
+        if (workspace_bytes < l.total)
+            return pkv::fail(PKV_ERR_INVALID, "%s: workspace too small (%zu < %zu bytes)", fn,
+                             workspace_bytes, l.total);
+        if (overlap(out, out_bytes, workspace, (int64_t)l.total))
+            return pkv::fail(PKV_ERR_INVALID, "%s: out overlaps the workspace", fn);
+    }
     int32_t* err = pkv::device_error_word();
     if (!err) return pkv::fail(PKV_ERR_CUDA, "%s: no CUDA device", fn);
-    Args a = {static_cast<uint16_t*>(out), static_cast<const uint16_t*>(q),
-              static_cast<const uint16_t*>(k), static_cast<const uint16_t*>(k_rope),
-              static_cast<const uint16_t*>(v), q_stride, q_head_stride, k_stride, k_head_stride,
-              k_rope_stride, v_stride, v_head_stride, query_start, key_start, scale_log2, num_seqs,
-              num_heads, max_query_len, max_key_len, num_query_tokens, num_key_tokens, err};
-    using Kernel = void (*)(Args);
-    const Kernel kernel =
-        dtype == PKV_F16 ? (head_dim == 64 ? (Kernel)latent_prefill_simple<__half, 64>
-                                           : (Kernel)latent_prefill_simple<__half, 128>)
-                         : (head_dim == 64 ? (Kernel)latent_prefill_simple<__nv_bfloat16, 64>
-                                           : (Kernel)latent_prefill_simple<__nv_bfloat16, 128>);
-    const cudaError_t e = pkv::launch_pdl(
-        kernel, dim3((unsigned)max_query_len, (unsigned)num_heads, (unsigned)num_seqs), dim3(128),
-        stream, a);
+    int dev = 0;
+    cudaError_t e = cudaGetDevice(&dev);
+    if (e != cudaSuccess) return pkv::cuda_fail(e, fn);
+    const int sms = pkv::sm_count(dev);
+    if (sms < 2) return pkv::fail(PKV_ERR_CUDA, "%s: no multiprocessors", fn);
+
+    const bool bf16 = dtype == PKV_BF16;
+    CUtensorMap tq, tk, tr, tv;
+    if (!head_map(&tq, bf16, q, head_dim + kP, num_heads, num_query_tokens, q_stride, q_head_stride,
+                  kQBoxRows) ||
+        !head_map(&tk, bf16, k, head_dim, num_heads, num_key_tokens, k_stride, k_head_stride,
+                  kBoxRows) ||
+        !head_map(&tv, bf16, v, head_dim, num_heads, num_key_tokens, v_stride, v_head_stride,
+                  kBoxRows) ||
+        !head_map(&tr, bf16, k_rope, kP, 1, num_key_tokens, k_rope_stride, kP, kBoxRows))
+        return pkv::fail(PKV_ERR_CUDA, "%s: tensor maps", fn);
+
+    Args a = {};
+    a.out = static_cast<uint16_t*>(out);
+    a.v = static_cast<const uint16_t*>(v);
+    a.v_stride = v_stride;
+    a.v_head = v_head_stride;
+    a.q_start = query_start;
+    a.k_start = key_start;
+    // (a hidden score is infinite and stays so under any scale but 0)
+    a.scale_log2 = scale_log2 == 0.f ? FLT_MIN : scale_log2;
+    a.S = num_seqs;
+    a.H = num_heads;
+    a.max_q = max_query_len;
+    a.max_k = max_key_len;
+    a.Tq = num_query_tokens;
+    a.Tk = num_key_tokens;
+    a.out_v8 = aligned(out, 32) ? 1 : 0;
+    a.whole = l.total == 0;
+    a.slot_rows = l.rows;
+    // pairs: no more than there can be steps (items, where they stay whole)
+    int64_t pairs = sms / 2 < kMaxPairs ? sms / 2 : kMaxPairs;
+    const int64_t items = (int64_t)num_seqs * num_heads * ((max_query_len + kRows - 1) / kRows);
+    const int64_t each = a.whole ? 1 : ((int64_t)max_key_len + kKeys - 1) / kKeys;
+    if (items < pairs && items * each < pairs) pairs = items * each;
+    a.pairs = (int)pairs;
+    char* ws = static_cast<char*>(workspace);
+    a.rec = reinterpret_cast<Rec*>(ws);
+    a.ml = reinterpret_cast<float2*>(ws + l.ml);
+    a.acc = reinterpret_cast<float*>(ws + l.acc);
+    a.err = err;
+    if (bf16)
+        e = head_dim == 128 ? launch<__nv_bfloat16, 128>(tq, tk, tr, tv, a, stream)
+                            : launch<__nv_bfloat16, 64>(tq, tk, tr, tv, a, stream);
+    else
+        e = head_dim == 128 ? launch<__half, 128>(tq, tk, tr, tv, a, stream)
+                            : launch<__half, 64>(tq, tk, tr, tv, a, stream);
     if (e != cudaSuccess) return pkv::cuda_fail(e, fn);
     return PKV_OK;
 }

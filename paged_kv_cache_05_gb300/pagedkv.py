@@ -93,9 +93,10 @@ def lib():
                                                 P, i32, f32, P, f32, i32, i32, i32, i32, i32, i64,
                                                 i32, P], i32),
             "pkv_gather_latent": ([P, P, P, P, i32, i32, i32, i32, i32, i64, i32, i32, P], i32),
+            "pkv_latent_prefill_workspace_size": ([i32, i32, i32, ctypes.POINTER(sz)], i32),
             "pkv_latent_attention_prefill": ([P, P, i64, i64, P, i64, i64, P, i64, P, i64, i64, P,
                                               P, f32, i32, i32, i32, i32, i32, i32, i32, i32, i32,
-                                              P], i32),
+                                              P, sz, P], i32),
             "pkv_latent_decode_workspace_size": ([i32, i32, i32, i32, ctypes.POINTER(sz)], i32),
             "pkv_latent_attention_decode": ([P, P, P, P, P, P, P, f32, i32, i32, i32, i32, i32, i32,
                                              i64, i32, i32, i32, P, sz, P], i32),
@@ -623,14 +624,24 @@ def gather_latent(rows, cache, block_tables, key_start, stream=None):
     return rows
 
 
+def latent_prefill_workspace_size(head_dim, max_query_len, max_key_len) -> int:
+    """Bytes of workspace latent_attention_prefill takes for these sizes (0: none)."""
+    n = ctypes.c_size_t(0)
+    _check("pkv_latent_prefill_workspace_size",
+           lib().pkv_latent_prefill_workspace_size(int(head_dim), int(max_query_len),
+                                                   int(max_key_len), ctypes.byref(n)))
+    return n.value
+
+
 def latent_attention_prefill(out, q, k, k_rope, v, query_start, key_start, scale, max_query_len,
-                             max_key_len, stream=None):
+                             max_key_len, workspace=None, stream=None):
     """Causal attention of prompts in the expanded form: q [Tq, H, N + 64], per-head
     keys and values k, v [Tk, H, N], the shared key part k_rope [Tk, 64] (all may be
     slices), ragged by query_start and key_start [S + 1]; a sequence's rows are the
-    last of its keys.  out [Tq, H, N]."""
+    last of its keys.  out [Tq, H, N].  workspace: uint8 of
+    latent_prefill_workspace_size() bytes, or memory of the call's own."""
     st = (_bind or _binding()).latent_attention_prefill(
-        out, q, k, k_rope, v, query_start, key_start, scale, max_query_len, max_key_len,
+        out, q, k, k_rope, v, query_start, key_start, scale, max_query_len, max_key_len, workspace,
         None if stream is None else stream.cuda_stream)
     if st:
         _check("pkv_latent_attention_prefill", st)
