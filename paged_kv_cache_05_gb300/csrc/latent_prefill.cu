@@ -14,8 +14,8 @@
 // cycle of them, of the 36 that the copies reach, and read 128 bytes a cycle of its
 // shared memory, all there are: 96 here.)
 //
-// Twelve warps a CTA: keys, products (the first CTA's), values and queries a warp each,
-// then four of softmax a slot, a thread a row.  The slots take turns: while one's
+// Twelve warps a CTA: keys, products (the first CTA's), values and queries a warp each (the
+// last walks the run and hands its items to the others through shared memory), then four of softmax a slot, a thread a row.  The slots take turns: while one's
 // softmax runs, the tensor cores work for the other.  Weights P are written over the
 // scores S in tensor memory, in halves, so that P V begins on the first.  Products
 // complete in order: S of a slot's step means that P V of its step before is done.  The
@@ -68,7 +68,7 @@ struct Cfg {
     static constexpr int K_OFF = 2 * Q_SLOT;
     static constexpr int V_OFF = K_OFF + KS * K_STAGE;
     static constexpr int SMEM = V_OFF + VS * V_STAGE + 1024;   // 1 KiB of alignment slack
-    static_assert(SMEM + 1024 <= 232448, "shared memory");
+    static_assert(SMEM + 1536 <= 232448, "shared memory");
 };
 
 enum : int {
@@ -82,8 +82,10 @@ enum : int {
     kPFull = 22,     // + 2 slot + half: weights written, O rescaled (first CTA's)
     kODone = 26,     // + slot: an item's last P V done
     kORead = 28,     // + slot: its output read from tensor memory (first CTA's)
-    kSpare = 30,
-    kBars = 31
+    kItFull = 30,    // + entry (4)
+    kItEmpty = 34,   // + entry
+    kSpare = 38,
+    kBars = 39
 };
 
 struct Args {
@@ -146,14 +148,14 @@ struct Start {
 struct Item {
     int q0, k0, klen, h;              // first row of all, first key of all
     int off;                          // the last key that its row 0 sees
-    int rows;
-    int n[2];                         // steps of each slot's rows
-    int j0, j1, steps;
+    int rows;                         // 0: no more items
+    int j0, j1, steps;                // (steps: of the whole item)
+    int end[2];                       // of each slot's rows: steps [j0, end), none where end <= j0
     int slot;                         // of a part: 0 the run's first, 1 another
     __device__ __forceinline__ bool whole() const { return j0 == 0 && j1 == steps; }
-    __device__ __forceinline__ bool active(int x) const { return n[x] > j0; }
-    __device__ __forceinline__ int end(int x) const { return min(n[x], j1); }
+    __device__ __forceinline__ bool active(int x) const { return end[x] > j0; }
 };
+constexpr int kRing = 4;              // items on their way from the warp that walks the run
 
 struct Walker {
     Seq q, next;
@@ -196,10 +198,10 @@ struct Walker {
         it.off = q.klen - q.qlen + t * kRows;
         it.rows = min(kRows, q.qlen - t * kRows);
         it.steps = q.steps(t);
-        it.n[0] = (it.off + min(it.rows, kRows / 2) + kKeys - 1) / kKeys;
-        it.n[1] = it.rows > kRows / 2 ? it.steps : 0;
         it.j0 = j;
         it.j1 = a.whole ? it.steps : (int)min((int64_t)it.steps, j + left);
+        it.end[0] = min((it.off + min(it.rows, kRows / 2) + kKeys - 1) / kKeys, it.j1);
+        it.end[1] = it.rows > kRows / 2 ? it.j1 : 0;
         it.slot = first ? 0 : 1;
         first = false;
         left -= it.j1 - it.j0;
@@ -221,6 +223,7 @@ __global__ void __launch_bounds__(kThreads, 1)
     __shared__ uint32_t s_tmem;
     __shared__ int s_abort;
     __shared__ Start s_start;
+    __shared__ Item s_items[kRing];
     __shared__ int64_t s_scan[2][kThreads / 32];
 
     const int tid = threadIdx.x, warp = tid >> 5, lane = tid & 31;
@@ -244,8 +247,10 @@ __global__ void __launch_bounds__(kThreads, 1)
             for (int i = 0; i < kBars; ++i) {
                 const bool two = i < kQEmpty || (i >= kKFull && i < kKEmpty) ||
                                  (i >= kVFull && i < kVEmpty);
-                const bool warps = (i >= kPFull && i < kODone) || (i >= kORead && i < kSpare);
-                mbar_init(bar(i), two ? 2 : warps ? 8 : 1);
+                const bool warps = (i >= kPFull && i < kODone) || (i >= kORead && i < kItFull);
+                // an item's readers: keys, values, eight of softmax, the products
+                const int n = two ? 2 : warps ? 8 : i >= kItEmpty && i < kSpare ? 11 - (int)rank : 1;
+                mbar_init(bar(i), n);
             }
             mbar_init_fence();
             s_abort = 0;
@@ -332,15 +337,24 @@ __global__ void __launch_bounds__(kThreads, 1)
         *abort_flag = 1;
     };
 
+    // the next item of the run, from the warp that walks it
+    int items = 0;
+    auto next_item = [&](Item& it) {
+        const int e = items % kRing;
+        ok = ok && warp_wait(bar(kItFull + e), (uint32_t)((items / kRing) & 1), abort_flag);
+        it = s_items[e];
+        __syncwarp();
+        if (lane == 0) mbar_arrive(bar(kItEmpty + e));
+        ++items;
+        return ok && it.rows > 0;
+    };
     if (warp == 0) {
         // ================================================= keys
-        Walker wk;
-        wk.init(a, start);
         Item it;
         int kc = 0;
         constexpr int BOXES = 64 / kBoxRows;
         const int c = lane / BOXES, r = (lane - c * BOXES) * kBoxRows;   // a lane's box
-        while (ok && wk.get(a, it)) {
+        while (next_item(it)) {
             for (int j = it.j0; j < it.j1; ++j, ++kc) {
                 const int st = kc % C::KS, n = kc / C::KS;
                 if (n > 0 && !warp_wait(bar(kKEmpty + st), (uint32_t)((n - 1) & 1), abort_flag)) {
@@ -359,12 +373,10 @@ __global__ void __launch_bounds__(kThreads, 1)
         if (!ok) fail();
     } else if (warp == 2) {
         // ================================================= values
-        Walker wk;
-        wk.init(a, start);
         Item it;
         int vc = 0;
         constexpr int BOXES = kKeys / kBoxRows;
-        while (ok && wk.get(a, it)) {
+        while (next_item(it)) {
             for (int j = it.j0; j < it.j1; ++j, ++vc) {
                 const int st = vc % C::VS, n = vc / C::VS;
                 if (n > 0 && !warp_wait(bar(kVEmpty + st), (uint32_t)((n - 1) & 1), abort_flag)) {
@@ -403,14 +415,26 @@ __global__ void __launch_bounds__(kThreads, 1)
         }
         if (!ok) fail();
     } else if (warp == 3) {
-        // ================================================= queries
+        // ================================================= items and queries
         Walker wk;
         wk.init(a, start);
         Item it;
         int count[2] = {0, 0};
         constexpr int BOXES = 128 / kQBoxRows;
         const int c = lane / BOXES, r = (lane - c * BOXES) * kQBoxRows;
-        while (ok && wk.get(a, it)) {
+        for (int n = 0; ok; ++n) {
+            const bool more = wk.get(a, it);
+            if (!more) it.rows = 0;
+            const int e = n % kRing;
+            if (n >= kRing && !warp_wait(bar(kItEmpty + e), (uint32_t)((n / kRing - 1) & 1), abort_flag)) {
+                ok = false;
+                break;
+            }
+            if (lane == 0) {
+                s_items[e] = it;
+                mbar_arrive(bar(kItFull + e));
+            }
+            if (!more) break;
             for (int x = 0; x < 2; ++x) {
                 if (!it.active(x)) continue;
                 const int n = count[x]++;
@@ -434,9 +458,15 @@ __global__ void __launch_bounds__(kThreads, 1)
             constexpr uint32_t ID_PV = idesc(El<T>::kType, true, N, 256);
             const uint64_t dQ = sdesc(sQ, 16, 1024), dK = sdesc(sK, 16, 1024),
                            dV = sdesc(sV, 1024, 1024);
-            Walker wk;
-            wk.init(a, start);
             Item it, nit;
+            auto next = [&](Item& i) {
+                const int e = items % kRing;
+                ok = ok && mbar_wait<false>(bar(kItFull + e), (uint32_t)((items / kRing) & 1), abort_flag);
+                i = s_items[e];
+                mbar_arrive(bar(kItEmpty + e));
+                ++items;
+                return ok && i.rows > 0;
+            };
             int kc = 0, vc = 0;
             int qs[2] = {0, 0}, ps[2] = {0, 0}, os[2] = {0, 0};
             // S of slot x for step j of item i from the keys in stage kc
@@ -451,20 +481,20 @@ __global__ void __launch_bounds__(kThreads, 1)
                     umma_pair(tmem + x * 128, da + (((e >> 2) * C::Q_CHUNK + (e & 3) * 32) >> 4),
                               db + (((e >> 2) * C::K_CHUNK + (e & 3) * 32) >> 4), ID_S, e > 0);
                 commit_pair(bar(kSFull + x));
-                if (j == i.end(x) - 1) commit_pair(bar(kQEmpty + x));
+                if (j == i.end[x] - 1) commit_pair(bar(kQEmpty + x));
                 return true;
             };
             auto keys = [&]() {
                 return mbar_wait<false>(bar(kKFull + kc % C::KS), (uint32_t)((kc / C::KS) & 1), abort_flag);
             };
-            bool have = wk.get(a, nit);
+            bool have = next(nit);
             int j = 0;
             if (have) {
                 it = nit;
                 j = it.j0;
                 ok = keys();
                 for (int x = 0; ok && x < 2; ++x)
-                    if (j < it.end(x)) ok = form_s(x, it, j);
+                    if (j < it.end[x]) ok = form_s(x, it, j);
                 commit_pair(bar(kKEmpty + kc % C::KS));
                 ++kc;
             }
@@ -473,11 +503,11 @@ __global__ void __launch_bounds__(kThreads, 1)
                 const bool same = j + 1 < it.j1;
                 const int nj = same ? j + 1 : 0;
                 bool more = same;
-                if (!same) more = wk.get(a, nit);
+                if (!same) more = next(nit);
                 const int nextj = same ? nj : nit.j0;
                 bool got_k = false, got_v = false;
                 for (int x = 0; ok && x < 2; ++x) {
-                    if (j < it.end(x)) {
+                    if (j < it.end[x]) {
                         const uint64_t db = dV + (uint64_t)(((vc % C::VS) * C::V_STAGE) >> 4);
                         for (int half = 0; ok && half < 2; ++half) {
                             ok = mbar_wait<false>(bar(kPFull + 2 * x + half), (uint32_t)(ps[x] & 1), abort_flag);
@@ -495,12 +525,12 @@ __global__ void __launch_bounds__(kThreads, 1)
                                              j > it.j0 || half > 0 || e > 0);
                         }
                         ++ps[x];
-                        if (ok && j == it.end(x) - 1) {
+                        if (ok && j == it.end[x] - 1) {
                             commit_pair(bar(kODone + x));
                             ++os[x];
                         }
                     }
-                    if (ok && more && nextj < (same ? it.end(x) : nit.end(x))) {
+                    if (ok && more && nextj < (same ? it.end[x] : nit.end[x])) {
                         if (!got_k) ok = got_k = keys();
                         if (ok) ok = form_s(x, same ? it : nit, nextj);
                     }
@@ -533,49 +563,57 @@ __global__ void __launch_bounds__(kThreads, 1)
         const uint32_t pfull = at_rank(bar(kPFull + 2 * x), 0), oread = at_rank(bar(kORead + x), 0);
         const int rw = x * 256 + (int)rank * 128 + quad * 32;     // the warp's first row of an item
         const int row = rw + lane;
-        Walker wk;
-        wk.init(a, start);
         Item it;
         int sc = 0, oc = 0;
         const float scale = a.scale_log2;
         const uint64_t scale2 = f2(scale, scale);
-        while (wk.get(a, it)) {
+        while (next_item(it)) {
             const bool live = rw < it.rows;                  // the warp has rows
             const int64_t slot = pair * 2 + it.slot;
             const bool whole = it.whole();
             float m = -INFINITY;
             uint64_t l2 = 0;                                 // two partial sums
-            for (int j = it.j0; j < it.end(x); ++j, ++sc) {
+            for (int j = it.j0; j < it.end[x]; ++j, ++sc) {
                 ok = ok && warp_wait(bar(kSFull + x), (uint32_t)(sc & 1), abort_flag);
                 fence_after();
                 if (live) {
-                    uint32_t z[2][64];
-                    ld64(tS, z[0]);
-                    ld64(tS + 64, z[1]);
-                    ld_wait(z[0]);
-                    ld_wait(z[1]);
+                    // the later half is looked at for the max first and loaded again for the
+                    // weights: both halves held at once would spill
+                    const bool hides = it.off + rw + 1 - j * kKeys < kKeys;
                     const int n = it.off + row + 1 - j * kKeys;   // keys of the step that it sees
-                    if (it.off + rw + 1 - j * kKeys < kKeys) {
-                        // a hidden key's score: lowest of the scaled ones
-                        const float hide = scale < 0.f ? INFINITY : -INFINITY;
+                    // a hidden key's score: lowest of the scaled ones
+                    const uint32_t hide = __float_as_uint(scale < 0.f ? INFINITY : -INFINITY);
+                    uint32_t z[64];
+                    auto cover = [&](int from) {
+                        if (!hides) return;
 #pragma unroll
-                        for (int e = 0; e < 128; ++e)
-                            if (e >= n) z[e >> 6][e & 63] = __float_as_uint(hide);
-                    }
-                    float top = __uint_as_float(z[0][0]);
-                    if (scale >= 0.f) {
-                        float t1 = __uint_as_float(z[1][0]);
+                        for (int e = 0; e < 64; ++e)
+                            if (from + e >= n) z[e] = hide;
+                    };
+                    auto largest = [&]() {               // largest of the scaled ones, unscaled
+                        float top = __uint_as_float(z[0]), t1 = __uint_as_float(z[1]);
+                        if (scale >= 0.f) {
 #pragma unroll
-                        for (int e = 1; e < 63; e += 2) {
-                            top = max3(top, __uint_as_float(z[0][e]), __uint_as_float(z[0][e + 1]));
-                            t1 = max3(t1, __uint_as_float(z[1][e]), __uint_as_float(z[1][e + 1]));
+                            for (int e = 2; e < 62; e += 4) {
+                                top = max3(top, __uint_as_float(z[e]), __uint_as_float(z[e + 1]));
+                                t1 = max3(t1, __uint_as_float(z[e + 2]), __uint_as_float(z[e + 3]));
+                            }
+                            return fmaxf(max3(top, __uint_as_float(z[62]), __uint_as_float(z[63])), t1);
                         }
-                        top = fmaxf(max3(top, __uint_as_float(z[0][63]), __uint_as_float(z[1][63])), t1);
-                    } else {
 #pragma unroll
-                        for (int e = 1; e < 128; ++e) top = fminf(top, __uint_as_float(z[e >> 6][e & 63]));
-                    }
-                    // (a row whose scores are all hidden has none: scale 0 times infinity)
+                        for (int e = 2; e < 64; ++e) top = fminf(top, __uint_as_float(z[e]));
+                        return fminf(top, t1);
+                    };
+                    ld64(tS + 64, z);
+                    ld_wait(z);
+                    cover(64);
+                    const float later = largest();
+                    ld64(tS, z);
+                    ld_wait(z);
+                    cover(0);
+                    float top = largest();
+                    top = scale >= 0.f ? fmaxf(top, later) : fminf(top, later);
+                    // (none where all are hidden: scaled, infinity times the scale)
                     top = fabsf(top) == INFINITY ? -INFINITY : top * scale;
                     float alpha = 1.f;
                     if (top > m + El<T>::kRescale || m == -INFINITY) {
@@ -612,18 +650,28 @@ __global__ void __launch_bounds__(kThreads, 1)
                     uint64_t sum[2] = {0, 0};
 #pragma unroll
                     for (int half = 0; half < 2; ++half) {
-                        uint32_t w[32];
-#pragma unroll
-                        for (int e = 0; e < 32; ++e) {
-                            float p, q;
-                            f2_split(fma2(f2(__uint_as_float(z[half][2 * e]),
-                                             __uint_as_float(z[half][2 * e + 1])),
-                                          scale2, minus2),
-                                     p, q);
-                            w[e] = El<T>::pack(ex2(p), ex2(q));
-                            sum[e & 1] = add2(sum[e & 1], El<T>::unpack(w[e]));
+                        if (half) {
+                            ld64(tS + 64, z);
+                            ld_wait(z);
+                            cover(64);
                         }
-                        st32(tS + half * 32, w);
+#pragma unroll
+                        for (int c = 0; c < 2; ++c) {
+                            uint32_t w[16];
+#pragma unroll
+                            for (int e = 0; e < 16; ++e) {
+                                float p, q;
+                                f2_split(fma2(f2(__uint_as_float(z[32 * c + 2 * e]),
+                                                 __uint_as_float(z[32 * c + 2 * e + 1])),
+                                              scale2, minus2),
+                                         p, q);
+                                p = ex2(p);
+                                q = ex2(q);
+                                sum[e & 1] = add2(sum[e & 1], f2(p, q));
+                                w[e] = El<T>::pack(p, q);
+                            }
+                            st16(tS + half * 32 + c * 16, w);
+                        }
                         st_wait();
                         fence_before();
                         __syncwarp();

@@ -27,6 +27,9 @@ __device__ __forceinline__ void mbar_init(uint32_t bar, uint32_t count) {
 __device__ __forceinline__ void mbar_init_fence() {
     asm volatile("fence.mbarrier_init.release.cluster;" ::: "memory");
 }
+__device__ __forceinline__ void mbar_arrive(uint32_t bar) {
+    asm volatile("mbarrier.arrive.shared::cta.b64 _, [%0];" ::"r"(bar) : "memory");
+}
 // The address of a shared variable of this CTA in CTA `rank` of the cluster.
 __device__ __forceinline__ uint32_t at_rank(uint32_t addr, uint32_t rank) {
     uint32_t r;
