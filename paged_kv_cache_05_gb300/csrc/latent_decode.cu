@@ -238,14 +238,12 @@ __global__ void __launch_bounds__(kThreads, 1)
     mine.nt = mine.nr = 0;
     bool good = tid >= a.S || mine.load(a, tid);
     if (warp == 1) {
-        if (lane == 0) {
-            for (int i = 0; i < kBars; ++i) {
-                const bool two = i < kKEmpty || (i >= kVFull && i < kVEmpty) || i == kQFull;
-                mbar_init(bar(i), two ? 2 : i == kPFull || i == kORead ? 8 : 1);
-            }
-            mbar_init_fence();
-            s_abort = 0;
+        for (int i = lane; i < kBars; i += 32) {
+            const bool two = i < kKEmpty || (i >= kVFull && i < kVEmpty) || i == kQFull;
+            mbar_init(bar(i), two ? 2 : i == kPFull || i == kORead ? 8 : 1);
         }
+        mbar_init_fence();
+        if (lane == 0) s_abort = 0;
         __syncwarp();
         alloc_pair(smem_u32(&s_tmem));
     } else if (warp == 0 && lane == 0) {
@@ -278,7 +276,7 @@ __global__ void __launch_bounds__(kThreads, 1)
         if (tid == 0) s_start.n = 0;
         fence_before();
         __syncthreads();
-        asm volatile("barrier.cluster.arrive.release.aligned;" ::: "memory");
+        asm volatile("barrier.cluster.arrive.relaxed.aligned;" ::: "memory");   // (see mbar_init_fence)
         int64_t total = 0, before = 0;
         for (int w = 0; w < 8; ++w) {
             if (w < warp) incl += s_scan[0][w];
@@ -286,8 +284,8 @@ __global__ void __launch_bounds__(kThreads, 1)
             total += s_scan[0][w] + s_scan[1][w];
         }
         const int64_t np = min((int64_t)a.pairs, total);
-        const int64_t b = pair < np ? total * pair / np : 0;
-        const int64_t e = pair < np ? total * (pair + 1) / np : 0;
+        const int64_t b = pair < np ? run_begin(total, np, pair) : 0;
+        const int64_t e = pair < np ? run_begin(total, np, pair + 1) : 0;
         auto found = [&](int s) {                // the sequence that holds step b
             if (e > b && incl > b && incl - n <= b) s_start = Start{s, mine, b - (incl - n), e - b, total};
         };
@@ -722,11 +720,11 @@ __global__ void __launch_bounds__(kThreads, 1)
             if (!g.whole && g.j0 == 0 && rank == 0 && warp == 2 && lane == 0) {
                 // steps of the tile from this run's end on, and the runs they fall in
                 const int64_t total = start.total, np = min((int64_t)a.pairs, total);
-                const int64_t e = total * (pair + 1) / np;   // first step after this run
+                const int64_t e = run_begin(total, np, pair + 1);   // first step after this run
                 const int64_t z = e + (wk.q.nt - g.j1) - 1;  // the tile's last
                 int64_t last = z * np / total;               // the run that holds it
-                while (last + 1 < np && total * (last + 1) / np <= z) ++last;
-                while (total * last / np > z) --last;
+                while (last + 1 < np && run_begin(total, np, last + 1) <= z) ++last;
+                while (run_begin(total, np, last) > z) --last;
                 a.rec[pair] = Rec{g.q0 * a.H + g.row, ok ? g.rows : 0, pair * 2 + g.slot,
                                   (int)(last - pair) + 1};
             }

@@ -78,14 +78,14 @@ enum : int {
     kKEmpty = 8,     // + stage
     kVFull = 12,     // + stage
     kVEmpty = 16,    // + stage
-    kSFull = 20,     // + slot: S formed, every earlier product done
-    kPFull = 22,     // + 2 slot + half: weights written, O rescaled (first CTA's)
-    kODone = 26,     // + slot: an item's last P V done
-    kORead = 28,     // + slot: its output read from tensor memory (first CTA's)
-    kItFull = 30,    // + entry (4)
-    kItEmpty = 34,   // + entry
-    kSpare = 38,
-    kBars = 39
+    kSFull = 20,     // + 2 slot + columns: the slot's S formed there
+    kPFull = 24,     // + 2 columns + half: weights written, O rescaled (first CTA's)
+    kPvDone = 28,    // + slot: P V of a step done
+    kORead = 30,     // + slot: its output read from tensor memory (first CTA's)
+    kItFull = 32,    // + entry (4)
+    kItEmpty = 36,   // + entry
+    kSpare = 40,
+    kBars = 41
 };
 
 struct Args {
@@ -144,16 +144,33 @@ struct Start {
     int64_t total;                    // steps of all
 };
 
-// Steps [j0, j1) of an item.
+// Steps [j0, j1) of an item.  Up to step `both` the two slots take turns, each with its
+// scores in its own columns; in the steps from there on one slot is alone, and its scores
+// alternate between the two, so that a step's are formed while the one before is weighed.
+// An item of 256 rows or fewer has one slot, the other than the one before it had.
 struct Item {
     int q0, k0, klen, h;              // first row of all, first key of all
     int off;                          // the last key that its row 0 sees
     int rows;                         // 0: no more items
     int j0, j1, steps;                // (steps: of the whole item)
-    int end[2];                       // of each slot's rows: steps [j0, end), none where end <= j0
+    int both, alone;                  // j0 <= both <= j1; the slot that is then alone,
+    int start;                        // and the columns of its first step
+    int row1, live0, live1;           // slot 1's first row, each slot's rows
     int slot;                         // of a part: 0 the run's first, 1 another
     __device__ __forceinline__ bool whole() const { return j0 == 0 && j1 == steps; }
-    __device__ __forceinline__ bool active(int x) const { return end[x] > j0; }
+    // a slot's steps are [j0, end)
+    __device__ __forceinline__ int end(int x) const { return x == alone ? j1 : both; }
+    // the slot whose scores are in columns r at step j, and the next step that uses them
+    __device__ __forceinline__ int slot_of(int r, int j) const { return j < both ? r : alone; }
+    __device__ __forceinline__ int columns(int j) const { return (start + j - both) & 1; }   // (alone)
+    __device__ __forceinline__ int first_use(int r) const {
+        const int j = both > j0 ? j0 : j0 + (r ^ start);
+        return j < j1 ? j : -1;
+    }
+    __device__ __forceinline__ int next_use(int r, int j) const {
+        const int n = j + 1 < both ? j + 1 : j < both ? both + (r ^ start) : j + 2;
+        return n < j1 ? n : -1;
+    }
 };
 constexpr int kRing = 4;              // items on their way from the warp that walks the run
 
@@ -161,17 +178,20 @@ struct Walker {
     Seq q, next;
     int s, h, t, j;
     int64_t left;
+    int turn;                         // the slot of the next item that has one
+    int free;                         // the columns that the item before leaves first
     bool first;
     __device__ __forceinline__ void init(const Args& a, const Start& st) {
         s = st.s;
         q = st.q;
         left = st.n;
         first = true;
+        turn = free = 0;
         h = t = j = 0;
         if (left <= 0) return;
         if (s + 1 < a.S) next.load(a, s + 1);
         const int64_t per = q.head_steps();
-        h = (int)(st.off / per);
+        h = per < (1 << 30) && st.off < (1 << 30) ? (int)st.off / (int)per : (int)(st.off / per);
         int64_t rest = st.off - h * per;
         while (rest >= q.steps(t)) rest -= q.steps(t++);
         j = (int)rest;
@@ -200,8 +220,26 @@ struct Walker {
         it.steps = q.steps(t);
         it.j0 = j;
         it.j1 = a.whole ? it.steps : (int)min((int64_t)it.steps, j + left);
-        it.end[0] = min((it.off + min(it.rows, kRows / 2) + kKeys - 1) / kKeys, it.j1);
-        it.end[1] = it.rows > kRows / 2 ? it.j1 : 0;
+        if (it.rows > kRows / 2) {
+            // slot 0's rows end earlier
+            it.both = max(min((it.off + kRows / 2 + kKeys - 1) / kKeys, it.j1), j);
+            it.alone = 1;
+            turn = 0;
+        } else {
+            it.both = j;
+            it.alone = turn;
+            turn ^= 1;
+        }
+        it.start = it.both > j ? 0 : free;
+        free = it.j1 > it.both ? it.columns(it.j1) : 0;
+        if (it.rows > kRows / 2) {
+            it.row1 = it.live0 = kRows / 2;
+            it.live1 = it.rows - kRows / 2;
+        } else {
+            it.row1 = 0;
+            it.live0 = it.alone == 0 ? it.rows : 0;
+            it.live1 = it.alone == 1 ? it.rows : 0;
+        }
         it.slot = first ? 0 : 1;
         first = false;
         left -= it.j1 - it.j0;
@@ -243,18 +281,16 @@ __global__ void __launch_bounds__(kThreads, 1)
     mine.qlen = 0;
     bool good = tid >= a.S || mine.load(a, tid);
     if (warp == 1) {
-        if (lane == 0) {
-            for (int i = 0; i < kBars; ++i) {
-                const bool two = i < kQEmpty || (i >= kKFull && i < kKEmpty) ||
-                                 (i >= kVFull && i < kVEmpty);
-                const bool warps = (i >= kPFull && i < kODone) || (i >= kORead && i < kItFull);
-                // an item's readers: keys, values, eight of softmax, the products
-                const int n = two ? 2 : warps ? 8 : i >= kItEmpty && i < kSpare ? 11 - (int)rank : 1;
-                mbar_init(bar(i), n);
-            }
-            mbar_init_fence();
-            s_abort = 0;
+        for (int i = lane; i < kBars; i += 32) {
+            const bool two = i < kQEmpty || (i >= kKFull && i < kKEmpty) ||
+                             (i >= kVFull && i < kVEmpty);
+            const bool warps = (i >= kPFull && i < kPvDone) || (i >= kORead && i < kItFull);
+            // an item's readers: keys, values, eight of softmax, the products
+            const int n = two ? 2 : warps ? 8 : i >= kItEmpty && i < kSpare ? 11 - (int)rank : 1;
+            mbar_init(bar(i), n);
         }
+        mbar_init_fence();
+        if (lane == 0) s_abort = 0;
         __syncwarp();
         alloc_pair(smem_u32(&s_tmem));
     } else if (warp == 0 && lane == 0) {
@@ -289,7 +325,7 @@ __global__ void __launch_bounds__(kThreads, 1)
         if (tid == 0) s_start.n = 0;
         fence_before();
         __syncthreads();
-        asm volatile("barrier.cluster.arrive.release.aligned;" ::: "memory");
+        asm volatile("barrier.cluster.arrive.relaxed.aligned;" ::: "memory");   // (see mbar_init_fence)
         int64_t total = 0, before = 0;
         for (int w = 0; w < kWarps; ++w) {
             if (w < warp) incl += s_scan[0][w];
@@ -297,8 +333,8 @@ __global__ void __launch_bounds__(kThreads, 1)
             total += s_scan[0][w] + s_scan[1][w];
         }
         const int64_t np = min((int64_t)a.pairs, total);
-        const int64_t b = pair < np ? total * pair / np : 0;
-        const int64_t e = pair < np ? total * (pair + 1) / np : 0;
+        const int64_t b = pair < np ? run_begin(total, np, pair) : 0;
+        const int64_t e = pair < np ? run_begin(total, np, pair + 1) : 0;
         auto found = [&](int s) {                // the sequence that holds step b
             if (e > b && incl > b && incl - n <= b)
                 s_start = Start{s, mine, b - (incl - n), e - b, total};
@@ -436,7 +472,7 @@ __global__ void __launch_bounds__(kThreads, 1)
             }
             if (!more) break;
             for (int x = 0; x < 2; ++x) {
-                if (!it.active(x)) continue;
+                if (it.end(x) <= it.j0) continue;
                 const int n = count[x]++;
                 if (n > 0 && !warp_wait(bar(kQEmpty + x), (uint32_t)((n - 1) & 1), abort_flag)) {
                     ok = false;
@@ -447,7 +483,7 @@ __global__ void __launch_bounds__(kThreads, 1)
                 __syncwarp();
                 if (c < C::CH)
                     tma_3d_pair(sQ + x * C::Q_SLOT + c * C::Q_CHUNK + r * 128, &tm_q, c * 64, it.h,
-                                it.q0 + x * 256 + 128 * (int)rank + r, full);
+                                it.q0 + (x ? it.row1 : 0) + 128 * (int)rank + r, full);
             }
         }
         if (!ok) fail();
@@ -467,83 +503,93 @@ __global__ void __launch_bounds__(kThreads, 1)
                 ++items;
                 return ok && i.rows > 0;
             };
-            int kc = 0, vc = 0;
-            int qs[2] = {0, 0}, ps[2] = {0, 0}, os[2] = {0, 0};
-            // S of slot x for step j of item i from the keys in stage kc
-            auto form_s = [&](int x, const Item& i, int j) {
-                if (j == i.j0 && !mbar_wait<false>(bar(kQFull + x), (uint32_t)(qs[x]++ & 1), abort_flag))
+            // (bits by slot, or by columns: phases, and outputs that were left to read)
+            uint32_t qs = 0, os = 0, ps = 0, outs = 0;
+            uint32_t half_read = 0;          // stages of keys that one of two slots has read
+            // S in columns r for step j of item i, whose step j0 is the run's step g0
+            auto form = [&](const Item& i, int g0, int r, int j) {
+                const int x = i.slot_of(r, j), g = g0 + j - i.j0, st = g % C::KS;
+                if (j == i.j0) {
+                    if (!mbar_wait<false>(bar(kQFull + x), qs >> x & 1, abort_flag)) return false;
+                    qs ^= 1u << x;
+                }
+                if (!mbar_wait<false>(bar(kKFull + st), (uint32_t)((g / C::KS) & 1), abort_flag))
                     return false;
-                fence_after();
                 const uint64_t da = dQ + (uint64_t)((x * C::Q_SLOT) >> 4);
-                const uint64_t db = dK + (uint64_t)(((kc % C::KS) * C::K_STAGE) >> 4);
+                const uint64_t db = dK + (uint64_t)((st * C::K_STAGE) >> 4);
 #pragma unroll
                 for (int e = 0; e < C::CH * 4; ++e)
-                    umma_pair(tmem + x * 128, da + (((e >> 2) * C::Q_CHUNK + (e & 3) * 32) >> 4),
+                    umma_pair(tmem + r * 128, da + (((e >> 2) * C::Q_CHUNK + (e & 3) * 32) >> 4),
                               db + (((e >> 2) * C::K_CHUNK + (e & 3) * 32) >> 4), ID_S, e > 0);
-                commit_pair(bar(kSFull + x));
-                if (j == i.end[x] - 1) commit_pair(bar(kQEmpty + x));
+                commit_pair(bar(kSFull + 2 * x + r));
+                if (j < i.both && !(half_read >> st & 1)) {
+                    half_read |= 1u << st;
+                } else {
+                    half_read &= ~(1u << st);
+                    commit_pair(bar(kKEmpty + st));
+                }
+                if (j == i.end(x) - 1) commit_pair(bar(kQEmpty + x));
                 return true;
             };
-            auto keys = [&]() {
-                return mbar_wait<false>(bar(kKFull + kc % C::KS), (uint32_t)((kc / C::KS) & 1), abort_flag);
-            };
-            bool have = next(nit);
-            int j = 0;
-            if (have) {
-                it = nit;
-                j = it.j0;
-                ok = keys();
-                for (int x = 0; ok && x < 2; ++x)
-                    if (j < it.end[x]) ok = form_s(x, it, j);
-                commit_pair(bar(kKEmpty + kc % C::KS));
-                ++kc;
-            }
-            while (ok && have) {
-                // the step after this one
-                const bool same = j + 1 < it.j1;
-                const int nj = same ? j + 1 : 0;
-                bool more = same;
-                if (!same) more = next(nit);
-                const int nextj = same ? nj : nit.j0;
-                bool got_k = false, got_v = false;
-                for (int x = 0; ok && x < 2; ++x) {
-                    if (j < it.end[x]) {
-                        const uint64_t db = dV + (uint64_t)(((vc % C::VS) * C::V_STAGE) >> 4);
-                        for (int half = 0; ok && half < 2; ++half) {
-                            ok = mbar_wait<false>(bar(kPFull + 2 * x + half), (uint32_t)(ps[x] & 1), abort_flag);
-                            if (ok && half == 0 && j == it.j0 && os[x] > 0)
-                                ok = mbar_wait<false>(bar(kORead + x), (uint32_t)((os[x] - 1) & 1), abort_flag);
-                            if (ok && !got_v)
-                                ok = got_v = mbar_wait<false>(bar(kVFull + vc % C::VS),
-                                                              (uint32_t)((vc / C::VS) & 1), abort_flag);
-                            if (!ok) break;
-                            fence_after();
+            // O += P V of the step whose weights are in columns r
+            auto weigh = [&](const Item& i, int g0, int r, int j) {
+                const int x = i.slot_of(r, j), g = g0 + j - i.j0, st = g % C::VS;
+                const uint64_t db = dV + (uint64_t)((st * C::V_STAGE) >> 4);
+                const uint32_t par = ps >> r & 1;
+                ps ^= 1u << r;
 #pragma unroll
-                            for (int e = 0; e < 4; ++e)
-                                umma_ts_pair(tmem + kColO + x * N, tmem + x * 128 + half * 32 + e * 8,
-                                             db + ((half * 8192 + e * 2048) >> 4), ID_PV,
-                                             j > it.j0 || half > 0 || e > 0);
+                for (int half = 0; half < 2; ++half) {
+                    if (!mbar_wait<false>(bar(kPFull + 2 * r + half), par, abort_flag)) return false;
+                    if (half == 0) {
+                        if (j == i.j0 && (outs >> x & 1)) {
+                            if (!mbar_wait<false>(bar(kORead + x), os >> x & 1, abort_flag)) return false;
+                            os ^= 1u << x;
                         }
-                        ++ps[x];
-                        if (ok && j == it.end[x] - 1) {
-                            commit_pair(bar(kODone + x));
-                            ++os[x];
-                        }
+                        if (!mbar_wait<false>(bar(kVFull + st), (uint32_t)((g / C::VS) & 1), abort_flag))
+                            return false;
                     }
-                    if (ok && more && nextj < (same ? it.end[x] : nit.end[x])) {
-                        if (!got_k) ok = got_k = keys();
-                        if (ok) ok = form_s(x, same ? it : nit, nextj);
-                    }
+                    fence_after();
+#pragma unroll
+                    for (int e = 0; e < 4; ++e)
+                        umma_ts_pair(tmem + kColO + x * N, tmem + r * 128 + half * 32 + e * 8,
+                                     db + ((half * 8192 + e * 2048) >> 4), ID_PV,
+                                     j > i.j0 || half > 0 || e > 0);
+                }
+                commit_pair(bar(kPvDone + x));
+                if (j == i.end(x) - 1) outs |= 1u << x;
+                if (j >= i.both || r == 1) commit_pair(bar(kVEmpty + st));
+                return true;
+            };
+            bool have = next(it);
+            int g0 = 0;
+            uint32_t formed = 0;             // columns that hold the item's first S already
+            while (ok && have) {
+                for (int k = 0; ok && k < 2; ++k) {
+                    const int r = it.start ^ k, j = it.first_use(r);
+                    if (!(formed >> r & 1) && j >= 0) ok = form(it, g0, r, j);
                 }
                 if (!ok) break;
-                commit_pair(bar(kVEmpty + vc % C::VS));
-                ++vc;
-                if (more) {
-                    commit_pair(bar(kKEmpty + kc % C::KS));
-                    ++kc;
-                }
-                if (!same) it = nit;
-                j = nextj;
+                const bool more = next(nit);
+                const int n0 = g0 + it.j1 - it.j0;
+                formed = 0;
+                for (int j = it.j0; ok && j < it.j1; ++j)
+                    for (int r = 0; ok && r < 2; ++r) {
+                        if (j >= it.both && r != it.columns(j)) continue;
+                        ok = weigh(it, g0, r, j);
+                        // the columns are free for their next scores
+                        const int u = it.next_use(r, j);
+                        if (!ok) break;
+                        const int f = nit.first_use(r);
+                        if (u >= 0) {
+                            ok = form(it, g0, r, u);
+                        } else if (more && f >= 0 && (f == nit.j0 || (formed >> nit.start & 1))) {
+                            // (a slot's scores are formed in the order of its steps)
+                            ok = form(nit, n0, r, f);
+                            formed |= 1u << r;
+                        }
+                    }
+                it = nit;
+                g0 = n0;
                 have = more;
             }
             if (!ok) {
@@ -559,22 +605,29 @@ __global__ void __launch_bounds__(kThreads, 1)
         // ================================================= softmax
         const int x = warp >= 8, quad = warp & 3;
         const uint32_t lanes = (uint32_t)(quad * 32) << 16;
-        const uint32_t tS = tmem + lanes + x * 128, tO = tmem + lanes + kColO + x * N;
-        const uint32_t pfull = at_rank(bar(kPFull + 2 * x), 0), oread = at_rank(bar(kORead + x), 0);
-        const int rw = x * 256 + (int)rank * 128 + quad * 32;     // the warp's first row of an item
-        const int row = rw + lane;
+        const uint32_t tO = tmem + lanes + kColO + x * N;
+        const uint32_t pfull0 = at_rank(bar(kPFull), 0), oread = at_rank(bar(kORead + x), 0);
         Item it;
-        int sc = 0, oc = 0;
+        uint32_t uses = 0;                   // of each columns, by this slot: odd
+        int pv = 0;                          // steps of this slot
         const float scale = a.scale_log2;
         const uint64_t scale2 = f2(scale, scale);
         while (next_item(it)) {
-            const bool live = rw < it.rows;                  // the warp has rows
+            const int at = (int)rank * 128 + quad * 32;      // the warp's first row of the slot's
+            const int mine_rows = x ? it.live1 : it.live0;
+            const bool live = at < mine_rows;
+            const int rw = (x ? it.row1 : 0) + at, row = rw + lane;      // and of the item's
             const int64_t slot = pair * 2 + it.slot;
+            const int end = it.end(x);
             const bool whole = it.whole();
             float m = -INFINITY;
             uint64_t l2 = 0;                                 // two partial sums
-            for (int j = it.j0; j < it.end[x]; ++j, ++sc) {
-                ok = ok && warp_wait(bar(kSFull + x), (uint32_t)(sc & 1), abort_flag);
+            for (int j = it.j0; j < end; ++j, ++pv) {
+                const bool apart = j < it.both;
+                const int r = apart ? x : it.columns(j);                 // its columns
+                const uint32_t tS = tmem + lanes + r * 128, pfull = pfull0 + r * 16;
+                ok = ok && warp_wait(bar(kSFull + 2 * x + r), uses >> r & 1, abort_flag);
+                uses ^= 1u << r;
                 fence_after();
                 if (live) {
                     // the later half is looked at for the max first and loaded again for the
@@ -626,25 +679,6 @@ __global__ void __launch_bounds__(kThreads, 1)
                             m = mn;
                         }
                     }
-                    if (j > it.j0 && __any_sync(0xffffffffu, alpha != 1.f)) {
-                        const uint64_t al2 = f2(alpha, alpha);
-#pragma unroll 1
-                        for (int c = 0; c < N; c += 16) {
-                            uint32_t o[16];
-                            ld16(tO + c, o);
-                            ld_wait(o);
-#pragma unroll
-                            for (int e = 0; e < 8; ++e) {
-                                float p, q;
-                                f2_split(mul2(f2(__uint_as_float(o[2 * e]), __uint_as_float(o[2 * e + 1])),
-                                              al2),
-                                         p, q);
-                                o[2 * e] = __float_as_uint(p);
-                                o[2 * e + 1] = __float_as_uint(q);
-                            }
-                            st16(tO + c, o);
-                        }
-                    }
                     const float minus = m == -INFINITY ? 0.f : El<T>::kLift - m;
                     const uint64_t minus2 = f2(minus, minus);
                     uint64_t sum[2] = {0, 0};
@@ -672,6 +706,30 @@ __global__ void __launch_bounds__(kThreads, 1)
                             }
                             st16(tS + half * 32 + c * 16, w);
                         }
+                        // (S of a step alone is formed before P V of the step before it)
+                        if (half == 0 && j > it.j0 && !apart) {
+                            ok = ok && warp_wait(bar(kPvDone + x), (uint32_t)((pv - 1) & 1), abort_flag);
+                            fence_after();
+                        }
+                        if (half == 0 && j > it.j0 && __any_sync(0xffffffffu, alpha != 1.f)) {
+                            const uint64_t al2 = f2(alpha, alpha);
+#pragma unroll 1
+                            for (int c = 0; c < N; c += 16) {
+                                uint32_t o[16];
+                                ld16(tO + c, o);
+                                ld_wait(o);
+#pragma unroll
+                                for (int e = 0; e < 8; ++e) {
+                                    float p, q;
+                                    f2_split(mul2(f2(__uint_as_float(o[2 * e]), __uint_as_float(o[2 * e + 1])),
+                                                  al2),
+                                             p, q);
+                                    o[2 * e] = __float_as_uint(p);
+                                    o[2 * e + 1] = __float_as_uint(q);
+                                }
+                                st16(tO + c, o);
+                            }
+                        }
                         st_wait();
                         fence_before();
                         __syncwarp();
@@ -679,6 +737,8 @@ __global__ void __launch_bounds__(kThreads, 1)
                     }
                     l2 = fma2(l2, f2(alpha, alpha), add2(sum[0], sum[1]));
                 } else {
+                    if (j > it.j0 && !apart)
+                        ok = ok && warp_wait(bar(kPvDone + x), (uint32_t)((pv - 1) & 1), abort_flag);
                     fence_before();
                     __syncwarp();
                     if (lane == 0) {
@@ -691,10 +751,10 @@ __global__ void __launch_bounds__(kThreads, 1)
             float p, q;
             f2_split(l2, p, q);
             const float l = p + q;
-            const bool mine = row < it.rows && ok;
+            const bool mine = at + lane < mine_rows && ok;
             if (mine && !whole) a.ml[slot * a.slot_rows + row] = make_float2(m, l);
-            if (it.active(x)) {
-                ok = ok && warp_wait(bar(kODone + x), (uint32_t)(oc++ & 1), abort_flag);
+            if (end > it.j0) {
+                ok = ok && warp_wait(bar(kPvDone + x), (uint32_t)((pv - 1) & 1), abort_flag);
                 fence_after();
                 if (live) {
                     const float inv = 1.f / l;
@@ -739,11 +799,11 @@ __global__ void __launch_bounds__(kThreads, 1)
             // the first part of an item that goes on in the next pairs' runs
             if (!whole && it.j0 == 0 && rank == 0 && warp == 4 && lane == 0) {
                 const int64_t total = start.total, np = min((int64_t)a.pairs, total);
-                const int64_t e = total * (pair + 1) / np;   // first step after this run
+                const int64_t e = run_begin(total, np, pair + 1);   // first step after this run
                 const int64_t z = e + (it.steps - it.j1) - 1;    // the item's last
                 int64_t last = z * np / total;               // the run that holds it
-                while (last + 1 < np && total * (last + 1) / np <= z) ++last;
-                while (total * last / np > z) --last;
+                while (last + 1 < np && run_begin(total, np, last + 1) <= z) ++last;
+                while (run_begin(total, np, last) > z) --last;
                 a.rec[pair] = Rec{it.q0, ok ? it.rows : 0, it.h, pair * 2 + it.slot,
                                   (int)(last - pair) + 1, {0, 0, 0}};
             }

@@ -284,6 +284,12 @@ __device__ __forceinline__ float ex2(float x) {
     asm("ex2.approx.ftz.f32 %0, %1;" : "=f"(y) : "f"(x));
     return y;
 }
+// The first of `total` steps that run k of n equal ones takes (total and n up to 2^54 and
+// 2^7; in 32 bits where they do).
+__device__ __forceinline__ int64_t run_begin(int64_t total, int64_t n, int64_t k) {
+    if (total < (1 << 24)) return (uint32_t)total * (uint32_t)k / (uint32_t)n;
+    return total * k / n;
+}
 // 32 bytes to global memory in one instruction (32-byte aligned address)
 __device__ __forceinline__ void st_global_v8(void* p, const uint32_t* w) {
     asm volatile("st.global.v8.b32 [%0], {%1, %2, %3, %4, %5, %6, %7, %8};" ::"l"(p), "r"(w[0]),
