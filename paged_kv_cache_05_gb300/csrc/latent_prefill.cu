@@ -6,20 +6,23 @@
 // in log2 units, with the running max and sum of the softmax (one pass over the keys).
 //
 // Bound: the tensor cores: 2 (2 N + 64) operations a (row, key) pair of a head, against
-// one exponential.  An item is 512 query rows of one head, its steps 128 keys each.  The
+// one exponential.  An item is 512 query rows of one head, its steps 64 keys each.  The
 // products are pairs' (clusters of two CTAs, cta_group::2, M = 256): each CTA holds 128
 // rows of each of two slots (rows 0-255 and 256-511 of the item) and half of a step's
-// keys and values (64 keys; N / 2 elements of every value), so that a step's 80 KB come
+// keys and values (32 keys; N / 2 elements of every value), so that a step's 40 KB come
 // to the SMs once for 512 rows.  (One CTA with 256 rows alone would need 31 bytes a
 // cycle of them, of the 36 that the copies reach, and read 128 bytes a cycle of its
 // shared memory, all there are: 96 here.)
 //
-// Twelve warps a CTA: keys, products (the first CTA's), values and queries a warp each (the
-// last walks the run and hands its items to the others through shared memory), then four of softmax a slot, a thread a row.  The slots take turns: while one's
-// softmax runs, the tensor cores work for the other.  Weights P are written over the
-// scores S in tensor memory, in halves, so that P V begins on the first.  Products
-// complete in order: S of a slot's step means that P V of its step before is done.  The
-// max is raised only past a growth of kRescale, so that most steps leave O alone.
+// Thirteen warps a CTA: keys, values and queries a warp each (the last walks the run and
+// hands its items to the others through shared memory), one that issues the products for
+// the scores and one for the outputs (the first CTA's), and four of softmax a slot, a
+// thread a row.  A slot's scores S alternate between two places in
+// tensor memory: a step's are formed while the one before is weighed.  (With steps of 128
+// keys and one place a slot, S waits for P V of the step before, which waits for its
+// softmax: 3150 cycles a step of 512 rows, where the products take 2560.)  Weights P are
+// written over the scores.  The max is raised only past a growth of kRescale, so that
+// most steps leave O alone.
 //
 // The steps of all items are dealt to the pairs in equal runs; parts of an item are left
 // in the workspace and joined by a second kernel.  Where no item has more than
@@ -46,22 +49,22 @@ using pkv::rows16::pack2;
 
 constexpr int kP = 64;
 constexpr int kRows = 512;            // rows of an item: two slots of a pair's 256
-constexpr int kKeys = 128;            // keys of a step
-constexpr int kThreads = 384;
+constexpr int kKeys = 64;             // keys of a step
+constexpr int kThreads = 416;
 constexpr int kMaxPairs = 96;
-constexpr int kWholeSteps = 4;
+constexpr int kWholeSteps = 8;
 constexpr int kBoxRows = 16;          // keys, or values, of a box
 constexpr int kQBoxRows = 32;
-constexpr uint32_t kColO = 256;       // tensor memory: S (and P over it) at 0 and 128, O from here
+constexpr uint32_t kColO = 256;       // tensor memory: S (and P over it) at 64 (2 slot + place), O from here
 
 template <int N>
 struct Cfg {
     static constexpr int CH = (N + kP) / 64;          // chunks of 64 elements of a key
-    static constexpr int KS = N == 128 ? 3 : 4;       // stages
-    static constexpr int VS = N == 128 ? 3 : 4;
+    static constexpr int KS = N == 128 ? 6 : 8;       // stages
+    static constexpr int VS = KS;
     static constexpr int Q_CHUNK = 128 * 128;         // a slot's rows of a chunk
     static constexpr int Q_SLOT = CH * Q_CHUNK;
-    static constexpr int K_CHUNK = 64 * 128;          // a CTA's keys of a chunk
+    static constexpr int K_CHUNK = kKeys / 2 * 128;   // a CTA's keys of a chunk
     static constexpr int K_STAGE = CH * K_CHUNK;
     static constexpr int V_STAGE = kKeys * 128;       // 64 elements (N = 64: 32 and zeros)
     static constexpr int Q_OFF = 0;
@@ -74,18 +77,18 @@ struct Cfg {
 enum : int {
     kQFull = 0,      // + slot: its rows are there (first CTA's barrier)
     kQEmpty = 2,     // + slot: an item's last S formed
-    kKFull = 4,      // + stage (up to 4)
-    kKEmpty = 8,     // + stage
-    kVFull = 12,     // + stage
-    kVEmpty = 16,    // + stage
-    kSFull = 20,     // + 2 slot + columns: the slot's S formed there
-    kPFull = 24,     // + 2 columns + half: weights written, O rescaled (first CTA's)
-    kPvDone = 28,    // + slot: P V of a step done
-    kORead = 30,     // + slot: its output read from tensor memory (first CTA's)
-    kItFull = 32,    // + entry (4)
-    kItEmpty = 36,   // + entry
-    kSpare = 40,
-    kBars = 41
+    kKFull = 4,      // + stage (up to 8)
+    kKEmpty = 12,    // + stage
+    kVFull = 20,     // + stage
+    kVEmpty = 28,    // + stage
+    kSFull = 36,     // + 2 slot + place: S formed
+    kPFull = 40,     // + 2 slot + place: weights written, O rescaled (first CTA's)
+    kPvDone = 44,    // + 2 slot + place: P V done
+    kORead = 48,     // + slot: its output read from tensor memory (first CTA's)
+    kItFull = 50,    // + entry (4)
+    kItEmpty = 54,   // + entry
+    kSpare = 58,     // + one of the products' threads
+    kBars = 60
 };
 
 struct Args {
@@ -144,33 +147,20 @@ struct Start {
     int64_t total;                    // steps of all
 };
 
-// Steps [j0, j1) of an item.  Up to step `both` the two slots take turns, each with its
-// scores in its own columns; in the steps from there on one slot is alone, and its scores
-// alternate between the two, so that a step's are formed while the one before is weighed.
-// An item of 256 rows or fewer has one slot, the other than the one before it had.
+// Steps [j0, j1) of an item.  Slot 0's rows see fewer of the last steps' keys: up to step
+// `both` the two slots work, then one alone.  An item of 256 rows or fewer has one slot,
+// the other than the one before it had.
 struct Item {
     int q0, k0, klen, h;              // first row of all, first key of all
     int off;                          // the last key that its row 0 sees
     int rows;                         // 0: no more items
     int j0, j1, steps;                // (steps: of the whole item)
-    int both, alone;                  // j0 <= both <= j1; the slot that is then alone,
-    int start;                        // and the columns of its first step
+    int both, alone;                  // j0 <= both <= j1; the slot that is then alone
     int row1, live0, live1;           // slot 1's first row, each slot's rows
     int slot;                         // of a part: 0 the run's first, 1 another
     __device__ __forceinline__ bool whole() const { return j0 == 0 && j1 == steps; }
     // a slot's steps are [j0, end)
     __device__ __forceinline__ int end(int x) const { return x == alone ? j1 : both; }
-    // the slot whose scores are in columns r at step j, and the next step that uses them
-    __device__ __forceinline__ int slot_of(int r, int j) const { return j < both ? r : alone; }
-    __device__ __forceinline__ int columns(int j) const { return (start + j - both) & 1; }   // (alone)
-    __device__ __forceinline__ int first_use(int r) const {
-        const int j = both > j0 ? j0 : j0 + (r ^ start);
-        return j < j1 ? j : -1;
-    }
-    __device__ __forceinline__ int next_use(int r, int j) const {
-        const int n = j + 1 < both ? j + 1 : j < both ? both + (r ^ start) : j + 2;
-        return n < j1 ? n : -1;
-    }
 };
 constexpr int kRing = 4;              // items on their way from the warp that walks the run
 
@@ -179,14 +169,13 @@ struct Walker {
     int s, h, t, j;
     int64_t left;
     int turn;                         // the slot of the next item that has one
-    int free;                         // the columns that the item before leaves first
     bool first;
     __device__ __forceinline__ void init(const Args& a, const Start& st) {
         s = st.s;
         q = st.q;
         left = st.n;
         first = true;
-        turn = free = 0;
+        turn = 0;
         h = t = j = 0;
         if (left <= 0) return;
         if (s + 1 < a.S) next.load(a, s + 1);
@@ -230,8 +219,6 @@ struct Walker {
             it.alone = turn;
             turn ^= 1;
         }
-        it.start = it.both > j ? 0 : free;
-        free = it.j1 > it.both ? it.columns(it.j1) : 0;
         if (it.rows > kRows / 2) {
             it.row1 = it.live0 = kRows / 2;
             it.live1 = it.rows - kRows / 2;
@@ -284,9 +271,9 @@ __global__ void __launch_bounds__(kThreads, 1)
         for (int i = lane; i < kBars; i += 32) {
             const bool two = i < kQEmpty || (i >= kKFull && i < kKEmpty) ||
                              (i >= kVFull && i < kVEmpty);
-            const bool warps = (i >= kPFull && i < kPvDone) || (i >= kORead && i < kItFull);
-            // an item's readers: keys, values, eight of softmax, the products
-            const int n = two ? 2 : warps ? 8 : i >= kItEmpty && i < kSpare ? 11 - (int)rank : 1;
+            const bool warps = (i >= kPFull && i < kPvDone) || i == kORead || i == kORead + 1;
+            // an item's readers: keys, values, eight of softmax, the two of products
+            const int n = two ? 2 : warps ? 8 : i >= kItEmpty && i < kSpare ? (rank ? 10 : 12) : 1;
             mbar_init(bar(i), n);
         }
         mbar_init_fence();
@@ -384,11 +371,19 @@ __global__ void __launch_bounds__(kThreads, 1)
         ++items;
         return ok && it.rows > 0;
     };
+    auto next_alone = [&](Item& it) {            // (by one thread)
+        const int e = items % kRing;
+        ok = ok && mbar_wait<false>(bar(kItFull + e), (uint32_t)((items / kRing) & 1), abort_flag);
+        it = s_items[e];
+        mbar_arrive(bar(kItEmpty + e));
+        ++items;
+        return ok && it.rows > 0;
+    };
     if (warp == 0) {
         // ================================================= keys
         Item it;
         int kc = 0;
-        constexpr int BOXES = 64 / kBoxRows;
+        constexpr int BOXES = kKeys / 2 / kBoxRows;
         const int c = lane / BOXES, r = (lane - c * BOXES) * kBoxRows;   // a lane's box
         while (next_item(it)) {
             for (int j = it.j0; j < it.j1; ++j, ++kc) {
@@ -401,7 +396,7 @@ __global__ void __launch_bounds__(kThreads, 1)
                 if (lane == 0) mbar_expect_tx_cluster(full, C::K_STAGE);
                 __syncwarp();
                 const uint32_t to = sK + st * C::K_STAGE + c * C::K_CHUNK + r * 128;
-                const int key = it.k0 + j * kKeys + 64 * (int)rank + r;
+                const int key = it.k0 + j * kKeys + kKeys / 2 * (int)rank + r;
                 if (c < C::CH - 1) tma_3d_pair(to, &tm_k, c * 64, it.h, key, full);
                 else if (c == C::CH - 1) tma_3d_pair(to, &tm_r, 0, 0, key, full);
             }
@@ -488,109 +483,44 @@ __global__ void __launch_bounds__(kThreads, 1)
         }
         if (!ok) fail();
     } else if (warp == 1) {
-        // ================================================= products
+        // ================================================= scores
         if (rank == 0 && elect_one()) {
             constexpr uint32_t ID_S = idesc(El<T>::kType, false, kKeys, 256);
-            constexpr uint32_t ID_PV = idesc(El<T>::kType, true, N, 256);
-            const uint64_t dQ = sdesc(sQ, 16, 1024), dK = sdesc(sK, 16, 1024),
-                           dV = sdesc(sV, 1024, 1024);
-            Item it, nit;
-            auto next = [&](Item& i) {
-                const int e = items % kRing;
-                ok = ok && mbar_wait<false>(bar(kItFull + e), (uint32_t)((items / kRing) & 1), abort_flag);
-                i = s_items[e];
-                mbar_arrive(bar(kItEmpty + e));
-                ++items;
-                return ok && i.rows > 0;
-            };
-            // (bits by slot, or by columns: phases, and outputs that were left to read)
-            uint32_t qs = 0, os = 0, ps = 0, outs = 0;
-            uint32_t half_read = 0;          // stages of keys that one of two slots has read
-            // S in columns r for step j of item i, whose step j0 is the run's step g0
-            auto form = [&](const Item& i, int g0, int r, int j) {
-                const int x = i.slot_of(r, j), g = g0 + j - i.j0, st = g % C::KS;
-                if (j == i.j0) {
-                    if (!mbar_wait<false>(bar(kQFull + x), qs >> x & 1, abort_flag)) return false;
-                    qs ^= 1u << x;
-                }
-                if (!mbar_wait<false>(bar(kKFull + st), (uint32_t)((g / C::KS) & 1), abort_flag))
-                    return false;
-                const uint64_t da = dQ + (uint64_t)((x * C::Q_SLOT) >> 4);
-                const uint64_t db = dK + (uint64_t)((st * C::K_STAGE) >> 4);
+            const uint64_t dQ = sdesc(sQ, 16, 1024), dK = sdesc(sK, 16, 1024);
+            Item it;
+            int g = 0, n[2] = {0, 0};        // steps of the run, of each slot
+            uint32_t qs = 0;                 // a slot's phase of its queries, by bits
+            while (next_alone(it)) {
+                for (int j = it.j0; ok && j < it.j1; ++j, ++g) {
+                    const int st = g % C::KS;
+                    ok = mbar_wait<false>(bar(kKFull + st), (uint32_t)((g / C::KS) & 1), abort_flag);
 #pragma unroll
-                for (int e = 0; e < C::CH * 4; ++e)
-                    umma_pair(tmem + r * 128, da + (((e >> 2) * C::Q_CHUNK + (e & 3) * 32) >> 4),
-                              db + (((e >> 2) * C::K_CHUNK + (e & 3) * 32) >> 4), ID_S, e > 0);
-                commit_pair(bar(kSFull + 2 * x + r));
-                if (j < i.both && !(half_read >> st & 1)) {
-                    half_read |= 1u << st;
-                } else {
-                    half_read &= ~(1u << st);
+                    for (int x = 0; x < 2; ++x) {
+                        if (!ok || j >= it.end(x)) continue;
+                        if (j == it.j0) {
+                            ok = mbar_wait<false>(bar(kQFull + x), qs >> x & 1, abort_flag);
+                            qs ^= 1u << x;
+                        }
+                        // the place is free once P V of the step before the last is done
+                        const int p = n[x] & 1;
+                        if (ok && n[x] >= 2)
+                            ok = mbar_wait<false>(bar(kPvDone + 2 * x + p),
+                                                  (uint32_t)(((n[x] - 2) >> 1) & 1), abort_flag);
+                        if (!ok) continue;
+                        fence_after();
+                        const uint64_t da = dQ + (uint64_t)((x * C::Q_SLOT) >> 4);
+                        const uint64_t db = dK + (uint64_t)((st * C::K_STAGE) >> 4);
+#pragma unroll
+                        for (int e = 0; e < C::CH * 4; ++e)
+                            umma_pair(tmem + (2 * x + p) * 64,
+                                      da + (((e >> 2) * C::Q_CHUNK + (e & 3) * 32) >> 4),
+                                      db + (((e >> 2) * C::K_CHUNK + (e & 3) * 32) >> 4), ID_S, e > 0);
+                        commit_pair(bar(kSFull + 2 * x + p));
+                        if (j == it.end(x) - 1) commit_pair(bar(kQEmpty + x));
+                        ++n[x];
+                    }
                     commit_pair(bar(kKEmpty + st));
                 }
-                if (j == i.end(x) - 1) commit_pair(bar(kQEmpty + x));
-                return true;
-            };
-            // O += P V of the step whose weights are in columns r
-            auto weigh = [&](const Item& i, int g0, int r, int j) {
-                const int x = i.slot_of(r, j), g = g0 + j - i.j0, st = g % C::VS;
-                const uint64_t db = dV + (uint64_t)((st * C::V_STAGE) >> 4);
-                const uint32_t par = ps >> r & 1;
-                ps ^= 1u << r;
-#pragma unroll
-                for (int half = 0; half < 2; ++half) {
-                    if (!mbar_wait<false>(bar(kPFull + 2 * r + half), par, abort_flag)) return false;
-                    if (half == 0) {
-                        if (j == i.j0 && (outs >> x & 1)) {
-                            if (!mbar_wait<false>(bar(kORead + x), os >> x & 1, abort_flag)) return false;
-                            os ^= 1u << x;
-                        }
-                        if (!mbar_wait<false>(bar(kVFull + st), (uint32_t)((g / C::VS) & 1), abort_flag))
-                            return false;
-                    }
-                    fence_after();
-#pragma unroll
-                    for (int e = 0; e < 4; ++e)
-                        umma_ts_pair(tmem + kColO + x * N, tmem + r * 128 + half * 32 + e * 8,
-                                     db + ((half * 8192 + e * 2048) >> 4), ID_PV,
-                                     j > i.j0 || half > 0 || e > 0);
-                }
-                commit_pair(bar(kPvDone + x));
-                if (j == i.end(x) - 1) outs |= 1u << x;
-                if (j >= i.both || r == 1) commit_pair(bar(kVEmpty + st));
-                return true;
-            };
-            bool have = next(it);
-            int g0 = 0;
-            uint32_t formed = 0;             // columns that hold the item's first S already
-            while (ok && have) {
-                for (int k = 0; ok && k < 2; ++k) {
-                    const int r = it.start ^ k, j = it.first_use(r);
-                    if (!(formed >> r & 1) && j >= 0) ok = form(it, g0, r, j);
-                }
-                if (!ok) break;
-                const bool more = next(nit);
-                const int n0 = g0 + it.j1 - it.j0;
-                formed = 0;
-                for (int j = it.j0; ok && j < it.j1; ++j)
-                    for (int r = 0; ok && r < 2; ++r) {
-                        if (j >= it.both && r != it.columns(j)) continue;
-                        ok = weigh(it, g0, r, j);
-                        // the columns are free for their next scores
-                        const int u = it.next_use(r, j);
-                        if (!ok) break;
-                        const int f = nit.first_use(r);
-                        if (u >= 0) {
-                            ok = form(it, g0, r, u);
-                        } else if (more && f >= 0 && (f == nit.j0 || (formed >> nit.start & 1))) {
-                            // (a slot's scores are formed in the order of its steps)
-                            ok = form(nit, n0, r, f);
-                            formed |= 1u << r;
-                        }
-                    }
-                it = nit;
-                g0 = n0;
-                have = more;
             }
             if (!ok) {
                 fail();
@@ -601,15 +531,58 @@ __global__ void __launch_bounds__(kThreads, 1)
             }
         }
         __syncwarp();
+    } else if (warp == 12) {
+        // ================================================= outputs
+        if (rank == 0 && elect_one()) {
+            constexpr uint32_t ID_PV = idesc(El<T>::kType, true, N, 256);
+            const uint64_t dV = sdesc(sV, 1024, 1024);
+            Item it;
+            int g = 0, n[2] = {0, 0};        // steps of the run, of each slot
+            uint32_t left = 0, os = 0;       // by bits: slots that left an output, its phase
+            while (next_alone(it)) {
+                for (int j = it.j0; ok && j < it.j1; ++j, ++g) {
+                    const int st = g % C::VS;
+                    ok = mbar_wait<false>(bar(kVFull + st), (uint32_t)((g / C::VS) & 1), abort_flag);
+#pragma unroll
+                    for (int x = 0; x < 2; ++x) {
+                        if (!ok || j >= it.end(x)) continue;
+                        const int p = n[x] & 1;
+                        ok = mbar_wait<false>(bar(kPFull + 2 * x + p), (uint32_t)(n[x] >> 1 & 1),
+                                              abort_flag);
+                        if (ok && j == it.j0 && (left >> x & 1)) {
+                            ok = mbar_wait<false>(bar(kORead + x), os >> x & 1, abort_flag);
+                            os ^= 1u << x;
+                        }
+                        if (!ok) continue;
+                        fence_after();
+                        const uint64_t db = dV + (uint64_t)((st * C::V_STAGE) >> 4);
+#pragma unroll
+                        for (int e = 0; e < kKeys / 16; ++e)
+                            umma_ts_pair(tmem + kColO + x * N, tmem + (2 * x + p) * 64 + e * 8,
+                                         db + ((e * 2048) >> 4), ID_PV, j > it.j0 || e > 0);
+                        commit_pair(bar(kPvDone + 2 * x + p));
+                        left |= 1u << x;
+                        ++n[x];
+                    }
+                    commit_pair(bar(kVEmpty + st));
+                }
+            }
+            if (!ok) {
+                fail();
+                volatile int never = 0;
+                commit_pair(bar(kSpare + 1));
+                mbar_wait(bar(kSpare + 1), 0, &never);
+            }
+        }
+        __syncwarp();
     } else {
         // ================================================= softmax
         const int x = warp >= 8, quad = warp & 3;
         const uint32_t lanes = (uint32_t)(quad * 32) << 16;
         const uint32_t tO = tmem + lanes + kColO + x * N;
-        const uint32_t pfull0 = at_rank(bar(kPFull), 0), oread = at_rank(bar(kORead + x), 0);
+        const uint32_t pfull = at_rank(bar(kPFull + 2 * x), 0), oread = at_rank(bar(kORead + x), 0);
         Item it;
-        uint32_t uses = 0;                   // of each columns, by this slot: odd
-        int pv = 0;                          // steps of this slot
+        int n = 0;                           // steps of this slot
         const float scale = a.scale_log2;
         const uint64_t scale2 = f2(scale, scale);
         while (next_item(it)) {
@@ -622,50 +595,36 @@ __global__ void __launch_bounds__(kThreads, 1)
             const bool whole = it.whole();
             float m = -INFINITY;
             uint64_t l2 = 0;                                 // two partial sums
-            for (int j = it.j0; j < end; ++j, ++pv) {
-                const bool apart = j < it.both;
-                const int r = apart ? x : it.columns(j);                 // its columns
-                const uint32_t tS = tmem + lanes + r * 128, pfull = pfull0 + r * 16;
-                ok = ok && warp_wait(bar(kSFull + 2 * x + r), uses >> r & 1, abort_flag);
-                uses ^= 1u << r;
+            for (int j = it.j0; j < end; ++j, ++n) {
+                const int place = n & 1;
+                const uint32_t tS = tmem + lanes + (2 * x + place) * 64;
+                ok = ok && warp_wait(bar(kSFull + 2 * x + place), (uint32_t)(n >> 1 & 1), abort_flag);
                 fence_after();
                 if (live) {
-                    // the later half is looked at for the max first and loaded again for the
-                    // weights: both halves held at once would spill
-                    const bool hides = it.off + rw + 1 - j * kKeys < kKeys;
-                    const int n = it.off + row + 1 - j * kKeys;   // keys of the step that it sees
-                    // a hidden key's score: lowest of the scaled ones
-                    const uint32_t hide = __float_as_uint(scale < 0.f ? INFINITY : -INFINITY);
                     uint32_t z[64];
-                    auto cover = [&](int from) {
-                        if (!hides) return;
-#pragma unroll
-                        for (int e = 0; e < 64; ++e)
-                            if (from + e >= n) z[e] = hide;
-                    };
-                    auto largest = [&]() {               // largest of the scaled ones, unscaled
-                        float top = __uint_as_float(z[0]), t1 = __uint_as_float(z[1]);
-                        if (scale >= 0.f) {
-#pragma unroll
-                            for (int e = 2; e < 62; e += 4) {
-                                top = max3(top, __uint_as_float(z[e]), __uint_as_float(z[e + 1]));
-                                t1 = max3(t1, __uint_as_float(z[e + 2]), __uint_as_float(z[e + 3]));
-                            }
-                            return fmaxf(max3(top, __uint_as_float(z[62]), __uint_as_float(z[63])), t1);
-                        }
-#pragma unroll
-                        for (int e = 2; e < 64; ++e) top = fminf(top, __uint_as_float(z[e]));
-                        return fminf(top, t1);
-                    };
-                    ld64(tS + 64, z);
-                    ld_wait(z);
-                    cover(64);
-                    const float later = largest();
                     ld64(tS, z);
                     ld_wait(z);
-                    cover(0);
-                    float top = largest();
-                    top = scale >= 0.f ? fmaxf(top, later) : fminf(top, later);
+                    // a hidden key's score: lowest of the scaled ones
+                    if (it.off + rw + 1 - j * kKeys < kKeys) {
+                        const int seen = it.off + row + 1 - j * kKeys;
+                        const uint32_t hide = __float_as_uint(scale < 0.f ? INFINITY : -INFINITY);
+#pragma unroll
+                        for (int e = 0; e < 64; ++e)
+                            if (e >= seen) z[e] = hide;
+                    }
+                    float top = __uint_as_float(z[0]), t1 = __uint_as_float(z[1]);
+                    if (scale >= 0.f) {
+#pragma unroll
+                        for (int e = 2; e < 62; e += 4) {
+                            top = max3(top, __uint_as_float(z[e]), __uint_as_float(z[e + 1]));
+                            t1 = max3(t1, __uint_as_float(z[e + 2]), __uint_as_float(z[e + 3]));
+                        }
+                        top = fmaxf(max3(top, __uint_as_float(z[62]), __uint_as_float(z[63])), t1);
+                    } else {
+#pragma unroll
+                        for (int e = 2; e < 64; ++e) top = fminf(top, __uint_as_float(z[e]));
+                        top = fminf(top, t1);
+                    }
                     // (none where all are hidden: scaled, infinity times the scale)
                     top = fabsf(top) == INFINITY ? -INFINITY : top * scale;
                     float alpha = 1.f;
@@ -683,69 +642,52 @@ __global__ void __launch_bounds__(kThreads, 1)
                     const uint64_t minus2 = f2(minus, minus);
                     uint64_t sum[2] = {0, 0};
 #pragma unroll
-                    for (int half = 0; half < 2; ++half) {
-                        if (half) {
-                            ld64(tS + 64, z);
-                            ld_wait(z);
-                            cover(64);
-                        }
+                    for (int c = 0; c < 2; ++c) {
+                        uint32_t w[16];
 #pragma unroll
-                        for (int c = 0; c < 2; ++c) {
-                            uint32_t w[16];
+                        for (int e = 0; e < 16; ++e) {
+                            float p, q;
+                            f2_split(fma2(f2(__uint_as_float(z[32 * c + 2 * e]),
+                                             __uint_as_float(z[32 * c + 2 * e + 1])),
+                                          scale2, minus2),
+                                     p, q);
+                            p = ex2(p);
+                            q = ex2(q);
+                            sum[e & 1] = add2(sum[e & 1], f2(p, q));
+                            w[e] = El<T>::pack(p, q);
+                        }
+                        st16(tS + c * 16, w);
+                    }
+                    l2 = fma2(l2, f2(alpha, alpha), add2(sum[0], sum[1]));
+                    if (j > it.j0 && __any_sync(0xffffffffu, alpha != 1.f)) {
+                        // P V of the step before has to be in O (that of the one before it is:
+                        // this step's scores took its place)
+                        ok = ok && warp_wait(bar(kPvDone + 2 * x + (place ^ 1)),
+                                             (uint32_t)((n - 1) >> 1 & 1), abort_flag);
+                        fence_after();
+                        const uint64_t al2 = f2(alpha, alpha);
+#pragma unroll 1
+                        for (int c = 0; c < N; c += 32) {
+                            uint32_t o[32];
+                            ld32(tO + c, o);
+                            ld_wait(o);
 #pragma unroll
                             for (int e = 0; e < 16; ++e) {
                                 float p, q;
-                                f2_split(fma2(f2(__uint_as_float(z[32 * c + 2 * e]),
-                                                 __uint_as_float(z[32 * c + 2 * e + 1])),
-                                              scale2, minus2),
+                                f2_split(mul2(f2(__uint_as_float(o[2 * e]), __uint_as_float(o[2 * e + 1])),
+                                              al2),
                                          p, q);
-                                p = ex2(p);
-                                q = ex2(q);
-                                sum[e & 1] = add2(sum[e & 1], f2(p, q));
-                                w[e] = El<T>::pack(p, q);
+                                o[2 * e] = __float_as_uint(p);
+                                o[2 * e + 1] = __float_as_uint(q);
                             }
-                            st16(tS + half * 32 + c * 16, w);
+                            st32(tO + c, o);
                         }
-                        // (S of a step alone is formed before P V of the step before it)
-                        if (half == 0 && j > it.j0 && !apart) {
-                            ok = ok && warp_wait(bar(kPvDone + x), (uint32_t)((pv - 1) & 1), abort_flag);
-                            fence_after();
-                        }
-                        if (half == 0 && j > it.j0 && __any_sync(0xffffffffu, alpha != 1.f)) {
-                            const uint64_t al2 = f2(alpha, alpha);
-#pragma unroll 1
-                            for (int c = 0; c < N; c += 16) {
-                                uint32_t o[16];
-                                ld16(tO + c, o);
-                                ld_wait(o);
-#pragma unroll
-                                for (int e = 0; e < 8; ++e) {
-                                    float p, q;
-                                    f2_split(mul2(f2(__uint_as_float(o[2 * e]), __uint_as_float(o[2 * e + 1])),
-                                                  al2),
-                                             p, q);
-                                    o[2 * e] = __float_as_uint(p);
-                                    o[2 * e + 1] = __float_as_uint(q);
-                                }
-                                st16(tO + c, o);
-                            }
-                        }
-                        st_wait();
-                        fence_before();
-                        __syncwarp();
-                        if (lane == 0) mbar_arrive_cluster(pfull + half * 8);
                     }
-                    l2 = fma2(l2, f2(alpha, alpha), add2(sum[0], sum[1]));
-                } else {
-                    if (j > it.j0 && !apart)
-                        ok = ok && warp_wait(bar(kPvDone + x), (uint32_t)((pv - 1) & 1), abort_flag);
-                    fence_before();
-                    __syncwarp();
-                    if (lane == 0) {
-                        mbar_arrive_cluster(pfull);
-                        mbar_arrive_cluster(pfull + 8);
-                    }
+                    st_wait();
                 }
+                fence_before();
+                __syncwarp();
+                if (lane == 0) mbar_arrive_cluster(pfull + place * 8);
             }
             // the slot's output
             float p, q;
@@ -754,7 +696,7 @@ __global__ void __launch_bounds__(kThreads, 1)
             const bool mine = at + lane < mine_rows && ok;
             if (mine && !whole) a.ml[slot * a.slot_rows + row] = make_float2(m, l);
             if (end > it.j0) {
-                ok = ok && warp_wait(bar(kPvDone + x), (uint32_t)((pv - 1) & 1), abort_flag);
+                ok = ok && warp_wait(bar(kPvDone + 2 * x + ((n - 1) & 1)), (uint32_t)((n - 1) >> 1 & 1), abort_flag);
                 fence_after();
                 if (live) {
                     const float inv = 1.f / l;
