@@ -123,10 +123,15 @@ struct Rec {
 struct Seq {
     int q0, qlen, ctx;
     int nt, nr;                       // steps of a row tile, row tiles (0: nothing to do)
-    __device__ __forceinline__ bool load(const Args& a, int s) {
+    // what a sequence's lengths are, as they lie in memory ...
+    __device__ __forceinline__ void fetch(const Args& a, int s) {
         q0 = a.q_start ? a.q_start[s] : s;
-        qlen = a.q_start ? a.q_start[s + 1] - q0 : 1;
+        qlen = a.q_start ? a.q_start[s + 1] : s + 1;
         ctx = a.ctx[s];
+    }
+    // ... and looked at (the loads are waited for here)
+    __device__ __forceinline__ bool look(const Args& a) {
+        qlen -= q0;
         nt = nr = 0;
         if (ctx < 0 || (int64_t)ctx > (int64_t)a.max_blocks * a.B || qlen < 0 ||
             qlen > a.max_qlen || q0 < 0 || (int64_t)q0 + qlen > a.T || (ctx > 0 && qlen > ctx))
@@ -136,6 +141,10 @@ struct Seq {
             nr = (int)(((int64_t)qlen * a.H + kRows - 1) / kRows);
         }
         return true;
+    }
+    __device__ __forceinline__ bool load(const Args& a, int s) {
+        fetch(a, s);
+        return look(a);
     }
     __device__ __forceinline__ int64_t steps() const { return (int64_t)nt * nr; }
 };
@@ -169,7 +178,7 @@ struct Walker {
         left = st.n;
         first = true;
         q = st.q;
-        if (left > 0 && s + 1 < a.S) next.load(a, s + 1);
+        if (left > 0 && s + 1 < a.S) next.fetch(a, s + 1);
     }
     __device__ __forceinline__ bool get(const Args& a, Seg& g) {
         if (left <= 0) return false;
@@ -177,9 +186,10 @@ struct Walker {
             if (++s >= a.S) return false;
             off = 0;
             q = next;
-            if (s + 1 < a.S) next.load(a, s + 1);
+            q.look(a);
+            if (s + 1 < a.S) next.fetch(a, s + 1);
         }
-        const int rt = (int)(off / q.nt);
+        const int rt = off < (1 << 30) ? (int)off / q.nt : (int)(off / q.nt);
         g.s = s;
         g.q0 = q.q0;
         g.qlen = q.qlen;
@@ -680,35 +690,31 @@ __global__ void __launch_bounds__(kThreads, 1)
                 const float inv = l > 0.f ? 1.f / l : l;     // (NaN stays NaN)
                 uint16_t* orow = a.out + ((int64_t)g.q0 * a.H + g.row + row) * R + half * (R / 2);
                 float* prow = a.acc + ((slot * (R / 8) + half * (R / 16)) * a.slot_rows + row) * 8;
-                uint32_t next[32];
-                ld32(tmem + lanes + kColO, next);
 #pragma unroll 1
-                for (int c = 0; c < R / 2; c += 32) {
-                    uint32_t o[32];
-                    ld_wait(next);
-#pragma unroll
-                    for (int e = 0; e < 32; ++e) o[e] = next[e];
-                    if (c + 32 < R / 2) ld32(tmem + lanes + kColO + c + 32, next);
+                for (int c = 0; c < R / 2; c += 64) {
+                    uint32_t o[64];
+                    ld64(tmem + lanes + kColO + c, o);
+                    ld_wait(o);
                     if (!mine) continue;
                     if (g.whole) {
-                        uint32_t p[16];
+                        uint32_t p[32];
 #pragma unroll
-                        for (int e = 0; e < 16; ++e)
+                        for (int e = 0; e < 32; ++e)
                             p[e] = inv != 0.f ? El<T>::pack(__uint_as_float(o[2 * e]) * inv,
                                                             __uint_as_float(o[2 * e + 1]) * inv)
                                               : 0u;
                         if (a.out_v8) {
-                            st_global_v8(orow + c, p);
-                            st_global_v8(orow + c + 16, p + 8);
+#pragma unroll
+                            for (int e = 0; e < 4; ++e) st_global_v8(orow + c + 16 * e, p + 8 * e);
                         } else {
 #pragma unroll
-                            for (int e = 0; e < 4; ++e)
+                            for (int e = 0; e < 8; ++e)
                                 *reinterpret_cast<uint4*>(orow + c + 8 * e) =
                                     make_uint4(p[4 * e], p[4 * e + 1], p[4 * e + 2], p[4 * e + 3]);
                         }
                     } else {
 #pragma unroll
-                        for (int e = 0; e < 4; ++e)
+                        for (int e = 0; e < 8; ++e)
                             st_global_v8(prow + (int64_t)(c / 8 + e) * a.slot_rows * 8, o + 8 * e);
                     }
                 }
@@ -740,7 +746,7 @@ __global__ void __launch_bounds__(kThreads, 1)
     }
     fence_before();
     __syncthreads();
-    cluster_sync();
+    cluster_meet();
     if (warp == 1) {
         fence_after();
         dealloc_pair(tmem);

@@ -115,17 +115,27 @@ struct Rec {
 
 struct Seq {
     int q0, k0, qlen, klen;           // qlen 0: nothing to do
-    __device__ __forceinline__ bool load(const Args& a, int s) {
+    // what a sequence's lengths are, as they lie in memory ...
+    __device__ __forceinline__ void fetch(const Args& a, int s) {
         q0 = a.q_start[s];
-        qlen = a.q_start[s + 1] - q0;
+        qlen = a.q_start[s + 1];
         k0 = a.k_start[s];
-        klen = a.k_start[s + 1] - k0;
+        klen = a.k_start[s + 1];
+    }
+    // ... and looked at (the loads are waited for here)
+    __device__ __forceinline__ bool look(const Args& a) {
+        qlen -= q0;
+        klen -= k0;
         if (qlen < 0 || qlen > a.max_q || q0 < 0 || (int64_t)q0 + qlen > a.Tq || klen < qlen ||
             klen > a.max_k || k0 < 0 || (int64_t)k0 + klen > a.Tk) {
             qlen = 0;
             return false;
         }
         return true;
+    }
+    __device__ __forceinline__ bool load(const Args& a, int s) {
+        fetch(a, s);
+        return look(a);
     }
     __device__ __forceinline__ int items() const { return (qlen + kRows - 1) / kRows; }
     // steps of item t: to the key of its last row
@@ -178,7 +188,7 @@ struct Walker {
         turn = 0;
         h = t = j = 0;
         if (left <= 0) return;
-        if (s + 1 < a.S) next.load(a, s + 1);
+        if (s + 1 < a.S) next.fetch(a, s + 1);
         const int64_t per = q.head_steps();
         h = per < (1 << 30) && st.off < (1 << 30) ? (int)st.off / (int)per : (int)(st.off / per);
         int64_t rest = st.off - h * per;
@@ -198,7 +208,8 @@ struct Walker {
             h = 0;
             if (++s >= a.S) return false;
             q = next;
-            if (s + 1 < a.S) next.load(a, s + 1);
+            q.look(a);
+            if (s + 1 < a.S) next.fetch(a, s + 1);
         }
         it.q0 = q.q0 + t * kRows;
         it.k0 = q.k0;
@@ -761,7 +772,7 @@ __global__ void __launch_bounds__(kThreads, 1)
     }
     fence_before();
     __syncthreads();
-    cluster_sync();
+    cluster_meet();
     if (warp == 1) {
         fence_after();
         dealloc_pair(tmem);

@@ -108,9 +108,11 @@ __device__ __forceinline__ uint32_t cluster_rank() {
     asm volatile("mov.u32 %0, %%cluster_ctarank;" : "=r"(r));
     return r;
 }
-__device__ __forceinline__ void cluster_sync() {
+// Both CTAs have come here.  Nothing that they wrote is ordered by it: a release would
+// wait for all of their stores, about 1000 cycles.
+__device__ __forceinline__ void cluster_meet() {
     asm volatile(
-        "barrier.cluster.arrive.release.aligned;\n\t"
+        "barrier.cluster.arrive.relaxed.aligned;\n\t"
         "barrier.cluster.wait.acquire.aligned;" ::
             : "memory");
 }
