@@ -347,6 +347,7 @@ __global__ void __launch_bounds__(kThreads, 1)
             int y = row_of(g.j0);
             for (int j = g.j0; j < g.j1; ++j) {
                 const int yn = j + 1 < g.j1 ? row_of(j + 1) : -1;
+#pragma unroll
                 for (int u = 0; u < C::KSUB; ++u, ++kc) {
                     const int st = kc % C::KS, n = kc / C::KS;
                     if (n > 0 && !warp_wait(bar(kKEmpty + st), (uint32_t)((n - 1) & 1), abort_flag)) {
@@ -354,7 +355,7 @@ __global__ void __launch_bounds__(kThreads, 1)
                         break;
                     }
                     const uint32_t full = at_rank(bar(kKFull + st), 0);
-                    if (lane == 0) mbar_expect_tx_cluster(full, C::K_SLOT);
+                    if (lane == 0) mbar_expect_tx_relaxed(full, C::K_SLOT);
                     __syncwarp();
                     if (lane < 8)
                         tma_3d_pair(sK + st * C::K_SLOT + lane * C::KC * 1024, &tm_k, 0,
@@ -377,7 +378,7 @@ __global__ void __launch_bounds__(kThreads, 1)
                 break;
             }
             const bool live = g.rows > 64 * (int)rank;
-            if (lane == 0) mbar_expect_tx_cluster(qfull, live ? C::Q_BYTES : 0);
+            if (lane == 0) mbar_expect_tx_relaxed(qfull, live ? C::Q_BYTES : 0);
             __syncwarp();
             if (live && lane < 8)
                 tma_3d_pair(sQ + lane * C::CH * 1024, &tm_q, 0,
@@ -417,20 +418,28 @@ __global__ void __launch_bounds__(kThreads, 1)
                     if (has_tail) {
                         const int yt = __shfl_sync(0xffffffffu, y, tail & 15);
                         const uint32_t to = slot + (tail & 3) * C::V_GROUP;
-                        for (int i = lane; i < C::VCH * 64; i += 32) {
-                            const int r = i / (C::VCH * 8), c = i - r * (C::VCH * 8);
-                            uint4 w = make_uint4(0u, 0u, 0u, 0u);
+                        uint4 w[2 * C::VCH];
+#pragma unroll
+                        for (int e = 0; e < 2 * C::VCH; ++e) {
+                            const int i = 32 * e + lane, r = i / (C::VCH * 8), c = i - r * (C::VCH * 8);
+                            w[e] = make_uint4(0u, 0u, 0u, 0u);
                             if (yt >= 0 && r < (left & 7))
-                                w = *reinterpret_cast<const uint4*>(
+                                w[e] = *reinterpret_cast<const uint4*>(
                                     a.cache + (int64_t)(yt + r) * C::W + (int)rank * (R / 2) + c * 8);
-                            st_shared_v4(to + (c >> 3) * 1024 + r * 128 + (((c & 7) ^ r) << 4), w.x,
-                                         w.y, w.z, w.w);
+                        }
+#pragma unroll
+                        for (int e = 0; e < 2 * C::VCH; ++e) {
+                            const int i = 32 * e + lane, r = i / (C::VCH * 8), c = i - r * (C::VCH * 8);
+                            st_shared_v4(to + (c >> 3) * 1024 + r * 128 + (((c & 7) ^ r) << 4), w[e].x,
+                                         w[e].y, w[e].z, w[e].w);
                         }
                         fence_async_smem();
                         __syncwarp();
                     }
-                    if (lane == 0)
-                        mbar_expect_tx_cluster(full, has_tail ? 3 * C::V_GROUP : C::V_SLOT);
+                    if (lane == 0) {
+                        if (has_tail) mbar_expect_tx_cluster(full, 3 * C::V_GROUP);
+                        else mbar_expect_tx_relaxed(full, C::V_SLOT);
+                    }
                     __syncwarp();
                     if ((lane >> 2) == v && lane != tail)
                         tma_3d_pair(slot + (lane & 3) * C::V_GROUP, &tm_v, 0, y < 0 ? none : y,
@@ -467,7 +476,10 @@ __global__ void __launch_bounds__(kThreads, 1)
                         return false;
                     const int left = cur.ctx - j * kTok;
                     const int subs = left >= kTok ? 4 : (left + 31) / 32;
-                    for (int v = 0; v < subs; ++v, ++vc) {
+                    // (unrolled: a jump back costs the issuing thread 200 cycles)
+#pragma unroll
+                    for (int v = 0; v < 4; ++v) {
+                        if (v >= subs) break;
                         if (!mbar_wait<false>(v_full(vc), v_par(vc), abort_flag)) return false;
                         fence_after();
                         const uint64_t da = dP + (uint64_t)(((v >> 1) * 8192 + (v & 1) * 64) >> 4);
@@ -481,6 +493,7 @@ __global__ void __launch_bounds__(kThreads, 1)
                                           j > cur.j0 || v > 0 || k > 0);
                         }
                         commit_pair(bar(kVEmpty + vc % C::VS));
+                        ++vc;
                     }
                     commit_pair(bar(kPvDone));
                     ++pc;
@@ -491,6 +504,7 @@ __global__ void __launch_bounds__(kThreads, 1)
                     break;
                 }
                 for (int j = cur.j0; ok && j < cur.j1; ++j) {
+#pragma unroll
                     for (int u = 0; u < C::KSUB; ++u, ++kc) {
                         if (!mbar_wait<false>(k_full(kc), k_par(kc), abort_flag)) {
                             ok = false;
@@ -721,7 +735,7 @@ __global__ void __launch_bounds__(kThreads, 1)
             }
             fence_before();
             __syncwarp();
-            if (lane == 0) mbar_arrive_cluster(oread);
+            if (lane == 0) mbar_arrive_relaxed(oread);
             // the first part of a tile that goes on in the next pairs' runs
             if (!g.whole && g.j0 == 0 && rank == 0 && warp == 2 && lane == 0) {
                 // steps of the tile from this run's end on, and the runs they fall in

@@ -404,7 +404,7 @@ __global__ void __launch_bounds__(kThreads, 1)
                     break;
                 }
                 const uint32_t full = at_rank(bar(kKFull + st), 0);
-                if (lane == 0) mbar_expect_tx_cluster(full, C::K_STAGE);
+                if (lane == 0) mbar_expect_tx_relaxed(full, C::K_STAGE);
                 __syncwarp();
                 const uint32_t to = sK + st * C::K_STAGE + c * C::K_CHUNK + r * 128;
                 const int key = it.k0 + j * kKeys + kKeys / 2 * (int)rank + r;
@@ -434,19 +434,27 @@ __global__ void __launch_bounds__(kThreads, 1)
                 if (tail >= 0) {
                     const uint16_t* from = a.v + (int64_t)(it.k0 + j * kKeys + tail * kBoxRows) * a.v_stride +
                                            it.h * a.v_head + (int)rank * (N / 2);
-                    for (int i = lane; i < kBoxRows * 8; i += 32) {
-                        const int r = i >> 3, p = i & 7;
-                        uint4 w = make_uint4(0u, 0u, 0u, 0u);
+                    uint4 w[kBoxRows / 4];
+#pragma unroll
+                    for (int e = 0; e < kBoxRows / 4; ++e) {
+                        const int r = 4 * e + (lane >> 3), p = lane & 7;
+                        w[e] = make_uint4(0u, 0u, 0u, 0u);
                         if (r < left % kBoxRows && p < N / 16)
-                            w = *reinterpret_cast<const uint4*>(from + r * a.v_stride + p * 8);
-                        st_shared_v4(stage + (tail * kBoxRows + r) * 128 + ((p ^ (r & 7)) << 4), w.x,
-                                     w.y, w.z, w.w);
+                            w[e] = *reinterpret_cast<const uint4*>(from + r * a.v_stride + p * 8);
+                    }
+#pragma unroll
+                    for (int e = 0; e < kBoxRows / 4; ++e) {
+                        const int r = 4 * e + (lane >> 3), p = lane & 7;
+                        st_shared_v4(stage + (tail * kBoxRows + r) * 128 + ((p ^ (r & 7)) << 4), w[e].x,
+                                     w[e].y, w[e].z, w[e].w);
                     }
                     fence_async_smem();
                     __syncwarp();
                 }
-                if (lane == 0)
-                    mbar_expect_tx_cluster(full, C::V_STAGE - (tail >= 0 ? kBoxRows * 128 : 0));
+                if (lane == 0) {
+                    if (tail >= 0) mbar_expect_tx_cluster(full, C::V_STAGE - kBoxRows * 128);
+                    else mbar_expect_tx_relaxed(full, C::V_STAGE);
+                }
                 __syncwarp();
                 // boxes behind the last key: past the tensor's end, zeros
                 if (lane < BOXES && lane != tail)
@@ -485,7 +493,7 @@ __global__ void __launch_bounds__(kThreads, 1)
                     break;
                 }
                 const uint32_t full = at_rank(bar(kQFull + x), 0);
-                if (lane == 0) mbar_expect_tx_cluster(full, C::Q_SLOT);
+                if (lane == 0) mbar_expect_tx_relaxed(full, C::Q_SLOT);
                 __syncwarp();
                 if (c < C::CH)
                     tma_3d_pair(sQ + x * C::Q_SLOT + c * C::Q_CHUNK + r * 128, &tm_q, c * 64, it.h,
@@ -747,7 +755,7 @@ __global__ void __launch_bounds__(kThreads, 1)
                 }
                 fence_before();
                 __syncwarp();
-                if (lane == 0) mbar_arrive_cluster(oread);
+                if (lane == 0) mbar_arrive_relaxed(oread);
             }
             // the first part of an item that goes on in the next pairs' runs
             if (!whole && it.j0 == 0 && rank == 0 && warp == 4 && lane == 0) {

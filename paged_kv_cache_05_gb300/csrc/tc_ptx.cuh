@@ -36,12 +36,23 @@ __device__ __forceinline__ uint32_t at_rank(uint32_t addr, uint32_t rank) {
     asm("mapa.shared::cluster.u32 %0, %1, %2;" : "=r"(r) : "r"(addr), "r"(rank));
     return r;
 }
-// Arrivals on a barrier of either CTA of the cluster (at_rank).  What they order went
-// through fence_async_smem and is read by the tensor cores: a release at cluster scope
-// would be a fence of all of the thread's memory, about 1000 cycles each.
+// Arrivals on a barrier of either CTA of the cluster (at_rank).  What mbar_arrive_cluster
+// orders went through fence_async_smem and is read by the tensor cores: a release at
+// cluster scope would be a fence of all of the thread's memory, about 1000 cycles each.
+// The others order nothing that the thread itself wrote or read (copies complete on the
+// barrier by themselves), and do not wait for its loads and stores on their way.
 __device__ __forceinline__ void mbar_arrive_cluster(uint32_t bar) {
     asm volatile("mbarrier.arrive.shared::cluster.b64 _, [%0];" ::"r"(bar) : "memory");
 }
+__device__ __forceinline__ void mbar_arrive_relaxed(uint32_t bar) {
+    asm volatile("mbarrier.arrive.relaxed.cluster.shared::cluster.b64 _, [%0];" ::"r"(bar) : "memory");
+}
+__device__ __forceinline__ void mbar_expect_tx_relaxed(uint32_t bar, uint32_t bytes) {
+    asm volatile("mbarrier.arrive.expect_tx.relaxed.cluster.shared::cluster.b64 _, [%0], %1;" ::"r"(bar),
+                 "r"(bytes)
+                 : "memory");
+}
+// (after the thread's own writes of a part of what the barrier is for)
 __device__ __forceinline__ void mbar_expect_tx_cluster(uint32_t bar, uint32_t bytes) {
     asm volatile("mbarrier.arrive.expect_tx.shared::cluster.b64 _, [%0], %1;" ::"r"(bar), "r"(bytes)
                  : "memory");
