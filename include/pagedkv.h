@@ -573,6 +573,10 @@ pkv_status pkv_swap_blocks(void* dst_k_cache, void* dst_v_cache, const void* src
  *   cache   [num_blocks][block_size][latent_dim + rope_dim], one pool
  * latent_dim 256 or 512, rope_dim 64, fp16 or bf16 storage, block_size 8, 16, 32
  * or 64; block tables, context lengths, slots and errors as above.
+ * Numerics of both attention calls: scores, the running max, sums and outputs in
+ * fp32; a weight 2^(z - m) is rounded once to the storage type for its product with
+ * the values (the absorbed form's sum takes it rounded too).  fp16 weights are formed
+ * 2^9 higher: those below 2^-33 of the row's largest add nothing.
  */
 
 /*
@@ -665,7 +669,9 @@ pkv_status pkv_latent_attention_prefill(
  * with ctx < 0 or past the table, 0 < ctx < qlen, qlen past max_query_len or rows
  * outside [0, num_query_tokens) is skipped (PKV_DEVERR_BAD_CONTEXT); a block past
  * the pool is left out (PKV_DEVERR_BAD_BLOCK).  Rows of no sequence are left as they
- * are.  num_blocks * block_size must stay below 2^31.
+ * are.  What cached places past a sequence's last token hold does not matter; a
+ * visible token with elements that are not finite may show in the sequence's other
+ * rows.  num_blocks * block_size must stay below 2^31.
  * workspace: device memory of pkv_latent_decode_workspace_size(...) bytes, 256-byte
  * aligned, no initialisation; two calls in flight at once must not share it.
  */
