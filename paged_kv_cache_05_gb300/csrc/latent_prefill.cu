@@ -17,8 +17,8 @@
 // Thirteen warps a CTA: keys, values and queries a warp each (the last walks the run and
 // hands its items to the others through shared memory), one that issues the products for
 // the scores and one for the outputs (the first CTA's), and four of softmax a slot, a
-// thread a row.  A slot's scores S alternate between two places in
-// tensor memory: a step's are formed while the one before is weighed.  (With steps of 128
+// thread a row.  A slot's scores S go round two places (N = 64:
+// three) in tensor memory: a step's are formed while the one before is weighed.  (With steps of 128
 // keys and one place a slot, S waits for P V of the step before, which waits for its
 // softmax: 3150 cycles a step of 512 rows, where the products take 2560.)  Weights P are
 // written over the scores.  The max is raised only past a growth of kRescale, so that
@@ -55,13 +55,16 @@ constexpr int kMaxPairs = 96;
 constexpr int kWholeSteps = 8;
 constexpr int kBoxRows = 16;          // keys, or values, of a box
 constexpr int kQBoxRows = 32;
-constexpr uint32_t kColO = 256;       // tensor memory: S (and P over it) at 64 (2 slot + place), O from here
 
 template <int N>
 struct Cfg {
     static constexpr int CH = (N + kP) / 64;          // chunks of 64 elements of a key
     static constexpr int KS = N == 128 ? 6 : 8;       // stages
     static constexpr int VS = KS;
+    // tensor memory: S (and P over it) at 64 (PL slot + place), then each slot's O
+    static constexpr int PL = N == 128 ? 2 : 3;
+    static constexpr uint32_t COL_O = 128 * PL;
+    static_assert(COL_O + 2 * N <= 512, "tensor memory");
     static constexpr int Q_CHUNK = 128 * 128;         // a slot's rows of a chunk
     static constexpr int Q_SLOT = CH * Q_CHUNK;
     static constexpr int K_CHUNK = kKeys / 2 * 128;   // a CTA's keys of a chunk
@@ -71,7 +74,7 @@ struct Cfg {
     static constexpr int K_OFF = 2 * Q_SLOT;
     static constexpr int V_OFF = K_OFF + KS * K_STAGE;
     static constexpr int SMEM = V_OFF + VS * V_STAGE + 1024;   // 1 KiB of alignment slack
-    static_assert(SMEM + 1536 <= 232448, "shared memory");
+    static_assert(SMEM + 2048 <= 232448, "shared memory");
 };
 
 enum : int {
@@ -81,14 +84,14 @@ enum : int {
     kKEmpty = 12,    // + stage
     kVFull = 20,     // + stage
     kVEmpty = 28,    // + stage
-    kSFull = 36,     // + 2 slot + place: S formed
-    kPFull = 40,     // + 2 slot + place: weights written, O rescaled (first CTA's)
-    kPvDone = 44,    // + 2 slot + place: P V done
-    kORead = 48,     // + slot: its output read from tensor memory (first CTA's)
-    kItFull = 50,    // + entry (4)
-    kItEmpty = 54,   // + entry
-    kSpare = 58,     // + one of the products' threads
-    kBars = 60
+    kSFull = 36,     // + PL slot + place: S formed
+    kPFull = 42,     // + PL slot + place: weights written, O rescaled (first CTA's)
+    kPvDone = 48,    // + PL slot + place: P V done
+    kORead = 54,     // + slot: its output read from tensor memory (first CTA's)
+    kItFull = 56,    // + entry (4)
+    kItEmpty = 60,   // + entry
+    kSpare = 64,     // + one of the products' threads
+    kBars = 66
 };
 
 struct Args {
@@ -520,21 +523,21 @@ __global__ void __launch_bounds__(kThreads, 1)
                             ok = mbar_wait<false>(bar(kQFull + x), qs >> x & 1, abort_flag);
                             qs ^= 1u << x;
                         }
-                        // the place is free once P V of the step before the last is done
-                        const int p = n[x] & 1;
-                        if (ok && n[x] >= 2)
-                            ok = mbar_wait<false>(bar(kPvDone + 2 * x + p),
-                                                  (uint32_t)(((n[x] - 2) >> 1) & 1), abort_flag);
+                        // the place is free once P V of the step that had it is done
+                        const int p = n[x] % C::PL;
+                        if (ok && n[x] >= C::PL)
+                            ok = mbar_wait<false>(bar(kPvDone + C::PL * x + p),
+                                                  (uint32_t)(n[x] / C::PL - 1) & 1, abort_flag);
                         if (!ok) continue;
                         fence_after();
                         const uint64_t da = dQ + (uint64_t)((x * C::Q_SLOT) >> 4);
                         const uint64_t db = dK + (uint64_t)((st * C::K_STAGE) >> 4);
 #pragma unroll
                         for (int e = 0; e < C::CH * 4; ++e)
-                            umma_pair(tmem + (2 * x + p) * 64,
+                            umma_pair(tmem + (C::PL * x + p) * 64,
                                       da + (((e >> 2) * C::Q_CHUNK + (e & 3) * 32) >> 4),
                                       db + (((e >> 2) * C::K_CHUNK + (e & 3) * 32) >> 4), ID_S, e > 0);
-                        commit_pair(bar(kSFull + 2 * x + p));
+                        commit_pair(bar(kSFull + C::PL * x + p));
                         if (j == it.end(x) - 1) commit_pair(bar(kQEmpty + x));
                         ++n[x];
                     }
@@ -565,9 +568,9 @@ __global__ void __launch_bounds__(kThreads, 1)
 #pragma unroll
                     for (int x = 0; x < 2; ++x) {
                         if (!ok || j >= it.end(x)) continue;
-                        const int p = n[x] & 1;
-                        ok = mbar_wait<false>(bar(kPFull + 2 * x + p), (uint32_t)(n[x] >> 1 & 1),
-                                              abort_flag);
+                        const int p = n[x] % C::PL;
+                        ok = mbar_wait<false>(bar(kPFull + C::PL * x + p),
+                                              (uint32_t)(n[x] / C::PL) & 1, abort_flag);
                         if (ok && j == it.j0 && (left >> x & 1)) {
                             ok = mbar_wait<false>(bar(kORead + x), os >> x & 1, abort_flag);
                             os ^= 1u << x;
@@ -577,9 +580,9 @@ __global__ void __launch_bounds__(kThreads, 1)
                         const uint64_t db = dV + (uint64_t)((st * C::V_STAGE) >> 4);
 #pragma unroll
                         for (int e = 0; e < kKeys / 16; ++e)
-                            umma_ts_pair(tmem + kColO + x * N, tmem + (2 * x + p) * 64 + e * 8,
+                            umma_ts_pair(tmem + C::COL_O + x * N, tmem + (C::PL * x + p) * 64 + e * 8,
                                          db + ((e * 2048) >> 4), ID_PV, j > it.j0 || e > 0);
-                        commit_pair(bar(kPvDone + 2 * x + p));
+                        commit_pair(bar(kPvDone + C::PL * x + p));
                         left |= 1u << x;
                         ++n[x];
                     }
@@ -598,8 +601,8 @@ __global__ void __launch_bounds__(kThreads, 1)
         // ================================================= softmax
         const int x = warp >= 8, quad = warp & 3;
         const uint32_t lanes = (uint32_t)(quad * 32) << 16;
-        const uint32_t tO = tmem + lanes + kColO + x * N;
-        const uint32_t pfull = at_rank(bar(kPFull + 2 * x), 0), oread = at_rank(bar(kORead + x), 0);
+        const uint32_t tO = tmem + lanes + C::COL_O + x * N;
+        const uint32_t pfull = at_rank(bar(kPFull + C::PL * x), 0), oread = at_rank(bar(kORead + x), 0);
         Item it;
         int n = 0;                           // steps of this slot
         const float scale = a.scale_log2;
@@ -615,9 +618,10 @@ __global__ void __launch_bounds__(kThreads, 1)
             float m = -INFINITY;
             uint64_t l2 = 0;                                 // two partial sums
             for (int j = it.j0; j < end; ++j, ++n) {
-                const int place = n & 1;
-                const uint32_t tS = tmem + lanes + (2 * x + place) * 64;
-                ok = ok && warp_wait(bar(kSFull + 2 * x + place), (uint32_t)(n >> 1 & 1), abort_flag);
+                const int place = n % C::PL;
+                const uint32_t tS = tmem + lanes + (C::PL * x + place) * 64;
+                ok = ok && warp_wait(bar(kSFull + C::PL * x + place), (uint32_t)(n / C::PL) & 1,
+                                     abort_flag);
                 fence_after();
                 if (live) {
                     uint32_t z[64];
@@ -679,10 +683,9 @@ __global__ void __launch_bounds__(kThreads, 1)
                     }
                     l2 = fma2(l2, f2(alpha, alpha), add2(sum[0], sum[1]));
                     if (j > it.j0 && __any_sync(0xffffffffu, alpha != 1.f)) {
-                        // P V of the step before has to be in O (that of the one before it is:
-                        // this step's scores took its place)
-                        ok = ok && warp_wait(bar(kPvDone + 2 * x + (place ^ 1)),
-                                             (uint32_t)((n - 1) >> 1 & 1), abort_flag);
+                        // P V of the step before has to be in O
+                        ok = ok && warp_wait(bar(kPvDone + C::PL * x + (n - 1) % C::PL),
+                                             (uint32_t)((n - 1) / C::PL) & 1, abort_flag);
                         fence_after();
                         const uint64_t al2 = f2(alpha, alpha);
 #pragma unroll 1
@@ -715,7 +718,8 @@ __global__ void __launch_bounds__(kThreads, 1)
             const bool mine = at + lane < mine_rows && ok;
             if (mine && !whole) a.ml[slot * a.slot_rows + row] = make_float2(m, l);
             if (end > it.j0) {
-                ok = ok && warp_wait(bar(kPvDone + 2 * x + ((n - 1) & 1)), (uint32_t)((n - 1) >> 1 & 1), abort_flag);
+                ok = ok && warp_wait(bar(kPvDone + C::PL * x + (n - 1) % C::PL),
+                                     (uint32_t)((n - 1) / C::PL) & 1, abort_flag);
                 fence_after();
                 if (live) {
                     const float inv = 1.f / l;
