@@ -17,9 +17,15 @@
 // every row and computes their angles once; the latent row and the key part are
 // one warp's, 16 or 8 latent elements a lane.
 //
+// Measured: 16001 tokens, 32 heads, R 256: 26.2 us (5.79 TB/s, 0.86 of a plain copy);
+// 16384 tokens, 16 heads, R 512: 17.3 us (6.08 TB/s); 64 tokens 2.8 us, one 2.2.
+// Passes loaded at a time: 2 took 28.2 us, 8 26.1 but 19.7 for the narrower batch; more
+// blocks an SM by fewer registers 28.9; one warp a token at eight passes and more 29.9.
+//
 // Gather.  Rows key_start[s] + t of the output are the cached rows of tokens t of
 // sequence s.  A warp moves four rows, every 16-byte piece of them loaded before
-// the first is stored.
+// the first is stored.  Measured: 74000 rows of R 512 26.6 us (6.44 TB/s, 0.95 of a plain
+// copy; eight rows a warp 27.9), 700 rows 2.0 us.
 #include <cuda_bf16.h>
 #include <cuda_fp16.h>
 #include <cuda_runtime.h>

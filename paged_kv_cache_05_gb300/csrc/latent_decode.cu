@@ -18,11 +18,19 @@
 //                  elements of all 128 tokens (half of B's columns)
 // A token's row thus comes to each CTA of the pair in part as a key and in part as a
 // value, 17/9 of its bytes in all: the copies' rate into the SMs (10-11 TB/s of boxes
-// of 8 rows, measured) bounds long contexts at 5.8 TB/s of the cache.
+// of 8 rows, measured) bounds long contexts at 5.8 TB/s of the cache.  A product's
+// instruction of M = 128 takes 66 cycles (measured), 52 of them a step of R = 512.
+//
+// Measured (graph of calls, the joining kernel counted): 8 sequences of 8192-32768, 16
+// heads, R 512: 49.4 us (4.0 TB/s of the cache); 64 of 1-2048, 128 heads, R 512: 38.3 us;
+// 33 trees of 13 behind 77-4095, 20 heads, R 256: 30.7 us; one sequence of 500, 16 heads:
+// 9.9 us.  Boxes of 16 and more rows free a step's keys later (53 us for the long ones),
+// one thread issuing a step's boxes in turn 57, prefetches into L2 changed nothing.
 //
 // Eight warps a CTA:
-//   warp 0      keys: boxes of 8 rows x KC chunks of 64 elements, one lane a box, a ring
-//               of KS slots of KC chunks of the tile's 64 tokens, freed slot by slot as S
+//   warp 0      keys: boxes of 8 rows x KC chunks of 64 elements, one lane a box (lanes'
+//               copies start side by side, a thread's one after the other), a ring of
+//               KS slots of KC chunks of the tile's 64 tokens, freed slot by slot as S
 //               is formed
 //   warp 6      values: boxes of 8 rows x R / 128 chunks, a ring of VS slots of 32 tokens
 //   warp 7      queries
