@@ -16,6 +16,8 @@
 //                  its rows against tokens 0-63, lanes 64-127 against tokens 64-127
 //   O += P V       each CTA holds its rows' weights P (A) and half of the values' R
 //                  elements of all 128 tokens (half of B's columns)
+// R = 256 takes half of that, so that a pair can hold a tile of 256 rows as well, 128 a CTA:
+// a lane a row, its scores in 128 columns, weights over the scores.
 // A token's row thus comes to each CTA of the pair in part as a key and in part as a
 // value, 17/9 of its bytes in all: the copies' rate into the SMs (10-11 TB/s of boxes
 // of 8 rows, measured) bounds long contexts at 5.8 TB/s of the cache.  A product's
@@ -27,7 +29,7 @@
 // 9.9 us.  Boxes of 16 and more rows free a step's keys later (53 us for the long ones),
 // one thread issuing a step's boxes in turn 57, prefetches into L2 changed nothing.
 //
-// Eight warps a CTA:
+// Eight warps a CTA (256 rows: twelve):
 //   warp 0      keys: boxes of 8 rows x KC chunks of 64 elements, one lane a box (lanes'
 //               copies start side by side, a thread's one after the other), a ring of
 //               KS slots of KC chunks of the tile's 64 tokens, freed slot by slot as S
@@ -35,9 +37,9 @@
 //   warp 6      values: boxes of 8 rows x R / 128 chunks, a ring of VS slots of 32 tokens
 //   warp 7      queries
 //   warp 1      (of the first CTA) issues the products
-//   warps 2-5   softmax: a thread a row and half of the tile's tokens; the two halves
-//               of a row meet in shared memory.  The max is raised only past a growth of
-//               kRescale, so that most steps leave O alone.
+//   warps 2-5   softmax (256 rows: 8-11 too): a thread a row and half of the tile's tokens;
+//               the two halves of a row meet in shared memory.  The max is raised only
+//               past a growth of kRescale, so that most steps leave O alone.
 // S is double-buffered: S of step j + 1 is formed while the softmax of step j runs.
 //
 // The steps of all (sequence, row tile)s are dealt to the pairs in equal runs.  A run
@@ -63,13 +65,10 @@ using pkv::rows16::overlap;
 using pkv::rows16::pack2;
 
 constexpr int kP = 64;
-constexpr int kRows = 128;            // rows of a pair's tile
 constexpr int kTok = 128;             // tokens of a step
-constexpr int kThreads = 256;
 constexpr int kMaxPairs = 96;
-constexpr uint32_t kColO = 128;       // tensor memory: S at 0 and 64, O from here
 
-template <int R>
+template <int R, int TILE>
 struct Cfg {
     static constexpr int W = R + kP;
     static constexpr int CH = W / 64;                 // chunks of a row
@@ -77,17 +76,27 @@ struct Cfg {
     static constexpr int KC = R == 512 ? 3 : 5;       // chunks of a key slot
     static constexpr int KSUB = CH / KC;              // slots of a step
     static constexpr int KS = R == 512 ? 3 : 2;
-    static constexpr int VS = R == 512 ? 4 : 8;
+    static constexpr int VS = R == 512 ? 4 : TILE == 128 ? 8 : 7;
+    static constexpr bool WIDE = TILE == 256;         // P over S in tensor memory
+    static constexpr int RC = TILE / 2;               // rows of a CTA
+    static constexpr int SOFTMAX = RC / 16;           // its softmax warps
+    static constexpr int WARPS = 4 + SOFTMAX;
+    static constexpr int THREADS = 32 * WARPS;
+    // tensor memory: two of S, then O
+    static constexpr uint32_t COL_S = RC;             // columns of one
+    static constexpr uint32_t COL_O = 2 * COL_S;
     static constexpr int K_SLOT = KC * 8192;
     static constexpr int V_GROUP = VCH * 1024;        // 8 tokens
     static constexpr int V_SLOT = 4 * V_GROUP;
-    static constexpr int Q_BYTES = CH * 8192;
+    static constexpr int Q_BYTES = CH * RC * 128;
     static constexpr int Q_OFF = 0;
     static constexpr int K_OFF = Q_OFF + Q_BYTES;
     static constexpr int V_OFF = K_OFF + KS * K_SLOT;
     static constexpr int P_OFF = V_OFF + VS * V_SLOT;
-    static constexpr int SMEM = P_OFF + 16384 + 1024; // 1 KiB of alignment slack
-    static_assert(SMEM + 2048 <= 232448, "shared memory");
+    static constexpr int P_BYTES = WIDE ? 0 : 16384;
+    static constexpr int SMEM = P_OFF + P_BYTES + 1024;   // 1 KiB of alignment slack
+    static_assert(SMEM + (WIDE ? 3072 : 2048) <= 232448, "shared memory");
+    static_assert(COL_O + R * TILE / 256 <= 512, "tensor memory");
     static_assert(KSUB * KC == CH, "chunks");
 };
 
@@ -115,6 +124,7 @@ struct Args {
     int S, H, B, max_blocks, max_qlen, T;
     int64_t num_blocks;
     int pairs, slot_rows;             // rows of a part in the workspace
+    int log_rows;                     // of a tile
     int out_v8;                       // out is 32-byte aligned: 32-byte stores
     struct Rec* rec;                  // [pairs]
     float2* ml;                       // [2 pairs][slot_rows]
@@ -146,7 +156,7 @@ struct Seq {
             return false;
         if (qlen > 0 && ctx > 0) {
             nt = (ctx + kTok - 1) / kTok;
-            nr = (int)(((int64_t)qlen * a.H + kRows - 1) / kRows);
+            nr = (int)(((int64_t)qlen * a.H + (1 << a.log_rows) - 1) >> a.log_rows);
         }
         return true;
     }
@@ -202,8 +212,8 @@ struct Walker {
         g.q0 = q.q0;
         g.qlen = q.qlen;
         g.ctx = q.ctx;
-        g.row = rt * kRows;
-        g.rows = min(kRows, q.qlen * a.H - g.row);
+        g.row = rt << a.log_rows;
+        g.rows = min(1 << a.log_rows, q.qlen * a.H - g.row);
         g.j0 = (int)(off - (int64_t)rt * q.nt);
         g.j1 = (int)min((int64_t)q.nt, g.j0 + left);
         g.whole = g.j0 == 0 && g.j1 == q.nt;
@@ -224,19 +234,19 @@ __device__ __forceinline__ int cache_row(const Args& a, const Seg& g, int t) {
     return id * a.B + (t - b * a.B);
 }
 
-template <typename T, int R>
-__global__ void __launch_bounds__(kThreads, 1)
+template <typename T, int R, int TILE>
+__global__ void __launch_bounds__(Cfg<R, TILE>::THREADS, 1)
     latent_decode_pair(const __grid_constant__ CUtensorMap tm_q,
                        const __grid_constant__ CUtensorMap tm_k,
                        const __grid_constant__ CUtensorMap tm_v, const Args a) {
-    using C = Cfg<R>;
+    using C = Cfg<R, TILE>;
     extern __shared__ __align__(1024) uint8_t smem_raw[];
     __shared__ __align__(8) uint64_t bars[kBars];
     __shared__ uint32_t s_tmem;
     __shared__ int s_abort;
     __shared__ Start s_start;
-    __shared__ int64_t s_scan[2][8];
-    __shared__ float s_x[2][2][64];              // a row's maxima (or sums) by halves
+    __shared__ int64_t s_scan[2][C::WARPS];
+    __shared__ float s_x[2][2][C::RC];              // a row's maxima (or sums) by halves
 
     const int tid = threadIdx.x, warp = tid >> 5, lane = tid & 31;
     const uint32_t rank = cluster_rank();
@@ -258,7 +268,7 @@ __global__ void __launch_bounds__(kThreads, 1)
     if (warp == 1) {
         for (int i = lane; i < kBars; i += 32) {
             const bool two = i < kKEmpty || (i >= kVFull && i < kVEmpty) || i == kQFull;
-            mbar_init(bar(i), two ? 2 : i == kPFull || i == kORead ? 8 : 1);
+            mbar_init(bar(i), two ? 2 : i == kPFull || i == kORead ? 2 * C::SOFTMAX : 1);
         }
         mbar_init_fence();
         if (lane == 0) s_abort = 0;
@@ -272,7 +282,7 @@ __global__ void __launch_bounds__(kThreads, 1)
     {
         // this thread's steps, and those of the threads before it in the warp
         int64_t n = mine.steps(), incl = n, rest = 0;
-        for (int s = tid + kThreads; s < a.S; s += kThreads) {
+        for (int s = tid + C::THREADS; s < a.S; s += C::THREADS) {
             Seq q;
             good &= q.load(a, s);
             rest += q.steps();
@@ -283,7 +293,7 @@ __global__ void __launch_bounds__(kThreads, 1)
             const int64_t y = __shfl_up_sync(0xffffffffu, incl, o);
             if (lane >= o) incl += y;
         }
-        if (a.S > kThreads) {
+        if (a.S > C::THREADS) {
 #pragma unroll
             for (int o = 16; o > 0; o >>= 1) rest += __shfl_xor_sync(0xffffffffu, rest, o);
         }
@@ -296,7 +306,7 @@ __global__ void __launch_bounds__(kThreads, 1)
         __syncthreads();
         asm volatile("barrier.cluster.arrive.relaxed.aligned;" ::: "memory");   // (see mbar_init_fence)
         int64_t total = 0, before = 0;
-        for (int w = 0; w < 8; ++w) {
+        for (int w = 0; w < C::WARPS; ++w) {
             if (w < warp) incl += s_scan[0][w];
             before += s_scan[0][w];
             total += s_scan[0][w] + s_scan[1][w];
@@ -308,7 +318,7 @@ __global__ void __launch_bounds__(kThreads, 1)
             if (e > b && incl > b && incl - n <= b) s_start = Start{s, mine, b - (incl - n), e - b, total};
         };
         found(tid);
-        for (int s0 = kThreads; s0 < a.S && before <= b && e > b; s0 += kThreads) {
+        for (int s0 = C::THREADS; s0 < a.S && before <= b && e > b; s0 += C::THREADS) {
             mine.nt = mine.nr = 0;
             if (s0 + tid < a.S) mine.load(a, s0 + tid);
             n = incl = mine.steps();
@@ -321,7 +331,7 @@ __global__ void __launch_bounds__(kThreads, 1)
             if (lane == 31) s_scan[0][warp] = incl;
             __syncthreads();
             incl += before;
-            for (int w = 0; w < 8; ++w) {
+            for (int w = 0; w < C::WARPS; ++w) {
                 if (w < warp) incl += s_scan[0][w];
                 before += s_scan[0][w];
             }
@@ -385,12 +395,12 @@ __global__ void __launch_bounds__(kThreads, 1)
                 fail();
                 break;
             }
-            const bool live = g.rows > 64 * (int)rank;
+            const bool live = g.rows > C::RC * (int)rank;
             if (lane == 0) mbar_expect_tx_relaxed(qfull, live ? C::Q_BYTES : 0);
             __syncwarp();
-            if (live && lane < 8)
+            if (live && lane < C::RC / 8)
                 tma_3d_pair(sQ + lane * C::CH * 1024, &tm_q, 0,
-                            g.q0 * a.H + g.row + 64 * (int)rank + 8 * lane, 0, qfull);
+                            g.q0 * a.H + g.row + C::RC * (int)rank + 8 * lane, 0, qfull);
         }
     } else if (warp == 6) {
         // ================================================= values
@@ -461,8 +471,8 @@ __global__ void __launch_bounds__(kThreads, 1)
     } else if (warp == 1) {
         // ================================================= products
         if (rank == 0 && elect_one()) {
-            constexpr uint32_t ID_S = idesc(El<T>::kType, false, kTok, kRows);
-            constexpr uint32_t ID_PV = idesc(El<T>::kType, true, 256, kRows);
+            constexpr uint32_t ID_S = idesc(El<T>::kType, false, kTok, TILE);
+            constexpr uint32_t ID_PV = idesc(El<T>::kType, true, 256, TILE);
             const uint64_t dQ = sdesc(sQ, 16, C::CH * 1024), dK = sdesc(sK, 16, C::KC * 1024),
                            dV = sdesc(sV, 1024, C::V_GROUP), dP = sdesc(sP, 16, 1024);
             Walker wk;
@@ -495,10 +505,16 @@ __global__ void __launch_bounds__(kThreads, 1)
 #pragma unroll
                         for (int k = 0; k < 2; ++k) {
 #pragma unroll
-                            for (int n = 0; n < R / 256; ++n)
-                                umma_pair(tmem + kColO + n * 128, da + 2 * k,
-                                          db + ((k * 2 * C::V_GROUP + n * 2048) >> 4), ID_PV,
-                                          j > cur.j0 || v > 0 || k > 0);
+                            for (int n = 0; n < R / 256; ++n) {
+                                const uint64_t b = db + ((k * 2 * C::V_GROUP + n * 2048) >> 4);
+                                const bool add = j > cur.j0 || v > 0 || k > 0;
+                                if (!C::WIDE)
+                                    umma_pair(tmem + C::COL_O + n * 128, da + 2 * k, b, ID_PV, add);
+                                else
+                                    umma_ts_pair(tmem + C::COL_O,
+                                                 tmem + (pc & 1) * C::COL_S + (2 * v + k) * 8, b,
+                                                 ID_PV, add);
+                            }
                         }
                         commit_pair(bar(kVEmpty + vc % C::VS));
                         ++vc;
@@ -512,6 +528,12 @@ __global__ void __launch_bounds__(kThreads, 1)
                     break;
                 }
                 for (int j = cur.j0; ok && j < cur.j1; ++j) {
+                    // the weights that these scores overwrite have been read
+                    if (C::WIDE && pc > 0 &&
+                        !mbar_wait<false>(bar(kPvDone), (uint32_t)((pc - 1) & 1), abort_flag)) {
+                        ok = false;
+                        break;
+                    }
 #pragma unroll
                     for (int u = 0; u < C::KSUB; ++u, ++kc) {
                         if (!mbar_wait<false>(k_full(kc), k_par(kc), abort_flag)) {
@@ -524,7 +546,7 @@ __global__ void __launch_bounds__(kThreads, 1)
 #pragma unroll
                         for (int i = 0; i < C::KC * 4; ++i) {
                             const int c = i >> 2, k = i & 3;
-                            umma_pair(tmem + (sc & 1) * 64, da + ((c * 1024 + k * 32) >> 4),
+                            umma_pair(tmem + (sc & 1) * C::COL_S, da + ((c * 1024 + k * 32) >> 4),
                                       db + ((c * 1024 + k * 32) >> 4), ID_S, u > 0 || i > 0);
                         }
                         commit_pair(bar(kKEmpty + kc % C::KS));
@@ -547,14 +569,18 @@ __global__ void __launch_bounds__(kThreads, 1)
             }
         }
         __syncwarp();
-    } else if (warp >= 2 && warp < 6) {
+    } else {
         // ================================================= softmax
-        const int quad = warp & 3, half = quad >> 1;
-        const int rl = (quad & 1) * 32 + lane;               // row of this CTA's 64
+        // its block of 32 rows, its half of the tile's tokens: those of lanes 64-127 of a
+        // product of 128 rows, of the columns' second half of one of 256
+        const int quad = warp & 3, half = C::WIDE ? warp >> 3 : quad >> 1;
+        const int block = C::WIDE ? quad : quad & 1;
+        const int rl = block * 32 + lane;                    // row of this CTA's
+        const uint32_t scol = C::WIDE ? half * 64 : 0, ocol = C::WIDE ? half * (R / 2) : 0;
         const uint32_t lanes = (uint32_t)(quad * 32) << 16;
         const uint32_t pfull = at_rank(bar(kPFull), 0), oread = at_rank(bar(kORead), 0);
         // sequences without a token: rows of zero
-        for (int s = pair * 2 + (int)rank; s < a.S; s += 2 * a.pairs) {
+        for (int s = pair * 2 + (int)rank; warp < 6 && s < a.S; s += 2 * a.pairs) {
             Seq q;
             if (!q.load(a, s) || q.ctx != 0 || q.qlen == 0) continue;
             uint4* o = reinterpret_cast<uint4*>(a.out + (int64_t)q.q0 * a.H * R);
@@ -567,8 +593,8 @@ __global__ void __launch_bounds__(kThreads, 1)
         int sc = 0, par = 0;
         const uint64_t scale2 = f2(a.scale_log2, a.scale_log2);
         while (wk.get(a, g)) {
-            const int row = 64 * (int)rank + rl;             // of the tile
-            const bool live = 64 * (int)rank + (quad & 1) * 32 < g.rows;   // the warp's
+            const int row = C::RC * (int)rank + rl;          // of the tile
+            const bool live = C::RC * (int)rank + block * 32 < g.rows;   // the warp's
             const int i = (g.row + min(row, g.rows - 1)) / a.H;            // its token
             const int first = g.ctx - g.qlen;                // tokens that every row sees
             // the new tokens that the row sees, by bits (a chain's row i: the first i + 1)
@@ -596,7 +622,7 @@ __global__ void __launch_bounds__(kThreads, 1)
                 float alpha = 1.f;
                 if (live) {
                     uint32_t z[64];
-                    ld64(tmem + lanes + (uint32_t)((sc & 1) * 64), z);
+                    ld64(tmem + lanes + (uint32_t)(sc & 1) * C::COL_S + scol, z);
                     ld_wait(z);
 #pragma unroll
                     for (int e = 0; e < 32; ++e) {
@@ -630,7 +656,7 @@ __global__ void __launch_bounds__(kThreads, 1)
                         top = max3(top, __uint_as_float(z[e]), __uint_as_float(z[e + 1]));
                     top = fmaxf(top, __uint_as_float(z[63]));
                     s_x[par][half][rl] = top;
-                    named_sync(1 + (quad & 1), 64);
+                    named_sync(1 + block, 64);
                     top = fmaxf(top, s_x[par][1 - half][rl]);
                     par ^= 1;
                     if (top > m + El<T>::kRescale || m == -INFINITY) {
@@ -666,7 +692,7 @@ __global__ void __launch_bounds__(kThreads, 1)
 #pragma unroll 1
                         for (int c = 0; c < R / 2; c += 32) {
                             uint32_t o[32];
-                            ld32(tmem + lanes + kColO + c, o);
+                            ld32(tmem + lanes + C::COL_O + ocol + c, o);
                             ld_wait(o);
 #pragma unroll
                             for (int e = 0; e < 16; ++e) {
@@ -678,17 +704,24 @@ __global__ void __launch_bounds__(kThreads, 1)
                                 o[2 * e] = __float_as_uint(x);
                                 o[2 * e + 1] = __float_as_uint(y);
                             }
-                            st32(tmem + lanes + kColO + c, o);
+                            st32(tmem + lanes + C::COL_O + ocol + c, o);
                         }
+                        if (!C::WIDE) st_wait();
+                    }
+                    if (!C::WIDE) {
+                        // row rl of the half's 64 tokens: 128 bytes, 16-byte piece c at
+                        // c ^ (rl % 8)
+                        const uint32_t p = sP + half * 8192 + rl * 128;
+#pragma unroll
+                        for (int c = 0; c < 8; ++c)
+                            st_shared_v4(p + ((c ^ (rl & 7)) << 4), w[4 * c], w[4 * c + 1],
+                                         w[4 * c + 2], w[4 * c + 3]);
+                        fence_async_smem();
+                    } else {
+                        // over the step's scores, which both halves' warps have read
+                        st32(tmem + lanes + (uint32_t)(sc & 1) * C::COL_S + half * 32, w);
                         st_wait();
                     }
-                    // row rl of the half's 64 tokens: 128 bytes, 16-byte piece c at c ^ (rl % 8)
-                    const uint32_t p = sP + half * 8192 + rl * 128;
-#pragma unroll
-                    for (int c = 0; c < 8; ++c)
-                        st_shared_v4(p + ((c ^ (rl & 7)) << 4), w[4 * c], w[4 * c + 1], w[4 * c + 2],
-                                     w[4 * c + 3]);
-                    fence_async_smem();
                 }
                 fence_before();
                 __syncwarp();
@@ -702,7 +735,7 @@ __global__ void __launch_bounds__(kThreads, 1)
                 f2_split(l2, x, y);
                 float l = x + y;
                 s_x[par][half][rl] = l;
-                named_sync(1 + (quad & 1), 64);
+                named_sync(1 + block, 64);
                 l += s_x[par][1 - half][rl];
                 par ^= 1;
                 const bool mine = row < g.rows && ok;
@@ -715,7 +748,7 @@ __global__ void __launch_bounds__(kThreads, 1)
 #pragma unroll 1
                 for (int c = 0; c < R / 2; c += 64) {
                     uint32_t o[64];
-                    ld64(tmem + lanes + kColO + c, o);
+                    ld64(tmem + lanes + C::COL_O + ocol + c, o);
                     ld_wait(o);
                     if (!mine) continue;
                     if (g.whole) {
@@ -843,10 +876,10 @@ struct Layout {
     size_t ml, acc, total;
     int rows;
 };
-Layout layout(int H, int R, int max_qlen) {
+Layout layout(int H, int R, int max_qlen, int tile) {
     Layout l;
     const int64_t rows = (int64_t)H * (max_qlen > 0 ? max_qlen : 1);
-    l.rows = (int)(rows < kRows ? rows : kRows);
+    l.rows = (int)(rows < tile ? rows : tile);
     l.ml = pkv::align_up(sizeof(Rec) * kMaxPairs, 256);
     l.acc = pkv::align_up(l.ml + 8 * (size_t)(2 * kMaxPairs) * l.rows, 256);
     l.total = l.acc + 4 * (size_t)(2 * kMaxPairs) * l.rows * R;
@@ -867,16 +900,17 @@ bool chunk_map(CUtensorMap* m, bool bf16, const void* at, int64_t rows, int row,
               CU_TENSOR_MAP_FLOAT_OOB_FILL_NONE) == CUDA_SUCCESS;
 }
 
-template <typename T, int R>
+template <typename T, int R, int TILE>
 cudaError_t launch(const CUtensorMap& tq, const CUtensorMap& tk, const CUtensorMap& tv,
                    const Args& a, cudaStream_t stream) {
-    cudaError_t e = cudaFuncSetAttribute(latent_decode_pair<T, R>,
-                                         cudaFuncAttributeMaxDynamicSharedMemorySize, Cfg<R>::SMEM);
+    cudaError_t e = cudaFuncSetAttribute(latent_decode_pair<T, R, TILE>,
+                                         cudaFuncAttributeMaxDynamicSharedMemorySize,
+                                         Cfg<R, TILE>::SMEM);
     if (e != cudaSuccess) return e;
     cudaLaunchConfig_t cfg = {};
     cfg.gridDim = dim3((unsigned)(2 * a.pairs));
-    cfg.blockDim = dim3(kThreads);
-    cfg.dynamicSmemBytes = Cfg<R>::SMEM;
+    cfg.blockDim = dim3(Cfg<R, TILE>::THREADS);
+    cfg.dynamicSmemBytes = Cfg<R, TILE>::SMEM;
     cfg.stream = stream;
     cudaLaunchAttribute attr[2];
     attr[0].id = cudaLaunchAttributeClusterDimension;
@@ -887,7 +921,7 @@ cudaError_t launch(const CUtensorMap& tq, const CUtensorMap& tk, const CUtensorM
     attr[1].val.programmaticStreamSerializationAllowed = 1;
     cfg.attrs = attr;
     cfg.numAttrs = 2;
-    e = cudaLaunchKernelEx(&cfg, latent_decode_pair<T, R>, tq, tk, tv, a);
+    e = cudaLaunchKernelEx(&cfg, latent_decode_pair<T, R, TILE>, tq, tk, tv, a);
     if (e != cudaSuccess) return e;
     // (the same split of the SMs' memory as the kernel before: no change of it between)
     e = cudaFuncSetAttribute(latent_decode_join<T, R>,
@@ -914,7 +948,7 @@ pkv_status pkv_latent_decode_workspace_size(int num_seqs, int num_heads, int lat
     if (num_seqs < 0 || num_heads < 1 || (latent_dim != 256 && latent_dim != 512) ||
         max_query_len < 0)
         return pkv::fail(PKV_ERR_INVALID, "%s: bad sizes", fn);
-    *bytes = layout(num_heads, latent_dim, max_query_len).total;
+    *bytes = layout(num_heads, latent_dim, max_query_len, latent_dim == 256 ? 256 : 128).total;
     return PKV_OK;
 }
 
@@ -966,7 +1000,14 @@ pkv_status pkv_latent_attention_decode(
                          "%s: misaligned block_tables, context_lens, query_start or ancestors", fn);
     if (!aligned(workspace, 256))
         return pkv::fail(PKV_ERR_INVALID, "%s: workspace must be 256-byte aligned", fn);
-    const Layout l = layout(num_heads, latent_dim, max_query_len);
+    // R = 256 leaves tensor memory for tiles of 256 rows: half the copies and steps where the
+    // sequences' rows fill them, each step about a fifth longer.  16 sequences of 1000-4000,
+    // 128 heads x 4 tokens: 42.3 us by 128 rows, 34.4 by 256; 32 of 20 heads x 12 42.4 and 34.8;
+    // 32 of 128 heads x 1 27.2 and 32.0; 33 trees of 140 rows on average 31.1 and 31.8.
+    const bool wide = latent_dim == 256 &&
+                      (int64_t)num_query_tokens * num_heads > (int64_t)192 * num_seqs;
+    const int tile = wide ? 256 : 128;
+    const Layout l = layout(num_heads, latent_dim, max_query_len, tile);
     if (workspace_bytes < l.total)
         return pkv::fail(PKV_ERR_INVALID, "%s: workspace too small (%zu < %zu bytes)", fn,
                          workspace_bytes, l.total);
@@ -989,7 +1030,7 @@ pkv_status pkv_latent_attention_decode(
     const int64_t places = num_blocks * block_size;
     if (!chunk_map(&tq, bf16, q, rows, W, W / 64))
         return pkv::fail(PKV_ERR_CUDA, "%s: tensor map of q", fn);
-    if (!chunk_map(&tk, bf16, cache, places, W, latent_dim == 512 ? Cfg<512>::KC : Cfg<256>::KC) ||
+    if (!chunk_map(&tk, bf16, cache, places, W, latent_dim == 512 ? Cfg<512, 128>::KC : Cfg<256, 128>::KC) ||
         !chunk_map(&tv, bf16, cache, places, W, latent_dim / 128))
         return pkv::fail(PKV_ERR_CUDA, "%s: tensor map of the cache", fn);
 
@@ -1009,11 +1050,13 @@ pkv_status pkv_latent_attention_decode(
     a.T = num_query_tokens;
     a.num_blocks = num_blocks;
     a.slot_rows = l.rows;
+    a.log_rows = wide ? 8 : 7;
     a.out_v8 = aligned(out, 32) ? 1 : 0;
     // pairs: no more than there can be steps
     int64_t pairs = sms / 2 < kMaxPairs ? sms / 2 : kMaxPairs;
     const int64_t per_seq = (((int64_t)max_blocks_per_seq * block_size + kTok - 1) / kTok) *
-                            (((int64_t)max_query_len * num_heads + kRows - 1) / kRows);
+                            (((int64_t)max_query_len * num_heads + (1 << a.log_rows) - 1) >>
+                             a.log_rows);
     if (per_seq < pairs && per_seq * num_seqs < pairs) pairs = per_seq * num_seqs;
     a.pairs = (int)pairs;
     char* ws = static_cast<char*>(workspace);
@@ -1022,11 +1065,13 @@ pkv_status pkv_latent_attention_decode(
     a.acc = reinterpret_cast<float*>(ws + l.acc);
     a.err = err;
     if (bf16)
-        e = latent_dim == 512 ? launch<__nv_bfloat16, 512>(tq, tk, tv, a, stream)
-                              : launch<__nv_bfloat16, 256>(tq, tk, tv, a, stream);
+        e = latent_dim == 512 ? launch<__nv_bfloat16, 512, 128>(tq, tk, tv, a, stream)
+            : wide            ? launch<__nv_bfloat16, 256, 256>(tq, tk, tv, a, stream)
+                              : launch<__nv_bfloat16, 256, 128>(tq, tk, tv, a, stream);
     else
-        e = latent_dim == 512 ? launch<__half, 512>(tq, tk, tv, a, stream)
-                              : launch<__half, 256>(tq, tk, tv, a, stream);
+        e = latent_dim == 512 ? launch<__half, 512, 128>(tq, tk, tv, a, stream)
+            : wide            ? launch<__half, 256, 256>(tq, tk, tv, a, stream)
+                              : launch<__half, 256, 128>(tq, tk, tv, a, stream);
     if (e != cudaSuccess) return pkv::cuda_fail(e, fn);
     return PKV_OK;
 }
