@@ -383,6 +383,8 @@ __global__ void __launch_bounds__(Cfg<R, TILE>::THREADS, 1)
                 y = yn;
             }
         }
+        // (the products' last releases arrive before the CTA ends: see cluster_meet)
+        ok = ok && ring_ended(bar(kKEmpty), C::KS, kc, abort_flag);
         if (!ok) fail();
     } else if (warp == 7) {
         // ================================================= queries
@@ -390,9 +392,10 @@ __global__ void __launch_bounds__(Cfg<R, TILE>::THREADS, 1)
         wk.init(a, start);
         Seg g;
         const uint32_t qfull = at_rank(bar(kQFull), 0);
-        for (int segs = 0; wk.get(a, g); ++segs) {
+        int segs = 0;
+        for (; wk.get(a, g); ++segs) {
             if (segs > 0 && !warp_wait(bar(kQEmpty), (uint32_t)((segs - 1) & 1), abort_flag)) {
-                fail();
+                ok = false;
                 break;
             }
             const bool live = g.rows > C::RC * (int)rank;
@@ -402,6 +405,8 @@ __global__ void __launch_bounds__(Cfg<R, TILE>::THREADS, 1)
                 tma_3d_pair(sQ + lane * C::CH * 1024, &tm_q, 0,
                             g.q0 * a.H + g.row + C::RC * (int)rank + 8 * lane, 0, qfull);
         }
+        ok = ok && ring_ended(bar(kQEmpty), 1, segs, abort_flag);
+        if (!ok) fail();
     } else if (warp == 6) {
         // ================================================= values
         Walker wk;
@@ -467,6 +472,7 @@ __global__ void __launch_bounds__(Cfg<R, TILE>::THREADS, 1)
                 y = yn;
             }
         }
+        ok = ok && ring_ended(bar(kVEmpty), C::VS, vc, abort_flag);
         if (!ok) fail();
     } else if (warp == 1) {
         // ================================================= products
@@ -560,6 +566,9 @@ __global__ void __launch_bounds__(Cfg<R, TILE>::THREADS, 1)
                 if (ok && !pv(cur.j1 - 1)) ok = false;
                 ++segs;
             }
+            // the last output's readers, of both CTAs, have arrived before this one ends
+            if (ok && segs > 0)
+                ok = mbar_wait<false>(bar(kORead), (uint32_t)((segs - 1) & 1), abort_flag);
             if (!ok) {
                 fail();
                 // what was issued completes before the tensor memory goes

@@ -421,6 +421,8 @@ __global__ void __launch_bounds__(kThreads, 1)
                 else if (c == C::CH - 1) tma_3d_pair(to, &tm_r, 0, 0, key, full);
             }
         }
+        // (the products' last releases arrive before the CTA ends: see cluster_meet)
+        ok = ok && ring_ended(bar(kKEmpty), C::KS, kc, abort_flag);
         if (!ok) fail();
     } else if (warp == 2) {
         // ================================================= values
@@ -472,6 +474,7 @@ __global__ void __launch_bounds__(kThreads, 1)
                                 full);
             }
         }
+        ok = ok && ring_ended(bar(kVEmpty), C::VS, vc, abort_flag);
         if (!ok) fail();
     } else if (warp == 3) {
         // ================================================= items and queries
@@ -509,6 +512,7 @@ __global__ void __launch_bounds__(kThreads, 1)
                                 it.q0 + (x ? it.row1 : 0) + 128 * (int)rank + r, full);
             }
         }
+        for (int x = 0; x < 2; ++x) ok = ok && ring_ended(bar(kQEmpty + x), 1, count[x], abort_flag);
         if (!ok) fail();
     } else if (warp == 1) {
         // ================================================= scores
@@ -595,6 +599,10 @@ __global__ void __launch_bounds__(kThreads, 1)
                     commit_pair(bar(kVEmpty + st));
                 }
             }
+            // the last outputs' readers, of both CTAs, have arrived before this one ends
+            for (int x = 0; x < 2; ++x)
+                if (ok && (left >> x & 1))
+                    ok = mbar_wait<false>(bar(kORead + x), os >> x & 1, abort_flag);
             if (!ok) {
                 fail();
                 volatile int never = 0;
@@ -779,6 +787,7 @@ __global__ void __launch_bounds__(kThreads, 1)
                                   (int)(last - pair) + 1, {0, 0, 0}};
             }
         }
+        ok = ok && ring_ended(bar(kPvDone + C::PL * x), C::PL, n, abort_flag);
         if (!ok && lane == 0) fail();
     }
 

@@ -119,8 +119,17 @@ __device__ __forceinline__ uint32_t cluster_rank() {
     asm volatile("mov.u32 %0, %%cluster_ctarank;" : "=r"(r));
     return r;
 }
+// The last phase of each of a ring's `slots` barriers (from bar0 on, used `used` times in
+// all, in turn) has completed.
+__device__ __forceinline__ bool ring_ended(uint32_t bar0, int slots, int used, volatile int* abort) {
+    for (int i = used > slots ? used - slots : 0; i < used; ++i)
+        if (!warp_wait(bar0 + 8 * (i % slots), (uint32_t)((i / slots) & 1), abort)) return false;
+    return true;
+}
 // Both CTAs have come here.  Nothing that they wrote is ordered by it: a release would
-// wait for all of their stores, about 1000 cycles.
+// wait for all of their stores, about 1000 cycles.  So an arrival on the other CTA's barrier
+// (by a thread or, later, by a commit) may still be on its way, and must not find that CTA
+// gone: each phase that arrivals from outside complete has been waited for in its CTA before.
 __device__ __forceinline__ void cluster_meet() {
     asm volatile(
         "barrier.cluster.arrive.relaxed.aligned;\n\t"
