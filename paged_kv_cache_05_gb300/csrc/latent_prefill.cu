@@ -387,7 +387,8 @@ __global__ void __launch_bounds__(kThreads, 1)
         ok = ok && warp_wait(bar(kItFull + e), (uint32_t)((items / kRing) & 1), abort_flag);
         it = s_items[e];
         __syncwarp();
-        if (lane == 0) mbar_arrive(bar(kItEmpty + e));
+        // (one that gave up hands nothing back: others may not have read the entry)
+        if (ok && lane == 0) mbar_arrive(bar(kItEmpty + e));
         ++items;
         return ok && it.rows > 0;
     };
@@ -395,7 +396,7 @@ __global__ void __launch_bounds__(kThreads, 1)
         const int e = items % kRing;
         ok = ok && mbar_wait<false>(bar(kItFull + e), (uint32_t)((items / kRing) & 1), abort_flag);
         it = s_items[e];
-        mbar_arrive(bar(kItEmpty + e));
+        if (ok) mbar_arrive(bar(kItEmpty + e));
         ++items;
         return ok && it.rows > 0;
     };
@@ -551,6 +552,8 @@ __global__ void __launch_bounds__(kThreads, 1)
                         if (j == it.end(x) - 1) commit_pair(bar(kQEmpty + x));
                         ++n[x];
                     }
+                    // (a stage whose copy may be on its way is never handed back)
+                    if (!ok) break;
                     commit_pair(bar(kKEmpty + st));
                 }
             }
@@ -596,6 +599,7 @@ __global__ void __launch_bounds__(kThreads, 1)
                         left |= 1u << x;
                         ++n[x];
                     }
+                    if (!ok) break;
                     commit_pair(bar(kVEmpty + st));
                 }
             }
