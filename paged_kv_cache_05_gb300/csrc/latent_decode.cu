@@ -111,8 +111,7 @@ enum : int {
     kQFull = 26,
     kQEmpty = 27,    // a segment's last S formed
     kORead = 28,     // a segment's output read from tensor memory (first CTA's)
-    kSpare = 29,
-    kBars = 30
+    kBars = 29
 };
 
 struct Args {
@@ -234,6 +233,36 @@ __device__ __forceinline__ int cache_row(const Args& a, const Seg& g, int t) {
     return id * a.B + (t - b * a.B);
 }
 
+// Either CTA gave up: what is in flight ends before they do, products (by their commits, of
+// which the first CTA keeps count) and copies (counted by roles that gave up; one that did
+// not has seen the last of its ring used).  bar0: the barriers, used0: the phases used of each
+// ring, at its first barrier's place.  (Not inlined, and no count kept otherwise: those cost
+// calls that never come here up to 3 %.)
+template <class C>
+__device__ __noinline__ void end_given_up(uint32_t bar0, uint32_t used0) {
+    cluster_sync();
+    if (threadIdx.x < 32) {
+        const uint32_t rank = cluster_rank();
+        volatile int never = 0;
+        auto used = [&](int b, uint32_t r) { return ld_cluster(at_rank(used0 + 4 * b, r)); };
+        auto products = [&](int b, int slots) { ring_ended(bar0 + 8 * b, slots, used(b, 0), &never); };
+        auto copies = [&](int b, int slots) {
+            if (rank == 0) copies_ended(bar0 + 8 * b, slots, used(b, 0), used(b, 1));
+        };
+        products(kKEmpty, C::KS);
+        products(kVEmpty, C::VS);
+        products(kSFull, 2);
+        products(kPvDone, 1);
+        products(kQEmpty, 1);
+        copies(kKFull, C::KS);
+        copies(kVFull, C::VS);
+        copies(kQFull, 1);
+    }
+    fence_before();
+    __syncthreads();
+    cluster_sync();
+}
+
 template <typename T, int R, int TILE>
 __global__ void __launch_bounds__(Cfg<R, TILE>::THREADS, 1)
     latent_decode_pair(const __grid_constant__ CUtensorMap tm_q,
@@ -244,6 +273,7 @@ __global__ void __launch_bounds__(Cfg<R, TILE>::THREADS, 1)
     __shared__ __align__(8) uint64_t bars[kBars];
     __shared__ uint32_t s_tmem;
     __shared__ int s_abort;
+    __shared__ int s_used[kBars];                   // phases of a ring, at its first barrier's place
     __shared__ Start s_start;
     __shared__ int64_t s_scan[2][C::WARPS];
     __shared__ float s_x[2][2][C::RC];              // a row's maxima (or sums) by halves
@@ -271,6 +301,7 @@ __global__ void __launch_bounds__(Cfg<R, TILE>::THREADS, 1)
             mbar_init(bar(i), two ? 2 : i == kPFull || i == kORead ? 2 * C::SOFTMAX : 1);
         }
         mbar_init_fence();
+        for (int i = lane; i < kBars; i += 32) s_used[i] = kNotCounted;
         if (lane == 0) s_abort = 0;
         __syncwarp();
         alloc_pair(smem_u32(&s_tmem));
@@ -349,6 +380,7 @@ __global__ void __launch_bounds__(Cfg<R, TILE>::THREADS, 1)
     auto fail = [&]() {
         if (!*abort_flag) atomicOr(a.err, PKV_DEVERR_TIMEOUT);
         *abort_flag = 1;
+        set_cluster(at_rank(smem_u32(&s_abort), cluster_rank() ^ 1), 1);
     };
 
     if (warp == 0) {
@@ -385,7 +417,10 @@ __global__ void __launch_bounds__(Cfg<R, TILE>::THREADS, 1)
         }
         // (the products' last releases arrive before the CTA ends: see cluster_meet)
         ok = ok && ring_ended(bar(kKEmpty), C::KS, kc, abort_flag);
-        if (!ok) fail();
+        if (!ok) {
+            if (lane == 0) s_used[kKFull] = kc;
+            fail();
+        }
     } else if (warp == 7) {
         // ================================================= queries
         Walker wk;
@@ -406,7 +441,10 @@ __global__ void __launch_bounds__(Cfg<R, TILE>::THREADS, 1)
                             g.q0 * a.H + g.row + C::RC * (int)rank + 8 * lane, 0, qfull);
         }
         ok = ok && ring_ended(bar(kQEmpty), 1, segs, abort_flag);
-        if (!ok) fail();
+        if (!ok) {
+            if (lane == 0) s_used[kQFull] = segs;
+            fail();
+        }
     } else if (warp == 6) {
         // ================================================= values
         Walker wk;
@@ -473,7 +511,10 @@ __global__ void __launch_bounds__(Cfg<R, TILE>::THREADS, 1)
             }
         }
         ok = ok && ring_ended(bar(kVEmpty), C::VS, vc, abort_flag);
-        if (!ok) fail();
+        if (!ok) {
+            if (lane == 0) s_used[kVFull] = vc;
+            fail();
+        }
     } else if (warp == 1) {
         // ================================================= products
         if (rank == 0 && elect_one()) {
@@ -484,7 +525,7 @@ __global__ void __launch_bounds__(Cfg<R, TILE>::THREADS, 1)
             Walker wk;
             wk.init(a, start);
             Seg g;
-            int kc = 0, vc = 0, sc = 0, pc = 0, segs = 0;
+            int kc = 0, vc = 0, sc = 0, pc = 0, qc = 0, segs = 0;
             auto k_full = [&](int k) { return bar(kKFull + k % C::KS); };
             auto k_par = [&](int k) { return (uint32_t)((k / C::KS) & 1); };
             auto v_full = [&](int v) { return bar(kVFull + v % C::VS); };
@@ -560,7 +601,10 @@ __global__ void __launch_bounds__(Cfg<R, TILE>::THREADS, 1)
                     if (!ok) break;
                     commit_pair(bar(kSFull + (sc & 1)));
                     ++sc;
-                    if (j == cur.j1 - 1) commit_pair(bar(kQEmpty));
+                    if (j == cur.j1 - 1) {
+                        commit_pair(bar(kQEmpty));
+                        ++qc;
+                    }
                     if (j > cur.j0 && !pv(j - 1)) ok = false;
                 }
                 if (ok && !pv(cur.j1 - 1)) ok = false;
@@ -569,13 +613,12 @@ __global__ void __launch_bounds__(Cfg<R, TILE>::THREADS, 1)
             // the last output's readers, of both CTAs, have arrived before this one ends
             if (ok && segs > 0)
                 ok = mbar_wait<false>(bar(kORead), (uint32_t)((segs - 1) & 1), abort_flag);
-            if (!ok) {
-                fail();
-                // what was issued completes before the tensor memory goes
-                volatile int never = 0;
-                commit_pair(bar(kSpare));
-                mbar_wait(bar(kSpare), 0, &never);
-            }
+            s_used[kKEmpty] = kc;
+            s_used[kVEmpty] = vc;
+            s_used[kSFull] = sc;
+            s_used[kPvDone] = pc;
+            s_used[kQEmpty] = qc;
+            if (!ok) fail();
         }
         __syncwarp();
     } else {
@@ -789,7 +832,7 @@ __global__ void __launch_bounds__(Cfg<R, TILE>::THREADS, 1)
             // the first part of a tile that goes on in the next pairs' runs
             if (!g.whole && g.j0 == 0 && rank == 0 && warp == 2 && lane == 0) {
                 // steps of the tile from this run's end on, and the runs they fall in
-                const int64_t total = start.total, np = min((int64_t)a.pairs, total);
+                const int64_t total = s_start.total, np = min((int64_t)a.pairs, total);
                 const int64_t e = run_begin(total, np, pair + 1);   // first step after this run
                 const int64_t z = e + (wk.q.nt - g.j1) - 1;  // the tile's last
                 int64_t last = z * np / total;               // the run that holds it
@@ -803,14 +846,10 @@ __global__ void __launch_bounds__(Cfg<R, TILE>::THREADS, 1)
     }
 
     __syncwarp();
-    if (*abort_flag) {
-        // copies in flight end before the CTA does
-        const uint64_t t = global_ns();
-        while (global_ns() - t < 200000ull) __nanosleep(1000);
-    }
     fence_before();
     __syncthreads();
     cluster_meet();
+    if (*abort_flag) end_given_up<C>(smem_u32(bars), smem_u32(s_used));
     if (warp == 1) {
         fence_after();
         dealloc_pair(tmem);

@@ -96,8 +96,7 @@ enum : int {
     kORead = 54,     // + slot: its output read from tensor memory (first CTA's)
     kItFull = 56,    // + entry (4)
     kItEmpty = 60,   // + entry
-    kSpare = 64,     // + one of the products' threads
-    kBars = 66
+    kBars = 64
 };
 
 struct Args {
@@ -256,6 +255,38 @@ struct Walker {
     }
 };
 
+// Either CTA gave up: what is in flight ends before they do, products (by their commits, of
+// which the first CTA keeps count) and copies (counted by roles that gave up; one that did
+// not has seen the last of its ring used).  bar0: the barriers, used0: the phases used of each
+// ring, at its first barrier's place.  (Not inlined, and no count kept otherwise: those cost
+// calls that never come here up to 3 %.)
+template <class C>
+__device__ __noinline__ void end_given_up(uint32_t bar0, uint32_t used0) {
+    cluster_sync();
+    if (threadIdx.x < 32) {
+        const uint32_t rank = cluster_rank();
+        volatile int never = 0;
+        auto used = [&](int b, uint32_t r) { return ld_cluster(at_rank(used0 + 4 * b, r)); };
+        auto products = [&](int b, int slots) { ring_ended(bar0 + 8 * b, slots, used(b, 0), &never); };
+        auto copies = [&](int b, int slots) {
+            if (rank == 0) copies_ended(bar0 + 8 * b, slots, used(b, 0), used(b, 1));
+        };
+        products(kKEmpty, C::KS);
+        products(kVEmpty, C::VS);
+        copies(kKFull, C::KS);
+        copies(kVFull, C::VS);
+        for (int x = 0; x < 2; ++x) {
+            products(kSFull + C::PL * x, C::PL);
+            products(kPvDone + C::PL * x, C::PL);
+            products(kQEmpty + x, 1);
+            copies(kQFull + x, 1);
+        }
+    }
+    fence_before();
+    __syncthreads();
+    cluster_sync();
+}
+
 template <typename T, int N>
 __global__ void __launch_bounds__(kThreads, 1)
     latent_prefill_pair(const __grid_constant__ CUtensorMap tm_q,
@@ -267,6 +298,7 @@ __global__ void __launch_bounds__(kThreads, 1)
     __shared__ __align__(8) uint64_t bars[kBars];
     __shared__ uint32_t s_tmem;
     __shared__ int s_abort;
+    __shared__ int s_used[kBars];                   // phases of a ring, at its first barrier's place
     __shared__ Start s_start;
     __shared__ Item s_items[kRing];
     __shared__ int64_t s_scan[2][kThreads / 32];
@@ -293,10 +325,11 @@ __global__ void __launch_bounds__(kThreads, 1)
                              (i >= kVFull && i < kVEmpty);
             const bool warps = (i >= kPFull && i < kPvDone) || i == kORead || i == kORead + 1;
             // an item's readers: keys, values, eight of softmax, the two of products
-            const int n = two ? 2 : warps ? 8 : i >= kItEmpty && i < kSpare ? (rank ? 10 : 12) : 1;
+            const int n = two ? 2 : warps ? 8 : i >= kItEmpty ? (rank ? 10 : 12) : 1;
             mbar_init(bar(i), n);
         }
         mbar_init_fence();
+        for (int i = lane; i < kBars; i += 32) s_used[i] = kNotCounted;
         if (lane == 0) s_abort = 0;
         __syncwarp();
         alloc_pair(smem_u32(&s_tmem));
@@ -378,6 +411,7 @@ __global__ void __launch_bounds__(kThreads, 1)
     auto fail = [&]() {
         if (!*abort_flag) atomicOr(a.err, PKV_DEVERR_TIMEOUT);
         *abort_flag = 1;
+        set_cluster(at_rank(smem_u32(&s_abort), cluster_rank() ^ 1), 1);
     };
 
     // the next item of the run, from the warp that walks it
@@ -424,7 +458,10 @@ __global__ void __launch_bounds__(kThreads, 1)
         }
         // (the products' last releases arrive before the CTA ends: see cluster_meet)
         ok = ok && ring_ended(bar(kKEmpty), C::KS, kc, abort_flag);
-        if (!ok) fail();
+        if (!ok) {
+            if (lane == 0) s_used[kKFull] = kc;
+            fail();
+        }
     } else if (warp == 2) {
         // ================================================= values
         Item it;
@@ -476,7 +513,10 @@ __global__ void __launch_bounds__(kThreads, 1)
             }
         }
         ok = ok && ring_ended(bar(kVEmpty), C::VS, vc, abort_flag);
-        if (!ok) fail();
+        if (!ok) {
+            if (lane == 0) s_used[kVFull] = vc;
+            fail();
+        }
     } else if (warp == 3) {
         // ================================================= items and queries
         Walker wk;
@@ -500,7 +540,7 @@ __global__ void __launch_bounds__(kThreads, 1)
             if (!more) break;
             for (int x = 0; x < 2; ++x) {
                 if (it.end(x) <= it.j0) continue;
-                const int n = count[x]++;
+                const int n = count[x];
                 if (n > 0 && !warp_wait(bar(kQEmpty + x), (uint32_t)((n - 1) & 1), abort_flag)) {
                     ok = false;
                     break;
@@ -511,10 +551,17 @@ __global__ void __launch_bounds__(kThreads, 1)
                 if (c < C::CH)
                     tma_3d_pair(sQ + x * C::Q_SLOT + c * C::Q_CHUNK + r * 128, &tm_q, c * 64, it.h,
                                 it.q0 + (x ? it.row1 : 0) + 128 * (int)rank + r, full);
+                ++count[x];
             }
         }
         for (int x = 0; x < 2; ++x) ok = ok && ring_ended(bar(kQEmpty + x), 1, count[x], abort_flag);
-        if (!ok) fail();
+        if (!ok) {
+            if (lane == 0) {
+                s_used[kQFull] = count[0];
+                s_used[kQFull + 1] = count[1];
+            }
+            fail();
+        }
     } else if (warp == 1) {
         // ================================================= scores
         if (rank == 0 && elect_one()) {
@@ -522,6 +569,7 @@ __global__ void __launch_bounds__(kThreads, 1)
             const uint64_t dQ = sdesc(sQ, 16, 1024), dK = sdesc(sK, 16, 1024);
             Item it;
             int g = 0, n[2] = {0, 0};        // steps of the run, of each slot
+            int ends[2] = {0, 0};            // items of each slot whose scores are all formed
             uint32_t qs = 0;                 // a slot's phase of its queries, by bits
             while (next_alone(it)) {
                 for (int j = it.j0; ok && j < it.j1; ++j, ++g) {
@@ -549,7 +597,10 @@ __global__ void __launch_bounds__(kThreads, 1)
                                       da + (((e >> 2) * C::Q_CHUNK + (e & 3) * 32) >> 4),
                                       db + (((e >> 2) * C::K_CHUNK + (e & 3) * 32) >> 4), ID_S, e > 0);
                         commit_pair(bar(kSFull + C::PL * x + p));
-                        if (j == it.end(x) - 1) commit_pair(bar(kQEmpty + x));
+                        if (j == it.end(x) - 1) {
+                            commit_pair(bar(kQEmpty + x));
+                            ++ends[x];
+                        }
                         ++n[x];
                     }
                     // (a stage whose copy may be on its way is never handed back)
@@ -557,13 +608,12 @@ __global__ void __launch_bounds__(kThreads, 1)
                     commit_pair(bar(kKEmpty + st));
                 }
             }
-            if (!ok) {
-                fail();
-                // what was issued completes before the tensor memory goes
-                volatile int never = 0;
-                commit_pair(bar(kSpare));
-                mbar_wait(bar(kSpare), 0, &never);
+            s_used[kKEmpty] = g;
+            for (int x = 0; x < 2; ++x) {
+                s_used[kSFull + C::PL * x] = n[x];
+                s_used[kQEmpty + x] = ends[x];
             }
+            if (!ok) fail();
         }
         __syncwarp();
     } else if (warp == 12) {
@@ -607,12 +657,9 @@ __global__ void __launch_bounds__(kThreads, 1)
             for (int x = 0; x < 2; ++x)
                 if (ok && (left >> x & 1))
                     ok = mbar_wait<false>(bar(kORead + x), os >> x & 1, abort_flag);
-            if (!ok) {
-                fail();
-                volatile int never = 0;
-                commit_pair(bar(kSpare + 1));
-                mbar_wait(bar(kSpare + 1), 0, &never);
-            }
+            s_used[kVEmpty] = g;
+            for (int x = 0; x < 2; ++x) s_used[kPvDone + C::PL * x] = n[x];
+            if (!ok) fail();
         }
         __syncwarp();
     } else {
@@ -781,7 +828,7 @@ __global__ void __launch_bounds__(kThreads, 1)
             }
             // the first part of an item that goes on in the next pairs' runs
             if (!whole && it.j0 == 0 && rank == 0 && warp == 4 && lane == 0) {
-                const int64_t total = start.total, np = min((int64_t)a.pairs, total);
+                const int64_t total = s_start.total, np = min((int64_t)a.pairs, total);
                 const int64_t e = run_begin(total, np, pair + 1);   // first step after this run
                 const int64_t z = e + (it.steps - it.j1) - 1;    // the item's last
                 int64_t last = z * np / total;               // the run that holds it
@@ -796,14 +843,10 @@ __global__ void __launch_bounds__(kThreads, 1)
     }
 
     __syncwarp();
-    if (*abort_flag) {
-        // copies in flight end before the CTA does
-        const uint64_t t = global_ns();
-        while (global_ns() - t < 200000ull) __nanosleep(1000);
-    }
     fence_before();
     __syncthreads();
     cluster_meet();
+    if (*abort_flag) end_given_up<C>(smem_u32(bars), smem_u32(s_used));
     if (warp == 1) {
         fence_after();
         dealloc_pair(tmem);

@@ -136,6 +136,43 @@ __device__ __forceinline__ void cluster_meet() {
         "barrier.cluster.wait.acquire.aligned;" ::
             : "memory");
 }
+// The same with everything before it done and seen, arrivals on the other CTA's barriers too.
+__device__ __forceinline__ void cluster_sync() {
+    asm volatile(
+        "barrier.cluster.arrive.release.aligned;\n\t"
+        "barrier.cluster.wait.acquire.aligned;" ::
+            : "memory");
+}
+// A word of the other CTA's shared memory (at_rank).
+__device__ __forceinline__ int ld_cluster(uint32_t addr) {
+    int v;
+    asm volatile("ld.relaxed.cluster.shared::cluster.s32 %0, [%1];" : "=r"(v) : "r"(addr) : "memory");
+    return v;
+}
+// Set, and seen by whoever meets this thread at a barrier of the cluster later.
+__device__ __forceinline__ void set_cluster(uint32_t addr, int v) {
+    asm volatile(
+        "st.relaxed.cluster.shared::cluster.s32 [%0], %1;\n\t"
+        "fence.acq_rel.cluster;" ::"r"(addr), "r"(v)
+        : "memory");
+}
+// After a wait that ran out, once no thread of the pair issues anything more.  The copies
+// into a ring that the two CTAs fill side by side complete on the first CTA's barriers, each
+// phase after an arrival of both: `mine` and `theirs` stages have been armed by this CTA and
+// the other; a ring that either of them does not count has been used up.  A phase that one of
+// them never came to is completed in its place, so that every copy on its way has been waited
+// for.  One warp.
+constexpr int kNotCounted = -1;
+__device__ __forceinline__ void copies_ended(uint32_t bar0, int slots, int mine, int theirs) {
+    if (mine == kNotCounted || theirs == kNotCounted) return;
+    const int most = max(mine, theirs), both = min(mine, theirs);
+    volatile int never = 0;
+    for (int i = max(most - slots, 0); i < most; ++i) {
+        if (i >= both && (threadIdx.x & 31) == 0) mbar_arrive(bar0 + 8 * (i % slots));
+        __syncwarp();
+        warp_wait(bar0 + 8 * (i % slots), (uint32_t)((i / slots) & 1), &never);
+    }
+}
 __device__ __forceinline__ void named_sync(int id, int threads) {
     asm volatile("bar.sync %0, %1;" ::"r"(id), "r"(threads) : "memory");
 }
