@@ -278,8 +278,9 @@ pkv_status pkv_paged_attention_decode_grouped(
  * warp waiting for a ring stage's copy, the producer waiting for a free stage
  * or for a claimed chunk's query slice, the consumer warps meeting at the end
  * of a piece), for every later launch of pkv_paged_attention_decode, its
- * _noalloc, _append, _shared and _grouped forms and
- * pkv_contiguous_attention_decode from any host thread.  Default 1 s; at
+ * _noalloc, _append, _shared and _grouped forms,
+ * pkv_contiguous_attention_decode, pkv_latent_attention_decode and
+ * pkv_latent_attention_prefill from any host thread.  Default 1 s; at
  * most 10 s (larger values: PKV_ERR_INVALID, nothing changed).  A wait that
  * runs out sets PKV_DEVERR_TIMEOUT; the CTA then stops issuing copies, its
  * other waits give up at once, its results for the call are not valid, and it

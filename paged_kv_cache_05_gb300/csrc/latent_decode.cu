@@ -129,6 +129,7 @@ struct Args {
     float2* ml;                       // [2 pairs][slot_rows]
     float* acc;                       // [2 pairs][R / 8][slot_rows][8]
     int32_t* err;
+    uint64_t wait_ns;                 // of a wait (pkv_set_decode_wait_limit)
 };
 
 // What is left to join: rows of the output whose parts lie in `parts` slots: `slot`,
@@ -243,9 +244,9 @@ __device__ __noinline__ void end_given_up(uint32_t bar0, uint32_t used0) {
     cluster_sync();
     if (threadIdx.x < 32) {
         const uint32_t rank = cluster_rank();
-        volatile int never = 0;
+        volatile Limit longest = {kWaitLimitNs, 0};     // (whatever the call's)
         auto used = [&](int b, uint32_t r) { return ld_cluster(at_rank(used0 + 4 * b, r)); };
-        auto products = [&](int b, int slots) { ring_ended(bar0 + 8 * b, slots, used(b, 0), &never); };
+        auto products = [&](int b, int slots) { ring_ended(bar0 + 8 * b, slots, used(b, 0), &longest); };
         auto copies = [&](int b, int slots) {
             if (rank == 0) copies_ended(bar0 + 8 * b, slots, used(b, 0), used(b, 1));
         };
@@ -272,7 +273,7 @@ __global__ void __launch_bounds__(Cfg<R, TILE>::THREADS, 1)
     extern __shared__ __align__(1024) uint8_t smem_raw[];
     __shared__ __align__(8) uint64_t bars[kBars];
     __shared__ uint32_t s_tmem;
-    __shared__ int s_abort;
+    __shared__ Limit s_limit;
     __shared__ int s_used[kBars];                   // phases of a ring, at its first barrier's place
     __shared__ Start s_start;
     __shared__ int64_t s_scan[2][C::WARPS];
@@ -281,7 +282,7 @@ __global__ void __launch_bounds__(Cfg<R, TILE>::THREADS, 1)
     const int tid = threadIdx.x, warp = tid >> 5, lane = tid & 31;
     const uint32_t rank = cluster_rank();
     const int pair = (int)(blockIdx.x >> 1);
-    volatile int* const abort_flag = &s_abort;
+    volatile Limit* const limit = &s_limit;
     const uint32_t base = (smem_u32(smem_raw) + 1023) & ~1023u;
     const uint32_t sQ = base + C::Q_OFF, sK = base + C::K_OFF, sV = base + C::V_OFF,
                    sP = base + C::P_OFF;
@@ -302,7 +303,7 @@ __global__ void __launch_bounds__(Cfg<R, TILE>::THREADS, 1)
         }
         mbar_init_fence();
         for (int i = lane; i < kBars; i += 32) s_used[i] = kNotCounted;
-        if (lane == 0) s_abort = 0;
+        if (lane == 0) s_limit = Limit{a.wait_ns, 0};
         __syncwarp();
         alloc_pair(smem_u32(&s_tmem));
     } else if (warp == 0 && lane == 0) {
@@ -378,9 +379,9 @@ __global__ void __launch_bounds__(Cfg<R, TILE>::THREADS, 1)
     const Start start = s_start;
     bool ok = true;
     auto fail = [&]() {
-        if (!*abort_flag) atomicOr(a.err, PKV_DEVERR_TIMEOUT);
-        *abort_flag = 1;
-        set_cluster(at_rank(smem_u32(&s_abort), cluster_rank() ^ 1), 1);
+        if (!limit->gave_up) atomicOr(a.err, PKV_DEVERR_TIMEOUT);
+        limit->gave_up = 1;
+        set_cluster(at_rank(smem_u32(&s_limit.gave_up), cluster_rank() ^ 1), 1);
     };
 
     if (warp == 0) {
@@ -400,7 +401,7 @@ __global__ void __launch_bounds__(Cfg<R, TILE>::THREADS, 1)
 #pragma unroll
                 for (int u = 0; u < C::KSUB; ++u, ++kc) {
                     const int st = kc % C::KS, n = kc / C::KS;
-                    if (n > 0 && !warp_wait(bar(kKEmpty + st), (uint32_t)((n - 1) & 1), abort_flag)) {
+                    if (n > 0 && !warp_wait(bar(kKEmpty + st), (uint32_t)((n - 1) & 1), limit)) {
                         ok = false;
                         break;
                     }
@@ -416,7 +417,7 @@ __global__ void __launch_bounds__(Cfg<R, TILE>::THREADS, 1)
             }
         }
         // (the products' last releases arrive before the CTA ends: see cluster_meet)
-        ok = ok && ring_ended(bar(kKEmpty), C::KS, kc, abort_flag);
+        ok = ok && ring_ended(bar(kKEmpty), C::KS, kc, limit);
         if (!ok) {
             if (lane == 0) s_used[kKFull] = kc;
             fail();
@@ -429,7 +430,7 @@ __global__ void __launch_bounds__(Cfg<R, TILE>::THREADS, 1)
         const uint32_t qfull = at_rank(bar(kQFull), 0);
         int segs = 0;
         for (; wk.get(a, g); ++segs) {
-            if (segs > 0 && !warp_wait(bar(kQEmpty), (uint32_t)((segs - 1) & 1), abort_flag)) {
+            if (segs > 0 && !warp_wait(bar(kQEmpty), (uint32_t)((segs - 1) & 1), limit)) {
                 ok = false;
                 break;
             }
@@ -440,7 +441,7 @@ __global__ void __launch_bounds__(Cfg<R, TILE>::THREADS, 1)
                 tma_3d_pair(sQ + lane * C::CH * 1024, &tm_q, 0,
                             g.q0 * a.H + g.row + C::RC * (int)rank + 8 * lane, 0, qfull);
         }
-        ok = ok && ring_ended(bar(kQEmpty), 1, segs, abort_flag);
+        ok = ok && ring_ended(bar(kQEmpty), 1, segs, limit);
         if (!ok) {
             if (lane == 0) s_used[kQFull] = segs;
             fail();
@@ -469,7 +470,7 @@ __global__ void __launch_bounds__(Cfg<R, TILE>::THREADS, 1)
                 const int tail = left < kTok && (left & 7) ? left >> 3 : -1;
                 for (int v = 0; v < subs; ++v, ++vc) {
                     const int st = vc % C::VS, n = vc / C::VS;
-                    if (n > 0 && !warp_wait(bar(kVEmpty + st), (uint32_t)((n - 1) & 1), abort_flag)) {
+                    if (n > 0 && !warp_wait(bar(kVEmpty + st), (uint32_t)((n - 1) & 1), limit)) {
                         ok = false;
                         break;
                     }
@@ -510,7 +511,7 @@ __global__ void __launch_bounds__(Cfg<R, TILE>::THREADS, 1)
                 y = yn;
             }
         }
-        ok = ok && ring_ended(bar(kVEmpty), C::VS, vc, abort_flag);
+        ok = ok && ring_ended(bar(kVEmpty), C::VS, vc, limit);
         if (!ok) {
             if (lane == 0) s_used[kVFull] = vc;
             fail();
@@ -535,9 +536,9 @@ __global__ void __launch_bounds__(Cfg<R, TILE>::THREADS, 1)
                 const Seg cur = g;
                 have = wk.get(a, g);
                 auto pv = [&](int j) {
-                    if (!mbar_wait<false>(bar(kPFull), (uint32_t)(pc & 1), abort_flag)) return false;
+                    if (!mbar_wait<false>(bar(kPFull), (uint32_t)(pc & 1), limit)) return false;
                     if (j == cur.j0 && segs > 0 &&
-                        !mbar_wait<false>(bar(kORead), (uint32_t)((segs - 1) & 1), abort_flag))
+                        !mbar_wait<false>(bar(kORead), (uint32_t)((segs - 1) & 1), limit))
                         return false;
                     const int left = cur.ctx - j * kTok;
                     const int subs = left >= kTok ? 4 : (left + 31) / 32;
@@ -545,7 +546,7 @@ __global__ void __launch_bounds__(Cfg<R, TILE>::THREADS, 1)
 #pragma unroll
                     for (int v = 0; v < 4; ++v) {
                         if (v >= subs) break;
-                        if (!mbar_wait<false>(v_full(vc), v_par(vc), abort_flag)) return false;
+                        if (!mbar_wait<false>(v_full(vc), v_par(vc), limit)) return false;
                         fence_after();
                         const uint64_t da = dP + (uint64_t)(((v >> 1) * 8192 + (v & 1) * 64) >> 4);
                         const uint64_t db = dV + (uint64_t)(((vc % C::VS) * C::V_SLOT) >> 4);
@@ -570,20 +571,20 @@ __global__ void __launch_bounds__(Cfg<R, TILE>::THREADS, 1)
                     ++pc;
                     return true;
                 };
-                if (!mbar_wait<false>(bar(kQFull), (uint32_t)(segs & 1), abort_flag)) {
+                if (!mbar_wait<false>(bar(kQFull), (uint32_t)(segs & 1), limit)) {
                     ok = false;
                     break;
                 }
                 for (int j = cur.j0; ok && j < cur.j1; ++j) {
                     // the weights that these scores overwrite have been read
                     if (C::WIDE && pc > 0 &&
-                        !mbar_wait<false>(bar(kPvDone), (uint32_t)((pc - 1) & 1), abort_flag)) {
+                        !mbar_wait<false>(bar(kPvDone), (uint32_t)((pc - 1) & 1), limit)) {
                         ok = false;
                         break;
                     }
 #pragma unroll
                     for (int u = 0; u < C::KSUB; ++u, ++kc) {
-                        if (!mbar_wait<false>(k_full(kc), k_par(kc), abort_flag)) {
+                        if (!mbar_wait<false>(k_full(kc), k_par(kc), limit)) {
                             ok = false;
                             break;
                         }
@@ -612,7 +613,7 @@ __global__ void __launch_bounds__(Cfg<R, TILE>::THREADS, 1)
             }
             // the last output's readers, of both CTAs, have arrived before this one ends
             if (ok && segs > 0)
-                ok = mbar_wait<false>(bar(kORead), (uint32_t)((segs - 1) & 1), abort_flag);
+                ok = mbar_wait<false>(bar(kORead), (uint32_t)((segs - 1) & 1), limit);
             s_used[kKEmpty] = kc;
             s_used[kVEmpty] = vc;
             s_used[kSFull] = sc;
@@ -668,7 +669,7 @@ __global__ void __launch_bounds__(Cfg<R, TILE>::THREADS, 1)
                     const bool in = t_group >= g.ctx || cache_row(a, g, t_group) >= 0;
                     groups = __ballot_sync(0xffffffffu, in) & 0xffu;
                 }
-                ok = ok && warp_wait(bar(kSFull + (sc & 1)), (uint32_t)((sc >> 1) & 1), abort_flag);
+                ok = ok && warp_wait(bar(kSFull + (sc & 1)), (uint32_t)((sc >> 1) & 1), limit);
                 fence_after();
                 uint32_t w[32];
                 float alpha = 1.f;
@@ -736,7 +737,7 @@ __global__ void __launch_bounds__(Cfg<R, TILE>::THREADS, 1)
                     l2 = fma2(l2, f2(alpha, alpha), add2(sum[0], sum[1]));
                 }
                 // the step before has read its weights and written O
-                ok = ok && (sc == 0 || warp_wait(bar(kPvDone), (uint32_t)((sc - 1) & 1), abort_flag));
+                ok = ok && (sc == 0 || warp_wait(bar(kPvDone), (uint32_t)((sc - 1) & 1), limit));
                 fence_after();
                 if (live) {
                     if (j > g.j0 && __any_sync(0xffffffffu, alpha != 1.f)) {
@@ -780,7 +781,7 @@ __global__ void __launch_bounds__(Cfg<R, TILE>::THREADS, 1)
                 if (lane == 0) mbar_arrive_cluster(pfull);
             }
             // the tile's output
-            ok = ok && warp_wait(bar(kPvDone), (uint32_t)((sc - 1) & 1), abort_flag);
+            ok = ok && warp_wait(bar(kPvDone), (uint32_t)((sc - 1) & 1), limit);
             fence_after();
             if (live) {
                 float x, y;
@@ -849,7 +850,7 @@ __global__ void __launch_bounds__(Cfg<R, TILE>::THREADS, 1)
     fence_before();
     __syncthreads();
     cluster_meet();
-    if (*abort_flag) end_given_up<C>(smem_u32(bars), smem_u32(s_used));
+    if (limit->gave_up) end_given_up<C>(smem_u32(bars), smem_u32(s_used));
     if (warp == 1) {
         fence_after();
         dealloc_pair(tmem);
@@ -1112,6 +1113,7 @@ pkv_status pkv_latent_attention_decode(
     a.ml = reinterpret_cast<float2*>(ws + l.ml);
     a.acc = reinterpret_cast<float*>(ws + l.acc);
     a.err = err;
+    a.wait_ns = pkv::decode_wait_ns();
     if (bf16)
         e = latent_dim == 512 ? launch<__nv_bfloat16, 512, 128>(tq, tk, tv, a, stream)
             : wide            ? launch<__nv_bfloat16, 256, 256>(tq, tk, tv, a, stream)

@@ -113,6 +113,7 @@ struct Args {
     float2* ml;                       // [2 pairs][slot_rows]
     float* acc;                       // [2 pairs][N / 8][slot_rows][8]
     int32_t* err;
+    uint64_t wait_ns;                 // of a wait (pkv_set_decode_wait_limit)
 };
 
 // What is left to join: rows of the output of a head whose parts lie in `parts` slots:
@@ -265,9 +266,9 @@ __device__ __noinline__ void end_given_up(uint32_t bar0, uint32_t used0) {
     cluster_sync();
     if (threadIdx.x < 32) {
         const uint32_t rank = cluster_rank();
-        volatile int never = 0;
+        volatile Limit longest = {kWaitLimitNs, 0};     // (whatever the call's)
         auto used = [&](int b, uint32_t r) { return ld_cluster(at_rank(used0 + 4 * b, r)); };
-        auto products = [&](int b, int slots) { ring_ended(bar0 + 8 * b, slots, used(b, 0), &never); };
+        auto products = [&](int b, int slots) { ring_ended(bar0 + 8 * b, slots, used(b, 0), &longest); };
         auto copies = [&](int b, int slots) {
             if (rank == 0) copies_ended(bar0 + 8 * b, slots, used(b, 0), used(b, 1));
         };
@@ -297,7 +298,7 @@ __global__ void __launch_bounds__(kThreads, 1)
     extern __shared__ __align__(1024) uint8_t smem_raw[];
     __shared__ __align__(8) uint64_t bars[kBars];
     __shared__ uint32_t s_tmem;
-    __shared__ int s_abort;
+    __shared__ Limit s_limit;
     __shared__ int s_used[kBars];                   // phases of a ring, at its first barrier's place
     __shared__ Start s_start;
     __shared__ Item s_items[kRing];
@@ -306,7 +307,7 @@ __global__ void __launch_bounds__(kThreads, 1)
     const int tid = threadIdx.x, warp = tid >> 5, lane = tid & 31;
     const uint32_t rank = cluster_rank();
     const int pair = (int)(blockIdx.x >> 1);
-    volatile int* const abort_flag = &s_abort;
+    volatile Limit* const limit = &s_limit;
     const uint32_t base = (smem_u32(smem_raw) + 1023) & ~1023u;
     const uint32_t sQ = base + C::Q_OFF, sK = base + C::K_OFF, sV = base + C::V_OFF;
     auto bar = [&](int i) { return smem_u32(&bars[i]); };
@@ -330,7 +331,7 @@ __global__ void __launch_bounds__(kThreads, 1)
         }
         mbar_init_fence();
         for (int i = lane; i < kBars; i += 32) s_used[i] = kNotCounted;
-        if (lane == 0) s_abort = 0;
+        if (lane == 0) s_limit = Limit{a.wait_ns, 0};
         __syncwarp();
         alloc_pair(smem_u32(&s_tmem));
     } else if (warp == 0 && lane == 0) {
@@ -409,16 +410,16 @@ __global__ void __launch_bounds__(kThreads, 1)
     const Start start = s_start;
     bool ok = true;
     auto fail = [&]() {
-        if (!*abort_flag) atomicOr(a.err, PKV_DEVERR_TIMEOUT);
-        *abort_flag = 1;
-        set_cluster(at_rank(smem_u32(&s_abort), cluster_rank() ^ 1), 1);
+        if (!limit->gave_up) atomicOr(a.err, PKV_DEVERR_TIMEOUT);
+        limit->gave_up = 1;
+        set_cluster(at_rank(smem_u32(&s_limit.gave_up), cluster_rank() ^ 1), 1);
     };
 
     // the next item of the run, from the warp that walks it
     int items = 0;
     auto next_item = [&](Item& it) {
         const int e = items % kRing;
-        ok = ok && warp_wait(bar(kItFull + e), (uint32_t)((items / kRing) & 1), abort_flag);
+        ok = ok && warp_wait(bar(kItFull + e), (uint32_t)((items / kRing) & 1), limit);
         it = s_items[e];
         __syncwarp();
         // (one that gave up hands nothing back: others may not have read the entry)
@@ -428,7 +429,7 @@ __global__ void __launch_bounds__(kThreads, 1)
     };
     auto next_alone = [&](Item& it) {            // (by one thread)
         const int e = items % kRing;
-        ok = ok && mbar_wait<false>(bar(kItFull + e), (uint32_t)((items / kRing) & 1), abort_flag);
+        ok = ok && mbar_wait<false>(bar(kItFull + e), (uint32_t)((items / kRing) & 1), limit);
         it = s_items[e];
         if (ok) mbar_arrive(bar(kItEmpty + e));
         ++items;
@@ -443,7 +444,7 @@ __global__ void __launch_bounds__(kThreads, 1)
         while (next_item(it)) {
             for (int j = it.j0; j < it.j1; ++j, ++kc) {
                 const int st = kc % C::KS, n = kc / C::KS;
-                if (n > 0 && !warp_wait(bar(kKEmpty + st), (uint32_t)((n - 1) & 1), abort_flag)) {
+                if (n > 0 && !warp_wait(bar(kKEmpty + st), (uint32_t)((n - 1) & 1), limit)) {
                     ok = false;
                     break;
                 }
@@ -457,7 +458,7 @@ __global__ void __launch_bounds__(kThreads, 1)
             }
         }
         // (the products' last releases arrive before the CTA ends: see cluster_meet)
-        ok = ok && ring_ended(bar(kKEmpty), C::KS, kc, abort_flag);
+        ok = ok && ring_ended(bar(kKEmpty), C::KS, kc, limit);
         if (!ok) {
             if (lane == 0) s_used[kKFull] = kc;
             fail();
@@ -470,7 +471,7 @@ __global__ void __launch_bounds__(kThreads, 1)
         while (next_item(it)) {
             for (int j = it.j0; j < it.j1; ++j, ++vc) {
                 const int st = vc % C::VS, n = vc / C::VS;
-                if (n > 0 && !warp_wait(bar(kVEmpty + st), (uint32_t)((n - 1) & 1), abort_flag)) {
+                if (n > 0 && !warp_wait(bar(kVEmpty + st), (uint32_t)((n - 1) & 1), limit)) {
                     ok = false;
                     break;
                 }
@@ -512,7 +513,7 @@ __global__ void __launch_bounds__(kThreads, 1)
                                 full);
             }
         }
-        ok = ok && ring_ended(bar(kVEmpty), C::VS, vc, abort_flag);
+        ok = ok && ring_ended(bar(kVEmpty), C::VS, vc, limit);
         if (!ok) {
             if (lane == 0) s_used[kVFull] = vc;
             fail();
@@ -529,7 +530,7 @@ __global__ void __launch_bounds__(kThreads, 1)
             const bool more = wk.get(a, it);
             if (!more) it.rows = 0;
             const int e = n % kRing;
-            if (n >= kRing && !warp_wait(bar(kItEmpty + e), (uint32_t)((n / kRing - 1) & 1), abort_flag)) {
+            if (n >= kRing && !warp_wait(bar(kItEmpty + e), (uint32_t)((n / kRing - 1) & 1), limit)) {
                 ok = false;
                 break;
             }
@@ -541,7 +542,7 @@ __global__ void __launch_bounds__(kThreads, 1)
             for (int x = 0; x < 2; ++x) {
                 if (it.end(x) <= it.j0) continue;
                 const int n = count[x];
-                if (n > 0 && !warp_wait(bar(kQEmpty + x), (uint32_t)((n - 1) & 1), abort_flag)) {
+                if (n > 0 && !warp_wait(bar(kQEmpty + x), (uint32_t)((n - 1) & 1), limit)) {
                     ok = false;
                     break;
                 }
@@ -554,7 +555,7 @@ __global__ void __launch_bounds__(kThreads, 1)
                 ++count[x];
             }
         }
-        for (int x = 0; x < 2; ++x) ok = ok && ring_ended(bar(kQEmpty + x), 1, count[x], abort_flag);
+        for (int x = 0; x < 2; ++x) ok = ok && ring_ended(bar(kQEmpty + x), 1, count[x], limit);
         if (!ok) {
             if (lane == 0) {
                 s_used[kQFull] = count[0];
@@ -574,19 +575,19 @@ __global__ void __launch_bounds__(kThreads, 1)
             while (next_alone(it)) {
                 for (int j = it.j0; ok && j < it.j1; ++j, ++g) {
                     const int st = g % C::KS;
-                    ok = mbar_wait<false>(bar(kKFull + st), (uint32_t)((g / C::KS) & 1), abort_flag);
+                    ok = mbar_wait<false>(bar(kKFull + st), (uint32_t)((g / C::KS) & 1), limit);
 #pragma unroll
                     for (int x = 0; x < 2; ++x) {
                         if (!ok || j >= it.end(x)) continue;
                         if (j == it.j0) {
-                            ok = mbar_wait<false>(bar(kQFull + x), qs >> x & 1, abort_flag);
+                            ok = mbar_wait<false>(bar(kQFull + x), qs >> x & 1, limit);
                             qs ^= 1u << x;
                         }
                         // the place is free once P V of the step that had it is done
                         const int p = n[x] % C::PL;
                         if (ok && n[x] >= C::PL)
                             ok = mbar_wait<false>(bar(kPvDone + C::PL * x + p),
-                                                  (uint32_t)(n[x] / C::PL - 1) & 1, abort_flag);
+                                                  (uint32_t)(n[x] / C::PL - 1) & 1, limit);
                         if (!ok) continue;
                         fence_after();
                         const uint64_t da = dQ + (uint64_t)((x * C::Q_SLOT) >> 4);
@@ -627,15 +628,15 @@ __global__ void __launch_bounds__(kThreads, 1)
             while (next_alone(it)) {
                 for (int j = it.j0; ok && j < it.j1; ++j, ++g) {
                     const int st = g % C::VS;
-                    ok = mbar_wait<false>(bar(kVFull + st), (uint32_t)((g / C::VS) & 1), abort_flag);
+                    ok = mbar_wait<false>(bar(kVFull + st), (uint32_t)((g / C::VS) & 1), limit);
 #pragma unroll
                     for (int x = 0; x < 2; ++x) {
                         if (!ok || j >= it.end(x)) continue;
                         const int p = n[x] % C::PL;
                         ok = mbar_wait<false>(bar(kPFull + C::PL * x + p),
-                                              (uint32_t)(n[x] / C::PL) & 1, abort_flag);
+                                              (uint32_t)(n[x] / C::PL) & 1, limit);
                         if (ok && j == it.j0 && (left >> x & 1)) {
-                            ok = mbar_wait<false>(bar(kORead + x), os >> x & 1, abort_flag);
+                            ok = mbar_wait<false>(bar(kORead + x), os >> x & 1, limit);
                             os ^= 1u << x;
                         }
                         if (!ok) continue;
@@ -656,7 +657,7 @@ __global__ void __launch_bounds__(kThreads, 1)
             // the last outputs' readers, of both CTAs, have arrived before this one ends
             for (int x = 0; x < 2; ++x)
                 if (ok && (left >> x & 1))
-                    ok = mbar_wait<false>(bar(kORead + x), os >> x & 1, abort_flag);
+                    ok = mbar_wait<false>(bar(kORead + x), os >> x & 1, limit);
             s_used[kVEmpty] = g;
             for (int x = 0; x < 2; ++x) s_used[kPvDone + C::PL * x] = n[x];
             if (!ok) fail();
@@ -686,7 +687,7 @@ __global__ void __launch_bounds__(kThreads, 1)
                 const int place = n % C::PL;
                 const uint32_t tS = tmem + lanes + (C::PL * x + place) * 64;
                 ok = ok && warp_wait(bar(kSFull + C::PL * x + place), (uint32_t)(n / C::PL) & 1,
-                                     abort_flag);
+                                     limit);
                 fence_after();
                 if (live) {
                     uint32_t z[64];
@@ -750,7 +751,7 @@ __global__ void __launch_bounds__(kThreads, 1)
                     if (j > it.j0 && __any_sync(0xffffffffu, alpha != 1.f)) {
                         // P V of the step before has to be in O
                         ok = ok && warp_wait(bar(kPvDone + C::PL * x + (n - 1) % C::PL),
-                                             (uint32_t)((n - 1) / C::PL) & 1, abort_flag);
+                                             (uint32_t)((n - 1) / C::PL) & 1, limit);
                         fence_after();
                         const uint64_t al2 = f2(alpha, alpha);
 #pragma unroll 1
@@ -784,7 +785,7 @@ __global__ void __launch_bounds__(kThreads, 1)
             if (mine && !whole) a.ml[slot * a.slot_rows + row] = make_float2(m, l);
             if (end > it.j0) {
                 ok = ok && warp_wait(bar(kPvDone + C::PL * x + (n - 1) % C::PL),
-                                     (uint32_t)((n - 1) / C::PL) & 1, abort_flag);
+                                     (uint32_t)((n - 1) / C::PL) & 1, limit);
                 fence_after();
                 if (live) {
                     const float inv = 1.f / l;
@@ -838,7 +839,7 @@ __global__ void __launch_bounds__(kThreads, 1)
                                   (int)(last - pair) + 1, {0, 0, 0}};
             }
         }
-        ok = ok && ring_ended(bar(kPvDone + C::PL * x), C::PL, n, abort_flag);
+        ok = ok && ring_ended(bar(kPvDone + C::PL * x), C::PL, n, limit);
         if (!ok && lane == 0) fail();
     }
 
@@ -846,7 +847,7 @@ __global__ void __launch_bounds__(kThreads, 1)
     fence_before();
     __syncthreads();
     cluster_meet();
-    if (*abort_flag) end_given_up<C>(smem_u32(bars), smem_u32(s_used));
+    if (limit->gave_up) end_given_up<C>(smem_u32(bars), smem_u32(s_used));
     if (warp == 1) {
         fence_after();
         dealloc_pair(tmem);
@@ -1111,6 +1112,7 @@ pkv_status pkv_latent_attention_prefill(
     a.ml = reinterpret_cast<float2*>(ws + l.ml);
     a.acc = reinterpret_cast<float*>(ws + l.acc);
     a.err = err;
+    a.wait_ns = pkv::decode_wait_ns();
     if (bf16)
         e = head_dim == 128 ? launch<__nv_bfloat16, 128>(tq, tk, tr, tv, a, stream)
                             : launch<__nv_bfloat16, 64>(tq, tk, tr, tv, a, stream);

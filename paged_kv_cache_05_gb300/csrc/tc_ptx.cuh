@@ -16,6 +16,12 @@ namespace tc {
 constexpr uint64_t kWaitLimitNs = 1000000000ull;
 constexpr uint32_t kWaitLimitIters = 1u << 26;
 
+// What bounds a CTA's waits, in its shared memory: the limit of each, and whether one ran out.
+struct Limit {
+    uint64_t ns;
+    int gave_up;
+};
+
 __device__ __forceinline__ uint32_t smem_u32(const void* p) {
     return static_cast<uint32_t>(__cvta_generic_to_shared(p));
 }
@@ -89,29 +95,31 @@ __device__ __forceinline__ uint64_t global_ns() {
     return t;
 }
 
-// Wait for the phase of `bar` with the given parity.  Gives up (false) after 1 s, after
-// kWaitLimitIters tests, or once *abort is set.
+// Wait for the phase of `bar` with the given parity.  Gives up (false) after the limit (one
+// of 0 at the first test), after kWaitLimitIters tests, or once another wait gave up.
 template <bool SUSPEND>
-__device__ __noinline__ bool wait_slow(uint32_t bar, uint32_t parity, volatile int* abort) {
+__device__ __noinline__ bool wait_slow(uint32_t bar, uint32_t parity, const volatile Limit* limit) {
+    const uint64_t ns = limit->ns;
+    if (ns == 0) return false;
     const uint64_t t0 = global_ns();
     for (uint32_t it = 1; it < kWaitLimitIters; ++it) {
         if (mbar_try<SUSPEND>(bar, parity)) return true;
         if ((it & 31) == 0) {
-            if (*abort) return false;
-            if (global_ns() - t0 > kWaitLimitNs) return false;
+            if (limit->gave_up) return false;
+            if (global_ns() - t0 > ns) return false;
         }
     }
     return false;
 }
 template <bool SUSPEND = true>
-__device__ __forceinline__ bool mbar_wait(uint32_t bar, uint32_t parity, volatile int* abort) {
+__device__ __forceinline__ bool mbar_wait(uint32_t bar, uint32_t parity, const volatile Limit* limit) {
     if (mbar_try<SUSPEND>(bar, parity)) return true;
-    return wait_slow<SUSPEND>(bar, parity, abort);
+    return wait_slow<SUSPEND>(bar, parity, limit);
 }
 
 // The same by a whole warp, with one answer for all of it.
-__device__ __forceinline__ bool warp_wait(uint32_t bar, uint32_t parity, volatile int* abort) {
-    return __all_sync(0xffffffffu, mbar_wait(bar, parity, abort));
+__device__ __forceinline__ bool warp_wait(uint32_t bar, uint32_t parity, const volatile Limit* limit) {
+    return __all_sync(0xffffffffu, mbar_wait(bar, parity, limit));
 }
 
 __device__ __forceinline__ uint32_t cluster_rank() {
@@ -121,9 +129,9 @@ __device__ __forceinline__ uint32_t cluster_rank() {
 }
 // The last phase of each of a ring's `slots` barriers (from bar0 on, used `used` times in
 // all, in turn) has completed.
-__device__ __forceinline__ bool ring_ended(uint32_t bar0, int slots, int used, volatile int* abort) {
+__device__ __forceinline__ bool ring_ended(uint32_t bar0, int slots, int used, const volatile Limit* limit) {
     for (int i = used > slots ? used - slots : 0; i < used; ++i)
-        if (!warp_wait(bar0 + 8 * (i % slots), (uint32_t)((i / slots) & 1), abort)) return false;
+        if (!warp_wait(bar0 + 8 * (i % slots), (uint32_t)((i / slots) & 1), limit)) return false;
     return true;
 }
 // Both CTAs have come here.  Nothing that they wrote is ordered by it: a release would
@@ -166,11 +174,11 @@ constexpr int kNotCounted = -1;
 __device__ __forceinline__ void copies_ended(uint32_t bar0, int slots, int mine, int theirs) {
     if (mine == kNotCounted || theirs == kNotCounted) return;
     const int most = max(mine, theirs), both = min(mine, theirs);
-    volatile int never = 0;
+    volatile Limit longest = {kWaitLimitNs, 0};
     for (int i = max(most - slots, 0); i < most; ++i) {
         if (i >= both && (threadIdx.x & 31) == 0) mbar_arrive(bar0 + 8 * (i % slots));
         __syncwarp();
-        warp_wait(bar0 + 8 * (i % slots), (uint32_t)((i / slots) & 1), &never);
+        warp_wait(bar0 + 8 * (i % slots), (uint32_t)((i / slots) & 1), &longest);
     }
 }
 __device__ __forceinline__ void named_sync(int id, int threads) {

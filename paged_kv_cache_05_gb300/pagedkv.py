@@ -737,7 +737,7 @@ def get_device_error(clear=True, stream=None) -> int:
 
 
 def set_decode_wait_limit(ns: int) -> int:
-    """Bound (ns) of the decode kernels' pipeline waits for later launches;
+    """Bound (ns) of the decode and latent attention kernels' pipeline waits for later launches;
     returns the bound it replaces (default 1 s).  Short bounds exist to
     exercise the timeout path."""
     prev = ctypes.c_uint64(0)
