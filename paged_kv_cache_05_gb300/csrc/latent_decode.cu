@@ -658,6 +658,8 @@ __global__ void __launch_bounds__(Cfg<R, TILE>::THREADS, 1)
                 bits = (uint64_t)a.ancestors[g.q0 + i];
                 if (g.qlen < 64) bits &= (1ull << g.qlen) - 1;
             }
+            // the row's weights are 2^(z - m), its scores z at most m + kLift + kRescale:
+            // m is the largest so far, or a little less, lowered by the lift
             float m = -INFINITY;
             uint64_t l2 = 0;                                 // two partial sums
             for (int j = g.j0; j < g.j1; ++j, ++sc) {
@@ -712,17 +714,14 @@ __global__ void __launch_bounds__(Cfg<R, TILE>::THREADS, 1)
                     named_sync(1 + block, 64);
                     top = fmaxf(top, s_x[par][1 - half][rl]);
                     par ^= 1;
-                    if (top > m + El<T>::kRescale || m == -INFINITY) {
-                        // raised a little past the largest for lifted weights, so that
-                        // scores' rounding, whatever their size, takes none past fp16
-                        const float mn = El<T>::kLift > 0.f && top > -INFINITY
-                                             ? fmaf(fabsf(top), 0x1p-22f, top) : top;
-                        if (mn > m) {
-                            alpha = ex2(m - mn);
-                            m = mn;
-                        }
+                    if (top - m > El<T>::kLift + El<T>::kRescale && top > -INFINITY) {
+                        // (rounded up: with scores so large that they are further apart
+                        // than the lift, m is the largest itself, and its weight 1)
+                        const float mn = __fadd_ru(top, -El<T>::kLift);
+                        alpha = ex2(m - mn);
+                        m = mn;
                     }
-                    const float minus = m == -INFINITY ? 0.f : El<T>::kLift - m;
+                    const float minus = m == -INFINITY ? 0.f : -m;
                     const uint64_t minus2 = f2(minus, minus);
                     uint64_t sum[2] = {0, 0};
 #pragma unroll
@@ -857,8 +856,9 @@ __global__ void __launch_bounds__(Cfg<R, TILE>::THREADS, 1)
     }
 }
 
-// Joins the parts of a row tile: with M the largest running max,
-//   out = sum_k 2^(m_k - M) acc_k / sum_k 2^(m_k - M) l_k.
+// Joins the parts of a row tile: with M the largest m of a part,
+//   out = sum_k 2^(m_k - M) acc_k / sum_k 2^(m_k - M) l_k
+// (m: what the row's weights were formed below).
 // blockIdx.x: the pair that left the first part; a block takes 8 rows and 256 elements,
 // a thread 8 elements of a row, in one pass over the parts, kJoinParts of them loaded
 // at a time.
