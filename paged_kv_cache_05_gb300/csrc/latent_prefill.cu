@@ -104,7 +104,8 @@ struct Args {
     const uint16_t* v;
     int64_t v_stride, v_head;
     const int32_t *q_start, *k_start;
-    float scale_log2;
+    float scale_log2;                 // above 0
+    int negative;                     // the scale is below: scores of -q
     int S, H, max_q, max_k, Tq, Tk;
     int pairs, slot_rows;             // rows of a part in the workspace
     int out_v8;                       // out is 32-byte aligned: 32-byte stores
@@ -566,7 +567,7 @@ __global__ void __launch_bounds__(kThreads, 1)
     } else if (warp == 1) {
         // ================================================= scores
         if (rank == 0 && elect_one()) {
-            constexpr uint32_t ID_S = idesc(El<T>::kType, false, kKeys, 256);
+            const uint32_t ID_S = idesc(El<T>::kType, false, kKeys, 256) | (a.negative ? kNegateA : 0);
             const uint64_t dQ = sdesc(sQ, 16, 1024), dK = sdesc(sK, 16, 1024);
             Item it;
             int g = 0, n[2] = {0, 0};        // steps of the run, of each slot
@@ -671,8 +672,7 @@ __global__ void __launch_bounds__(kThreads, 1)
         const uint32_t pfull = at_rank(bar(kPFull + C::PL * x), 0), oread = at_rank(bar(kORead + x), 0);
         Item it;
         int n = 0;                           // steps of this slot
-        const float scale = a.scale_log2;
-        const uint64_t scale2 = f2(scale, scale);
+        const uint64_t scale2 = f2(a.scale_log2, a.scale_log2);
         while (next_item(it)) {
             const int at = (int)rank * 128 + quad * 32;      // the warp's first row of the slot's
             const int mine_rows = x ? it.live1 : it.live0;
@@ -681,6 +681,8 @@ __global__ void __launch_bounds__(kThreads, 1)
             const int64_t slot = pair * 2 + it.slot;
             const int end = it.end(x);
             const bool whole = it.whole();
+            // the row's weights are 2^(z - m), its scores z at most m + kLift + kRescale:
+            // m is the largest so far, or a little less, lowered by the lift
             float m = -INFINITY;
             uint64_t l2 = 0;                                 // two partial sums
             for (int j = it.j0; j < end; ++j, ++n) {
@@ -693,41 +695,41 @@ __global__ void __launch_bounds__(kThreads, 1)
                     uint32_t z[64];
                     ld64(tS, z);
                     ld_wait(z);
-                    // a hidden key's score: lowest of the scaled ones
                     if (it.off + rw + 1 - j * kKeys < kKeys) {
                         const int seen = it.off + row + 1 - j * kKeys;
-                        const uint32_t hide = __float_as_uint(scale < 0.f ? INFINITY : -INFINITY);
 #pragma unroll
                         for (int e = 0; e < 64; ++e)
-                            if (e >= seen) z[e] = hide;
+                            if (e >= seen) z[e] = __float_as_uint(-INFINITY);
                     }
                     float top = __uint_as_float(z[0]), t1 = __uint_as_float(z[1]);
-                    if (scale >= 0.f) {
 #pragma unroll
-                        for (int e = 2; e < 62; e += 4) {
-                            top = max3(top, __uint_as_float(z[e]), __uint_as_float(z[e + 1]));
-                            t1 = max3(t1, __uint_as_float(z[e + 2]), __uint_as_float(z[e + 3]));
-                        }
-                        top = fmaxf(max3(top, __uint_as_float(z[62]), __uint_as_float(z[63])), t1);
-                    } else {
-#pragma unroll
-                        for (int e = 2; e < 64; ++e) top = fminf(top, __uint_as_float(z[e]));
-                        top = fminf(top, t1);
+                    for (int e = 2; e < 62; e += 4) {
+                        top = max3(top, __uint_as_float(z[e]), __uint_as_float(z[e + 1]));
+                        t1 = max3(t1, __uint_as_float(z[e + 2]), __uint_as_float(z[e + 3]));
                     }
-                    // (none where all are hidden: scaled, infinity times the scale)
-                    top = fabsf(top) == INFINITY ? -INFINITY : top * scale;
+                    top = fmaxf(max3(top, __uint_as_float(z[62]), __uint_as_float(z[63])), t1);
+                    top = fabsf(top) == INFINITY ? -INFINITY : __fmul_rn(top, a.scale_log2);
+                    // the scores, scaled and rounded as the largest was: in one operation with
+                    // its subtraction, what its rounding left, up to half a step of a large
+                    // score, would be in every weight
+#pragma unroll
+                    for (int e = 0; e < 32; ++e) {
+                        float p, q;
+                        f2_split(mul2(f2(__uint_as_float(z[2 * e]), __uint_as_float(z[2 * e + 1])),
+                                      scale2),
+                                 p, q);
+                        z[2 * e] = __float_as_uint(p);
+                        z[2 * e + 1] = __float_as_uint(q);
+                    }
                     float alpha = 1.f;
-                    if (top > m + El<T>::kRescale || m == -INFINITY) {
-                        // raised a little past the largest for lifted weights, so that
-                        // scores' rounding, whatever their size, takes none past fp16
-                        const float mn = El<T>::kLift > 0.f && top > -INFINITY
-                                             ? fmaf(fabsf(top), 0x1p-22f, top) : top;
-                        if (mn > m) {
-                            alpha = ex2(m - mn);
-                            m = mn;
-                        }
+                    if (top - m > El<T>::kLift + El<T>::kRescale && top > -INFINITY) {
+                        // (rounded up: with scores so large that they are further apart
+                        // than the lift, m is the largest itself, and its weight 1)
+                        const float mn = __fadd_ru(top, -El<T>::kLift);
+                        alpha = ex2(m - mn);
+                        m = mn;
                     }
-                    const float minus = m == -INFINITY ? 0.f : El<T>::kLift - m;
+                    const float minus = m == -INFINITY ? 0.f : -m;
                     const uint64_t minus2 = f2(minus, minus);
                     uint64_t sum[2] = {0, 0};
 #pragma unroll
@@ -736,9 +738,9 @@ __global__ void __launch_bounds__(kThreads, 1)
 #pragma unroll
                         for (int e = 0; e < 16; ++e) {
                             float p, q;
-                            f2_split(fma2(f2(__uint_as_float(z[32 * c + 2 * e]),
-                                             __uint_as_float(z[32 * c + 2 * e + 1])),
-                                          scale2, minus2),
+                            f2_split(add2_rz(f2(__uint_as_float(z[32 * c + 2 * e]),
+                                                __uint_as_float(z[32 * c + 2 * e + 1])),
+                                             minus2),
                                      p, q);
                             p = ex2(p);
                             q = ex2(q);
@@ -854,8 +856,9 @@ __global__ void __launch_bounds__(kThreads, 1)
     }
 }
 
-// Joins the parts of an item: with M the largest running max,
-//   out = sum_k 2^(m_k - M) acc_k / sum_k 2^(m_k - M) l_k.
+// Joins the parts of an item: with M the largest m of a part,
+//   out = sum_k 2^(m_k - M) acc_k / sum_k 2^(m_k - M) l_k
+// (m: what the row's weights were formed below).
 // blockIdx.x: the pair that left the first part; a block takes 8 rows and 256 / 8
 // eights of elements (N = 64: 32 rows), a thread 8 elements of a row, in one pass over
 // the parts, kJoinParts of them loaded at a time.
@@ -1091,7 +1094,8 @@ pkv_status pkv_latent_attention_prefill(
     a.q_start = query_start;
     a.k_start = key_start;
     // (a hidden score is infinite and stays so under any scale but 0)
-    a.scale_log2 = scale_log2 == 0.f ? FLT_MIN : scale_log2;
+    a.scale_log2 = scale_log2 == 0.f ? FLT_MIN : std::fabs(scale_log2);
+    a.negative = scale_log2 < 0.f;
     a.S = num_seqs;
     a.H = num_heads;
     a.max_q = max_query_len;

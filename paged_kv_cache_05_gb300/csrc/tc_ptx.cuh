@@ -224,7 +224,8 @@ __device__ __forceinline__ uint64_t sdesc(uint32_t addr, uint32_t lbo, uint32_t 
            ((uint64_t)((sbo >> 4) & 0x3FFFu) << 32) | (1ull << 46) | (2ull << 61);
 }
 // Instruction descriptor, kind::f16: fp32 accumulator, A and B both f16 (0) or both
-// bf16 (1), A K-major, B K-major or MN-major, N >> 3, M >> 4.
+// bf16 (1), A K-major, B K-major or MN-major, N >> 3, M >> 4; with kNegateA -A B.
+constexpr uint32_t kNegateA = 1u << 13;
 __host__ __device__ constexpr uint32_t idesc(uint32_t ab_type, bool b_mn_major, int n, int m) {
     return (1u << 4) | (ab_type << 7) | (ab_type << 10) | ((b_mn_major ? 1u : 0u) << 16) |
            ((uint32_t)(n >> 3) << 17) | ((uint32_t)(m >> 4) << 24);
@@ -325,6 +326,13 @@ __device__ __forceinline__ uint64_t fma2(uint64_t a, uint64_t b, uint64_t c) {
 __device__ __forceinline__ uint64_t add2(uint64_t a, uint64_t b) {
     uint64_t d;
     asm("add.rn.f32x2 %0, %1, %2;" : "=l"(d) : "l"(a), "l"(b));
+    return d;
+}
+// Rounded toward zero, which also keeps a product before it an operation of its own: the
+// compiler takes mul2 and add2 together as one fma2, although each says how it rounds.
+__device__ __forceinline__ uint64_t add2_rz(uint64_t a, uint64_t b) {
+    uint64_t d;
+    asm("add.rz.f32x2 %0, %1, %2;" : "=l"(d) : "l"(a), "l"(b));
     return d;
 }
 __device__ __forceinline__ uint64_t mul2(uint64_t a, uint64_t b) {
