@@ -670,9 +670,10 @@ pkv_status pkv_latent_attention_prefill(
  * with ctx < 0 or past the table, 0 < ctx < qlen, qlen past max_query_len or rows
  * outside [0, num_query_tokens) is skipped (PKV_DEVERR_BAD_CONTEXT); a block past
  * the pool is left out (PKV_DEVERR_BAD_BLOCK).  Rows of no sequence are left as they
- * are.  What cached places past a sequence's last token hold does not matter; a
- * visible token with elements that are not finite may show in the sequence's other
- * rows.  num_blocks * block_size must stay below 2^31.
+ * are.  What cached places past a sequence's last token hold does not matter, nor do
+ * drafted tokens that no row of their sequence attends (a tree padded to a fixed
+ * number of rows: bits of 0, slots below 0); an attended token with elements that are
+ * not finite may show in the sequence's other rows.  num_blocks * block_size must stay below 2^31.
  * workspace: device memory of pkv_latent_decode_workspace_size(...) bytes, 256-byte
  * aligned, no initialisation; two calls in flight at once must not share it.
  */

@@ -234,6 +234,50 @@ __device__ __forceinline__ int cache_row(const Args& a, const Seg& g, int t) {
     return id * a.B + (t - b * a.B);
 }
 
+// The values of a step that holds drafted tokens of a tree that no row attends, whose places may
+// hold anything: groups with such places are copied by the warp, zeros in those (a weight of 0
+// does not hide a value that is not finite), the others as ever.  Lane i < 16: group i's row y and
+// which of its 8 tokens to keep; `none`: a row past the pool; vc: slots filled so far.  Returns
+// vc after the step or, if a wait ran out, ~vc as it is by then.  (Not inlined: within the warp's
+// loop it cost calls without trees 2 %.)
+template <class C>
+__device__ __noinline__ int fill_kept(const uint16_t* cache, const CUtensorMap* map, uint32_t bar0,
+                                      uint32_t values, int none, int subs, int y, uint32_t keep, int vc,
+                                      const volatile Limit* limit) {
+    const int lane = threadIdx.x & 31;
+    const int rank = (int)cluster_rank();
+    if (keep == 0) y = -1;
+    const uint32_t parts = __ballot_sync(0xffffffffu, lane < 16 && keep != 0 && keep != 0xffu);
+    for (int v = 0; v < subs; ++v, ++vc) {
+        const int st = vc % C::VS, n = vc / C::VS;
+        if (n > 0 && !warp_wait(bar0 + 8 * (kVEmpty + st), (uint32_t)((n - 1) & 1), limit)) return ~vc;
+        const uint32_t full = at_rank(bar0 + 8 * (kVFull + st), 0);
+        const uint32_t slot = values + st * C::V_SLOT;
+        const uint32_t which = parts >> 4 * v & 15u;
+        for (uint32_t rest = which; rest; rest &= rest - 1) {
+            const int at = __ffs(rest) - 1;
+            const int yt = __shfl_sync(0xffffffffu, y, 4 * v + at);
+            const uint32_t kept = __shfl_sync(0xffffffffu, keep, 4 * v + at);
+            for (int i = lane; i < C::VCH * 64; i += 32) {
+                const int r = i / (C::VCH * 8), c = i - r * (C::VCH * 8);
+                uint4 w = make_uint4(0u, 0u, 0u, 0u);
+                if (yt >= 0 && (kept >> r & 1))
+                    w = *reinterpret_cast<const uint4*>(cache + (int64_t)(yt + r) * C::W +
+                                                        rank * ((C::W - kP) / 2) + c * 8);
+                st_shared_v4(slot + at * C::V_GROUP + (c >> 3) * 1024 + r * 128 + (((c & 7) ^ r) << 4),
+                             w.x, w.y, w.z, w.w);
+            }
+        }
+        fence_async_smem();
+        __syncwarp();
+        if (lane == 0) mbar_expect_tx_cluster(full, (4 - __popc(which)) * C::V_GROUP);
+        __syncwarp();
+        if ((lane >> 2) == v && !(parts >> lane & 1))
+            tma_3d_pair(slot + (lane & 3) * C::V_GROUP, map, 0, y < 0 ? none : y, rank * C::VCH, full);
+    }
+    return vc;
+}
+
 // Either CTA gave up: what is in flight ends before they do, products (by their commits, of
 // which the first CTA keeps count) and copies (counted by roles that gave up; one that did
 // not has seen the last of its ring used).  bar0: the barriers, used0: the phases used of each
@@ -262,6 +306,17 @@ __device__ __noinline__ void end_given_up(uint32_t bar0, uint32_t used0) {
     fence_before();
     __syncthreads();
     cluster_sync();
+}
+
+// Tokens of a group of 8, by bits: those before the sequence's end, `n` tokens on ...
+__device__ __forceinline__ uint32_t kept_of(int n) { return n >= 8 ? 0xffu : n > 0 ? (1u << n) - 1 : 0u; }
+// ... and of them those that are not drafted or that some row of the tree attends (`bits`, each
+// lane those of some rows).  One warp.
+__device__ __noinline__ uint32_t attended(uint64_t bits, int qlen, int n) {
+    const uint64_t gone = ~((uint64_t)__reduce_or_sync(0xffffffffu, (uint32_t)(bits >> 32)) << 32 |
+                            __reduce_or_sync(0xffffffffu, (uint32_t)bits));
+    const int d = qlen - n;                          // the group's first, drafted
+    return kept_of(n) & ~(d >= 64 || d <= -8 ? 0u : d >= 0 ? (uint32_t)(gone >> d) : (uint32_t)(gone << -d));
 }
 
 template <typename T, int R, int TILE>
@@ -458,6 +513,11 @@ __global__ void __launch_bounds__(Cfg<R, TILE>::THREADS, 1)
                 return lane < 16 ? cache_row(a, g, j * kTok + 8 * lane) : -1;
             };
             int y = row_of(g.j0);
+            uint64_t bits[2] = {0, 0};                       // of the lane's rows of a tree
+            if (a.ancestors) {
+                if (lane < g.qlen) bits[0] = (uint64_t)a.ancestors[g.q0 + lane];
+                if (lane + 32 < g.qlen) bits[1] = (uint64_t)a.ancestors[g.q0 + lane + 32];
+            }
             for (int j = g.j0; j < g.j1; ++j) {
                 const int yn = j + 1 < g.j1 ? row_of(j + 1) : -1;
                 const int left = g.ctx - j * kTok;           // tokens of the step and after
@@ -465,6 +525,19 @@ __global__ void __launch_bounds__(Cfg<R, TILE>::THREADS, 1)
                 // a block past the pool is left out
                 if (lane < 16 && y < 0 && 8 * lane < left && rank == 0)
                     atomicOr(a.err, PKV_DEVERR_BAD_BLOCK);
+                if (a.ancestors && left < g.qlen + kTok) {
+                    const uint32_t keep = attended(bits[0] | bits[1], g.qlen, left - 8 * lane);
+                    if (__any_sync(0xffffffffu, lane < 16 && keep != kept_of(left - 8 * lane))) {
+                        vc = fill_kept<C>(a.cache, &tm_v, bar(0), sV, none, subs, y, keep, vc, limit);
+                        if (vc < 0) {
+                            vc = ~vc;
+                            ok = false;
+                            break;
+                        }
+                        y = yn;
+                        continue;
+                    }
+                }
                 // the group that holds the last token and places behind it, whose
                 // values may be anything: copied by the warp, zeros behind the last
                 const int tail = left < kTok && (left & 7) ? left >> 3 : -1;
