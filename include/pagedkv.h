@@ -635,7 +635,8 @@ pkv_status pkv_gather_latent(void* rows, const void* cache, const int32_t* block
  * no memory with the others.  A sequence whose rows leave the tensors, with more
  * than max_query_len rows or max_key_len keys, or with fewer keys than rows is
  * skipped (PKV_DEVERR_BAD_CONTEXT).  Rows of no sequence are left as they are.
- * Values behind a sequence's last key do not reach its rows; a visible token whose
+ * num_seqs, num_query_tokens or max_query_len 0 launches nothing, and no lengths are
+ * looked at.  Values behind a sequence's last key do not reach its rows; a visible token whose
  * score or value is not finite may show in the other rows of its step.
  * workspace: device memory of pkv_latent_prefill_workspace_size(...) bytes, 256-byte
  * aligned, no initialisation; two calls in flight at once must not share it.  0 bytes
@@ -670,7 +671,8 @@ pkv_status pkv_latent_attention_prefill(
  * with ctx < 0 or past the table, 0 < ctx < qlen, qlen past max_query_len or rows
  * outside [0, num_query_tokens) is skipped (PKV_DEVERR_BAD_CONTEXT); a block past
  * the pool is left out (PKV_DEVERR_BAD_BLOCK).  Rows of no sequence are left as they
- * are.  What cached places past a sequence's last token hold does not matter, nor do
+ * are.  num_seqs, num_query_tokens or max_query_len 0 launches nothing, and no lengths
+ * are looked at.  What cached places past a sequence's last token hold does not matter, nor do
  * drafted tokens that no row of their sequence attends (a tree padded to a fixed
  * number of rows: bits of 0, slots below 0); an attended token with elements that are
  * not finite may show in the sequence's other rows.  num_blocks * block_size must stay below 2^31.

@@ -1043,7 +1043,8 @@ pkv_status pkv_latent_attention_prefill(
                              "at most 2^32",
                              fn, x.name);
     if (num_seqs == 0 || max_query_len == 0 || num_query_tokens == 0) return PKV_OK;
-    if (!out || !q || !query_start || !key_start || !k || !k_rope || !v)
+    // (without keys, no sequence may have a row: the kernel looks at that)
+    if (!out || !q || !query_start || !key_start || (num_key_tokens > 0 && (!k || !k_rope || !v)))
         return pkv::fail(PKV_ERR_INVALID, "%s: NULL pointer", fn);
     if (!aligned(out, 16) || !aligned(q, 16) || !aligned(k, 16) || !aligned(k_rope, 16) ||
         !aligned(v, 16))
@@ -1052,9 +1053,9 @@ pkv_status pkv_latent_attention_prefill(
     if (!aligned(query_start, 4) || !aligned(key_start, 4))
         return pkv::fail(PKV_ERR_INVALID, "%s: misaligned query_start or key_start", fn);
     const int64_t out_bytes = (int64_t)num_query_tokens * num_heads * head_dim * 2;
-    if (num_key_tokens == 0) return PKV_OK;           // no sequence has a row
     for (const auto& x : in)
-        if (overlap(out, out_bytes, x.at,
+        if (x.tokens > 0 &&
+            overlap(out, out_bytes, x.at,
                     ((x.tokens - 1) * x.token + (x.heads - 1) * x.head + x.row) * 2))
             return pkv::fail(PKV_ERR_INVALID, "%s: out overlaps %s", fn, x.name);
     const Layout l = layout(head_dim, max_query_len, max_key_len);
@@ -1077,13 +1078,13 @@ pkv_status pkv_latent_attention_prefill(
 
     const bool bf16 = dtype == PKV_BF16;
     CUtensorMap tq, tk, tr, tv;
+    const int64_t keys = num_key_tokens > 0 ? num_key_tokens : 1;
+    if (num_key_tokens == 0) k = v = k_rope = q;      // (maps of something, never used)
     if (!head_map(&tq, bf16, q, head_dim + kP, num_heads, num_query_tokens, q_stride, q_head_stride,
                   kQBoxRows) ||
-        !head_map(&tk, bf16, k, head_dim, num_heads, num_key_tokens, k_stride, k_head_stride,
-                  kBoxRows) ||
-        !head_map(&tv, bf16, v, head_dim, num_heads, num_key_tokens, v_stride, v_head_stride,
-                  kBoxRows) ||
-        !head_map(&tr, bf16, k_rope, kP, 1, num_key_tokens, k_rope_stride, kP, kBoxRows))
+        !head_map(&tk, bf16, k, head_dim, num_heads, keys, k_stride, k_head_stride, kBoxRows) ||
+        !head_map(&tv, bf16, v, head_dim, num_heads, keys, v_stride, v_head_stride, kBoxRows) ||
+        !head_map(&tr, bf16, k_rope, kP, 1, keys, k_rope_stride, kP, kBoxRows))
         return pkv::fail(PKV_ERR_CUDA, "%s: tensor maps", fn);
 
     Args a = {};
