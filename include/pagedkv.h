@@ -574,6 +574,11 @@ pkv_status pkv_swap_blocks(void* dst_k_cache, void* dst_v_cache, const void* src
  *   cache   [num_blocks][block_size][latent_dim + rope_dim], one pool
  * latent_dim 256 or 512, rope_dim 64, fp16 or bf16 storage, block_size 8, 16, 32
  * or 64; block tables, context lengths, slots and errors as above.
+ * The block manager's pairs are applied by pkv_copy_blocks and pkv_swap_blocks, which
+ * move whole blocks whatever they hold: a latent pool is one of num_heads =
+ * (latent_dim + rope_dim) / 64 and head_dim 64, two layers' pools are the two of a
+ * call, and a layer alone is passed as both (its blocks are written twice, with the
+ * same bytes).
  * Numerics of both attention calls: scores, the running max, sums and outputs in
  * fp32; a weight 2^(z - m) is rounded once to the storage type for its product with
  * the values (the absorbed form's sum takes it rounded too).  fp16 weights are formed
