@@ -579,10 +579,11 @@ pkv_status pkv_swap_blocks(void* dst_k_cache, void* dst_v_cache, const void* src
  * (latent_dim + rope_dim) / 64 and head_dim 64, two layers' pools are the two of a
  * call, and a layer alone is passed as both (its blocks are written twice, with the
  * same bytes).
- * Numerics of both attention calls: scores, the running max, sums and outputs in
- * fp32; a weight 2^(z - m) is rounded once to the storage type for its product with
- * the values (the absorbed form's sum takes it rounded too).  fp16 weights are formed
- * 2^9 higher: those below 2^-33 of the row's largest add nothing.
+ * Numerics of both attention calls: scores (rounded after the scale; of any finite
+ * size), the running max, sums and outputs in fp32; a weight 2^(z - m) is rounded once
+ * to the storage type for its product with the values (the absorbed form's sum takes
+ * it rounded too).  fp16 weights are formed 2^9 higher: those below 2^-23 of the row's
+ * largest lose bits step by step, those of 2^-34 and less add nothing to an output.
  */
 
 /*
@@ -680,7 +681,8 @@ pkv_status pkv_latent_attention_prefill(
  * are looked at.  What cached places past a sequence's last token hold does not matter, nor do
  * drafted tokens that no row of their sequence attends (a tree padded to a fixed
  * number of rows: bits of 0, slots below 0); an attended token with elements that are
- * not finite may show in the sequence's other rows.  num_blocks * block_size must stay below 2^31.
+ * not finite may show in the sequence's other rows.  num_blocks * block_size is at most
+ * 2^31 - 65.
  * workspace: device memory of pkv_latent_decode_workspace_size(...) bytes, 256-byte
  * aligned, no initialisation; two calls in flight at once must not share it.
  */

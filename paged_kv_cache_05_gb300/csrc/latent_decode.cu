@@ -20,12 +20,14 @@
 // a lane a row, its scores in 128 columns, weights over the scores.
 // A token's row thus comes to each CTA of the pair in part as a key and in part as a
 // value, 17/9 of its bytes in all: the copies' rate into the SMs (10-11 TB/s of boxes
-// of 8 rows, measured) bounds long contexts at 5.8 TB/s of the cache.  A product's
-// instruction of M = 128 takes 66 cycles (measured), 52 of them a step of R = 512.
+// of 8 rows, measured) bounds long contexts at 5.8 TB/s of the cache.  A step of R = 512 is
+// 36 products for S (N = 128, 50 cycles each, measured back to back) and 16 for O (N = 256,
+// 64): 2800 cycles of the 5000 that a step of 128 heads takes; what the rest is has not been
+// measured.
 //
 // Measured (graph of calls, the joining kernel counted): 8 sequences of 8192-32768, 16
-// heads, R 512: 49.4 us (4.0 TB/s of the cache); 64 of 1-2048, 128 heads, R 512: 38.3 us;
-// 33 trees of 13 behind 77-4095, 20 heads, R 256: 30.7 us; one sequence of 500, 16 heads:
+// heads, R 512: 49.8 us (4.0 TB/s of the cache); 64 of 1-2048, 128 heads, R 512: 39.0 us;
+// 33 trees of 13 behind 77-4095, 20 heads, R 256: 31.2 us; one sequence of 500, 16 heads:
 // 9.9 us.  Boxes of 16 and more rows free a step's keys later (53 us for the long ones),
 // one thread issuing a step's boxes in turn 57, prefetches into L2 changed nothing.
 //
@@ -1123,9 +1125,10 @@ pkv_status pkv_latent_attention_decode(
     if (!aligned(workspace, 256))
         return pkv::fail(PKV_ERR_INVALID, "%s: workspace must be 256-byte aligned", fn);
     // R = 256 leaves tensor memory for tiles of 256 rows: half the copies and steps where the
-    // sequences' rows fill them, each step about a fifth longer.  16 sequences of 1000-4000,
-    // 128 heads x 4 tokens: 42.3 us by 128 rows, 34.4 by 256; 32 of 20 heads x 12 42.4 and 34.8;
-    // 32 of 128 heads x 1 27.2 and 32.0; 33 trees of 140 rows on average 31.1 and 31.8.
+    // sequences' rows fill them, each step longer.  16 sequences of 1000-4000, 128 heads x 4
+    // tokens: 42.3 us by 128 rows, 34.4 by 256; 32 of 20 heads x 12 42.4 and 34.8; 32 of 128
+    // heads x 1 27.2 and 32.0; 33 trees of 20-260 rows, 140 on average, 31.1 (818 steps) and
+    // 31.8 (515).  The width is the launch's, so it goes by the call's average.
     const bool wide = latent_dim == 256 &&
                       (int64_t)num_query_tokens * num_heads > (int64_t)192 * num_seqs;
     const int tile = wide ? 256 : 128;

@@ -373,9 +373,10 @@ __device__ __forceinline__ void st_shared_v4(uint32_t a, uint32_t x, uint32_t y,
 // values take them.
 //   kLift     weights are 2^(z - max + kLift)
 //   kRescale  the max is raised past a growth of this, in log2 units
-// fp16 ends at 2^-24: unlifted, weights below 2^-25 of the row's largest would vanish,
-// which many thousands of them beside a large one show; lifted they keep to 2^-34 of
-// it, and the largest stays at 2^(9 + 4) (a little under fp16's 2^16).
+// fp16 ends at 2^-24: unlifted, weights of 2^-25 of the row's largest and less would vanish,
+// which many thousands of them beside a large one show.  Lifted, those above 2^-34 of it
+// count, and those above 2^-23 with all their bits; the largest is at most 2^(9 + 4), of the
+// 2^16 that fp16 ends at.
 template <typename T>
 struct El;
 template <>
