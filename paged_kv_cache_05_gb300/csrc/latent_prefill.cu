@@ -27,9 +27,9 @@
 // Measured (graph of calls, the joining kernel counted): 4 prompts of 1965-2036, 32 heads of
 // 128, bf16: 148 us (1108 TFLOP/s; calls on changing inputs 159 us); 4 chunks of 373-541 after
 // about 4100, 16 heads of 64, fp16: 80 us; one prompt of 61, 16 heads of 128: 7.1 us.  A step
-// of 512 rows takes 1480
-// cycles with N = 64: a softmax warp's chain of loads, mask, max, weights, stores and
-// hand-offs, not its arithmetic (without the exponentials N = 128 takes the same 145 us).
+// of 512 rows takes 1480 cycles with N = 64: a softmax warp's chain of loads, mask, max,
+// weights, stores and hand-offs, not its arithmetic (without the exponentials N = 128 takes
+// as long).
 //
 // The steps of all items are dealt to the pairs in equal runs; parts of an item are left
 // in the workspace and joined by a second kernel.  Where no item has more than
