@@ -355,7 +355,9 @@ pkv_status pkv_paged_attention_decode_noalloc(void* out, const void* q, const vo
  * tiled copies through the block table), fp32 accumulation, one launch, no
  * workspace.  In the products with V, weights keep about 16 bits with bf16 storage;
  * with fp16 they are rounded to 11 bits, those below 2^-14 of the row's largest to
- * 2^-25 of it (many thousands of such weights beside a large one are lost).
+ * 2^-25 of it (many thousands of such weights beside a large one are lost).  A row
+ * whose largest score is past 1.8 * 10^8 in size (fp16; bf16 1.4 * 10^9) may become
+ * infinite, NaN or 0.
  */
 pkv_status pkv_paged_attention_prefill(void* out, const void* q, const void* k_cache,
                                        const void* v_cache, const int32_t* block_tables,
@@ -412,6 +414,8 @@ pkv_status pkv_paged_attention_prefill_write(void* out, const void* q, const voi
  * pkv_paged_attention_prefill could answer -- num_kv_heads == num_heads, no cap,
  * slopes or window -- over at most 8192 tokens of capacity have its results, bit for
  * bit where they are not cut: fp16 weights below 2^-14 of the largest to 2^-25.)
+ * Otherwise an fp16 row whose largest score is past 3 * 10^7 in size loses bits, past
+ * 6 * 10^7 it may become 0.
  * workspace: NULL, or device memory of pkv_prefill_grouped_workspace_size(...)
  * bytes (256-byte aligned, no initialisation; two calls in flight at once must
  * not share it).  With it, batches of few query rows over long contexts (chunks
